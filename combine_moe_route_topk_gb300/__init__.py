@@ -30,6 +30,7 @@ MOE_ERR_TIMEOUT = -5
 
 MOE_BF16, MOE_F32, MOE_FP8E4M3_BLK128 = 0, 1, 2
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+MOE_EXPERT_LINEAR, MOE_EXPERT_SWIGLU = 0, 1  # include/moe_expert.h
 MOE_BIAS_SELECT_ONLY = 0x10  # OR into score_fn: the bias enters the selection key only
 
 STATUS_NAMES = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
@@ -96,6 +97,11 @@ def lib() -> ctypes.CDLL:
             L.moe_combine_rank.argtypes = [D, i32, P, P, P, P, P]
             L.moe_combine_partials.argtypes = [D, P, P, P, P, P, P]
             L.moe_combine_reduce_partials.argtypes = [D, P, P, P, P]
+            L.moe_expert_gemm.argtypes = [D, i32, i32, i32, P, P, P, P, P, P]
+            L.moe_expert_gemm_dgrad.argtypes = [D, i32, i32, P, P, P, P, P]
+            L.moe_expert_gemm_wgrad.argtypes = [D, i32, i32, P, P, P, P, i32, P]
+            L.moe_expert_swiglu_grad.argtypes = [D, i32, P, P, P, P, P]
+            L.moe_expert_gemm_fp8.argtypes = [D, i32, i32, i32, P, P, P, P, P, P, P, P]
             L.moe_read_status.argtypes = [P, P]
             L.moe_take_device_error.argtypes = [P]
             L.moe_selftest_bounded_wait.argtypes = [P, ctypes.c_int64, P]
@@ -106,7 +112,9 @@ def lib() -> ctypes.CDLL:
                        "moe_dispatch_pack", "moe_dispatch_pack_quant", "moe_dispatch_pack_rank",
                        "moe_dispatch_fused", "moe_dispatch_fused_static",
                        "moe_combine", "moe_combine_rank", "moe_combine_partials",
-                       "moe_combine_reduce_partials", "moe_read_status",
+                       "moe_combine_reduce_partials", "moe_expert_gemm", "moe_expert_gemm_dgrad",
+                       "moe_expert_gemm_wgrad", "moe_expert_swiglu_grad", "moe_expert_gemm_fp8",
+                       "moe_read_status",
                        "moe_take_device_error", "moe_selftest_bounded_wait"):
                 getattr(L, fn).restype = i32
             _lib = L
@@ -305,6 +313,79 @@ def dispatch_fused_quant(dims: MoeDims, logits, bias, score_fn, renormalize, x, 
         _ptr(packed_src, s["packed_src_bytes"], "packed_src", i32),
         _ptr(workspace, s["fused_workspace_bytes"], "workspace", optional=dims.N * dims.T == 0),
         _stream(stream)))
+
+
+def _expert_rows(dims: MoeDims) -> int:
+    """Rows of the receive buffers (of every rank's region)."""
+    return dims.N * buffer_sizes(dims)["cap_rows"]
+
+
+def expert_gemm(dims: MoeDims, K: int, F: int, act: int, x, w, expert_offsets, y, pre=None,
+                stream=None):
+    """Each expert's rows times its matrix in bf16: y = x w^T (MOE_EXPERT_LINEAR, y of
+    dims.y_dtype) or silu(g) * u of the gate and up halves (MOE_EXPERT_SWIGLU, y bf16,
+    g and u kept in `pre` where given)."""
+    rows, bf16 = _expert_rows(dims), torch.bfloat16
+    gated = int(act) == MOE_EXPERT_SWIGLU
+    yt = bf16 if gated else _TORCH_DTYPE[dims.y_dtype]
+    _check(lib().moe_expert_gemm(
+        ctypes.byref(dims), int(K), int(F), int(act), _ptr(x, rows * K * 2, "x", bf16),
+        _ptr(w, dims.E * F * K * (4 if gated else 2), "w", bf16),
+        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _ptr(y, rows * F * yt.itemsize, "y", yt),
+        _ptr(pre, rows * F * 4, "pre", bf16, optional=True), _stream(stream)))
+
+
+def expert_gemm_dgrad(dims: MoeDims, K: int, F: int, dy, w, expert_offsets, dx, stream=None):
+    """dx = dy w of each expert's rows (bf16)."""
+    rows, bf16 = _expert_rows(dims), torch.bfloat16
+    _check(lib().moe_expert_gemm_dgrad(
+        ctypes.byref(dims), int(K), int(F), _ptr(dy, rows * F * 2, "dy", bf16),
+        _ptr(w, dims.E * F * K * 2, "w", bf16),
+        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _ptr(dx, rows * K * 2, "dx", bf16), _stream(stream)))
+
+
+def expert_gemm_wgrad(dims: MoeDims, K: int, F: int, dy, x, expert_offsets, dw, stream=None):
+    """dw[e] = dy^T x over e's rows, 0 without any (dw bf16 or f32, written whole)."""
+    rows, bf16 = _expert_rows(dims), torch.bfloat16
+    if dw is not None and dw.dtype not in (bf16, torch.float32):
+        raise ValueError(f"dw must be {bf16} or {torch.float32} (got {dw.dtype})")
+    f32 = dw is not None and dw.dtype == torch.float32
+    _check(lib().moe_expert_gemm_wgrad(
+        ctypes.byref(dims), int(K), int(F), _ptr(dy, rows * F * 2, "dy", bf16),
+        _ptr(x, rows * K * 2, "x", bf16),
+        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _ptr(dw, dims.E * F * K * (4 if f32 else 2), "dw"), MOE_F32 if f32 else MOE_BF16,
+        _stream(stream)))
+
+
+def expert_swiglu_grad(dims: MoeDims, F: int, pre, dh, expert_offsets, dpre, stream=None):
+    """Gradient of silu(g) * u: dpre = (dg, du) from pre = (g, u) and dh (bf16)."""
+    rows, bf16 = _expert_rows(dims), torch.bfloat16
+    _check(lib().moe_expert_swiglu_grad(
+        ctypes.byref(dims), int(F), _ptr(pre, rows * F * 4, "pre", bf16),
+        _ptr(dh, rows * F * 2, "dh", bf16),
+        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _ptr(dpre, rows * F * 4, "dpre", bf16), _stream(stream)))
+
+
+def expert_gemm_fp8(dims: MoeDims, K: int, F: int, act: int, xq, x_scales, wq, w_scales,
+                    expert_offsets, y, y_scales=None, stream=None):
+    """Each expert's rows times its matrix in e4m3 with block scales (1 x 128 for the rows,
+    128 x 128 for the matrices): y of dims.y_dtype (MOE_EXPERT_LINEAR), or silu(g) * u
+    quantised again into codes y and scales y_scales (MOE_EXPERT_SWIGLU)."""
+    rows, f32, u8 = _expert_rows(dims), torch.float32, torch.uint8
+    gated = int(act) == MOE_EXPERT_SWIGLU
+    W = F * (2 if gated else 1)
+    yt = u8 if gated else _TORCH_DTYPE[dims.y_dtype]
+    _check(lib().moe_expert_gemm_fp8(
+        ctypes.byref(dims), int(K), int(F), int(act), _ptr(xq, rows * K, "xq", u8),
+        _ptr(x_scales, rows * (K // 128) * 4, "x_scales", f32), _ptr(wq, dims.E * W * K, "wq", u8),
+        _ptr(w_scales, dims.E * -(-W // 128) * (K // 128) * 4, "w_scales", f32),
+        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _ptr(y, rows * F * yt.itemsize, "y", yt),
+        _ptr(y_scales, rows * (F // 128) * 4, "y_scales", f32, optional=not gated), _stream(stream)))
 
 
 def combine(dims: MoeDims, y, pos, topk_w, out, stream=None):

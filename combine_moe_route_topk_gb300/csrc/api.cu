@@ -5,11 +5,15 @@
 #include <stdlib.h>
 #include <string.h>
 
-#include <cuda.h>  // CUcontext and CUresult only: the two driver calls are fetched at run time
+#include <cuda.h>  // types only: the driver calls are fetched at run time
 
+#include "expert_internal.cuh"
 #include "moe_internal.cuh"
 
 namespace moe {
+
+bool encode_map(CUtensorMap *m, int fp8, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                const uint32_t *box);  // declared for the kernels in tc_ops.cuh
 
 namespace {
 thread_local char g_err[512] = "";
@@ -53,6 +57,35 @@ unsigned long long context_key() {
     unsigned long long id = 0;
     if (fns.get_id(ctx, &id) != CUDA_SUCCESS) return 0;
     return id + 1;  // never 0 for a real context
+}
+
+// Tensor maps of the experts' products.
+bool encode_map(CUtensorMap *m, int fp8, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                const uint32_t *box) {
+    typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const EncodeFn encode = [] {  // initialised once, thread-safe
+        cudaDriverEntryPointQueryResult q;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess || q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    if (encode == nullptr) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return encode(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+                  const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int sm_count() {
@@ -157,6 +190,43 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 int cuda_result(cudaError_t e, const char *what) {
     if (e == cudaSuccess) return MOE_OK;
     return set_error(MOE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+// Checks of the experts' products: dims, the product's own sizes and act.
+// `gated`: the matrices have 2F rows; `elem`: bytes of an operand's element.
+int check_expert(const MoeDims *dims, int K, int F, bool gated, int elem, const int32_t *offsets, Derived *v,
+                 ExpertRows *r, const char *what) {
+    int rc = check_dims(dims, v, what);
+    if (rc != MOE_OK) return rc;
+    if (K < 8 || F < 8 || K % 8 != 0 || F % 8 != 0)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: K=%d and F=%d must be positive multiples of 8", what, K, F);
+    if (K > (1 << 24) || F > (1 << 24))
+        return set_error(MOE_ERR_UNSUPPORTED, "%s: this build supports K, F <= 2^24 (got K=%d F=%d)", what, K, F);
+    const int64_t wide = gated ? 2 * (int64_t)F : F;
+    if (wide * K * elem >= (int64_t)1 << 40)  // the stride of a tensor map
+        return set_error(MOE_ERR_UNSUPPORTED, "%s: a matrix of %lld x %d must stay below 2^40 bytes", what,
+                         (long long)wide, K);
+    const int64_t big = wide > K ? wide : K;
+    if ((v->pairs / 128 + dims->E) * ((big + 127) / 128) > kI32Max ||
+        (int64_t)dims->E * ((wide + 127) / 128) * (((int64_t)K + 127) / 128) > kI32Max)
+        return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles (N*T*R=%lld, E=%d, K=%d, F=%d)", what,
+                         (long long)v->pairs, dims->E, K, F);
+    if (!offsets || !aligned(offsets, 4))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: expert_offsets must be a 4-byte aligned pointer", what);
+    *r = ExpertRows{offsets, dims->E, dims->E / dims->N, v->cap, v->rows_total};
+    return MOE_OK;
+}
+
+bool bad_block_pointers(const void *a, const void *b, const void *c, const char *what, int *rc) {
+    if (!a || !b || !c) {
+        *rc = set_error(MOE_ERR_INVALID_ARG, "%s: a required pointer is NULL", what);
+        return true;
+    }
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(c, 16)) {
+        *rc = set_error(MOE_ERR_INVALID_ARG, "%s: rows, matrices and results must be 16-byte aligned", what);
+        return true;
+    }
+    return false;
 }
 
 }  // namespace
@@ -499,6 +569,93 @@ int moe_dispatch_fused_static(const MoeDims *dims, const float *logits, const fl
                               status, packed_x, packed_scales, packed_src, scratch, stream);
 }
 
+int moe_expert_gemm(const MoeDims *dims, int K, int F, int act, const void *x, const void *w,
+                    const int32_t *expert_offsets, void *y, void *pre, void *stream) {
+    const char *what = "moe_expert_gemm";
+    Derived v;
+    ExpertRows r;
+    int rc = check_expert(dims, K, F, act == MOE_EXPERT_SWIGLU, 2, expert_offsets, &v, &r, what);
+    if (rc != MOE_OK) return rc;
+    if (act != MOE_EXPERT_LINEAR && act != MOE_EXPERT_SWIGLU)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: unknown act %d", what, act);
+    if (act == MOE_EXPERT_LINEAR && pre)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: pre is an output of MOE_EXPERT_SWIGLU only", what);
+    if (v.NT == 0) return MOE_OK;
+    if (bad_block_pointers(x, w, y, what, &rc) || (pre && bad_block_pointers(pre, pre, pre, what, &rc))) return rc;
+    return cuda_result(launch_expert_gemm(r, K, F, act == MOE_EXPERT_SWIGLU, x, w, y, dims->y_dtype == MOE_F32, pre,
+                                          (cudaStream_t)stream),
+                       what);
+}
+
+int moe_expert_gemm_dgrad(const MoeDims *dims, int K, int F, const void *dy, const void *w,
+                          const int32_t *expert_offsets, void *dx, void *stream) {
+    const char *what = "moe_expert_gemm_dgrad";
+    Derived v;
+    ExpertRows r;
+    int rc = check_expert(dims, K, F, false, 2, expert_offsets, &v, &r, what);
+    if (rc != MOE_OK) return rc;
+    if (v.NT == 0) return MOE_OK;
+    if (bad_block_pointers(dy, w, dx, what, &rc)) return rc;
+    return cuda_result(launch_expert_dgrad(r, K, F, dy, w, dx, (cudaStream_t)stream), what);
+}
+
+int moe_expert_gemm_wgrad(const MoeDims *dims, int K, int F, const void *dy, const void *x,
+                          const int32_t *expert_offsets, void *dw, int dw_dtype, void *stream) {
+    const char *what = "moe_expert_gemm_wgrad";
+    Derived v;
+    ExpertRows r;
+    int rc = check_expert(dims, K, F, false, 2, expert_offsets, &v, &r, what);
+    if (rc != MOE_OK) return rc;
+    if (dw_dtype != MOE_BF16 && dw_dtype != MOE_F32)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: dw_dtype must be MOE_BF16 or MOE_F32 (got %d)", what, dw_dtype);
+    if (v.NT == 0) {  // no rows anywhere: every sum is empty
+        if (bad_block_pointers(dw, dw, dw, what, &rc)) return rc;
+        return cuda_result(cudaMemsetAsync(dw, 0, (size_t)dims->E * F * K * (dw_dtype == MOE_F32 ? 4 : 2),
+                                           (cudaStream_t)stream),
+                           what);
+    }
+    if (bad_block_pointers(dy, x, dw, what, &rc)) return rc;
+    return cuda_result(launch_expert_wgrad(r, K, F, dy, x, dw, dw_dtype == MOE_F32, (cudaStream_t)stream), what);
+}
+
+int moe_expert_swiglu_grad(const MoeDims *dims, int F, const void *pre, const void *dh,
+                           const int32_t *expert_offsets, void *dpre, void *stream) {
+    const char *what = "moe_expert_swiglu_grad";
+    Derived v;
+    ExpertRows r;
+    int rc = check_expert(dims, 8, F, false, 2, expert_offsets, &v, &r, what);
+    if (rc != MOE_OK) return rc;
+    if (v.NT == 0) return MOE_OK;
+    if (bad_block_pointers(pre, dh, dpre, what, &rc)) return rc;
+    return cuda_result(launch_expert_swiglu_grad(r, dims->N, F, pre, dh, dpre, (cudaStream_t)stream), what);
+}
+
+int moe_expert_gemm_fp8(const MoeDims *dims, int K, int F, int act, const void *xq, const float *x_scales,
+                        const void *wq, const float *w_scales, const int32_t *expert_offsets, void *y,
+                        float *y_scales, void *stream) {
+    const char *what = "moe_expert_gemm_fp8";
+    Derived v;
+    ExpertRows r;
+    const bool gated = act == MOE_EXPERT_SWIGLU;
+    int rc = check_expert(dims, K, F, gated, 1, expert_offsets, &v, &r, what);
+    if (rc != MOE_OK) return rc;
+    if (act != MOE_EXPERT_LINEAR && !gated) return set_error(MOE_ERR_INVALID_ARG, "%s: unknown act %d", what, act);
+    if (K % 128 != 0 || (gated && F % 128 != 0))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: K=%d, and F=%d of the gated product, must be multiples of 128",
+                         what, K, F);
+    if (!gated && y_scales)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: y_scales is an output of MOE_EXPERT_SWIGLU only", what);
+    if (v.NT == 0) return MOE_OK;
+    if (bad_block_pointers(xq, wq, y, what, &rc)) return rc;
+    if (!x_scales || !w_scales || (gated && !y_scales))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: a required pointer is NULL", what);
+    if (!aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(y_scales, 4))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", what);
+    return cuda_result(launch_expert_gemm_fp8(r, K, F, gated, xq, x_scales, wq, w_scales, y, dims->y_dtype == MOE_F32,
+                                              y_scales, (cudaStream_t)stream),
+                       what);
+}
+
 int moe_selftest_bounded_wait(int32_t *status, int64_t polls, void *stream) {
     g_err[0] = '\0';
     if (!status || !aligned(status, 4))
@@ -514,6 +671,12 @@ int moe_take_device_error(void *stream) {
     g_err[0] = '\0';
     int err = 0;
     cudaError_t e = take_device_error(&err, (cudaStream_t)stream);
+    cudaError_t (*const more[])(int *) = {take_expert_gemm_error, take_expert_wgrad_error, take_expert_fp8_error};
+    for (auto take : more) {  // the stream has been waited for
+        int one = 0;
+        if (e == cudaSuccess) e = take(&one);
+        if (err == 0) err = one;
+    }
     if (e != cudaSuccess) return cuda_result(e, "moe_take_device_error");
     return err;
 }

@@ -1,0 +1,89 @@
+// Gradient of the experts' gated activation h = silu(g) u, on the rows that
+// hold a token: with s = 1 / (1 + exp(-g)),
+//   dg = dh u s (1 + g (1 - s)),  du = dh g s.
+// Five values move per feature (g, u, dh in, dg, du out): bound by HBM.  A
+// block takes whole rows, a thread eight features at a time (16-byte
+// accesses); sums and products in f32, one rounding to bf16.
+#include <cuda_bf16.h>
+
+#include "expert_internal.cuh"
+#include "mem_ops.cuh"
+#include "pdl.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kActThreads = 256;
+
+__device__ __forceinline__ float lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+__device__ __forceinline__ void grad(float g, float u, float dh, float *dg, float *du) {
+    const float s = 1.f / (1.f + expf(-g));
+    *dg = dh * u * s * (1.f + g * (1.f - s));
+    *du = dh * g * s;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Rows of rank d that hold a token: [d cap, d cap + rows(d)).  They are dealt
+// out to blocks (and the thread rows of a block) round robin over all ranks.
+__global__ void __launch_bounds__(kActThreads)
+swiglu_grad_kernel(const int32_t *__restrict__ offsets, int N, int L, int64_t cap, int nvec, const uint4 *__restrict__ pre,
+                   const uint4 *__restrict__ dh, uint4 *__restrict__ dpre) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    int64_t at = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;  // this thread row's next row, counted from rank d's first
+    for (int d = 0; d < N; ++d) {
+        int64_t rows = (int64_t)__ldg(offsets + (d + 1) * L) - __ldg(offsets + d * L);
+        rows = rows < 0 ? 0 : (rows < cap ? rows : cap);
+        for (; at < rows; at += step) {
+            const int64_t row = d * cap + at;
+            const uint4 *g = pre + row * 2 * nvec, *u = g + nvec, *h = dh + row * nvec;
+            uint4 *o = dpre + row * 2 * nvec;
+            for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
+                const uint4 gv = ld_stream(g + c), uv = ld_stream(u + c), hv = ld_stream(h + c);
+                const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w},
+                               hw[4] = {hv.x, hv.y, hv.z, hv.w};
+                uint32_t dg[4], du[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float a0, a1, b0, b1;
+                    grad(lo(gw[i]), lo(uw[i]), lo(hw[i]), &a0, &b0);
+                    grad(hi(gw[i]), hi(uw[i]), hi(hw[i]), &a1, &b1);
+                    dg[i] = bf16x2(a0, a1);
+                    du[i] = bf16x2(b0, b1);
+                }
+                o[c] = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+                o[nvec + c] = make_uint4(du[0], du[1], du[2], du[3]);
+            }
+        }
+        at -= rows;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_expert_swiglu_grad(const ExpertRows &r, int N, int F, const void *pre, const void *dh, void *dpre,
+                                      cudaStream_t stream) {
+    const int nvec = F / 8;
+    int tx = 32;
+    while (tx < nvec && tx < kActThreads) tx *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(tx, kActThreads / tx);
+    const int64_t blocks = (r.rows_total + cfg.blockDim.y - 1) / cfg.blockDim.y, most = (int64_t)sm_count() * 8;
+    cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, swiglu_grad_kernel, r.offsets, N, r.L, r.cap, nvec,
+                              reinterpret_cast<const uint4 *>(pre), reinterpret_cast<const uint4 *>(dh),
+                              reinterpret_cast<uint4 *>(dpre));
+}
+
+}  // namespace moe

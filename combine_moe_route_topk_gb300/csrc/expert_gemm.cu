@@ -1,0 +1,295 @@
+// Products of the experts in bf16, on the layout that dispatch writes: rows
+// of expert e in its rank's receive region times the expert's matrix, and the
+// gradient with respect to the rows.
+//
+//   linear   y[p][f]  = sum_k x[p][k] w[e][f][k]
+//   gated    h[p][f]  = silu(g) u, g|u = sum_k x[p][k] w[e][f | F + f][k]
+//   dgrad    dx[p][k] = sum_f dy[p][f] w[e][f][k]
+//
+// The matrix is the operand with 128 fixed rows of tcgen05.mma (M) and the
+// expert's tokens are its columns (N), so a tile takes as many tokens as the
+// expert has, rounded up to 16, up to 256: an expert with 20 rows pays for
+// 32, and its matrix is read once.  Accumulators are f32 in TMEM, two of
+// 128 x 256 so that a tile's results leave while the next one is computed.
+#include <cuda_bf16.h>
+
+#include "expert_internal.cuh"
+#include "pdl.cuh"
+#include "tc_ops.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kM = 128;        // matrix rows of a tile
+constexpr int kTok = 256;      // most tokens of a tile
+constexpr int kK = 64;         // reduction elements of a stage: one 128-byte line
+constexpr int kBox = 32;       // token rows of one TMA load
+constexpr int kStages = 4;
+constexpr int kBytesA = kM * kK * 2;
+constexpr int kBytesB = kTok * kK * 2;
+constexpr int kStage = kBytesA + kBytesB;
+constexpr int kThreads = 192;  // 4 warps store results, one loads, one issues mma
+
+enum Form { kLinear, kGated, kDgrad };
+
+struct Args {
+    const int32_t *offsets;
+    void *y;
+    __nv_bfloat16 *pre;
+    int64_t cap;
+    int E, L, K, F;  // reduction length, result columns
+};
+
+__host__ __device__ inline int token_tiles(int count) { return (count + kTok - 1) / kTok; }
+
+struct Tile {
+    int e, m0, row, n;  // group, first matrix row (or feature), first token row, tokens
+};
+
+// Tiles of a group: its token tiles (of equal size, so that no tile is left
+// with a few rows) run fastest, so that blocks working at the same time share
+// the matrix rows through L2.
+__device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, int m_step) {
+    Tile r;
+    r.e = find_group(g, E, e, t);
+    const int c = g.count[r.e], nt = token_tiles(c), at = t - g.prefix[r.e];
+    const int size = ((c + nt - 1) / nt + 15) & ~15;
+    const int tt = at % nt;
+    r.m0 = at / nt * m_step;
+    r.row = g.row[r.e] + tt * size;
+    r.n = min(size, c - tt * size);
+    return r;
+}
+
+template <int kForm, bool kF32, bool kSave>
+__global__ void __launch_bounds__(kThreads, 1)
+expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_gave_up;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    int *tables = reinterpret_cast<int *>(smem_raw + (smem - smem_u32(smem_raw)) + kStages * kStage);
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages,
+                   tempty = tfull + 16, done = tempty + 16;
+    volatile int *gave_up = &s_gave_up;
+
+    if (warp == 4) tmem_alloc(smem_u32(&s_tmem), 512);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mb_init(full + 8 * i, 1);
+            mb_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mb_init(tfull + 8 * i, 1);
+            mb_init(tempty + 8 * i, 4);
+        }
+        mb_init(done, 1);
+        s_gave_up = 0;
+        mb_init_fence();
+        tma_prefetch_map(&map_w);
+        tma_prefetch_map(&map_x);
+    }
+    grid_dependency_wait();  // offsets and rows come from earlier kernels
+    grid_launch_dependents();
+    constexpr int kStep = kForm == kGated ? kM / 2 : kM;  // result columns of a tile
+    const int m_tiles = (a.F + kStep - 1) / kStep;
+    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap,
+                                 [&](int c) { return token_tiles(c) * m_tiles; });  // syncs the block
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int tiles = g.prefix[a.E], steps = (a.K + kK - 1) / kK;
+
+    if (warp == 4) {  // loads
+        if (lane == 0) {
+            Ring<kStages> r;
+            int e = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const Tile w = get_tile(g, a.E, e, t, kStep);
+                e = w.e;
+                const int boxes = (w.n + kBox - 1) / kBox;
+                for (int k = 0; k < steps; ++k) {
+                    ok = mb_wait(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                    if (!ok) break;
+                    const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + kBytesA;
+                    mb_expect_tx(bar, kBytesA + boxes * kBox * kK * 2);
+                    if constexpr (kForm == kLinear) {
+                        tma_load_3d(sa, &map_w, bar, k * kK, w.m0, w.e);
+                    } else if constexpr (kForm == kGated) {
+                        tma_load_5d(sa, &map_w, bar, k * kK, 0, 0, w.m0 / 8, w.e);
+                    } else {
+                        tma_load_3d(sa, &map_w, bar, w.m0, k * kK, w.e);
+                        tma_load_3d(sa + kBytesA / 2, &map_w, bar, w.m0 + 64, k * kK, w.e);
+                    }
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(sb + b * kBox * kK * 2, &map_x, bar, k * kK, w.row + b * kBox);
+                    r.next();
+                }
+            }
+            drain_loads(full, r);
+        }
+    } else if (warp == 5) {  // mma
+        if (lane == 0) {
+            Ring<kStages> r;
+            Ring<2> acc;
+            int e = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const Tile w = get_tile(g, a.E, e, t, kStep);
+                e = w.e;
+                const uint32_t desc = mma_desc(1, kForm == kDgrad, false, kM, (w.n + 15) & ~15);
+                const uint32_t d = tmem + acc.slot * kTok;
+                ok = mb_wait(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
+                tc_fence_after();
+                for (int k = 0; k < steps && ok; ++k) {
+                    ok = mb_wait(full + 8 * r.slot, r.phase, gave_up);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem + r.slot * kStage;
+                    // reduction contiguous: 16 elements are 32 bytes of the
+                    // line; else they are 16 lines
+                    const uint64_t da = kForm == kDgrad ? smem_operand(sa, kBytesA / 2, 1024) : smem_operand(sa, 16, 1024);
+                    const uint64_t db = smem_operand(sa + kBytesA, 16, 1024);
+                    constexpr int kStepA = kForm == kDgrad ? 2048 / 16 : 32 / 16;
+#pragma unroll
+                    for (int i = 0; i < kK / 16; ++i)
+                        mma_bf16(d, da + i * kStepA, db + i * 2, desc, (k | i) != 0);
+                    tc_commit(empty + 8 * r.slot);
+                    r.next();
+                }
+                tc_commit(tfull + 8 * acc.slot);
+                acc.next();
+            }
+            tc_commit(done);
+            mb_drain(done, 0);
+        }
+    } else {  // results: warp w holds matrix rows 32w.. of the tile, one per lane
+        Ring<2> acc;
+        int e = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
+            if (!__all_sync(0xffffffffu, mb_wait(tfull + 8 * acc.slot, acc.phase, gave_up))) break;
+            tc_fence_after();
+            const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(warp * 32) << 16);
+            for (int c0 = 0; c0 < w.n; c0 += 16) {
+                uint32_t v[16];
+                tmem_load16(src + c0, v);
+                if constexpr (kForm == kGated) {
+                    // lanes with bit 3 clear hold gate rows, the others the
+                    // up rows of the same features; of a pair of tokens each
+                    // half of the lanes finishes one
+                    const int f = w.m0 + warp * 16 + (lane >> 4) * 8 + (lane & 7), up = (lane >> 3) & 1;
+                    if constexpr (kSave) {
+                        if (f < a.F) {
+                            __nv_bfloat16 *p = a.pre + (int64_t)(w.row + c0) * 2 * a.F + up * a.F + f;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (c0 + j < w.n) p[(int64_t)j * 2 * a.F] = __float2bfloat16_rn(__uint_as_float(v[j]));
+                        }
+                    }
+                    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + (int64_t)(w.row + c0) * a.F + f;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 8);
+                        const float gate = __uint_as_float(up ? got : v[j]), lin = __uint_as_float(up ? v[j + 1] : got);
+                        const float h = gate / (1.f + expf(-gate)) * lin;
+                        if (f < a.F && c0 + j + up < w.n) y[(int64_t)(j + up) * a.F] = __float2bfloat16_rn(h);
+                    }
+                } else {
+                    const int f = w.m0 + warp * 32 + lane;
+                    if (f < a.F) {
+                        const int64_t at = (int64_t)(w.row + c0) * a.F + f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (c0 + j < w.n) {
+                                if constexpr (kF32)
+                                    static_cast<float *>(a.y)[at + (int64_t)j * a.F] = __uint_as_float(v[j]);
+                                else
+                                    static_cast<__nv_bfloat16 *>(a.y)[at + (int64_t)j * a.F] =
+                                        __float2bfloat16_rn(__uint_as_float(v[j]));
+                            }
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mb_arrive(tempty + 8 * acc.slot);
+            acc.next();
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && s_gave_up) record_timeout();
+    if (warp == 4) tmem_free(tmem, 512);
+}
+
+template <int kForm, bool kF32, bool kSave>
+cudaError_t launch(const CUtensorMap &map_w, const CUtensorMap &map_x, const Args &a, cudaStream_t stream) {
+    auto kern = expert_gemm_kernel<kForm, kF32, kSave>;
+    const int smem = 1024 + kStages * kStage + groups_bytes(a.E);
+    static thread_local AttrCache cache;
+    cudaError_t e = cache.allow_smem(reinterpret_cast<const void *>(kern), 1024 + kStages * kStage + groups_bytes(1024));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sm_count());
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, a);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, const void *x, const void *w, void *y,
+                               int y_f32, void *pre, cudaStream_t stream) {
+    CUtensorMap map_w, map_x;
+    const uint64_t row = (uint64_t)K * 2;
+    if (gated) {  // per feature block of 8: 8 gate rows, then its 8 up rows
+        const uint64_t dims[5] = {(uint64_t)K, 8, 2, (uint64_t)F / 8, (uint64_t)r.E};
+        const uint64_t strides[4] = {row, row * F, row * 8, row * F * 2};
+        const uint32_t box[5] = {kK, 8, 2, kM / 16, 1};
+        if (!encode_map(&map_w, 0, 5, w, dims, strides, box)) return cudaErrorInvalidValue;
+    } else {
+        const uint64_t dims[3] = {(uint64_t)K, (uint64_t)F, (uint64_t)r.E};
+        const uint64_t strides[2] = {row, row * F};
+        const uint32_t box[3] = {kK, kM, 1};
+        if (!encode_map(&map_w, 0, 3, w, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    const uint64_t xdims[2] = {(uint64_t)K, (uint64_t)r.rows_total};
+    const uint32_t xbox[2] = {kK, kBox};
+    if (!encode_map(&map_x, 0, 2, x, xdims, &row, xbox)) return cudaErrorInvalidValue;
+    const Args a{r.offsets, y, static_cast<__nv_bfloat16 *>(pre), r.cap, r.E, r.L, K, F};
+    if (gated) return pre ? launch<kGated, false, true>(map_w, map_x, a, stream)
+                          : launch<kGated, false, false>(map_w, map_x, a, stream);
+    return y_f32 ? launch<kLinear, true, false>(map_w, map_x, a, stream)
+                 : launch<kLinear, false, false>(map_w, map_x, a, stream);
+}
+
+cudaError_t launch_expert_dgrad(const ExpertRows &r, int K, int F, const void *dy, const void *w, void *dx,
+                                cudaStream_t stream) {
+    CUtensorMap map_w, map_x;
+    const uint64_t wdims[3] = {(uint64_t)K, (uint64_t)F, (uint64_t)r.E};
+    const uint64_t strides[2] = {(uint64_t)K * 2, (uint64_t)K * 2 * F};
+    const uint32_t wbox[3] = {64, kK, 1};
+    if (!encode_map(&map_w, 0, 3, w, wdims, strides, wbox)) return cudaErrorInvalidValue;
+    const uint64_t xdims[2] = {(uint64_t)F, (uint64_t)r.rows_total}, row = (uint64_t)F * 2;
+    const uint32_t xbox[2] = {kK, kBox};
+    if (!encode_map(&map_x, 0, 2, dy, xdims, &row, xbox)) return cudaErrorInvalidValue;
+    const Args a{r.offsets, dx, nullptr, r.cap, r.E, r.L, F, K};
+    return launch<kDgrad, false, false>(map_w, map_x, a, stream);
+}
+
+cudaError_t take_expert_gemm_error(int *err) { return take_tc_error(err); }
+
+}  // namespace moe

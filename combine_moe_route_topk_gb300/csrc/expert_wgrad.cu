@@ -1,0 +1,230 @@
+// Gradient of the experts' matrices: dw[e][f][k] = sum over e's rows p of
+// dy[p][f] x[p][k], zero for an expert without rows.
+//
+// Both operands have the reduction (the rows) as their outer dimension, so
+// TMA boxes of 64 columns by 64 rows are handed to tcgen05.mma as transposed
+// operands: M = 128 columns of dy, N = 256 columns of x, f32 sums in TMEM.  An
+// expert's rows end anywhere; rows behind them belong to the next expert or
+// hold anything (NaN too), so the mma warp zeroes them in shared memory, in
+// the last block of 64 only and up to the next multiple of 16.
+#include <cuda_bf16.h>
+
+#include "expert_internal.cuh"
+#include "pdl.cuh"
+#include "tc_ops.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kM = 128;  // columns of dy (rows of dw) of a tile
+constexpr int kN = 256;  // columns of x
+constexpr int kP = 64;   // rows of a stage
+constexpr int kBlock = kP * 128;  // bytes of 64 columns of a stage
+constexpr int kStages = 4;
+constexpr int kStage = (kM + kN) / 64 * kBlock;
+constexpr int kThreads = 192;
+
+struct Args {
+    const int32_t *offsets;
+    void *dw;
+    int64_t cap;
+    int E, L, K, F;
+};
+
+template <bool kF32>
+__global__ void __launch_bounds__(kThreads, 1)
+expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x, const Args a) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_gave_up;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char *stages = smem_raw + (smem - smem_u32(smem_raw));
+    int *tables = reinterpret_cast<int *>(stages + kStages * kStage);
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16,
+                   done = tempty + 16;
+    volatile int *gave_up = &s_gave_up;
+
+    if (warp == 4) tmem_alloc(smem_u32(&s_tmem), 512);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mb_init(full + 8 * i, 1);
+            mb_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mb_init(tfull + 8 * i, 1);
+            mb_init(tempty + 8 * i, 4);
+        }
+        mb_init(done, 1);
+        s_gave_up = 0;
+        mb_init_fence();
+        tma_prefetch_map(&map_dy);
+        tma_prefetch_map(&map_x);
+    }
+    grid_dependency_wait();  // offsets and rows come from earlier kernels
+    grid_launch_dependents();
+    const int mt = (a.F + kM - 1) / kM, per = mt * ((a.K + kN - 1) / kN);  // tiles of an expert
+    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, [&](int) { return per; });  // syncs the block
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int tiles = a.E * per;
+
+    if (warp == 4) {  // loads
+        if (lane == 0) {
+            Ring<kStages> r;
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const int e = t / per, at = t % per, m0 = at % mt * kM, n0 = at / mt * kN;
+                const int row = g.row[e], steps = (g.count[e] + kP - 1) / kP;
+                const int mb = min(kM, a.F - m0) > 64 ? 2 : 1, nb = (min(kN, a.K - n0) + 63) / 64;
+                for (int k = 0; k < steps; ++k) {
+                    ok = mb_wait(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                    if (!ok) break;
+                    const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + kM / 64 * kBlock;
+                    mb_expect_tx(bar, (mb + nb) * kBlock);
+                    for (int i = 0; i < mb; ++i) tma_load_2d(sa + i * kBlock, &map_dy, bar, m0 + i * 64, row + k * kP);
+                    for (int i = 0; i < nb; ++i) tma_load_2d(sb + i * kBlock, &map_x, bar, n0 + i * 64, row + k * kP);
+                    r.next();
+                }
+            }
+            drain_loads(full, r);
+        }
+    } else if (warp == 5) {  // mma (the whole warp runs the loop, lane 0 issues)
+        Ring<kStages> r;
+        Ring<2> acc;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const int e = t / per, at = t % per, n0 = at / mt * kN;
+            const int count = g.count[e], steps = (count + kP - 1) / kP;
+            if (steps == 0) continue;  // nothing to sum: the results are zeros
+            const uint32_t desc = mma_desc(1, true, true, kM, (min(kN, a.K - n0) + 15) & ~15);
+            const uint32_t d = tmem + acc.slot * kN;
+            ok = __all_sync(0xffffffffu, mb_wait(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up));
+            tc_fence_after();
+            for (int k = 0; k < steps && ok; ++k) {
+                ok = __all_sync(0xffffffffu, mb_wait(full + 8 * r.slot, r.phase, gave_up));
+                if (!ok) break;
+                const int left = min(kP, count - k * kP), slices = (left + 15) / 16;
+                if (left % 16 != 0) {
+                    const int words = (slices * 16 - left) * 8;  // 16-byte words of the lines behind the last row
+                    for (int i = 0; i < (kM + kN) / 64; ++i) {
+                        uint4 *line = reinterpret_cast<uint4 *>(stages + r.slot * kStage + i * kBlock + left * 128);
+                        for (int j = lane; j < words; j += 32) line[j] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t sa = smem + r.slot * kStage;
+                    const uint64_t da = smem_operand(sa, kBlock, 1024), db = smem_operand(sa + kM / 64 * kBlock, kBlock, 1024);
+                    for (int i = 0; i < slices; ++i)  // 16 rows are 16 lines of 128 bytes
+                        mma_bf16(d, da + i * 128, db + i * 128, desc, (k | i) != 0);
+                    tc_commit(empty + 8 * r.slot);
+                }
+                __syncwarp();
+                r.next();
+            }
+            if (lane == 0) tc_commit(tfull + 8 * acc.slot);
+            __syncwarp();
+            acc.next();
+        }
+        if (lane == 0) {
+            tc_commit(done);
+            mb_drain(done, 0);
+        }
+    } else {  // results: warp w holds rows 32w.. of the tile, one per lane
+        Ring<2> acc;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+            const int e = t / per, at = t % per, m0 = at % mt * kM, n0 = at / mt * kN;
+            const bool some = g.count[e] > 0;
+            if (some) {
+                if (!__all_sync(0xffffffffu, mb_wait(tfull + 8 * acc.slot, acc.phase, gave_up))) break;
+                tc_fence_after();
+            }
+            const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(warp * 32) << 16);
+            const int f = m0 + warp * 32 + lane, n = min(kN, a.K - n0);
+            const int64_t out = ((int64_t)e * a.F + f) * a.K + n0;
+            for (int c0 = 0; c0 < n; c0 += 16) {
+                uint32_t v[16];
+                if (some) {
+                    tmem_load16(src + c0, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = 0u;
+                }
+                if (f >= a.F) continue;
+#pragma unroll
+                for (int j = 0; j < 16; j += 8) {  // K is a multiple of 8
+                    if (c0 + j >= n) continue;
+                    if constexpr (kF32) {
+                        uint4 *p = reinterpret_cast<uint4 *>(static_cast<float *>(a.dw) + out + c0 + j);
+                        p[0] = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        p[1] = make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+                    } else {
+                        uint32_t b[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(v[j + 2 * i]),
+                                                                             __uint_as_float(v[j + 2 * i + 1]));
+                            b[i] = *reinterpret_cast<const uint32_t *>(&two);
+                        }
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dw) + out + c0 + j) =
+                            make_uint4(b[0], b[1], b[2], b[3]);
+                    }
+                }
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mb_arrive(tempty + 8 * acc.slot);
+                acc.next();
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && s_gave_up) record_timeout();
+    if (warp == 4) tmem_free(tmem, 512);
+}
+
+template <bool kF32>
+cudaError_t launch(const CUtensorMap &map_dy, const CUtensorMap &map_x, const Args &a, cudaStream_t stream) {
+    auto kern = expert_wgrad_kernel<kF32>;
+    const int smem = 1024 + kStages * kStage + groups_bytes(a.E);
+    static thread_local AttrCache cache;
+    cudaError_t e = cache.allow_smem(reinterpret_cast<const void *>(kern), 1024 + kStages * kStage + groups_bytes(1024));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sm_count());
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, map_dy, map_x, a);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_wgrad(const ExpertRows &r, int K, int F, const void *dy, const void *x, void *dw, int dw_f32,
+                                cudaStream_t stream) {
+    CUtensorMap map_dy, map_x;
+    const uint32_t box[2] = {64, kP};
+    const uint64_t ydims[2] = {(uint64_t)F, (uint64_t)r.rows_total}, yrow = (uint64_t)F * 2;
+    const uint64_t xdims[2] = {(uint64_t)K, (uint64_t)r.rows_total}, xrow = (uint64_t)K * 2;
+    if (!encode_map(&map_dy, 0, 2, dy, ydims, &yrow, box)) return cudaErrorInvalidValue;
+    if (!encode_map(&map_x, 0, 2, x, xdims, &xrow, box)) return cudaErrorInvalidValue;
+    const Args a{r.offsets, dw, r.cap, r.E, r.L, K, F};
+    return dw_f32 ? launch<true>(map_dy, map_x, a, stream) : launch<false>(map_dy, map_x, a, stream);
+}
+
+cudaError_t take_expert_wgrad_error(int *err) { return take_tc_error(err); }
+
+}  // namespace moe

@@ -1,0 +1,290 @@
+// Tensor-core building blocks of the experts' products: mbarriers with
+// bounded waits, tiled TMA loads, TMEM allocation and loads, tcgen05.mma
+// descriptors, and the schedule of tiles over ragged groups of rows.
+#pragma once
+
+#include <cuda.h>  // CUtensorMap and the encode call's types; the call itself is fetched at run time
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// ---- shared memory and mbarriers -------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mb_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mb_init_fence() {
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void mb_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mb_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mb_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Every wait is bounded: after kPolls polls (each may suspend briefly), or
+// once another warp of the block has given up, it returns false and the
+// block's word `gave_up` is set; each role then leaves its loop, copies in
+// flight are waited for (again bounded), TMEM is freed and the kernel ends.
+constexpr int kPolls = 1 << 20;
+__device__ __forceinline__ bool mb_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    for (int i = 0; i < kPolls; ++i) {
+        if (mb_try(bar, parity)) return true;
+        if ((i & 15) == 15 && *gave_up) return false;
+    }
+    *gave_up = 1;
+    return false;
+}
+__device__ __forceinline__ void mb_drain(uint32_t bar, uint32_t parity) {  // bounded, result not needed
+    for (int i = 0; i < kPolls && !mb_try(bar, parity); ++i) {
+    }
+}
+
+// Position in a ring of kSlots slots: the slot and the parity of its use.
+template <int kSlots>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Waits (bounded) for the last loads into every slot of a ring: r is the
+// producer's position after its last load.  Nothing may still be landing in
+// shared memory when the block ends.
+template <int kSlots>
+__device__ __forceinline__ void drain_loads(uint32_t full, Ring<kSlots> r) {
+    for (int i = 0; i < kSlots; ++i) {
+        mb_drain(full + 8 * r.slot, r.phase ^ 1u);
+        r.next();
+    }
+}
+
+// This translation unit's error word (device symbols are per unit): set by a
+// block whose wait gave up, read and cleared by take_tc_error.
+static __device__ int g_tc_error = 0;
+__device__ __forceinline__ void record_timeout() { atomicCAS(&g_tc_error, 0, MOE_ERR_TIMEOUT); }
+
+// ---- tiled TMA loads ---------------------------------------------------------
+
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1,
+                                            int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1,
+                                            int c2, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, "
+        "%7}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+
+// ---- TMEM and tcgen05.mma ----------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t cols) {  // one whole warp
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {  // the allocating warp
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Arrives on `bar` once every mma this thread has issued so far is done.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+// 32 lanes x 16 columns of 32 bits, complete on return; a warp reaches the
+// 32 lanes of its place in its group of four.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+// The same at two places.
+__device__ __forceinline__ void tmem_load16x2(uint32_t addr0, uint32_t *r, uint32_t addr1, uint32_t *q) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
+        : "r"(addr0), "r"(addr1)
+        : "memory");
+}
+
+// Shared-memory operand with 128-byte swizzle (the layout tiled TMA writes
+// with CU_TENSOR_MAP_SWIZZLE_128B from 1024-byte aligned tiles): groups of
+// eight 128-byte lines are `stride` bytes apart; for an operand whose
+// reduction is not the contiguous dimension, blocks of 64 16-bit elements of
+// the contiguous one are `lead` bytes apart.
+__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: f32 accumulation; formats 0 = f16 / e4m3, 1 = bf16;
+// transposed operands are those whose reduction is not contiguous.
+__host__ __device__ constexpr uint32_t mma_desc(int fmt, bool a_transposed, bool b_transposed, int M, int N) {
+    return (1u << 4) | ((uint32_t)fmt << 7) | ((uint32_t)fmt << 10) | ((uint32_t)a_transposed << 15) |
+           ((uint32_t)b_transposed << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// ---- groups of rows -----------------------------------------------------------
+
+// The experts' rows in the receive regions, one entry per expert, in shared
+// memory: first row, number of rows (what fits the region), and the
+// exclusive prefix sum of their tiles.
+struct Groups {
+    int *row;     // [E]
+    int *count;   // [E]
+    int *prefix;  // [E + 1]
+};
+__host__ __device__ constexpr int groups_bytes(int E) { return ((3 * E + 1) * 4 + 127) / 128 * 128; }
+
+// Fills the tables from expert_offsets; every thread of the block calls it.
+// tiles(count) is the number of tiles of a group.  Offsets that are not an
+// ascending sequence (no output of the count step) give groups that stay
+// inside the regions all the same.
+template <class Tiles>
+__device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restrict__ offsets, int E, int L, int64_t cap,
+                                              Tiles tiles) {
+    Groups g{mem, mem + E, mem + 2 * E};
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        const int d = e / L;
+        const int64_t base = __ldg(offsets + d * L);
+        int64_t lo = (int64_t)__ldg(offsets + e) - base, hi = (int64_t)__ldg(offsets + e + 1) - base;
+        lo = lo < 0 ? 0 : (lo < cap ? lo : cap);
+        hi = hi < lo ? lo : (hi < cap ? hi : cap);
+        g.row[e] = (int)(d * cap + lo);
+        g.count[e] = (int)(hi - lo);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, per = (E + 31) / 32, e0 = lane * per, e1 = min(E, e0 + per);
+        int sum = 0;
+        for (int e = e0; e < e1; ++e) sum += tiles(g.count[e]);
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        if (lane == 31) g.prefix[E] = before;
+        before -= sum;
+        for (int e = e0; e < e1; ++e) {
+            g.prefix[e] = before;
+            before += tiles(g.count[e]);
+        }
+    }
+    __syncthreads();
+    return g;
+}
+
+// The group that holds tile t (prefix[e] <= t < prefix[e + 1]), searched
+// from group e on: tiles are taken in ascending order, so e only grows.
+__device__ __forceinline__ int find_group(const Groups &g, int E, int e, int t) {
+    int step = 1;
+    while (e + step < E && g.prefix[e + step] <= t) {
+        e += step;
+        step <<= 1;
+    }
+    for (step >>= 1; step > 0; step >>= 1)
+        if (e + step < E && g.prefix[e + step] <= t) e += step;
+    return e;
+}
+
+// ---- host side ------------------------------------------------------------------
+
+// Reads and clears this unit's error word (the stream has been waited for).
+static inline cudaError_t take_tc_error(int *err) {
+    cudaError_t e = cudaMemcpyFromSymbol(err, g_tc_error, sizeof(int));
+    if (e != cudaSuccess || *err == 0) return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_tc_error, &zero, sizeof(int));
+}
+
+// Whether a kernel's dynamic shared memory limit has been raised in the
+// current device and context (one object per kernel and host thread).
+struct AttrCache {
+    int dev = -1;
+    unsigned long long ctx = 0;
+    cudaError_t allow_smem(const void *kernel, int bytes) {
+        int now = 0;
+        cudaError_t e = cudaGetDevice(&now);
+        if (e != cudaSuccess) return e;
+        const unsigned long long key = context_key();
+        if (now == dev && key != 0 && key == ctx) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        dev = now;
+        ctx = context_key();
+        return cudaSuccess;
+    }
+};
+
+// Tiled tensor map with 128-byte swizzle and zero fill out of bounds;
+// strides in bytes for dimensions 1.. (false: the driver refused it).
+bool encode_map(CUtensorMap *m, int fp8, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                const uint32_t *box);
+
+}  // namespace moe

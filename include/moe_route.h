@@ -407,9 +407,10 @@ const char *moe_last_error(void);
  * 1.2: moe_dispatch_fused_quant; the fused dispatch's workspace is
  * zero-filled once by the caller (no clearing inside the call) and may be
  * NULL for an empty batch; R up to 32 in the fused dispatch.
+ * 1.3: the experts' products (moe_expert.h).
  * A caller can compare MOE_VERSION (the header it was built against) with
  * moe_version() (the library it loaded). */
-#define MOE_VERSION 10200
+#define MOE_VERSION 10300
 int moe_version(void);
 
 #ifdef __cplusplus

@@ -1,0 +1,163 @@
+"""The experts' products against plain 64-bit products (tolerances: expert_ref)."""
+import pytest
+import torch
+
+import combine_moe_route_topk_gb300 as moe
+import expert_ref as ref
+from expert_ref import BF16_HALF, E4M3_HALF, F32_HALF, Batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from combine_moe_route_topk_gb300 import _build
+    _build.build()
+    yield
+    assert moe.take_device_error() == moe.MOE_OK
+
+
+# N, rows per expert, cap.  One row; tile edges on either side of 16, 32, 64,
+# 128 and 256 rows; empty experts first, last and in between; a region that
+# overflows (inside an expert, and before one); every expert empty.
+ROWS = [
+    (1, [1], 1),
+    (1, [5, 0, 16, 17], 40),
+    (2, [0, 33, 64, 65, 0, 1], 200),
+    (2, [127, 128, 129, 0], 257),
+    (1, [255, 256, 257], 800),
+    (2, [300, 31, 15, 2], 320),     # rank 0 loses 11 rows of its second expert
+    (2, [50, 9, 3, 0], 40),         # rank 0's second expert lies past the region
+    (1, [700], 700),
+    (3, [0, 0, 0], 8),
+    (4, [3, 0, 0, 2, 0, 0, 7, 1], 12),
+]
+SIZES = [(8, 8), (64, 128), (72, 136), (200, 264), (512, 96), (1000, 520)]
+
+
+def _ids(v):
+    return str(v).replace(" ", "")
+
+
+@pytest.mark.parametrize("K,F", SIZES, ids=_ids)
+@pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
+@pytest.mark.parametrize("f32", [False, True])
+def test_linear(N, counts, cap, K, F, f32):
+    b = Batch(N, counts, cap)
+    x, w = b.row_values(K), b.randn(b.E, F, K, scale=K ** -0.5)
+    y = b.out(F, torch.float32 if f32 else torch.bfloat16)
+    moe.expert_gemm(b.dims(moe.MOE_F32 if f32 else moe.MOE_BF16), K, F, moe.MOE_EXPERT_LINEAR, x, w, b.offsets, y)
+    want, mag = ref.product(b, x, w)
+    ref.check(y[b.valid], want[b.valid], ref.sum_error(K, mag)[b.valid], F32_HALF if f32 else BF16_HALF, "y")
+    ref.check_untouched(b, y)
+
+
+@pytest.mark.parametrize("K,F", SIZES, ids=_ids)
+@pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
+@pytest.mark.parametrize("save", [False, True])
+def test_gated(N, counts, cap, K, F, save):
+    b = Batch(N, counts, cap)
+    x, w = b.row_values(K), b.randn(b.E, 2 * F, K, scale=2 * K ** -0.5)
+    y, pre = b.out(F, torch.bfloat16), b.out(2 * F, torch.bfloat16) if save else None
+    moe.expert_gemm(b.dims(), K, F, moe.MOE_EXPERT_SWIGLU, x, w, b.offsets, y, pre)
+    want, mag = ref.product(b, x, w)
+    err = ref.sum_error(K, mag)
+    h, eh = ref.swiglu(want[:, :F], want[:, F:], err[:, :F], err[:, F:])
+    ref.check(y[b.valid], h[b.valid], eh[b.valid], BF16_HALF, "h")
+    ref.check_untouched(b, y)
+    if save:
+        ref.check(pre[b.valid], want[b.valid], err[b.valid], BF16_HALF, "pre")
+        ref.check_untouched(b, pre)
+
+
+@pytest.mark.parametrize("K,F", SIZES, ids=_ids)
+@pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
+def test_dgrad(N, counts, cap, K, F):
+    b = Batch(N, counts, cap)
+    dy, w = b.row_values(F), b.randn(b.E, F, K, scale=K ** -0.5)
+    dx = b.out(K, torch.bfloat16)
+    moe.expert_gemm_dgrad(b.dims(), K, F, dy, w, b.offsets, dx)
+    want, mag = ref.product(b, dy, w.transpose(1, 2))
+    ref.check(dx[b.valid], want[b.valid], ref.sum_error(F, mag)[b.valid], BF16_HALF, "dx")
+    ref.check_untouched(b, dx)
+
+
+@pytest.mark.parametrize("K,F", SIZES, ids=_ids)
+@pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
+@pytest.mark.parametrize("f32", [False, True])
+def test_wgrad(N, counts, cap, K, F, f32):
+    b = Batch(N, counts, cap)
+    dy, x = b.row_values(F), b.row_values(K)
+    dw = torch.full((b.E, F, K), ref.SENTINEL, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    moe.expert_gemm_wgrad(b.dims(), K, F, dy, x, b.offsets, dw)
+    for e in range(b.E):
+        r = b.span(e)
+        d, v = dy[r].double(), x[r].double()
+        ref.check(dw[e], d.t() @ v, ref.sum_error(r.stop - r.start, d.abs().t() @ v.abs()),
+                  F32_HALF if f32 else BF16_HALF, f"dw[{e}]")
+
+
+@pytest.mark.parametrize("F", [8, 136, 264, 2048, 2056])
+@pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
+def test_swiglu_grad(N, counts, cap, F):
+    b = Batch(N, counts, cap)
+    pre, dh = b.row_values(2 * F, scale=3.0), b.row_values(F)
+    if b.valid.any():  # extremes: exp overflows, and the sigmoid is 1
+        first = int(b.valid.nonzero()[0])
+        pre[first, :4] = torch.tensor([-300.0, 300.0, -88.5, 88.5])
+    dpre = b.out(2 * F, torch.bfloat16)
+    moe.expert_swiglu_grad(b.dims(), F, pre, dh, b.offsets, dpre)
+    g, u, d = pre[b.valid, :F].double(), pre[b.valid, F:].double(), dh[b.valid].double()
+    s, t = torch.special.expit(g), torch.special.expit(-g)
+    # s and 1 - s each carry a few f32 units; 1 - s is absolute, times g
+    du_err = 16 * F32_HALF * (d * g * s).abs() + 1e-36 * (d * g).abs()
+    dg_err = 16 * F32_HALF * (d * u * s).abs() * (1 + g.abs()) + 1e-36 * (d * u).abs() * (1 + g.abs())
+    ref.check(dpre[b.valid, :F], d * u * s * (1 + g * t), dg_err, BF16_HALF, "dg")
+    ref.check(dpre[b.valid, F:], d * g * s, du_err, BF16_HALF, "du")
+    ref.check_untouched(b, dpre)
+
+
+def _fp8_operands(b, K, W):
+    x = b.row_values(K)
+    x[~b.valid] = 0
+    xq, xs = ref.quantise(x)
+    xq[~b.valid] = 0x7f  # NaN codes and NaN scales where no token is
+    xs[~b.valid] = float("nan")
+    wq = (torch.randn(b.E, W, K, generator=b.g, device="cuda") * 64).to(torch.float8_e4m3fn).view(torch.uint8)
+    ws = (0.5 + torch.rand(b.E, -(-W // 128), K // 128, generator=b.g, device="cuda")) * (K ** -0.5 / 32)
+    return xq, xs, wq, ws
+
+
+@pytest.mark.parametrize("K,F", [(128, 8), (256, 128), (384, 136), (1152, 264), (640, 520)], ids=_ids)
+@pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
+@pytest.mark.parametrize("f32", [False, True])
+def test_fp8_linear(N, counts, cap, K, F, f32):
+    b = Batch(N, counts, cap)
+    xq, xs, wq, ws = _fp8_operands(b, K, F)
+    y = b.out(F, torch.float32 if f32 else torch.bfloat16)
+    moe.expert_gemm_fp8(b.dims(moe.MOE_F32 if f32 else moe.MOE_BF16), K, F, moe.MOE_EXPERT_LINEAR, xq, xs, wq, ws,
+                        b.offsets, y)
+    want, mag = ref.product(b, ref.dequant_rows(xq, xs), ref.dequant_matrix(wq, ws))
+    ref.check(y[b.valid], want[b.valid], ref.sum_error(K, mag)[b.valid], F32_HALF if f32 else BF16_HALF, "y")
+    ref.check_untouched(b, y)
+
+
+@pytest.mark.parametrize("K,F", [(128, 128), (384, 256), (1152, 384), (640, 640)], ids=_ids)
+@pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
+def test_fp8_gated(N, counts, cap, K, F):
+    b = Batch(N, counts, cap)
+    xq, xs, wq, ws = _fp8_operands(b, K, 2 * F)
+    y = torch.full((b.rows, F), 0xA5, dtype=torch.uint8, device="cuda")
+    ys = b.out(F // 128, torch.float32)
+    moe.expert_gemm_fp8(b.dims(), K, F, moe.MOE_EXPERT_SWIGLU, xq, xs, wq, ws, b.offsets, y, ys)
+    want, mag = ref.product(b, ref.dequant_rows(xq, xs), ref.dequant_matrix(wq, ws))
+    err = ref.sum_error(K, mag)
+    h, eh = ref.swiglu(want[:, :F], want[:, F:], err[:, :F], err[:, F:])
+    h, eh = h[b.valid].unflatten(1, (-1, 128)), eh[b.valid].unflatten(1, (-1, 128))
+    scale = h.abs().amax(2) / 448
+    ref.check(ys[b.valid], scale, eh.amax(2) / 448, 2 * F32_HALF, "scales")
+    got_s = ys[b.valid].double().unsqueeze(2)
+    got = ref.e4m3(y[b.valid]).unflatten(1, (-1, 128)) * got_s
+    ref.check(got, h, eh + got_s * 2.0 ** -10 + 4 * F32_HALF * h.abs(), E4M3_HALF, "codes")
+    ref.check_untouched(b, ys)
+    assert bool((y[~b.valid] == 0xA5).all())
