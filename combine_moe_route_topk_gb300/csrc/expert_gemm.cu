@@ -28,7 +28,10 @@ constexpr int kStages = 4;
 constexpr int kBytesA = kM * kK * 2;
 constexpr int kBytesB = kTok * kK * 2;
 constexpr int kStage = kBytesA + kBytesB;
+constexpr int kBuf = 4096;     // each storing warp's: 32 tokens' results, to be written as whole sectors
 constexpr int kThreads = 192;  // 4 warps store results, one loads, one issues mma
+
+constexpr int kSmem = 1024 + kStages * kStage + 4 * kBuf;
 
 enum Form { kLinear, kGated, kDgrad };
 
@@ -70,7 +73,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    int *tables = reinterpret_cast<int *>(smem_raw + (smem - smem_u32(smem_raw)) + kStages * kStage);
+    const uint32_t buf = smem + kStages * kStage + (warp & 3) * kBuf;
+    int *tables = reinterpret_cast<int *>(smem_raw + (smem - smem_u32(smem_raw)) + kStages * kStage + 4 * kBuf);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages,
                    tempty = tfull + 16, done = tempty + 16;
     volatile int *gave_up = &s_gave_up;
@@ -176,46 +180,76 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             if (!__all_sync(0xffffffffu, mb_wait(tfull + 8 * acc.slot, acc.phase, gave_up))) break;
             tc_fence_after();
             const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(warp * 32) << 16);
-            for (int c0 = 0; c0 < w.n; c0 += 16) {
-                uint32_t v[16];
-                tmem_load16(src + c0, v);
+            for (int c0 = 0; c0 < w.n; c0 += 32) {
+                uint32_t v[32];
+                tmem_load32(src + c0, v);
+                const int left = w.n - c0;
                 if constexpr (kForm == kGated) {
                     // lanes with bit 3 clear hold gate rows, the others the
                     // up rows of the same features; of a pair of tokens each
                     // half of the lanes finishes one
-                    const int f = w.m0 + warp * 16 + (lane >> 4) * 8 + (lane & 7), up = (lane >> 3) & 1;
+                    const int fl = (lane >> 4) * 8 + (lane & 7), up = (lane >> 3) & 1, f0 = w.m0 + warp * 16;
                     if constexpr (kSave) {
-                        if (f < a.F) {
-                            __nv_bfloat16 *p = a.pre + (int64_t)(w.row + c0) * 2 * a.F + up * a.F + f;
+                        const uint32_t to = buf + up * 32 + fl * 2;
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (c0 + j < w.n) p[(int64_t)j * 2 * a.F] = __float2bfloat16_rn(__uint_as_float(v[j]));
+                        for (int j = 0; j < 32; j += 2) {
+                            const uint32_t two = bf16x2(v[j], v[j + 1]);
+                            st_shared16(to + j * 64, two);
+                            st_shared16(to + j * 64 + 64, two >> 16);
                         }
-                    }
-                    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + (int64_t)(w.row + c0) * a.F + f;
+                        __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
+                        for (int i = 0; i < 4; ++i) {
+                            const int tok = i * 8 + lane / 4, half = (lane >> 1) & 1, f = f0 + (lane & 1) * 8;
+                            const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
+                            if (tok < left && f < a.F)
+                                *reinterpret_cast<uint4 *>(a.pre + ((int64_t)(w.row + c0 + tok) * 2 + half) * a.F + f) = q;
+                        }
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
                         const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 8);
                         const float gate = __uint_as_float(up ? got : v[j]), lin = __uint_as_float(up ? v[j + 1] : got);
-                        const float h = gate / (1.f + expf(-gate)) * lin;
-                        if (f < a.F && c0 + j + up < w.n) y[(int64_t)(j + up) * a.F] = __float2bfloat16_rn(h);
+                        const float h = silu_mul(gate, lin);
+                        st_shared16(buf + (j + up) * 32 + fl * 2, bf16x2(__float_as_uint(h), 0u));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int tok = i * 16 + lane / 2, f = f0 + (lane & 1) * 8;
+                        const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
+                        if (tok < left && f < a.F)
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) +
+                                                       (int64_t)(w.row + c0 + tok) * a.F + f) = q;
                     }
                 } else {
-                    const int f = w.m0 + warp * 32 + lane;
-                    if (f < a.F) {
-                        const int64_t at = (int64_t)(w.row + c0) * a.F + f;
+                    // one token's 32 features are 64 (f32: 128) bytes
+                    constexpr int kRow = kF32 ? 128 : 64, kElem = kF32 ? 4 : 2;
+                    if constexpr (kF32) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (c0 + j < w.n) {
-                                if constexpr (kF32)
-                                    static_cast<float *>(a.y)[at + (int64_t)j * a.F] = __uint_as_float(v[j]);
-                                else
-                                    static_cast<__nv_bfloat16 *>(a.y)[at + (int64_t)j * a.F] =
-                                        __float2bfloat16_rn(__uint_as_float(v[j]));
-                            }
+                        for (int j = 0; j < 32; ++j) st_shared32(buf + j * kRow + lane * 4, v[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const uint32_t two = bf16x2(v[j], v[j + 1]);
+                            st_shared16(buf + j * kRow + lane * 2, two);
+                            st_shared16(buf + (j + 1) * kRow + lane * 2, two >> 16);
                         }
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kRow / 16; ++i) {
+                        constexpr int kPer = kRow / 16;  // lanes of a token
+                        const int tok = i * (32 / kPer) + lane / kPer;
+                        const int f = w.m0 + warp * 32 + lane % kPer * (16 / kElem);
+                        const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
+                        if (tok < left && f < a.F)
+                            *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.y) +
+                                                       ((int64_t)(w.row + c0 + tok) * a.F + f) * kElem) = q;
+                    }
                 }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
@@ -234,9 +268,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 template <int kForm, bool kF32, bool kSave>
 cudaError_t launch(const CUtensorMap &map_w, const CUtensorMap &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_gemm_kernel<kForm, kF32, kSave>;
-    const int smem = 1024 + kStages * kStage + groups_bytes(a.E);
+    const int smem = kSmem + groups_bytes(a.E);
     static thread_local AttrCache cache;
-    cudaError_t e = cache.allow_smem(reinterpret_cast<const void *>(kern), 1024 + kStages * kStage + groups_bytes(1024));
+    cudaError_t e = cache.allow_smem(reinterpret_cast<const void *>(kern), kSmem + groups_bytes(1024));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sm_count());

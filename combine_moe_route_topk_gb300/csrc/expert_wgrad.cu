@@ -22,7 +22,9 @@ constexpr int kP = 64;   // rows of a stage
 constexpr int kBlock = kP * 128;  // bytes of 64 columns of a stage
 constexpr int kStages = 4;
 constexpr int kStage = (kM + kN) / 64 * kBlock;
+constexpr int kBuf = 4096;  // each storing warp's: 128 bytes of its 32 rows
 constexpr int kThreads = 192;
+constexpr int kSmem = 1024 + kStages * kStage + 4 * kBuf;
 
 struct Args {
     const int32_t *offsets;
@@ -41,7 +43,8 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *stages = smem_raw + (smem - smem_u32(smem_raw));
-    int *tables = reinterpret_cast<int *>(stages + kStages * kStage);
+    const uint32_t buf = smem + kStages * kStage + (warp & 3) * kBuf;
+    int *tables = reinterpret_cast<int *>(stages + kStages * kStage + 4 * kBuf);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16,
                    done = tempty + 16;
     volatile int *gave_up = &s_gave_up;
@@ -146,36 +149,44 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                 tc_fence_after();
             }
             const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(warp * 32) << 16);
-            const int f = m0 + warp * 32 + lane, n = min(kN, a.K - n0);
-            const int64_t out = ((int64_t)e * a.F + f) * a.K + n0;
-            for (int c0 = 0; c0 < n; c0 += 16) {
-                uint32_t v[16];
-                if (some) {
-                    tmem_load16(src + c0, v);
-                } else {
+            const int f0 = m0 + warp * 32, n = min(kN, a.K - n0);
+            // 128 bytes of each row at a time, turned in shared memory so that
+            // eight lanes write a row's 128 bytes (chunks of 16 bytes swapped
+            // by row against bank conflicts)
+            constexpr int kCols = kF32 ? 32 : 64, kElem = kF32 ? 4 : 2;
+            for (int c0 = 0; c0 < n; c0 += kCols) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = 0u;
-                }
-                if (f >= a.F) continue;
-#pragma unroll
-                for (int j = 0; j < 16; j += 8) {  // K is a multiple of 8
-                    if (c0 + j >= n) continue;
-                    if constexpr (kF32) {
-                        uint4 *p = reinterpret_cast<uint4 *>(static_cast<float *>(a.dw) + out + c0 + j);
-                        p[0] = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                        p[1] = make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+                for (int h = 0; h < kCols / 32; ++h) {
+                    uint32_t v[32];
+                    if (some) {
+                        tmem_load32(src + c0 + 32 * h, v);
                     } else {
-                        uint32_t b[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(v[j + 2 * i]),
-                                                                             __uint_as_float(v[j + 2 * i + 1]));
-                            b[i] = *reinterpret_cast<const uint32_t *>(&two);
-                        }
-                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dw) + out + c0 + j) =
-                            make_uint4(b[0], b[1], b[2], b[3]);
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 16 / kElem) {
+                        uint4 q;
+                        if constexpr (kF32)
+                            q = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        else
+                            q = make_uint4(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]),
+                                           bf16x2(v[j + 4], v[j + 5]), bf16x2(v[j + 6], v[j + 7]));
+                        const int chunk = (32 * h + j) * kElem / 16;
+                        st_shared128(buf + lane * 128 + ((chunk ^ (lane & 7)) * 16), q);
                     }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = i * 4 + lane / 8, chunk = lane & 7;
+                    const uint4 q = ld_shared128(buf + r * 128 + ((chunk ^ (r & 7)) * 16));
+                    const int k = c0 + chunk * 16 / kElem;
+                    if (f0 + r < a.F && k < n)
+                        *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.dw) +
+                                                   (((int64_t)e * a.F + f0 + r) * a.K + n0 + k) * kElem) = q;
+                }
+                __syncwarp();
             }
             if (some) {
                 tc_fence_before();
@@ -196,9 +207,9 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
 template <bool kF32>
 cudaError_t launch(const CUtensorMap &map_dy, const CUtensorMap &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_wgrad_kernel<kF32>;
-    const int smem = 1024 + kStages * kStage + groups_bytes(a.E);
+    const int smem = kSmem + groups_bytes(a.E);
     static thread_local AttrCache cache;
-    cudaError_t e = cache.allow_smem(reinterpret_cast<const void *>(kern), 1024 + kStages * kStage + groups_bytes(1024));
+    cudaError_t e = cache.allow_smem(reinterpret_cast<const void *>(kern), kSmem + groups_bytes(1024));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sm_count());

@@ -93,8 +93,11 @@ int moe_expert_swiglu_grad(const MoeDims *dims, int F, const void *pre, const vo
  *            (sum over k in block b of xq[p][k] wq[e][f][k]), every sum in f32
  *   act MOE_EXPERT_LINEAR: y [N*cap][F] of dims->y_dtype, y_scales NULL
  *   act MOE_EXPERT_SWIGLU (F % 128 == 0): h = silu(g) * u in f32, then
- *            quantised as moe_dispatch_pack_quant does: y e4m3 [N*cap][F] and
- *            y_scales f32 [N*cap][F/128], ready to be the next product's rows.
+ *            quantised: per 128 features of a row scale = fl32(amax/448) and code =
+ *            e4m3 of h * fl32(1/scale), to nearest even, saturated (amax = 0:
+ *            scale 0, codes 0): y e4m3 [N*cap][F] and y_scales f32
+ *            [N*cap][F/128], the layout moe_dispatch_pack_quant writes, ready
+ *            to be the next product's rows.
  * Backward passes use the bf16 calls: the fp8 dispatch is a serving form. */
 int moe_expert_gemm_fp8(const MoeDims *dims, int K, int F, int act, const void *xq, const float *x_scales,
                         const void *wq, const float *w_scales, const int32_t *expert_offsets, void *y,
