@@ -94,6 +94,8 @@ def lib() -> ctypes.CDLL:
                                              P, P, P, P, P]
             L.moe_dispatch_fused_static.argtypes = [D, P, P, i32, i32, P, P, P, P, P, P, P, P, P,
                                                     P, P, P, P, P, P]
+            L.moe_dispatch_fused_quant.argtypes = [D, P, P, i32, i32, P, P, P, P, P, P, P, P, P, P,
+                                                   P, P, P, P, P]
             L.moe_combine_rank.argtypes = [D, i32, P, P, P, P, P]
             L.moe_combine_partials.argtypes = [D, P, P, P, P, P, P]
             L.moe_combine_reduce_partials.argtypes = [D, P, P, P, P]
@@ -110,7 +112,7 @@ def lib() -> ctypes.CDLL:
             L.moe_version.restype = i32
             for fn in ("moe_buffer_sizes", "moe_route_topk", "moe_dispatch_count",
                        "moe_dispatch_pack", "moe_dispatch_pack_quant", "moe_dispatch_pack_rank",
-                       "moe_dispatch_fused", "moe_dispatch_fused_static",
+                       "moe_dispatch_fused", "moe_dispatch_fused_static", "moe_dispatch_fused_quant",
                        "moe_combine", "moe_combine_rank", "moe_combine_partials",
                        "moe_combine_reduce_partials", "moe_expert_gemm", "moe_expert_gemm_dgrad",
                        "moe_expert_gemm_wgrad", "moe_expert_swiglu_grad", "moe_expert_gemm_fp8",
@@ -152,29 +154,32 @@ def buffer_sizes(dims: MoeDims) -> dict:
     return d
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+def _stream(stream) -> int:
+    """The stream's handle (None: the current one), as an integer for a void* argument."""
+    if stream is None:  # the handle without a torch.cuda.Stream object, which costs 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t: torch.Tensor | None, nbytes: int, name: str, dtype=None, optional=False):
+    """t's address, as an integer for a void* argument, once t is seen to fit."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    if not t.is_cuda:
+    dev = t.get_device()  # -1 on the CPU
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    if t.device.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not the current device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-    have = t.numel() * t.element_size()
+    have = t.nbytes
     if have < nbytes:
         raise ValueError(f"{name} holds {have} bytes, needs {nbytes}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def route_topk(dims: MoeDims, logits, bias, score_fn, renormalize, topk_idx, topk_w, stream=None):

@@ -8,12 +8,16 @@
 // the next product reads).
 //
 // The scales are arbitrary f32 numbers, so the tensor core sums one block of
-// 128 at a time (four tcgen05.mma of 32, f32 in TMEM) and eight warps add
-// the blocks up in f32 registers: acc += (sx sw) * block.  As in the bf16
-// product the matrix rows are M; a tile is two blocks of 128 of them (the gate
-// and the up rows of the same features, or neighbours) by up to 128 tokens.
-// Of the last four warps one loads, one issues mma and two multiply the
-// scales of the coming blocks.
+// 128 at a time (four tcgen05.mma of 32, f32 in TMEM, two buffers) and eight
+// warps add the blocks up in f32 registers: acc += (sx sw) * block.  Here the
+// tokens are M, unlike in the bf16 product: a TMEM lane, hence a thread, is
+// then one token, its factor is one register per block of the matrix, and
+// the largest magnitude of a requantised row needs no exchange between lanes.
+// With the matrix rows as M the factors of 16 columns came from shared
+// memory for every 16 sums, which cost as much as the sums (2048 tokens, K =
+// F = 2048, gated: 143 us against 103 without those loads).  A tile is up to
+// 128 tokens by two blocks of 128 matrix rows: the gate and the up rows of
+// the same features, or neighbours.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -24,23 +28,23 @@
 namespace moe {
 namespace {
 
-constexpr int kM = 128;     // matrix rows of a block; a tile has two
-constexpr int kTok = 128;   // most tokens of a tile
+constexpr int kTok = 128;   // tokens of a tile (M)
+constexpr int kBlk = 128;   // matrix rows of a block: one scale
+constexpr int kN = 2 * kBlk;
 constexpr int kK = 128;     // reduction elements of a stage: one scale block, one 128-byte line
 constexpr int kBox = 32;    // token rows of one TMA load
 constexpr int kStages = 4;
-constexpr int kBytesA = kM * kK;  // one block
-constexpr int kBytesB = kTok * kK;
-constexpr int kStage = 2 * kBytesA + kBytesB;
-constexpr int kSlots = 8;   // blocks whose scale products are ready
+constexpr int kBytesA = kTok * kK;
+constexpr int kBytesB = kBlk * kK;  // one block
+constexpr int kStage = kBytesA + 2 * kBytesB;
 constexpr int kGroup = 4;   // blocks whose scales are loaded together
 constexpr int kSumWarps = 8;
-constexpr int kThreads = 32 * (kSumWarps + 4);
-constexpr int kBuf = 1024;  // each summing warp's: 16 tokens' bf16 (8 tokens' f32) results of 32 features
-constexpr int kSmem = 1024 + kStages * kStage + kSumWarps * kBuf;
-// Registers: 384 threads are launched with 168 each; the summing warps take
-// 208, the others give back to 88 (256 * 208 + 128 * 88 = 384 * 168).
+constexpr int kThreads = 32 * (kSumWarps + 4);  // one warp loads, one issues mma, two only share their registers
+// 384 threads are launched with 168 registers each; the summing warps take
+// 208, the others keep 88 (256 * 208 + 128 * 88 = 384 * 168).
 constexpr int kSumRegs = 208, kOtherRegs = 88;
+constexpr int kBuf = 2048;  // each summing warp's: 64 bytes of its 32 tokens' results
+constexpr int kSmem = 1024 + kStages * kStage + kSumWarps * kBuf;
 
 struct Args {
     const int32_t *offsets;
@@ -54,16 +58,17 @@ struct Args {
 __host__ __device__ inline int token_tiles(int count) { return (count + kTok - 1) / kTok; }
 
 struct Tile {
-    int e, m0, row, n;  // group, first result column, first token row, tokens
+    int e, f0, row, n;  // group, first result column, first token row, tokens
 };
 
-__device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, int m_step) {
+// Token tiles of a group (of equal size) run fastest: blocks working at the
+// same time share the matrix rows through L2.
+__device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, int f_step) {
     Tile r;
     r.e = find_group(g, E, e, t);
     const int c = g.count[r.e], nt = token_tiles(c), at = t - g.prefix[r.e];
-    const int size = ((c + nt - 1) / nt + 15) & ~15;
-    const int tt = at % nt;
-    r.m0 = at / nt * m_step;
+    const int size = (c + nt - 1) / nt, tt = at % nt;
+    r.f0 = at / nt * f_step;
     r.row = g.row[r.e] + tt * size;
     r.n = min(size, c - tt * size);
     return r;
@@ -87,26 +92,20 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {  
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ void st_shared8(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 template <bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[2 * kStages + 2 * kSlots + 5];
-    __shared__ __align__(16) float s_fac[kSlots][2][kTok];  // sx * sw of each token, per block of rows
-    __shared__ __align__(16) float s_amax[kTok][4];         // largest |h| of a token in each warp's features
-    __shared__ __align__(16) float s_inv[kTok];             // 1 / scale of its 128 features
+    __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
+    __shared__ float s_amax[2][kTok];  // largest |h| of a token in each half of the features
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t buf = smem + kStages * kStage + (warp & (kSumWarps - 1)) * kBuf;
     int *tables = reinterpret_cast<int *>(smem_raw + (smem - smem_u32(smem_raw)) + kStages * kStage + kSumWarps * kBuf);
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, sfull = empty + 8 * kStages,
-                   sempty = sfull + 8 * kSlots, tfull = sempty + 8 * kSlots, tempty = tfull + 16, done = tempty + 16;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16,
+                   done = tempty + 16;
     volatile int *gave_up = &s_gave_up;
 
     if (warp == kSumWarps) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -114,10 +113,6 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         for (int i = 0; i < kStages; ++i) {
             mb_init(full + 8 * i, 1);
             mb_init(empty + 8 * i, 1);
-        }
-        for (int i = 0; i < kSlots; ++i) {
-            mb_init(sfull + 8 * i, 2);
-            mb_init(sempty + 8 * i, kSumWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mb_init(tfull + 8 * i, 1);
@@ -131,10 +126,10 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     }
     grid_dependency_wait();  // offsets, rows and scales come from earlier kernels
     grid_launch_dependents();
-    constexpr int kStep = kGated ? kM : 2 * kM;  // result columns of a tile
-    const int m_tiles = (a.F + kStep - 1) / kStep;
+    constexpr int kStep = kGated ? kBlk : kN;  // result columns of a tile
+    const int f_tiles = (a.F + kStep - 1) / kStep;
     const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap,
-                                 [&](int c) { return token_tiles(c) * m_tiles; });  // syncs the block
+                                 [&](int c) { return token_tiles(c) * f_tiles; });  // syncs the block
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -142,8 +137,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     const int tiles = g.prefix[a.E], steps = a.K / kK;
     int e = 0;
 
-    if (warp >= kSumWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp >= kSumWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSumWarps) {  // loads
         if (lane == 0) {
             Ring<kStages> r;
@@ -152,16 +146,16 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 const Tile w = get_tile(g, a.E, e, t, kStep);
                 e = w.e;
                 const int boxes = (w.n + kBox - 1) / kBox;
-                const bool two = kGated || w.m0 + kM < a.F;  // the second block of rows exists
+                const bool two = kGated || w.f0 + kBlk < a.F;  // the second block of matrix rows exists
                 for (int k = 0; k < steps; ++k) {
                     ok = mb_wait(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
                     if (!ok) break;
-                    const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + 2 * kBytesA;
-                    mb_expect_tx(bar, (two ? 2 : 1) * kBytesA + boxes * kBox * kK);
-                    tma_load_3d(sa, &map_w, bar, k * kK, w.m0, w.e);
-                    if (two) tma_load_3d(sa + kBytesA, &map_w, bar, k * kK, w.m0 + (kGated ? a.F : kM), w.e);
+                    const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + kBytesA;
+                    mb_expect_tx(bar, (two ? 2 : 1) * kBytesB + boxes * kBox * kK);
+                    tma_load_3d(sb, &map_w, bar, k * kK, w.f0, w.e);
+                    if (two) tma_load_3d(sb + kBytesB, &map_w, bar, k * kK, w.f0 + (kGated ? a.F : kBlk), w.e);
                     for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(sb + b * kBox * kK, &map_x, bar, k * kK, w.row + b * kBox);
+                        tma_load_2d(sa + b * kBox * kK, &map_x, bar, k * kK, w.row + b * kBox);
                     r.next();
                 }
             }
@@ -175,21 +169,18 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const Tile w = get_tile(g, a.E, e, t, kStep);
                 e = w.e;
-                const uint32_t desc = mma_desc(0, false, false, kM, (w.n + 15) & ~15);
-                const int blocks = kGated || w.m0 + kM < a.F ? 2 : 1;
+                const int n = kGated ? kN : min(kN, (a.F - w.f0 + 15) & ~15);
+                const uint32_t desc = mma_desc(0, false, false, kTok, n);
                 for (int k = 0; k < steps; ++k) {
                     ok = mb_wait(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up) &&
                          mb_wait(full + 8 * r.slot, r.phase, gave_up);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t sa = smem + r.slot * kStage;
-                    const uint64_t db = smem_operand(sa + 2 * kBytesA, 16, 1024);
-                    for (int b = 0; b < blocks; ++b) {
-                        const uint64_t da = smem_operand(sa + b * kBytesA, 16, 1024);
-                        const uint32_t d = tmem + acc.slot * 2 * kTok + b * kTok;
+                    const uint64_t da = smem_operand(sa, 16, 1024), db = smem_operand(sa + kBytesA, 16, 1024);
+                    const uint32_t d = tmem + acc.slot * kN;
 #pragma unroll
-                        for (int i = 0; i < kK / 32; ++i) mma_fp8(d, da + i * 2, db + i * 2, desc, i != 0);
-                    }
+                    for (int i = 0; i < kK / 32; ++i) mma_fp8(d, da + i * 2, db + i * 2, desc, i != 0);
                     tc_commit(empty + 8 * r.slot);
                     tc_commit(tfull + 8 * acc.slot);
                     r.next();
@@ -199,206 +190,160 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             tc_commit(done);
             mb_drain(done, 0);
         }
-    } else if (warp >= kSumWarps + 2) {
-        // scale products; the two warps take 64 tokens each, two a lane.  The
-        // next blocks' scales are on their way while these wait for slots.
-        const int t0 = (warp - kSumWarps - 2) * 64 + lane;
-        const int fb = (a.w_rows + kM - 1) / kM;  // blocks of matrix rows
-        Ring<kSlots> s;
-        bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile w = get_tile(g, a.E, e, t, kStep);
-            e = w.e;
-            const bool in0 = t0 < w.n, in1 = t0 + 32 < w.n, two = kGated || w.m0 + kM < a.F;
-            const float *sx = a.x_scales + (int64_t)(w.row + t0) * steps, *sx1 = sx + (int64_t)32 * steps;
-            const float *sw0 = a.w_scales + ((int64_t)w.e * fb + w.m0 / kM) * steps;
-            const float *sw1 = sw0 + (kGated ? (int64_t)(a.F / kM) * steps : steps);
-            float next[kGroup][4];
-            auto load = [&](int k0) {
-#pragma unroll
-                for (int i = 0; i < kGroup; ++i) {
-                    const bool in = k0 + i < steps;
-                    next[i][0] = in && in0 ? __ldg(sx + k0 + i) : 0.f;
-                    next[i][1] = in && in1 ? __ldg(sx1 + k0 + i) : 0.f;
-                    next[i][2] = in ? __ldg(sw0 + k0 + i) : 0.f;
-                    next[i][3] = in && two ? __ldg(sw1 + k0 + i) : 0.f;
-                }
-            };
-            load(0);
-            for (int k0 = 0; k0 < steps && ok; k0 += kGroup) {
-                float now[kGroup][4];
-#pragma unroll
-                for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) now[i][j] = next[i][j];
-                load(k0 + kGroup);
-#pragma unroll
-                for (int i = 0; i < kGroup; ++i) {
-                    if (k0 + i >= steps || !ok) break;
-                    ok = __all_sync(0xffffffffu, mb_wait(sempty + 8 * s.slot, s.phase ^ 1u, gave_up));
-                    if (!ok) break;
-                    s_fac[s.slot][0][t0] = now[i][0] * now[i][2];
-                    s_fac[s.slot][1][t0] = now[i][0] * now[i][3];
-                    s_fac[s.slot][0][t0 + 32] = now[i][1] * now[i][2];
-                    s_fac[s.slot][1][t0 + 32] = now[i][1] * now[i][3];
-                    __syncwarp();
-                    if (lane == 0) mb_arrive(sfull + 8 * s.slot);
-                    s.next();
-                }
-            }
-        }
-    }
-    } else {
+    } else if (warp < kSumWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-        // sums and results: warp w holds the lanes (matrix rows) 32 (w % 4)..
-        // of both blocks and every other chunk of 16 tokens, 2 i + w / 4
+        // sums and results: warp w holds tokens 32 (w % 4).., one per lane,
+        // and 64 columns of both blocks, 64 (w / 4)..
         const int quarter = warp & 3, half = warp >> 2;
-        Ring<kSlots> s;
+        const int fb = (a.w_rows + kBlk - 1) / kBlk;  // blocks of matrix rows
         Ring<2> acc;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             const Tile w = get_tile(g, a.E, e, t, kStep);
             e = w.e;
-            const int chunks = (w.n + 31 - 16 * half) / 32;  // this warp's
-            uint64_t sum[4][2][8];  // [chunk][block][pair of tokens]
+            const bool some = quarter * 32 < w.n, mine = quarter * 32 + lane < w.n;
+            const int64_t row = w.row + quarter * 32 + lane;
+            const bool two = kGated || w.f0 + kBlk < a.F;
+            const float *sx = a.x_scales + row * steps;
+            const float *sw0 = a.w_scales + ((int64_t)w.e * fb + w.f0 / kBlk) * steps;
+            const float *sw1 = sw0 + (kGated ? (int64_t)(a.F / kBlk) * steps : steps);
+            uint64_t sum[2][4][8];  // [block][16 columns][pair]
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[i][b][j] = 0;
-            for (int k = 0; k < steps; ++k) {
-                ok = mb_wait(sfull + 8 * s.slot, s.phase, gave_up) && mb_wait(tfull + 8 * acc.slot, acc.phase, gave_up);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t src = tmem + acc.slot * 2 * kTok + ((uint32_t)(quarter * 32) << 16) + 16 * half;
-                const uint32_t fac = smem_u32(&s_fac[s.slot][0][16 * half]);
-                // the next 16 columns are on their way while these are added
-                uint32_t v[2][16];
-                if (chunks > 0) tmem_load16_async(src, v[0]);
+                    for (int j = 0; j < 8; ++j) sum[b][i][j] = 0;
+            float next0[kGroup], next1[kGroup];  // this token's factors of the coming blocks
+            auto load = [&](int k0) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i < chunks) {
+                for (int i = 0; i < kGroup; ++i) {
+                    const bool in = mine && k0 + i < steps;
+                    const float x = in ? __ldg(sx + k0 + i) : 0.f;
+                    next0[i] = in ? x * __ldg(sw0 + k0 + i) : 0.f;
+                    next1[i] = in && two ? x * __ldg(sw1 + k0 + i) : 0.f;
+                }
+            };
+            if (some) load(0);
+            for (int k0 = 0; k0 < steps && ok; k0 += kGroup) {
+                float now0[kGroup], now1[kGroup];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            tmem_wait16(v[b]);
-                            if (b == 0) tmem_load16_async(src + 32 * i + kTok, v[1]);
-                            else if (i + 1 < chunks) tmem_load16_async(src + 32 * (i + 1), v[0]);
+                for (int i = 0; i < kGroup; ++i) {
+                    now0[i] = next0[i];
+                    now1[i] = next1[i];
+                }
+                if (some) load(k0 + kGroup);
+                const int last = min(kGroup, steps - k0);
+                for (int i = 0; i < last; ++i) {
+                    ok = __all_sync(0xffffffffu, mb_wait(tfull + 8 * acc.slot, acc.phase, gave_up));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (some) {
+                        const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(quarter * 32) << 16) + 64 * half;
+                        const uint64_t f0 = pair(__float_as_uint(now0[0]), __float_as_uint(now0[0])),
+                                       f1 = pair(__float_as_uint(now1[0]), __float_as_uint(now1[0]));
+                        // the next 16 columns are on their way while these are added
+                        uint32_t v[2][16];
+                        tmem_load16_async(src, v[0]);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint4 f = ld_shared128(fac + (b * kTok + 32 * i + 4 * j) * 4);
-                                sum[i][b][2 * j] = fma2(pair(v[b][4 * j], v[b][4 * j + 1]), pair(f.x, f.y), sum[i][b][2 * j]);
-                                sum[i][b][2 * j + 1] =
-                                    fma2(pair(v[b][4 * j + 2], v[b][4 * j + 3]), pair(f.z, f.w), sum[i][b][2 * j + 1]);
-                            }
+                        for (int u = 0; u < 8; ++u) {
+                            tmem_wait16(v[u & 1]);
+                            if (u < 7) tmem_load16_async(src + (u + 1) / 4 * kBlk + (u + 1) % 4 * 16, v[(u + 1) & 1]);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                sum[u / 4][u % 4][j] = fma2(pair(v[u & 1][2 * j], v[u & 1][2 * j + 1]), u < 4 ? f0 : f1,
+                                                            sum[u / 4][u % 4][j]);
                         }
+                        tc_fence_before();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(tempty + 8 * acc.slot);
+                    acc.next();
+#pragma unroll
+                    for (int j = 0; j + 1 < kGroup; ++j) {
+                        now0[j] = now0[j + 1];
+                        now1[j] = now1[j + 1];
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mb_arrive(tempty + 8 * acc.slot);
-                    mb_arrive(sempty + 8 * s.slot);
-                }
-                s.next();
-                acc.next();
             }
             if (!ok) break;
+            if (!some) continue;
             if constexpr (!kGated) {
-                // 16 (f32: 8) tokens at a time through the warp's buffer, to
-                // write whole sectors
-                constexpr int kRow = kF32 ? 128 : 64, kElem = kF32 ? 4 : 2, kPass = kBuf / kRow, kPer = kRow / 16;
+                // 64 bytes of each token's row at a time, turned in shared
+                // memory so that four lanes write them (chunks of 16 bytes
+                // swapped by token against bank conflicts)
+                constexpr int kElem = kF32 ? 4 : 2, kCols = 64 / kElem;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int b = 0; b < 2; ++b) {
+                    const int f0 = w.f0 + b * kBlk + 64 * half;
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
+                    for (int c0 = 0; c0 < 64; c0 += kCols) {
+                        if (f0 + c0 < a.F) {
 #pragma unroll
-                        for (int j0 = 0; j0 < 16; j0 += kPass) {
-                            const int c0 = 16 * (2 * i + half) + j0;
-                            if (c0 < w.n) {
+                            for (int q = 0; q < 4; ++q) {
+                                uint4 v;
+                                if constexpr (kF32) {
+                                    const float2 x = unpair(sum[b][(c0 + 4 * q) / 16][(c0 + 4 * q) % 16 / 2]),
+                                                 y = unpair(sum[b][(c0 + 4 * q) / 16][(c0 + 4 * q) % 16 / 2 + 1]);
+                                    v = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
+                                                   __float_as_uint(y.y));
+                                } else {
+                                    uint32_t p[4];
 #pragma unroll
-                                for (int j = 0; j < kPass; j += 2) {
-                                    const float2 v = unpair(sum[i][b][(j0 + j) / 2]);
-                                    if constexpr (kF32) {
-                                        st_shared32(buf + j * kRow + lane * 4, __float_as_uint(v.x));
-                                        st_shared32(buf + (j + 1) * kRow + lane * 4, __float_as_uint(v.y));
-                                    } else {
-                                        const uint32_t two = bf16x2(__float_as_uint(v.x), __float_as_uint(v.y));
-                                        st_shared16(buf + j * kRow + lane * 2, two);
-                                        st_shared16(buf + (j + 1) * kRow + lane * 2, two >> 16);
+                                    for (int j = 0; j < 4; ++j) {
+                                        const float2 x = unpair(sum[b][(c0 + 8 * q) / 16][(c0 + 8 * q) % 16 / 2 + j]);
+                                        p[j] = bf16x2(__float_as_uint(x.x), __float_as_uint(x.y));
                                     }
+                                    v = make_uint4(p[0], p[1], p[2], p[3]);
                                 }
-                                __syncwarp();
-                                const int f = w.m0 + b * kM + quarter * 32 + lane % kPer * (16 / kElem);
-#pragma unroll
-                                for (int i2 = 0; i2 < kBuf / 512; ++i2) {
-                                    const int tok = i2 * (32 / kPer) + lane / kPer;
-                                    const uint4 q = ld_shared128(buf + i2 * 512 + lane * 16);
-                                    if (c0 + tok < w.n && f < a.F)
-                                        *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.y) +
-                                                                   ((int64_t)(w.row + c0 + tok) * a.F + f) * kElem) = q;
-                                }
-                                __syncwarp();
+                                st_shared128(buf + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16), v);
                             }
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int tok = i * 8 + lane / 4, q = lane & 3;
+                                const uint4 v = ld_shared128(buf + tok * 64 + ((q ^ ((tok >> 1) & 3)) * 16));
+                                const int f = f0 + c0 + q * 16 / kElem;
+                                if (quarter * 32 + tok < w.n && f < a.F)
+                                    *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.y) +
+                                                               ((int64_t)(w.row + quarter * 32 + tok) * a.F + f) * kElem) = v;
+                            }
+                            __syncwarp();
                         }
                     }
                 }
             } else {
                 // h takes the place of the gate's sums; its largest magnitude
-                // over the 128 features of a token: over the warp's 32 by a
-                // warp maximum of the (non-negative) float's bits, then over
-                // the four warps that hold the same tokens
+                // over the token's 128 features joins two warps
+                float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c0 = 16 * (2 * i + half);
-                    if (c0 < w.n) {
-                        uint32_t mine = 0;
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float2 gt = unpair(sum[i][0][j]), up = unpair(sum[i][1][j]);
-                            const uint32_t h0 = __float_as_uint(silu_mul(gt.x, up.x)),
-                                           h1 = __float_as_uint(silu_mul(gt.y, up.y));
-                            sum[i][0][j] = pair(h0, h1);
-                            const uint32_t m0 = __reduce_max_sync(0xffffffffu, h0 & 0x7fffffffu),
-                                           m1 = __reduce_max_sync(0xffffffffu, h1 & 0x7fffffffu);
-                            if (lane == 2 * j) mine = m0;
-                            if (lane == 2 * j + 1) mine = m1;
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 gt = unpair(sum[0][i][j]), up = unpair(sum[1][i][j]);
+                        const float h0 = silu_mul(gt.x, up.x), h1 = silu_mul(gt.y, up.y);
+                        sum[0][i][j] = pair(__float_as_uint(h0), __float_as_uint(h1));
+                        top = fmaxf(top, fmaxf(fabsf(h0), fabsf(h1)));
+                    }
+                s_amax[half][quarter * 32 + lane] = top;
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                top = fmaxf(top, s_amax[half ^ 1][quarter * 32 + lane]);
+                const float scale = __fdiv_rn(top, 448.f), inv = scale == 0.f ? 0.f : __fdiv_rn(1.f, scale);
+                if (mine) {
+                    uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.F + w.f0 + 64 * half;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 h0 = unpair(sum[0][i][2 * j]), h1 = unpair(sum[0][i][2 * j + 1]);
+                            p[j] = e4m3x2(h0.x * inv, h0.y * inv) | (e4m3x2(h1.x * inv, h1.y * inv) << 16);
                         }
-                        if (lane < 16) s_amax[c0 + lane][quarter] = __uint_as_float(mine);
+                        reinterpret_cast<uint4 *>(y)[i] = make_uint4(p[0], p[1], p[2], p[3]);
                     }
+                    if (half == 0) a.y_scales[row * (a.F / kBlk) + w.f0 / kBlk] = scale;
                 }
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-                if (lane < 16) {  // a warp for each of their chunks
-                    const int c = 16 * (2 * quarter + half) + lane;
-                    if (c < w.n) {
-                        const float4 m = *reinterpret_cast<const float4 *>(s_amax[c]);
-                        const float scale = __fdiv_rn(fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)), 448.f);
-                        s_inv[c] = scale == 0.f ? 0.f : __fdiv_rn(1.f, scale);
-                        a.y_scales[(int64_t)(w.row + c) * (a.F / kM) + w.m0 / kM] = scale;
-                    }
-                }
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c0 = 16 * (2 * i + half);
-                    if (c0 < w.n) {  // 16 tokens by 32 features: 512 bytes
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float2 h = unpair(sum[i][0][j]);
-                            const uint32_t two = e4m3x2(h.x * s_inv[c0 + 2 * j], h.y * s_inv[c0 + 2 * j + 1]);
-                            st_shared8(buf + 64 * j + lane, two);
-                            st_shared8(buf + 64 * j + 32 + lane, two >> 8);
-                        }
-                        __syncwarp();
-                        const uint4 q = ld_shared128(buf + lane * 16);
-                        if (c0 + lane / 2 < w.n)
-                            *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.y) +
-                                                       (int64_t)(w.row + c0 + lane / 2) * a.F + w.m0 + quarter * 32 +
-                                                       (lane & 1) * 16) = q;
-                        __syncwarp();
-                    }
-                }
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");  // s_amax is written again
             }
         }
     }
@@ -437,7 +382,7 @@ cudaError_t launch_expert_gemm_fp8(const ExpertRows &r, int K, int F, int gated,
     const int w_rows = gated ? 2 * F : F;
     const uint64_t wdims[3] = {(uint64_t)K, (uint64_t)w_rows, (uint64_t)r.E};
     const uint64_t strides[2] = {(uint64_t)K, (uint64_t)K * w_rows};
-    const uint32_t wbox[3] = {kK, kM, 1};
+    const uint32_t wbox[3] = {kK, kBlk, 1};
     if (!encode_map(&map_w, 1, 3, wq, wdims, strides, wbox)) return cudaErrorInvalidValue;
     const uint64_t xdims[2] = {(uint64_t)K, (uint64_t)r.rows_total}, row = (uint64_t)K;
     const uint32_t xbox[2] = {kK, kBox};
