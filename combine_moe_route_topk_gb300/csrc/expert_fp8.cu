@@ -32,7 +32,6 @@ constexpr int kTok = 128;   // tokens of a tile (M)
 constexpr int kBlk = 128;   // matrix rows of a block: one scale
 constexpr int kN = 2 * kBlk;
 constexpr int kK = 128;     // reduction elements of a stage: one scale block, one 128-byte line
-constexpr int kBox = 32;    // token rows of one TMA load
 constexpr int kStages = 4;
 constexpr int kBytesA = kTok * kK;
 constexpr int kBytesB = kBlk * kK;  // one block
@@ -94,7 +93,7 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low 
 }
 template <bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
-expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
+expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x, const Args a) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
     __shared__ float s_amax[2][kTok];  // largest |h| of a token in each half of the features
@@ -122,7 +121,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         s_gave_up = 0;
         mb_init_fence();
         tma_prefetch_map(&map_w);
-        tma_prefetch_map(&map_x);
+        for (int i = 1; i < 4; ++i) tma_prefetch_map(&map_x.m[i]);
     }
     grid_dependency_wait();  // offsets, rows and scales come from earlier kernels
     grid_launch_dependents();
@@ -145,17 +144,15 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const Tile w = get_tile(g, a.E, e, t, kStep);
                 e = w.e;
-                const int boxes = (w.n + kBox - 1) / kBox;
                 const bool two = kGated || w.f0 + kBlk < a.F;  // the second block of matrix rows exists
                 for (int k = 0; k < steps; ++k) {
                     ok = mb_wait(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
                     if (!ok) break;
                     const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + kBytesA;
-                    mb_expect_tx(bar, (two ? 2 : 1) * kBytesB + boxes * kBox * kK);
+                    mb_expect_tx(bar, (two ? 2 : 1) * kBytesB + rows_loaded(w.n) * 128);
                     tma_load_3d(sb, &map_w, bar, k * kK, w.f0, w.e);
                     if (two) tma_load_3d(sb + kBytesB, &map_w, bar, k * kK, w.f0 + (kGated ? a.F : kBlk), w.e);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(sa + b * kBox * kK, &map_x, bar, k * kK, w.row + b * kBox);
+                    load_rows(sa, map_x, bar, k * kK, w.row, w.n);
                     r.next();
                 }
             }
@@ -356,7 +353,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 }
 
 template <bool kGated, bool kF32>
-cudaError_t launch(const CUtensorMap &map_w, const CUtensorMap &map_x, const Args &a, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap &map_w, const RowMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_fp8_kernel<kGated, kF32>;
     const int smem = kSmem + groups_bytes(a.E);
     static thread_local AttrCache cache;
@@ -378,15 +375,14 @@ cudaError_t launch(const CUtensorMap &map_w, const CUtensorMap &map_x, const Arg
 cudaError_t launch_expert_gemm_fp8(const ExpertRows &r, int K, int F, int gated, const void *xq, const float *x_scales,
                                    const void *wq, const float *w_scales, void *y, int y_f32, float *y_scales,
                                    cudaStream_t stream) {
-    CUtensorMap map_w, map_x;
+    CUtensorMap map_w;
+    RowMaps map_x;
     const int w_rows = gated ? 2 * F : F;
     const uint64_t wdims[3] = {(uint64_t)K, (uint64_t)w_rows, (uint64_t)r.E};
     const uint64_t strides[2] = {(uint64_t)K, (uint64_t)K * w_rows};
     const uint32_t wbox[3] = {kK, kBlk, 1};
     if (!encode_map(&map_w, 1, 3, wq, wdims, strides, wbox)) return cudaErrorInvalidValue;
-    const uint64_t xdims[2] = {(uint64_t)K, (uint64_t)r.rows_total}, row = (uint64_t)K;
-    const uint32_t xbox[2] = {kK, kBox};
-    if (!encode_map(&map_x, 1, 2, xq, xdims, &row, xbox)) return cudaErrorInvalidValue;
+    if (!encode_rows(&map_x, 1, xq, K, r.rows_total)) return cudaErrorInvalidValue;
     const Args a{r.offsets, x_scales, w_scales, y, y_scales, r.cap, r.E, r.L, K, F, w_rows};
     if (gated) return launch<true, false>(map_w, map_x, a, stream);
     return y_f32 ? launch<false, true>(map_w, map_x, a, stream) : launch<false, false>(map_w, map_x, a, stream);

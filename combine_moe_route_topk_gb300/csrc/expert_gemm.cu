@@ -23,7 +23,6 @@ namespace {
 constexpr int kM = 128;        // matrix rows of a tile
 constexpr int kTok = 256;      // most tokens of a tile
 constexpr int kK = 64;         // reduction elements of a stage: one 128-byte line
-constexpr int kBox = 32;       // token rows of one TMA load
 constexpr int kStages = 4;
 constexpr int kBytesA = kM * kK * 2;
 constexpr int kBytesB = kTok * kK * 2;
@@ -66,7 +65,7 @@ __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, i
 
 template <int kForm, bool kF32, bool kSave>
 __global__ void __launch_bounds__(kThreads, 1)
-expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
+expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x, const Args a) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
     __shared__ uint32_t s_tmem;
@@ -93,7 +92,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         s_gave_up = 0;
         mb_init_fence();
         tma_prefetch_map(&map_w);
-        tma_prefetch_map(&map_x);
+        for (int i = 0; i < 4; ++i) tma_prefetch_map(&map_x.m[i]);
     }
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
@@ -115,12 +114,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const Tile w = get_tile(g, a.E, e, t, kStep);
                 e = w.e;
-                const int boxes = (w.n + kBox - 1) / kBox;
                 for (int k = 0; k < steps; ++k) {
                     ok = mb_wait(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
                     if (!ok) break;
                     const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + kBytesA;
-                    mb_expect_tx(bar, kBytesA + boxes * kBox * kK * 2);
+                    mb_expect_tx(bar, kBytesA + rows_loaded(w.n) * 128);
                     if constexpr (kForm == kLinear) {
                         tma_load_3d(sa, &map_w, bar, k * kK, w.m0, w.e);
                     } else if constexpr (kForm == kGated) {
@@ -129,8 +127,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                         tma_load_3d(sa, &map_w, bar, w.m0, k * kK, w.e);
                         tma_load_3d(sa + kBytesA / 2, &map_w, bar, w.m0 + 64, k * kK, w.e);
                     }
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(sb + b * kBox * kK * 2, &map_x, bar, k * kK, w.row + b * kBox);
+                    load_rows(sb, map_x, bar, k * kK, w.row, w.n);
                     r.next();
                 }
             }
@@ -266,7 +263,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 }
 
 template <int kForm, bool kF32, bool kSave>
-cudaError_t launch(const CUtensorMap &map_w, const CUtensorMap &map_x, const Args &a, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap &map_w, const RowMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_gemm_kernel<kForm, kF32, kSave>;
     const int smem = kSmem + groups_bytes(a.E);
     static thread_local AttrCache cache;
@@ -287,7 +284,8 @@ cudaError_t launch(const CUtensorMap &map_w, const CUtensorMap &map_x, const Arg
 
 cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, const void *x, const void *w, void *y,
                                int y_f32, void *pre, cudaStream_t stream) {
-    CUtensorMap map_w, map_x;
+    CUtensorMap map_w;
+    RowMaps map_x;
     const uint64_t row = (uint64_t)K * 2;
     if (gated) {  // per feature block of 8: 8 gate rows, then its 8 up rows
         const uint64_t dims[5] = {(uint64_t)K, 8, 2, (uint64_t)F / 8, (uint64_t)r.E};
@@ -300,9 +298,7 @@ cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, con
         const uint32_t box[3] = {kK, kM, 1};
         if (!encode_map(&map_w, 0, 3, w, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    const uint64_t xdims[2] = {(uint64_t)K, (uint64_t)r.rows_total};
-    const uint32_t xbox[2] = {kK, kBox};
-    if (!encode_map(&map_x, 0, 2, x, xdims, &row, xbox)) return cudaErrorInvalidValue;
+    if (!encode_rows(&map_x, 0, x, K, r.rows_total)) return cudaErrorInvalidValue;
     const Args a{r.offsets, y, static_cast<__nv_bfloat16 *>(pre), r.cap, r.E, r.L, K, F};
     if (gated) return pre ? launch<kGated, false, true>(map_w, map_x, a, stream)
                           : launch<kGated, false, false>(map_w, map_x, a, stream);
@@ -312,14 +308,13 @@ cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, con
 
 cudaError_t launch_expert_dgrad(const ExpertRows &r, int K, int F, const void *dy, const void *w, void *dx,
                                 cudaStream_t stream) {
-    CUtensorMap map_w, map_x;
+    CUtensorMap map_w;
+    RowMaps map_x;
     const uint64_t wdims[3] = {(uint64_t)K, (uint64_t)F, (uint64_t)r.E};
     const uint64_t strides[2] = {(uint64_t)K * 2, (uint64_t)K * 2 * F};
     const uint32_t wbox[3] = {64, kK, 1};
     if (!encode_map(&map_w, 0, 3, w, wdims, strides, wbox)) return cudaErrorInvalidValue;
-    const uint64_t xdims[2] = {(uint64_t)F, (uint64_t)r.rows_total}, row = (uint64_t)F * 2;
-    const uint32_t xbox[2] = {kK, kBox};
-    if (!encode_map(&map_x, 0, 2, dy, xdims, &row, xbox)) return cudaErrorInvalidValue;
+    if (!encode_rows(&map_x, 0, dy, F, r.rows_total)) return cudaErrorInvalidValue;
     const Args a{r.offsets, dx, nullptr, r.cap, r.E, r.L, F, K};
     return launch<kDgrad, false, false>(map_w, map_x, a, stream);
 }

@@ -26,6 +26,13 @@ constexpr int kBuf = 4096;  // each storing warp's: 128 bytes of its 32 rows
 constexpr int kThreads = 192;
 constexpr int kSmem = 1024 + kStages * kStage + 4 * kBuf;
 
+// An operand's columns: whole blocks of 64 are the third dimension of `blocks`,
+// so that one load takes all blocks of a tile; `cols` takes one block and
+// zero-fills behind the last column, for tiles that reach it.
+struct ColumnMaps {
+    CUtensorMap blocks, cols;
+};
+
 struct Args {
     const int32_t *offsets;
     void *dw;
@@ -35,7 +42,7 @@ struct Args {
 
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
-expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x, const Args a) {
+expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_constant__ ColumnMaps map_x, const Args a) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
     __shared__ uint32_t s_tmem;
@@ -62,8 +69,8 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
         mb_init(done, 1);
         s_gave_up = 0;
         mb_init_fence();
-        tma_prefetch_map(&map_dy);
-        tma_prefetch_map(&map_x);
+        tma_prefetch_map(&map_dy.blocks);
+        tma_prefetch_map(&map_x.blocks);
     }
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
@@ -82,14 +89,25 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const int e = t / per, at = t % per, m0 = at % mt * kM, n0 = at / mt * kN;
                 const int row = g.row[e], steps = (g.count[e] + kP - 1) / kP;
+                const bool whole_m = m0 + kM <= a.F, whole_n = n0 + kN <= a.K;
                 const int mb = min(kM, a.F - m0) > 64 ? 2 : 1, nb = (min(kN, a.K - n0) + 63) / 64;
                 for (int k = 0; k < steps; ++k) {
                     ok = mb_wait(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
                     if (!ok) break;
                     const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + kM / 64 * kBlock;
                     mb_expect_tx(bar, (mb + nb) * kBlock);
-                    for (int i = 0; i < mb; ++i) tma_load_2d(sa + i * kBlock, &map_dy, bar, m0 + i * 64, row + k * kP);
-                    for (int i = 0; i < nb; ++i) tma_load_2d(sb + i * kBlock, &map_x, bar, n0 + i * 64, row + k * kP);
+                    if (whole_m) {
+                        tma_load_3d(sa, &map_dy.blocks, bar, 0, row + k * kP, m0 / 64);
+                    } else {
+                        for (int i = 0; i < mb; ++i)
+                            tma_load_2d(sa + i * kBlock, &map_dy.cols, bar, m0 + i * 64, row + k * kP);
+                    }
+                    if (whole_n) {
+                        tma_load_3d(sb, &map_x.blocks, bar, 0, row + k * kP, n0 / 64);
+                    } else {
+                        for (int i = 0; i < nb; ++i)
+                            tma_load_2d(sb + i * kBlock, &map_x.cols, bar, n0 + i * 64, row + k * kP);
+                    }
                     r.next();
                 }
             }
@@ -205,7 +223,7 @@ expert_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
 }
 
 template <bool kF32>
-cudaError_t launch(const CUtensorMap &map_dy, const CUtensorMap &map_x, const Args &a, cudaStream_t stream) {
+cudaError_t launch(const ColumnMaps &map_dy, const ColumnMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_wgrad_kernel<kF32>;
     const int smem = kSmem + groups_bytes(a.E);
     static thread_local AttrCache cache;
@@ -222,16 +240,25 @@ cudaError_t launch(const CUtensorMap &map_dy, const CUtensorMap &map_x, const Ar
     return cudaLaunchKernelEx(&cfg, kern, map_dy, map_x, a);
 }
 
+// `tile`: columns of a tile.  Rows of less than one tile use `cols` alone.
+bool encode_columns(ColumnMaps *m, const void *base, int cols, int64_t rows, int tile) {
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, stride = (uint64_t)cols * 2;
+    const uint32_t box[2] = {64, kP};
+    if (!encode_map(&m->cols, 0, 2, base, dims, &stride, box)) return false;
+    m->blocks = m->cols;
+    if (cols < tile) return true;
+    const uint64_t dims3[3] = {64, (uint64_t)rows, (uint64_t)cols / 64}, strides3[2] = {stride, 128};
+    const uint32_t box3[3] = {64, kP, (uint32_t)tile / 64};
+    return encode_map(&m->blocks, 0, 3, base, dims3, strides3, box3);
+}
+
 }  // namespace
 
 cudaError_t launch_expert_wgrad(const ExpertRows &r, int K, int F, const void *dy, const void *x, void *dw, int dw_f32,
                                 cudaStream_t stream) {
-    CUtensorMap map_dy, map_x;
-    const uint32_t box[2] = {64, kP};
-    const uint64_t ydims[2] = {(uint64_t)F, (uint64_t)r.rows_total}, yrow = (uint64_t)F * 2;
-    const uint64_t xdims[2] = {(uint64_t)K, (uint64_t)r.rows_total}, xrow = (uint64_t)K * 2;
-    if (!encode_map(&map_dy, 0, 2, dy, ydims, &yrow, box)) return cudaErrorInvalidValue;
-    if (!encode_map(&map_x, 0, 2, x, xdims, &xrow, box)) return cudaErrorInvalidValue;
+    ColumnMaps map_dy, map_x;
+    if (!encode_columns(&map_dy, dy, F, r.rows_total, kM) || !encode_columns(&map_x, x, K, r.rows_total, kN))
+        return cudaErrorInvalidValue;
     const Args a{r.offsets, dw, r.cap, r.E, r.L, K, F};
     return dw_f32 ? launch<true>(map_dy, map_x, a, stream) : launch<false>(map_dy, map_x, a, stream);
 }
