@@ -8,9 +8,12 @@
 //
 // The matrix is the operand with 128 fixed rows of tcgen05.mma (M) and the
 // expert's tokens are its columns (N), so a tile takes as many tokens as the
-// expert has, rounded up to 16, up to 256: an expert with 20 rows pays for
+// expert has, rounded up to 32, up to 256: an expert with 20 rows pays for
 // 32, and its matrix is read once.  Accumulators are f32 in TMEM, two of
 // 128 x 256 so that a tile's results leave while the next one is computed.
+// Blocks work in pairs: one tcgen05.mma of the pair multiplies 256 matrix
+// rows by the tile's tokens, each block loading its 128 rows and half the
+// tokens, which halves what the tokens cost in L2 and shared memory.
 #include <cuda_bf16.h>
 
 #include "expert_internal.cuh"
@@ -20,12 +23,12 @@
 namespace moe {
 namespace {
 
-constexpr int kM = 128;        // matrix rows of a tile
+constexpr int kM = 128;        // matrix rows of a block's half of a tile
 constexpr int kTok = 256;      // most tokens of a tile
 constexpr int kK = 64;         // reduction elements of a stage: one 128-byte line
-constexpr int kStages = 4;
+constexpr int kStages = 6;
 constexpr int kBytesA = kM * kK * 2;
-constexpr int kBytesB = kTok * kK * 2;
+constexpr int kBytesB = kTok / 2 * kK * 2;
 constexpr int kStage = kBytesA + kBytesB;
 constexpr int kBuf = 4096;     // each storing warp's: 32 tokens' results, to be written as whole sectors
 constexpr int kThreads = 192;  // 4 warps store results, one loads, one issues mma
@@ -44,6 +47,9 @@ struct Args {
 
 __host__ __device__ inline int token_tiles(int count) { return (count + kTok - 1) / kTok; }
 
+// N of a pair's mma is a multiple of 32.
+__host__ __device__ inline int mma_tokens(int n) { return (n + 31) & ~31; }
+
 struct Tile {
     int e, m0, row, n;  // group, first matrix row (or feature), first token row, tokens
 };
@@ -55,7 +61,7 @@ __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, i
     Tile r;
     r.e = find_group(g, E, e, t);
     const int c = g.count[r.e], nt = token_tiles(c), at = t - g.prefix[r.e];
-    const int size = ((c + nt - 1) / nt + 15) & ~15;
+    const int size = mma_tokens((c + nt - 1) / nt);
     const int tt = at % nt;
     r.m0 = at / nt * m_step;
     r.row = g.row[r.e] + tt * size;
@@ -78,7 +84,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                    tempty = tfull + 16, done = tempty + 16;
     volatile int *gave_up = &s_gave_up;
 
-    if (warp == 4) tmem_alloc(smem_u32(&s_tmem), 512);
+    const uint32_t rank = cluster_rank();
+    if (warp == 4) tmem_alloc_pair(smem_u32(&s_tmem), 512);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mb_init(full + 8 * i, 1);
@@ -86,7 +93,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mb_init(tfull + 8 * i, 1);
-            mb_init(tempty + 8 * i, 4);
+            mb_init(tempty + 8 * i, 8);  // the storing warps of both blocks
         }
         mb_init(done, 1);
         s_gave_up = 0;
@@ -96,12 +103,13 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     }
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
-    constexpr int kStep = kForm == kGated ? kM / 2 : kM;  // result columns of a tile
+    constexpr int kHalf = kForm == kGated ? kM / 2 : kM;  // result columns of a block
+    constexpr int kStep = 2 * kHalf;
     const int m_tiles = (a.F + kStep - 1) / kStep;
     const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap,
                                  [&](int c) { return token_tiles(c) * m_tiles; });  // syncs the block
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();  // barriers and TMEM of both blocks are ready
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const int tiles = g.prefix[a.E], steps = (a.K + kK - 1) / kK;
@@ -111,38 +119,40 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             Ring<kStages> r;
             int e = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
                 const Tile w = get_tile(g, a.E, e, t, kStep);
                 e = w.e;
+                const int m0 = w.m0 + rank * kHalf, half = mma_tokens(w.n) / 2;  // this block's share
+                const int row = w.row + rank * half;
                 for (int k = 0; k < steps; ++k) {
                     ok = mb_wait(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
                     if (!ok) break;
-                    const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + kBytesA;
-                    mb_expect_tx(bar, kBytesA + rows_loaded(w.n) * 128);
+                    const uint32_t bar = at_leader(full + 8 * r.slot), sa = smem + r.slot * kStage, sb = sa + kBytesA;
+                    if (rank == 0) mb_expect_tx(full + 8 * r.slot, 2 * (kBytesA + rows_loaded(half) * 128));
                     if constexpr (kForm == kLinear) {
-                        tma_load_3d(sa, &map_w, bar, k * kK, w.m0, w.e);
+                        tma_load_3d_pair(sa, &map_w, bar, k * kK, m0, w.e);
                     } else if constexpr (kForm == kGated) {
-                        tma_load_5d(sa, &map_w, bar, k * kK, 0, 0, w.m0 / 8, w.e);
+                        tma_load_5d_pair(sa, &map_w, bar, k * kK, 0, 0, m0 / 8, w.e);
                     } else {
-                        tma_load_3d(sa, &map_w, bar, w.m0, k * kK, w.e);
-                        tma_load_3d(sa + kBytesA / 2, &map_w, bar, w.m0 + 64, k * kK, w.e);
+                        tma_load_3d_pair(sa, &map_w, bar, m0, k * kK, w.e);
+                        tma_load_3d_pair(sa + kBytesA / 2, &map_w, bar, m0 + 64, k * kK, w.e);
                     }
-                    load_rows(sb, map_x, bar, k * kK, w.row, w.n);
+                    load_rows_pair(sb, map_x, bar, k * kK, row, half);
                     r.next();
                 }
             }
-            drain_loads(full, r);
+            if (rank == 0) drain_loads(full, r);  // of both blocks
         }
     } else if (warp == 5) {  // mma
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             Ring<kStages> r;
             Ring<2> acc;
             int e = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
                 const Tile w = get_tile(g, a.E, e, t, kStep);
                 e = w.e;
-                const uint32_t desc = mma_desc(1, kForm == kDgrad, false, kM, (w.n + 15) & ~15);
+                const uint32_t desc = mma_desc(1, kForm == kDgrad, false, 2 * kM, mma_tokens(w.n));
                 const uint32_t d = tmem + acc.slot * kTok;
                 ok = mb_wait(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
                 tc_fence_after();
@@ -158,20 +168,20 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     constexpr int kStepA = kForm == kDgrad ? 2048 / 16 : 32 / 16;
 #pragma unroll
                     for (int i = 0; i < kK / 16; ++i)
-                        mma_bf16(d, da + i * kStepA, db + i * 2, desc, (k | i) != 0);
-                    tc_commit(empty + 8 * r.slot);
+                        mma_bf16_pair(d, da + i * kStepA, db + i * 2, desc, (k | i) != 0);
+                    tc_commit_pair(empty + 8 * r.slot);
                     r.next();
                 }
-                tc_commit(tfull + 8 * acc.slot);
+                tc_commit_pair(tfull + 8 * acc.slot);
                 acc.next();
             }
-            tc_commit(done);
+            tc_commit_pair(done);
             mb_drain(done, 0);
         }
     } else {  // results: warp w holds matrix rows 32w.. of the tile, one per lane
         Ring<2> acc;
         int e = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
             const Tile w = get_tile(g, a.E, e, t, kStep);
             e = w.e;
             if (!__all_sync(0xffffffffu, mb_wait(tfull + 8 * acc.slot, acc.phase, gave_up))) break;
@@ -185,7 +195,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     // lanes with bit 3 clear hold gate rows, the others the
                     // up rows of the same features; of a pair of tokens each
                     // half of the lanes finishes one
-                    const int fl = (lane >> 4) * 8 + (lane & 7), up = (lane >> 3) & 1, f0 = w.m0 + warp * 16;
+                    const int fl = (lane >> 4) * 8 + (lane & 7), up = (lane >> 3) & 1;
+                    const int f0 = w.m0 + rank * kHalf + warp * 16;
                     if constexpr (kSave) {
                         const uint32_t to = buf + up * 32 + fl * 2;
 #pragma unroll
@@ -239,7 +250,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     for (int i = 0; i < kRow / 16; ++i) {
                         constexpr int kPer = kRow / 16;  // lanes of a token
                         const int tok = i * (32 / kPer) + lane / kPer;
-                        const int f = w.m0 + warp * 32 + lane % kPer * (16 / kElem);
+                        const int f = w.m0 + rank * kHalf + warp * 32 + lane % kPer * (16 / kElem);
                         const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
                         if (tok < left && f < a.F)
                             *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.y) +
@@ -250,33 +261,37 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mb_arrive(tempty + 8 * acc.slot);
+            if (lane == 0) mb_arrive_remote(at_leader(tempty + 8 * acc.slot));
             acc.next();
         }
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();  // neither block leaves, or frees TMEM, while the other may reach it
     tc_fence_after();
     if (tid == 0 && s_gave_up) record_timeout();
-    if (warp == 4) tmem_free(tmem, 512);
+    if (warp == 4) tmem_free_pair(tmem, 512);
 }
 
 template <int kForm, bool kF32, bool kSave>
 cudaError_t launch(const CUtensorMap &map_w, const RowMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_gemm_kernel<kForm, kF32, kSave>;
-    const int smem = kSmem + groups_bytes(a.E);
-    static thread_local AttrCache cache;
-    cudaError_t e = cache.allow_smem(reinterpret_cast<const void *>(kern), kSmem + groups_bytes(1024));
-    if (e != cudaSuccess) return e;
+    static thread_local PairCache cache;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)sm_count());
+    cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmem + groups_bytes(1024);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
+    cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), (int)cfg.dynamicSmemBytes, cfg);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)cache.blocks);
+    cfg.dynamicSmemBytes = kSmem + groups_bytes(a.E);
     return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, a);
 }
 

@@ -215,6 +215,88 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t *r) {
         : "memory");
 }
 
+// ---- pairs of blocks (clusters of two; cta_group::2) --------------------------
+//
+// One tcgen05.mma spans the two SMs of a cluster: each block holds half of A
+// (its 128 rows of M) and half of B's columns, and gets its 128 rows of the
+// result in its own TMEM.  Both halves' loads are counted on the leader's
+// (rank 0's) barrier; the leader issues mma and its commits arrive on both
+// blocks' barriers.
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {  // every thread of both blocks
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t at_leader(uint32_t addr) {  // the same place in rank 0's shared memory
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void mb_arrive_remote(uint32_t bar) {  // bar from at_leader
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1,
+                                                 int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1,
+                                                 int c2, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+__device__ __forceinline__ void load_rows_pair(uint32_t dst, const RowMaps &maps, uint32_t bar, int c0, int row, int n) {
+    const int rows = rows_loaded(n);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {  // half of at most 256
+        const int box = 256 >> i;
+        if (rows & box) {
+            tma_load_2d_pair(dst, &maps.m[i], bar, c0, row);
+            dst += box * 128;
+            row += box;
+        }
+    }
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t cols) {  // one warp of each block
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {  // arrives in both blocks
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((unsigned short)3)
+        : "memory");
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
 // Shared-memory operand with 128-byte swizzle (the layout tiled TMA writes
 // with CU_TENSOR_MAP_SWIZZLE_128B from 1024-byte aligned tiles): groups of
 // eight 128-byte lines are `stride` bytes apart; for an operand whose
@@ -338,6 +420,26 @@ struct AttrCache {
         if (e != cudaSuccess) return e;
         dev = now;
         ctx = context_key();
+        return cudaSuccess;
+    }
+};
+
+// The same for a kernel launched in clusters of two blocks: also the number of
+// blocks that fit the device at once.
+struct PairCache {
+    AttrCache attr;
+    int dev = -1, blocks = 0;
+    unsigned long long ctx = 0;
+    cudaError_t prepare(const void *kernel, int most_smem, const cudaLaunchConfig_t &cfg) {
+        cudaError_t e = attr.allow_smem(kernel, most_smem);
+        if (e != cudaSuccess || (blocks > 0 && dev == attr.dev && ctx == attr.ctx && ctx != 0)) return e;
+        int clusters = 0;
+        e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        if (clusters < 1) return cudaErrorLaunchOutOfResources;
+        blocks = 2 * clusters;
+        dev = attr.dev;
+        ctx = attr.ctx;
         return cudaSuccess;
     }
 };
