@@ -115,18 +115,18 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     const int tiles = g.prefix[a.E], steps = (a.K + kK - 1) / kK;
 
     if (warp == 4) {  // loads
-        if (lane == 0) {
-            Ring<kStages> r;
-            int e = 0;
-            bool ok = true;
-            for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
-                const Tile w = get_tile(g, a.E, e, t, kStep);
-                e = w.e;
-                const int m0 = w.m0 + rank * kHalf, half = mma_tokens(w.n) / 2;  // this block's share
-                const int row = w.row + rank * half;
-                for (int k = 0; k < steps; ++k) {
-                    ok = mb_wait(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
-                    if (!ok) break;
+        Ring<kStages> r;
+        int e = 0;
+        bool ok = true;
+        for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
+            const int m0 = w.m0 + rank * kHalf, half = mma_tokens(w.n) / 2;  // this block's share
+            const int row = w.row + rank * half;
+            for (int k = 0; k < steps; ++k) {
+                ok = mb_wait_warp(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                if (!ok) break;
+                if (elect_one()) {
                     const uint32_t bar = at_leader(full + 8 * r.slot), sa = smem + r.slot * kStage, sb = sa + kBytesA;
                     if (rank == 0) mb_expect_tx(full + 8 * r.slot, 2 * (kBytesA + rows_loaded(half) * 128));
                     if constexpr (kForm == kLinear) {
@@ -138,13 +138,14 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                         tma_load_3d_pair(sa + kBytesA / 2, &map_w, bar, m0 + 64, k * kK, w.e);
                     }
                     load_rows_pair(sb, map_x, bar, k * kK, row, half);
-                    r.next();
                 }
+                __syncwarp();
+                r.next();
             }
-            if (rank == 0) drain_loads(full, r);  // of both blocks
         }
+        if (rank == 0) drain_loads(full, r);  // of both blocks
     } else if (warp == 5) {  // mma
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             Ring<kStages> r;
             Ring<2> acc;
             int e = 0;
@@ -154,28 +155,33 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 e = w.e;
                 const uint32_t desc = mma_desc(1, kForm == kDgrad, false, 2 * kM, mma_tokens(w.n));
                 const uint32_t d = tmem + acc.slot * kTok;
-                ok = mb_wait(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
+                ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
                 tc_fence_after();
                 for (int k = 0; k < steps && ok; ++k) {
-                    ok = mb_wait(full + 8 * r.slot, r.phase, gave_up);
+                    ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sa = smem + r.slot * kStage;
-                    // reduction contiguous: 16 elements are 32 bytes of the
-                    // line; else they are 16 lines
-                    const uint64_t da = kForm == kDgrad ? smem_operand(sa, kBytesA / 2, 1024) : smem_operand(sa, 16, 1024);
-                    const uint64_t db = smem_operand(sa + kBytesA, 16, 1024);
-                    constexpr int kStepA = kForm == kDgrad ? 2048 / 16 : 32 / 16;
+                    if (elect_one()) {
+                        const uint32_t sa = smem + r.slot * kStage;
+                        // reduction contiguous: 16 elements are 32 bytes of
+                        // the line; else they are 16 lines
+                        const uint64_t da = kForm == kDgrad ? smem_operand(sa, kBytesA / 2, 1024) : smem_operand(sa, 16, 1024);
+                        const uint64_t db = smem_operand(sa + kBytesA, 16, 1024);
+                        constexpr int kStepA = kForm == kDgrad ? 2048 / 16 : 32 / 16;
 #pragma unroll
-                    for (int i = 0; i < kK / 16; ++i)
-                        mma_bf16_pair(d, da + i * kStepA, db + i * 2, desc, (k | i) != 0);
-                    tc_commit_pair(empty + 8 * r.slot);
+                        for (int i = 0; i < kK / 16; ++i)
+                            mma_bf16_pair(d, da + i * kStepA, db + i * 2, desc, (k | i) != 0);
+                        tc_commit_pair(empty + 8 * r.slot);
+                    }
+                    __syncwarp();
                     r.next();
                 }
-                tc_commit_pair(tfull + 8 * acc.slot);
+                if (elect_one()) tc_commit_pair(tfull + 8 * acc.slot);
+                __syncwarp();
                 acc.next();
             }
-            tc_commit_pair(done);
+            if (elect_one()) tc_commit_pair(done);
+            __syncwarp();
             mb_drain(done, 0);
         }
     } else {  // results: warp w holds matrix rows 32w.. of the tile, one per lane
@@ -184,7 +190,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
             const Tile w = get_tile(g, a.E, e, t, kStep);
             e = w.e;
-            if (!__all_sync(0xffffffffu, mb_wait(tfull + 8 * acc.slot, acc.phase, gave_up))) break;
+            if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up)) break;
             tc_fence_after();
             const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(warp * 32) << 16);
             for (int c0 = 0; c0 < w.n; c0 += 32) {

@@ -83,7 +83,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     const int tiles = a.E * per;
 
     if (warp == 4) {  // loads
-        if (lane == 0) {
+        {
             Ring<kStages> r;
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
@@ -92,8 +92,9 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                 const bool whole_m = m0 + kM <= a.F, whole_n = n0 + kN <= a.K;
                 const int mb = min(kM, a.F - m0) > 64 ? 2 : 1, nb = (min(kN, a.K - n0) + 63) / 64;
                 for (int k = 0; k < steps; ++k) {
-                    ok = mb_wait(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                    ok = mb_wait_warp(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
                     if (!ok) break;
+                    if (elect_one()) {
                     const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + kM / 64 * kBlock;
                     mb_expect_tx(bar, (mb + nb) * kBlock);
                     if (whole_m) {
@@ -108,6 +109,8 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                         for (int i = 0; i < nb; ++i)
                             tma_load_2d(sb + i * kBlock, &map_x.cols, bar, n0 + i * 64, row + k * kP);
                     }
+                    }
+                    __syncwarp();
                     r.next();
                 }
             }
@@ -123,10 +126,10 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             if (steps == 0) continue;  // nothing to sum: the results are zeros
             const uint32_t desc = mma_desc(1, true, true, kM, (min(kN, a.K - n0) + 15) & ~15);
             const uint32_t d = tmem + acc.slot * kN;
-            ok = __all_sync(0xffffffffu, mb_wait(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up));
+            ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
             tc_fence_after();
             for (int k = 0; k < steps && ok; ++k) {
-                ok = __all_sync(0xffffffffu, mb_wait(full + 8 * r.slot, r.phase, gave_up));
+                ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
                 if (!ok) break;
                 const int left = min(kP, count - k * kP), slices = (left + 15) / 16;
                 if (left % 16 != 0) {
@@ -139,7 +142,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                     __syncwarp();
                 }
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t sa = smem + r.slot * kStage;
                     const uint64_t da = smem_operand(sa, kBlock, 1024), db = smem_operand(sa + kM / 64 * kBlock, kBlock, 1024);
                     for (int i = 0; i < slices; ++i)  // 16 rows are 16 lines of 128 bytes
@@ -149,21 +152,20 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                 __syncwarp();
                 r.next();
             }
-            if (lane == 0) tc_commit(tfull + 8 * acc.slot);
+            if (elect_one()) tc_commit(tfull + 8 * acc.slot);
             __syncwarp();
             acc.next();
         }
-        if (lane == 0) {
-            tc_commit(done);
-            mb_drain(done, 0);
-        }
+        if (elect_one()) tc_commit(done);
+        __syncwarp();
+        mb_drain(done, 0);
     } else {  // results: warp w holds rows 32w.. of the tile, one per lane
         Ring<2> acc;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
             const int e = t / per, at = t % per, m0 = at % mt * kM, n0 = at / mt * kN;
             const bool some = g.count[e] > 0;
             if (some) {
-                if (!__all_sync(0xffffffffu, mb_wait(tfull + 8 * acc.slot, acc.phase, gave_up))) break;
+                if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up)) break;
                 tc_fence_after();
             }
             const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(warp * 32) << 16);

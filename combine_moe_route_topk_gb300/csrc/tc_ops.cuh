@@ -39,6 +39,21 @@ __device__ __forceinline__ bool mb_try(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+// One lane of a converged warp, the same one every time.  The warps that issue
+// loads and mma run their loops whole and enclose only the issue in this
+// test: within `if (lane == 0)` around the loop, every operand that the
+// instructions want in a uniform register was fetched the slow way (fp8
+// product: 1100 cycles a block, 480 of them to issue four mma).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Every wait is bounded: after kPolls polls (each may suspend briefly), or
 // once another warp of the block has given up, it returns false and the
 // block's word `gave_up` is set; each role then leaves its loop, copies in
@@ -51,6 +66,9 @@ __device__ __forceinline__ bool mb_wait(uint32_t bar, uint32_t parity, volatile 
     }
     *gave_up = 1;
     return false;
+}
+__device__ __forceinline__ bool mb_wait_warp(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    return __all_sync(0xffffffffu, mb_wait(bar, parity, gave_up));
 }
 __device__ __forceinline__ void mb_drain(uint32_t bar, uint32_t parity) {  // bounded, result not needed
     for (int i = 0; i < kPolls && !mb_try(bar, parity); ++i) {
@@ -293,6 +311,15 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_fp8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
         : "memory");
 }

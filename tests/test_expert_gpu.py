@@ -31,6 +31,7 @@ ROWS = [
     (1, [700], 700),
     (3, [0, 0, 0], 8),
     (4, [3, 0, 0, 2, 0, 0, 7, 1], 12),
+    (1, [600, 1, 0, 200], 900),     # many rows on average, and experts with few
 ]
 SIZES = [(8, 8), (64, 128), (72, 136), (200, 264), (512, 96), (1000, 520)]
 
