@@ -73,11 +73,11 @@ struct Tile {
 template <int kTokens>
 __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, int f_step) {
     Tile r;
-    r.e = find_group(g, E, e, t);
-    const int c = g.count[r.e], nt = (c + kTokens - 1) / kTokens, at = t - g.prefix[r.e];
+    r.e = same(find_group(g, E, e, t));
+    const int c = same(g.count[r.e]), nt = (c + kTokens - 1) / kTokens, at = t - same(g.prefix[r.e]);
     const int size = (c + nt - 1) / nt, tt = at % nt;
     r.f0 = at / nt * f_step;
-    r.row = g.row[r.e] + tt * size;
+    r.row = same(g.row[r.e]) + tt * size;
     r.n = min(size, c - tt * size);
     return r;
 }
@@ -112,8 +112,8 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     __shared__ float s_amax[2][kTok];  // largest |h| of a token in each half of the features
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int rank = kPair ? (int)cluster_rank() : 0;
+    const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
+    const int rank = kPair ? same((int)cluster_rank()) : 0;
     const int unit = kPair ? blockIdx.x / 2 : blockIdx.x, units = kPair ? gridDim.x / 2 : gridDim.x;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t buf = smem + kStages * kStage + (warp & (kSumWarps - 1)) * kBuf;
@@ -152,8 +152,8 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     if constexpr (kPair) cluster_sync();  // barriers and TMEM of both blocks are ready
     else __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
-    const int tiles = g.prefix[a.E], steps = a.K / kK;
+    const uint32_t tmem = (uint32_t)same((int)s_tmem);
+    const int tiles = same(g.prefix[a.E]), steps = a.K / kK;
     int e = 0;
 
     // This block's tile: its tokens of the tile's (pair: half of them).

@@ -59,12 +59,12 @@ struct Tile {
 // the matrix rows through L2.
 __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, int m_step) {
     Tile r;
-    r.e = find_group(g, E, e, t);
-    const int c = g.count[r.e], nt = token_tiles(c), at = t - g.prefix[r.e];
+    r.e = same(find_group(g, E, e, t));
+    const int c = same(g.count[r.e]), nt = token_tiles(c), at = t - same(g.prefix[r.e]);
     const int size = mma_tokens((c + nt - 1) / nt);
     const int tt = at % nt;
     r.m0 = at / nt * m_step;
-    r.row = g.row[r.e] + tt * size;
+    r.row = same(g.row[r.e]) + tt * size;
     r.n = min(size, c - tt * size);
     return r;
 }
@@ -76,7 +76,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t buf = smem + kStages * kStage + (warp & 3) * kBuf;
     int *tables = reinterpret_cast<int *>(smem_raw + (smem - smem_u32(smem_raw)) + kStages * kStage + 4 * kBuf);
@@ -84,7 +84,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                    tempty = tfull + 16, done = tempty + 16;
     volatile int *gave_up = &s_gave_up;
 
-    const uint32_t rank = cluster_rank();
+    const int rank = same((int)cluster_rank());
     if (warp == 4) tmem_alloc_pair(smem_u32(&s_tmem), 512);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -111,8 +111,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     tc_fence_before();
     cluster_sync();  // barriers and TMEM of both blocks are ready
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
-    const int tiles = g.prefix[a.E], steps = (a.K + kK - 1) / kK;
+    const uint32_t tmem = (uint32_t)same((int)s_tmem);
+    const int tiles = same(g.prefix[a.E]), steps = (a.K + kK - 1) / kK;
 
     if (warp == 4) {  // loads
         Ring<kStages> r;

@@ -47,7 +47,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *stages = smem_raw + (smem - smem_u32(smem_raw));
     const uint32_t buf = smem + kStages * kStage + (warp & 3) * kBuf;
@@ -79,7 +79,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = (uint32_t)same((int)s_tmem);
     const int tiles = a.E * per;
 
     if (warp == 4) {  // loads
@@ -88,7 +88,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const int e = t / per, at = t % per, m0 = at % mt * kM, n0 = at / mt * kN;
-                const int row = g.row[e], steps = (g.count[e] + kP - 1) / kP;
+                const int row = same(g.row[e]), steps = (same(g.count[e]) + kP - 1) / kP;
                 const bool whole_m = m0 + kM <= a.F, whole_n = n0 + kN <= a.K;
                 const int mb = min(kM, a.F - m0) > 64 ? 2 : 1, nb = (min(kN, a.K - n0) + 63) / 64;
                 for (int k = 0; k < steps; ++k) {
@@ -122,7 +122,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             const int e = t / per, at = t % per, n0 = at / mt * kN;
-            const int count = g.count[e], steps = (count + kP - 1) / kP;
+            const int count = same(g.count[e]), steps = (count + kP - 1) / kP;
             if (steps == 0) continue;  // nothing to sum: the results are zeros
             const uint32_t desc = mma_desc(1, true, true, kM, (min(kN, a.K - n0) + 15) & ~15);
             const uint32_t d = tmem + acc.slot * kN;
@@ -163,7 +163,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
         Ring<2> acc;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
             const int e = t / per, at = t % per, m0 = at % mt * kM, n0 = at / mt * kN;
-            const bool some = g.count[e] > 0;
+            const bool some = same(g.count[e]) > 0;
             if (some) {
                 if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up)) break;
                 tc_fence_after();

@@ -39,6 +39,11 @@ __device__ __forceinline__ bool mb_try(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+// A value that every lane of a converged warp holds: the compiler then knows
+// that it is the same in all of them, keeps it in uniform registers and takes
+// branches on it without considering divergence.
+__device__ __forceinline__ int same(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // One lane of a converged warp, the same one every time.  The warps that issue
 // loads and mma run their loops whole and enclose only the issue in this
 // test: within `if (lane == 0)` around the loop, every operand that the
@@ -68,6 +73,7 @@ __device__ __forceinline__ bool mb_wait(uint32_t bar, uint32_t parity, volatile 
     return false;
 }
 __device__ __forceinline__ bool mb_wait_warp(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    if (__all_sync(0xffffffffu, mb_try(bar, parity))) return true;
     return __all_sync(0xffffffffu, mb_wait(bar, parity, gave_up));
 }
 __device__ __forceinline__ void mb_drain(uint32_t bar, uint32_t parity) {  // bounded, result not needed
