@@ -32,27 +32,21 @@ constexpr int kTok = 128;   // tokens of a tile (M)
 constexpr int kBlk = 128;   // matrix rows of a block: one scale
 constexpr int kN = 2 * kBlk;
 constexpr int kK = 128;     // reduction elements of a stage: one scale block, one 128-byte line
+constexpr int kStages = 4;
 constexpr int kBytesA = kTok * kK;
+constexpr int kBytesB = kN * kK;
+constexpr int kStage = kBytesA + kBytesB;
 constexpr int kGroup = 4;   // blocks whose scales are loaded together
 constexpr int kSumWarps = 8;
 constexpr int kThreads = 32 * (kSumWarps + 4);  // one warp loads, one issues mma, two bring the scales
 // 384 threads are launched with 168 registers each; the summing warps take
-// 208, the others keep 88 (256 * 208 + 128 * 88 = 384 * 168).
-constexpr int kSumRegs = 208, kOtherRegs = 88;
+// 216 (linear form: 224), the others keep 72 (56): 256 * 216 + 128 * 72 = 256 *
+// 224 + 128 * 56 = 384 * 168.  With these splits neither form spills; with the
+// other's it does (linear at 216: 86 us where 224 takes 72).
+constexpr int sum_regs(bool gated) { return gated ? 216 : 224; }
+constexpr int other_regs(bool gated) { return gated ? 72 : 56; }
 constexpr int kBuf = 2048;  // each summing warp's: 64 bytes of its 32 tokens' results
-
-constexpr int kPairRows = 192;  // rows of an expert, on average, from which blocks work in pairs
-
-// Solo: a block's tile is 128 tokens by 256 matrix rows.  Pair: two blocks'
-// tile is 256 tokens by 256 matrix rows, each block with 128 of both.
-template <bool kPair>
-struct Form {
-    static constexpr int kTokens = kPair ? 2 * kTok : kTok;     // of a tile
-    static constexpr int kBytesB = (kPair ? 1 : 2) * kBlk * kK;  // a block's part of the matrix rows
-    static constexpr int kStages = kPair ? 6 : 4;
-    static constexpr int kStage = kBytesA + kBytesB;
-    static constexpr int kSmem = 1024 + kStages * kStage + kSumWarps * kBuf;
-};
+constexpr int kSmem = 1024 + kStages * kStage + kSumWarps * kBuf;
 
 struct Args {
     const int32_t *offsets;
@@ -70,11 +64,12 @@ struct Tile {
 
 // Token tiles of a group (of equal size) run fastest: blocks working at the
 // same time share the matrix rows through L2.
-template <int kTokens>
+__host__ __device__ inline int token_tiles(int count) { return (count + kTok - 1) / kTok; }
+
 __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, int f_step) {
     Tile r;
     r.e = same(find_group(g, E, e, t));
-    const int c = same(g.count[r.e]), nt = (c + kTokens - 1) / kTokens, at = t - same(g.prefix[r.e]);
+    const int c = same(g.count[r.e]), nt = token_tiles(c), at = t - same(g.prefix[r.e]);
     const int size = (c + nt - 1) / nt, tt = at % nt;
     r.f0 = at / nt * f_step;
     r.row = same(g.row[r.e]) + tt * size;
@@ -100,11 +95,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {  
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-template <bool kGated, bool kF32, bool kPair>
+template <bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x, const Args a) {
-    using P = Form<kPair>;
-    constexpr int kStages = P::kStages, kStage = P::kStage;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 7];
     __shared__ float s_x[2][kTok];     // the tokens' scales of a block, per accumulator
@@ -113,8 +106,6 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
-    const int rank = kPair ? same((int)cluster_rank()) : 0;
-    const int unit = kPair ? blockIdx.x / 2 : blockIdx.x, units = kPair ? gridDim.x / 2 : gridDim.x;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t buf = smem + kStages * kStage + (warp & (kSumWarps - 1)) * kBuf;
     int *tables = reinterpret_cast<int *>(smem_raw + (smem - smem_u32(smem_raw)) + kStages * kStage + kSumWarps * kBuf);
@@ -122,10 +113,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                    sempty = tempty + 16, done = sempty + 16;
     volatile int *gave_up = &s_gave_up;
 
-    if (warp == kSumWarps) {
-        if constexpr (kPair) tmem_alloc_pair(smem_u32(&s_tmem), 512);
-        else tmem_alloc(smem_u32(&s_tmem), 512);
-    }
+    if (warp == kSumWarps) tmem_alloc(smem_u32(&s_tmem), 512);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mb_init(full + 8 * i, 1);
@@ -133,7 +121,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mb_init(tfull + 8 * i, 3);  // the block's sums, and its scales by two warps
-            mb_init(tempty + 8 * i, (kPair ? 2 : 1) * kSumWarps);
+            mb_init(tempty + 8 * i, kSumWarps);
             mb_init(sempty + 8 * i, kSumWarps);
         }
         mb_init(done, 1);
@@ -147,104 +135,68 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     constexpr int kStep = kGated ? kBlk : kN;  // result columns of a tile
     const int f_tiles = (a.F + kStep - 1) / kStep;
     const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap,
-                                 [&](int c) { return (c + P::kTokens - 1) / P::kTokens * f_tiles; });  // syncs the block
+                                 [&](int c) { return token_tiles(c) * f_tiles; });  // syncs the block
     tc_fence_before();
-    if constexpr (kPair) cluster_sync();  // barriers and TMEM of both blocks are ready
-    else __syncthreads();
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)same((int)s_tmem);
     const int tiles = same(g.prefix[a.E]), steps = a.K / kK;
     int e = 0;
 
-    // This block's tile: its tokens of the tile's (pair: half of them).
-    auto tile = [&](int t) {
-        Tile w = get_tile<P::kTokens>(g, a.E, e, t, kStep);
-        e = w.e;
-        if constexpr (kPair) {
-            const int first = (w.n + 1) / 2;
-            w.row += rank * first;
-            w.n = rank == 0 ? first : w.n - first;
-        }
-        return w;
-    };
-
-    if (warp >= kSumWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp >= kSumWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(kGated)));
     if (warp == kSumWarps) {  // loads
         Ring<kStages> r;
         bool ok = true;
-        for (int t = unit; t < tiles && ok; t += units) {
-            const Tile w = tile(t);
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
             const bool two = kGated || w.f0 + kBlk < a.F;  // the second block of matrix rows exists
             const int second = w.f0 + (kGated ? a.F : kBlk);
-            // the leader counts both blocks' bytes; its peer has as many
-            // tokens or one less
-            const int peer = kPair ? get_tile<P::kTokens>(g, a.E, e, t, kStep).n - w.n : 0;
             for (int k = 0; k < steps; ++k) {
                 ok = mb_wait_warp(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t bar = full + 8 * r.slot, sa = smem + r.slot * kStage, sb = sa + kBytesA;
-                    if constexpr (kPair) {
-                        if (rank == 0)
-                            mb_expect_tx(bar, 2 * P::kBytesB + (rows_loaded(w.n) + rows_loaded(peer)) * 128);
-                        const uint32_t both = at_leader(bar);
-                        tma_load_3d_pair(sb, &map_w, both, k * kK, rank == 0 ? w.f0 : second, w.e);
-                        load_rows_pair(sa, map_x, both, k * kK, w.row, w.n);
-                    } else {
-                        mb_expect_tx(bar, (two ? 2 : 1) * kBlk * kK + rows_loaded(w.n) * 128);
-                        tma_load_3d(sb, &map_w, bar, k * kK, w.f0, w.e);
-                        if (two) tma_load_3d(sb + kBlk * kK, &map_w, bar, k * kK, second, w.e);
-                        load_rows(sa, map_x, bar, k * kK, w.row, w.n);
-                    }
+                    mb_expect_tx(bar, (two ? 2 : 1) * kBlk * kK + rows_loaded(w.n) * 128);
+                    tma_load_3d(sb, &map_w, bar, k * kK, w.f0, w.e);
+                    if (two) tma_load_3d(sb + kBlk * kK, &map_w, bar, k * kK, second, w.e);
+                    load_rows(sa, map_x, bar, k * kK, w.row, w.n);
                 }
                 __syncwarp();
                 r.next();
             }
         }
-        if (rank == 0) drain_loads(full, r);
+        drain_loads(full, r);
     } else if (warp == kSumWarps + 1) {  // mma
-        if (rank == 0) {
-            Ring<kStages> r;
-            Ring<2> acc;
-            bool ok = true;
-            for (int t = unit; t < tiles && ok; t += units) {
-                const Tile w = tile(t);
-                const int n = kPair || kGated ? kN : min(kN, (a.F - w.f0 + 15) & ~15);
-                const uint32_t desc = mma_desc(0, false, false, kPair ? 2 * kTok : kTok, n);
-                for (int k = 0; k < steps; ++k) {
-                    ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up) &&
-                         mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t sa = smem + r.slot * kStage;
-                        const uint64_t da = smem_operand(sa, 16, 1024), db = smem_operand(sa + kBytesA, 16, 1024);
-                        const uint32_t d = tmem + acc.slot * kN;
+        Ring<kStages> r;
+        Ring<2> acc;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
+            const uint32_t desc = mma_desc(0, false, false, kTok, kGated ? kN : min(kN, (a.F - w.f0 + 15) & ~15));
+            for (int k = 0; k < steps; ++k) {
+                ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up) &&
+                     mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t sa = smem + r.slot * kStage;
+                    const uint64_t da = smem_operand(sa, 16, 1024), db = smem_operand(sa + kBytesA, 16, 1024);
+                    const uint32_t d = tmem + acc.slot * kN;
 #pragma unroll
-                        for (int i = 0; i < kK / 32; ++i) {
-                            if constexpr (kPair) mma_fp8_pair(d, da + i * 2, db + i * 2, desc, i != 0);
-                            else mma_fp8(d, da + i * 2, db + i * 2, desc, i != 0);
-                        }
-                        if constexpr (kPair) {
-                            tc_commit_pair(tfull + 8 * acc.slot);
-                            tc_commit_pair(empty + 8 * r.slot);
-                        } else {
-                            tc_commit(tfull + 8 * acc.slot);
-                            tc_commit(empty + 8 * r.slot);
-                        }
-                    }
-                    __syncwarp();
-                    r.next();
-                    acc.next();
+                    for (int i = 0; i < kK / 32; ++i) mma_fp8(d, da + i * 2, db + i * 2, desc, i != 0);
+                    tc_commit(tfull + 8 * acc.slot);
+                    tc_commit(empty + 8 * r.slot);
                 }
+                __syncwarp();
+                r.next();
+                acc.next();
             }
-            if (elect_one()) {
-                if constexpr (kPair) tc_commit_pair(done);
-                else tc_commit(done);
-            }
-            __syncwarp();
-            mb_drain(done, 0);
         }
+        if (elect_one()) tc_commit(done);
+        __syncwarp();
+        mb_drain(done, 0);
     } else if (warp >= kSumWarps + 2) {
         // scales: each of two warps takes 64 tokens, two a lane; the next
         // blocks' are on their way while these wait for their accumulator
@@ -253,8 +205,9 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         const bool first = t0 == 0;
         Ring<2> acc;
         bool ok = true;
-        for (int t = unit; t < tiles && ok; t += units) {
-            const Tile w = tile(t);
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
             const bool in0 = t0 < w.n, in1 = t0 + 32 < w.n, two = kGated || w.f0 + kBlk < a.F;
             const float *sx = a.x_scales + (int64_t)(w.row + t0) * steps, *sx1 = sx + (int64_t)32 * steps;
             const float *sw0 = a.w_scales + ((int64_t)w.e * fb + w.f0 / kBlk) * steps;
@@ -293,14 +246,15 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             }
         }
     } else if (warp < kSumWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(sum_regs(kGated)));
         // sums and results: warp w holds tokens 32 (w % 4).., one per lane,
         // and 64 columns of both blocks, 64 (w / 4)..
         const int quarter = warp & 3, half = warp >> 2;
         Ring<2> acc;
         bool ok = true;
-        for (int t = unit; t < tiles && ok; t += units) {
-            const Tile w = tile(t);
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
             const bool some = quarter * 32 < w.n, mine = quarter * 32 + lane < w.n;
             uint64_t sum[2][4][8];  // [block][16 columns][pair]
 #pragma unroll
@@ -315,29 +269,34 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 tc_fence_after();
                 if (some) {
                     const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(quarter * 32) << 16) + 64 * half;
-                    // the next 16 columns are on their way while these are added
-                    uint32_t v[2][16];
-                    tmem_load16_async(src, v[0]);
+                    // the next 32 columns are on their way while these are added
+                    uint32_t v[2][32];
+                    tmem_load32_async(src, v[0]);
                     const float x = s_x[acc.slot][quarter * 32 + lane];
                     const float2 sw = s_w[acc.slot];
                     const uint32_t x0 = __float_as_uint(x * sw.x), x1 = __float_as_uint(x * sw.y);
                     const uint64_t f0 = pair(x0, x0), f1 = pair(x1, x1);
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        tmem_wait16(v[u & 1]);
-                        if (u < 7) tmem_load16_async(src + (u + 1) / 4 * kBlk + (u + 1) % 4 * 16, v[(u + 1) & 1]);
+                    for (int u = 0; u < 4; ++u) {
+                        tmem_wait32(v[u & 1]);
+                        if (u < 3) {
+                            tmem_load32_async(src + (u + 1) / 2 * kBlk + (u + 1) % 2 * 32, v[(u + 1) & 1]);
+                        } else {  // everything is in registers: the accumulator is free
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mb_arrive(tempty + 8 * acc.slot);
+                                mb_arrive(sempty + 8 * acc.slot);
+                            }
+                        }
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            sum[u / 4][u % 4][j] =
-                                fma2(pair(v[u & 1][2 * j], v[u & 1][2 * j + 1]), u < 4 ? f0 : f1, sum[u / 4][u % 4][j]);
+                        for (int j = 0; j < 16; ++j)
+                            sum[u / 2][u % 2 * 2 + j / 8][j % 8] = fma2(pair(v[u & 1][2 * j], v[u & 1][2 * j + 1]),
+                                                                        u < 2 ? f0 : f1, sum[u / 2][u % 2 * 2 + j / 8][j % 8]);
                     }
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) {
+                } else if (lane == 0) {
+                    mb_arrive(tempty + 8 * acc.slot);
                     mb_arrive(sempty + 8 * acc.slot);
-                    if constexpr (kPair) mb_arrive_remote(at_leader(tempty + 8 * acc.slot));
-                    else mb_arrive(tempty + 8 * acc.slot);
                 }
                 acc.next();
             }
@@ -348,43 +307,43 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 // memory so that four lanes write them (chunks of 16 bytes
                 // swapped by token against bank conflicts)
                 constexpr int kElem = kF32 ? 4 : 2, kCols = 64 / kElem;
+                const int t0 = lane / 4, left = w.n - quarter * 32 - t0;  // first token that this lane writes
+                const int cols = a.F - (w.f0 + 64 * half) - (lane & 3) * (16 / kElem);
+                unsigned char *to = static_cast<unsigned char *>(a.y) +
+                                    ((int64_t)(w.row + quarter * 32 + t0) * a.F + (a.F - cols)) * kElem;
+                const int64_t step = (int64_t)8 * a.F * kElem;
+                const uint32_t put = buf + lane * 64, get = buf + t0 * 64 + (((lane & 3) ^ ((t0 >> 1) & 3)) * 16);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const int f0 = w.f0 + b * kBlk + 64 * half;
 #pragma unroll
                     for (int c0 = 0; c0 < 64; c0 += kCols) {
-                        if (f0 + c0 < a.F) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint4 v;
-                                if constexpr (kF32) {
-                                    const float2 x = unpair(sum[b][(c0 + 4 * q) / 16][(c0 + 4 * q) % 16 / 2]),
-                                                 y = unpair(sum[b][(c0 + 4 * q) / 16][(c0 + 4 * q) % 16 / 2 + 1]);
-                                    v = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
-                                                   __float_as_uint(y.y));
-                                } else {
-                                    uint32_t p[4];
+                        for (int q = 0; q < 4; ++q) {
+                            uint4 v;
+                            if constexpr (kF32) {
+                                const float2 x = unpair(sum[b][(c0 + 4 * q) / 16][(c0 + 4 * q) % 16 / 2]),
+                                             y = unpair(sum[b][(c0 + 4 * q) / 16][(c0 + 4 * q) % 16 / 2 + 1]);
+                                v = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
+                                               __float_as_uint(y.y));
+                            } else {
+                                uint32_t p[4];
 #pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        const float2 x = unpair(sum[b][(c0 + 8 * q) / 16][(c0 + 8 * q) % 16 / 2 + j]);
-                                        p[j] = bf16x2(__float_as_uint(x.x), __float_as_uint(x.y));
-                                    }
-                                    v = make_uint4(p[0], p[1], p[2], p[3]);
+                                for (int j = 0; j < 4; ++j) {
+                                    const float2 x = unpair(sum[b][(c0 + 8 * q) / 16][(c0 + 8 * q) % 16 / 2 + j]);
+                                    p[j] = bf16x2(__float_as_uint(x.x), __float_as_uint(x.y));
                                 }
-                                st_shared128(buf + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16), v);
+                                v = make_uint4(p[0], p[1], p[2], p[3]);
                             }
-                            __syncwarp();
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int tok = i * 8 + lane / 4, q = lane & 3;
-                                const uint4 v = ld_shared128(buf + tok * 64 + ((q ^ ((tok >> 1) & 3)) * 16));
-                                const int f = f0 + c0 + q * 16 / kElem;
-                                if (quarter * 32 + tok < w.n && f < a.F)
-                                    *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.y) +
-                                                               ((int64_t)(w.row + quarter * 32 + tok) * a.F + f) * kElem) = v;
-                            }
-                            __syncwarp();
+                            st_shared128(put + ((q ^ ((lane >> 1) & 3)) * 16), v);
                         }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {  // tokens t0 + 8 i: the same swap, 8 tokens being 512 bytes
+                            const uint4 v = ld_shared128(get + i * 512);
+                            if (8 * i < left && b * kBlk + c0 < cols)
+                                *reinterpret_cast<uint4 *>(to + i * step + (b * kBlk + c0) * kElem) = v;
+                        }
+                        __syncwarp();
                     }
                 }
             } else {
@@ -425,55 +384,27 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     }
     __syncwarp();
     tc_fence_before();
-    if constexpr (kPair) cluster_sync();  // neither block leaves while the other may reach it
-    else __syncthreads();
+    __syncthreads();
     tc_fence_after();
     if (tid == 0 && s_gave_up) record_timeout();
-    if (warp == kSumWarps) {
-        if constexpr (kPair) tmem_free_pair(tmem, 512);
-        else tmem_free(tmem, 512);
-    }
+    if (warp == kSumWarps) tmem_free(tmem, 512);
 }
 
-template <bool kGated, bool kF32, bool kPair>
+template <bool kGated, bool kF32>
 cudaError_t launch(const CUtensorMap &map_w, const RowMaps &map_x, const Args &a, cudaStream_t stream) {
-    auto kern = expert_fp8_kernel<kGated, kF32, kPair>;
-    const int most = Form<kPair>::kSmem + groups_bytes(1024);
+    auto kern = expert_fp8_kernel<kGated, kF32>;
+    static thread_local AttrCache cache;
+    cudaError_t e = cache.allow_smem(reinterpret_cast<const void *>(kern), kSmem + groups_bytes(1024));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
+    cfg.gridDim = dim3((unsigned)sm_count());
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = most;
+    cfg.dynamicSmemBytes = kSmem + groups_bytes(a.E);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
-    if constexpr (kPair) {
-        static thread_local PairCache cache;
-        cfg.numAttrs = 2;
-        cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), most, cfg);
-        if (e != cudaSuccess) return e;
-        cfg.gridDim = dim3((unsigned)cache.blocks);
-    } else {
-        static thread_local AttrCache cache;
-        cfg.numAttrs = 1;
-        cudaError_t e = cache.allow_smem(reinterpret_cast<const void *>(kern), most);
-        if (e != cudaSuccess) return e;
-        cfg.gridDim = dim3((unsigned)sm_count());
-    }
-    cfg.dynamicSmemBytes = Form<kPair>::kSmem + groups_bytes(a.E);
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, a);
-}
-
-// A pair needs more than 128 tokens of an expert to keep both blocks busy.
-bool pairs_of_blocks(const ExpertRows &r) { return r.pairs / r.E >= kPairRows; }
-
-template <bool kPair>
-cudaError_t launch(int gated, int y_f32, const CUtensorMap &map_w, const RowMaps &map_x, const Args &a,
-                   cudaStream_t stream) {
-    if (gated) return launch<true, false, kPair>(map_w, map_x, a, stream);
-    return y_f32 ? launch<false, true, kPair>(map_w, map_x, a, stream) : launch<false, false, kPair>(map_w, map_x, a, stream);
 }
 
 }  // namespace
@@ -490,8 +421,8 @@ cudaError_t launch_expert_gemm_fp8(const ExpertRows &r, int K, int F, int gated,
     if (!encode_map(&map_w, 1, 3, wq, wdims, strides, wbox)) return cudaErrorInvalidValue;
     if (!encode_rows(&map_x, 1, xq, K, r.rows_total)) return cudaErrorInvalidValue;
     const Args a{r.offsets, x_scales, w_scales, y, y_scales, r.cap, r.E, r.L, K, F, w_rows};
-    return pairs_of_blocks(r) ? launch<true>(gated, y_f32, map_w, map_x, a, stream)
-                              : launch<false>(gated, y_f32, map_w, map_x, a, stream);
+    if (gated) return launch<true, false>(map_w, map_x, a, stream);
+    return y_f32 ? launch<false, true>(map_w, map_x, a, stream) : launch<false, false>(map_w, map_x, a, stream);
 }
 
 cudaError_t take_expert_fp8_error(int *err) { return take_tc_error(err); }

@@ -10,7 +10,7 @@ namespace moe {
 struct ExpertRows {
     const int32_t *offsets;  // device, [E + 1]
     int E, L;                // experts, experts per rank
-    int64_t cap, rows_total, pairs;  // rows of a region, of all; routed rows
+    int64_t cap, rows_total;
 };
 
 cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, const void *x, const void *w, void *y,
