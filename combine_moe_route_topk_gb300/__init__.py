@@ -154,10 +154,15 @@ def buffer_sizes(dims: MoeDims) -> dict:
     return d
 
 
+# torch.cuda.current_device() without its check for lazy initialisation (0.2 us an argument): asked
+# once a CUDA tensor is at hand
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream) -> int:
     """The stream's handle (None: the current one), as an integer for a void* argument."""
     if stream is None:  # the handle without a torch.cuda.Stream object, which costs 3 us
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -170,7 +175,7 @@ def _ptr(t: torch.Tensor | None, nbytes: int, name: str, dtype=None, optional=Fa
     dev = t.get_device()  # -1 on the CPU
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{name} is on {t.device}, not the current device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")

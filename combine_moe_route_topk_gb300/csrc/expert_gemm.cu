@@ -283,22 +283,12 @@ template <int kForm, bool kF32, bool kSave>
 cudaError_t launch(const CUtensorMap &map_w, const RowMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_gemm_kernel<kForm, kF32, kSave>;
     static thread_local PairCache cache;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem + groups_bytes(1024);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), (int)cfg.dynamicSmemBytes, cfg);
+    PairLaunch l(kThreads, kSmem + groups_bytes(1024), stream);
+    cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), l.cfg);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)cache.blocks);
-    cfg.dynamicSmemBytes = kSmem + groups_bytes(a.E);
-    return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, a);
+    l.cfg.gridDim = dim3((unsigned)cache.blocks);
+    l.cfg.dynamicSmemBytes = kSmem + groups_bytes(a.E);
+    return cudaLaunchKernelEx(&l.cfg, kern, map_w, map_x, a);
 }
 
 }  // namespace

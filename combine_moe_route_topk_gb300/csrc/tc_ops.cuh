@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "moe_internal.cuh"
+#include "pdl.cuh"
 
 namespace moe {
 
@@ -440,14 +441,33 @@ struct AttrCache {
     }
 };
 
-// The same for a kernel launched in clusters of two blocks: also the number of
-// blocks that fit the device at once.
+// Launch of a persistent kernel in clusters of two blocks.
+struct PairLaunch {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = {};
+    PairLaunch(int threads, int smem, cudaStream_t stream) {
+        attr[0] = pdl_attribute();
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+    PairLaunch(const PairLaunch &) = delete;
+};
+
+// Such a kernel's shared memory limit, as above, and the number of its blocks
+// that fit the device at once.
 struct PairCache {
     AttrCache attr;
     int dev = -1, blocks = 0;
     unsigned long long ctx = 0;
-    cudaError_t prepare(const void *kernel, int most_smem, const cudaLaunchConfig_t &cfg) {
-        cudaError_t e = attr.allow_smem(kernel, most_smem);
+    cudaError_t prepare(const void *kernel, const cudaLaunchConfig_t &cfg) {  // cfg with the most shared memory
+        cudaError_t e = attr.allow_smem(kernel, (int)cfg.dynamicSmemBytes);
         if (e != cudaSuccess || (blocks > 0 && dev == attr.dev && ctx == attr.ctx && ctx != 0)) return e;
         int clusters = 0;
         e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
