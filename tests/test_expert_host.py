@@ -1,0 +1,134 @@
+"""Host-side checks of the experts' products: exports and refusals.  Nothing is launched."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import combine_moe_route_topk_gb300 as moe
+from combine_moe_route_topk_gb300 import _build
+from conftest import ROOT
+
+OK = ctypes.c_void_p(0x10000)      # aligned, never dereferenced on the host
+ODD = ctypes.c_void_p(0x10008)     # not 16-byte aligned
+ODD4 = ctypes.c_void_p(0x10002)    # not 4-byte aligned
+LINEAR, SWIGLU = moe.MOE_EXPERT_LINEAR, moe.MOE_EXPERT_SWIGLU
+INVALID, UNSUPPORTED = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return moe.lib()
+
+
+def _dims(**kw):
+    return moe.make_dims(**{**dict(N=2, T=8, E=4, R=2, H=8, cap_rows=16), **kw})
+
+
+def _call(lib, name, d=None, K=128, F=128, act=LINEAR, a=OK, s=OK, b=OK, t=OK, off=OK, out=OK, extra=None, dtype=0):
+    d = ctypes.byref(d if d is not None else _dims())
+    if name == "gemm":
+        return lib.moe_expert_gemm(d, K, F, act, a, b, off, out, extra, None)
+    if name == "dgrad":
+        return lib.moe_expert_gemm_dgrad(d, K, F, a, b, off, out, None)
+    if name == "wgrad":
+        return lib.moe_expert_gemm_wgrad(d, K, F, a, b, off, out, dtype, None)
+    if name == "swiglu_grad":
+        return lib.moe_expert_swiglu_grad(d, F, a, b, off, out, None)
+    return lib.moe_expert_gemm_fp8(d, K, F, act, a, s, b, t, off, out, extra, None)
+
+
+EVERY = ["gemm", "dgrad", "wgrad", "swiglu_grad", "fp8"]
+
+
+def test_library_exports_every_declared_symbol(lib):
+    text = open(os.path.join(ROOT, "include", "moe_expert.h")).read()
+    names = set(re.findall(r"\b(moe_expert_[a-z0-9_]+)\s*\(", re.sub(r"/\*.*?\*/", "", text, flags=re.S)))
+    assert len(names) == 5
+    for name in names:
+        assert hasattr(lib, name), name
+
+
+@pytest.mark.parametrize("name", EVERY)
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(F=0), INVALID, "multiples of 8"),
+    (dict(F=132), INVALID, "multiples of 8"),
+    (dict(F=-8), INVALID, "multiples of 8"),
+    (dict(F=(1 << 24) + 8), UNSUPPORTED, "2^24"),
+    (dict(off=None), INVALID, "expert_offsets"),
+    (dict(off=ODD4), INVALID, "expert_offsets"),
+    (dict(a=None), INVALID, "NULL"),
+    (dict(b=None), INVALID, "NULL"),
+    (dict(out=None), INVALID, "NULL"),
+    (dict(a=ODD), INVALID, "16-byte"),
+    (dict(b=ODD), INVALID, "16-byte"),
+    (dict(out=ODD), INVALID, "16-byte"),
+    (dict(d=_dims(E=5)), INVALID, "multiple of N"),
+    (dict(d=_dims(R=5)), INVALID, "exceeds E"),
+    (dict(d=_dims(N=64, T=100000, E=384, R=8, cap_rows=0)), UNSUPPORTED, "2^31"),
+])
+def test_bad_arguments_are_refused_before_anything_is_enqueued(lib, name, kw, code, msg):
+    assert _call(lib, name, **kw) == code
+    assert msg in lib.moe_last_error().decode()
+
+
+@pytest.mark.parametrize("name", ["gemm", "dgrad", "wgrad", "fp8"])
+@pytest.mark.parametrize("K", [0, 4, 132, -128])
+def test_bad_reduction_length_is_refused(lib, name, K):
+    assert _call(lib, name, K=K) == INVALID
+
+
+def test_fp8_wants_whole_scale_blocks(lib):
+    assert _call(lib, "fp8", K=136) == INVALID and "128" in lib.moe_last_error().decode()
+    assert _call(lib, "fp8", act=SWIGLU, F=136, extra=OK) == INVALID and "128" in lib.moe_last_error().decode()
+
+
+@pytest.mark.parametrize("name", ["gemm", "fp8"])
+@pytest.mark.parametrize("act", [-1, 2, 16])
+def test_unknown_act_is_refused(lib, name, act):
+    assert _call(lib, name, act=act) == INVALID and "act" in lib.moe_last_error().decode()
+
+
+def test_outputs_of_the_gated_form_are_refused_in_the_linear_one(lib):
+    assert _call(lib, "gemm", extra=OK) == INVALID and "pre" in lib.moe_last_error().decode()
+    assert _call(lib, "fp8", extra=OK) == INVALID and "y_scales" in lib.moe_last_error().decode()
+    assert _call(lib, "fp8", act=SWIGLU, extra=None) == INVALID and "NULL" in lib.moe_last_error().decode()
+    assert _call(lib, "gemm", act=SWIGLU, extra=ODD) == INVALID
+
+
+def test_scales_are_required_and_aligned(lib):
+    for kw in (dict(s=None), dict(t=None), dict(s=ODD4), dict(t=ODD4), dict(act=SWIGLU, extra=ODD4)):
+        assert _call(lib, "fp8", **kw) == INVALID
+
+
+@pytest.mark.parametrize("dtype", [-1, 2, 7])
+def test_wgrad_refuses_other_result_types(lib, dtype):
+    assert _call(lib, "wgrad", dtype=dtype) == INVALID and "dw_dtype" in lib.moe_last_error().decode()
+
+
+def test_sizes_beyond_a_tensor_map_or_the_tile_count_are_refused(lib):
+    assert _call(lib, "gemm", K=1 << 20, F=1 << 20) == UNSUPPORTED and "2^40" in lib.moe_last_error().decode()
+    big = _dims(N=1, T=1 << 26, E=64, R=16, cap_rows=1 << 30)
+    assert _call(lib, "gemm", d=big, K=64, F=1 << 20) == UNSUPPORTED and "tiles" in lib.moe_last_error().decode()
+
+
+@pytest.mark.parametrize("name", ["gemm", "dgrad", "swiglu_grad", "fp8"])
+def test_an_empty_batch_is_accepted_without_buffers(lib, name):
+    assert _call(lib, name, d=_dims(T=0), a=None, b=None, out=None) == moe.MOE_OK
+
+
+def test_binding_refuses_cpu_tensors_and_other_types():
+    d = _dims()
+    bf, u8, f32, i32 = (dict(dtype=t) for t in (torch.bfloat16, torch.uint8, torch.float32, torch.int32))
+    x, w, y, off = torch.zeros(32, 8, **bf), torch.zeros(4, 8, 8, **bf), torch.zeros(32, 8, **bf), torch.zeros(5, **i32)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        moe.expert_gemm(d, 8, 8, LINEAR, x, w, off, y)
+    with pytest.raises(ValueError, match="required"):
+        moe.expert_gemm(d, 8, 8, LINEAR, None, w, off, y)
+    with pytest.raises(ValueError, match="dw must be"):
+        moe.expert_gemm_wgrad(d, 8, 8, y, x, off, torch.zeros(4, 8, 8, dtype=torch.float16))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        moe.expert_gemm_fp8(d, 128, 8, LINEAR, torch.zeros(32, 128, **u8), torch.zeros(32, 1, **f32),
+                            torch.zeros(4, 8, 128, **u8), torch.zeros(4, 1, 1, **f32), off, y)
