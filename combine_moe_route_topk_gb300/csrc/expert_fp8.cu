@@ -53,7 +53,7 @@ struct Args {
     const float *x_scales, *w_scales;
     void *y;
     float *y_scales;
-    int64_t cap;
+    int64_t cap, most;
     int E, L, K, F, w_rows;  // reduction length, result columns, matrix rows of an expert
 };
 
@@ -128,13 +128,13 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         s_gave_up = 0;
         mb_init_fence();
         tma_prefetch_map(&map_w);
-        for (int i = 1; i < 4; ++i) tma_prefetch_map(&map_x.m[i]);
+        prefetch_maps(map_x);
     }
     grid_dependency_wait();  // offsets, rows and scales come from earlier kernels
     grid_launch_dependents();
     constexpr int kStep = kGated ? kBlk : kN;  // result columns of a tile
     const int f_tiles = (a.F + kStep - 1) / kStep;
-    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap,
+    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, a.most,
                                  [&](int c) { return token_tiles(c) * f_tiles; });  // syncs the block
     tc_fence_before();
     __syncthreads();
@@ -419,8 +419,8 @@ cudaError_t launch_expert_gemm_fp8(const ExpertRows &r, int K, int F, int gated,
     const uint64_t strides[2] = {(uint64_t)K, (uint64_t)K * w_rows};
     const uint32_t wbox[3] = {kK, kBlk, 1};
     if (!encode_map(&map_w, 1, 3, wq, wdims, strides, wbox)) return cudaErrorInvalidValue;
-    if (!encode_rows(&map_x, 1, xq, K, r.rows_total)) return cudaErrorInvalidValue;
-    const Args a{r.offsets, x_scales, w_scales, y, y_scales, r.cap, r.E, r.L, K, F, w_rows};
+    if (!encode_rows(&map_x, 1, xq, K, r.rows_total, r.most < kTok ? r.most : kTok)) return cudaErrorInvalidValue;
+    const Args a{r.offsets, x_scales, w_scales, y, y_scales, r.cap, r.most, r.E, r.L, K, F, w_rows};
     if (gated) return launch<true, false>(map_w, map_x, a, stream);
     return y_f32 ? launch<false, true>(map_w, map_x, a, stream) : launch<false, false>(map_w, map_x, a, stream);
 }

@@ -41,7 +41,7 @@ struct Args {
     const int32_t *offsets;
     void *y;
     __nv_bfloat16 *pre;
-    int64_t cap;
+    int64_t cap, most;
     int E, L, K, F;  // reduction length, result columns
 };
 
@@ -99,14 +99,14 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         s_gave_up = 0;
         mb_init_fence();
         tma_prefetch_map(&map_w);
-        for (int i = 0; i < 4; ++i) tma_prefetch_map(&map_x.m[i]);
+        prefetch_maps(map_x);
     }
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
     constexpr int kHalf = kForm == kGated ? kM / 2 : kM;  // result columns of a block
     constexpr int kStep = 2 * kHalf;
     const int m_tiles = (a.F + kStep - 1) / kStep;
-    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap,
+    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, a.most,
                                  [&](int c) { return token_tiles(c) * m_tiles; });  // syncs the block
     tc_fence_before();
     cluster_sync();  // barriers and TMEM of both blocks are ready
@@ -291,6 +291,9 @@ cudaError_t launch(const CUtensorMap &map_w, const RowMaps &map_x, const Args &a
     return cudaLaunchKernelEx(&l.cfg, kern, map_w, map_x, a);
 }
 
+// Most tokens that a block loads: half a pair's.
+int64_t half_tile(const ExpertRows &r) { return (r.most < kTok ? mma_tokens((int)r.most) : kTok) / 2; }
+
 }  // namespace
 
 cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, const void *x, const void *w, void *y,
@@ -309,8 +312,8 @@ cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, con
         const uint32_t box[3] = {kK, kM, 1};
         if (!encode_map(&map_w, 0, 3, w, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    if (!encode_rows(&map_x, 0, x, K, r.rows_total)) return cudaErrorInvalidValue;
-    const Args a{r.offsets, y, static_cast<__nv_bfloat16 *>(pre), r.cap, r.E, r.L, K, F};
+    if (!encode_rows(&map_x, 0, x, K, r.rows_total, half_tile(r))) return cudaErrorInvalidValue;
+    const Args a{r.offsets, y, static_cast<__nv_bfloat16 *>(pre), r.cap, r.most, r.E, r.L, K, F};
     if (gated) return pre ? launch<kGated, false, true>(map_w, map_x, a, stream)
                           : launch<kGated, false, false>(map_w, map_x, a, stream);
     return y_f32 ? launch<kLinear, true, false>(map_w, map_x, a, stream)
@@ -325,8 +328,8 @@ cudaError_t launch_expert_dgrad(const ExpertRows &r, int K, int F, const void *d
     const uint64_t strides[2] = {(uint64_t)K * 2, (uint64_t)K * 2 * F};
     const uint32_t wbox[3] = {64, kK, 1};
     if (!encode_map(&map_w, 0, 3, w, wdims, strides, wbox)) return cudaErrorInvalidValue;
-    if (!encode_rows(&map_x, 0, dy, F, r.rows_total)) return cudaErrorInvalidValue;
-    const Args a{r.offsets, dx, nullptr, r.cap, r.E, r.L, F, K};
+    if (!encode_rows(&map_x, 0, dy, F, r.rows_total, half_tile(r))) return cudaErrorInvalidValue;
+    const Args a{r.offsets, dx, nullptr, r.cap, r.most, r.E, r.L, F, K};
     return launch<kDgrad, false, false>(map_w, map_x, a, stream);
 }
 

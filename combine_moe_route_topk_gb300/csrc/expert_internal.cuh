@@ -10,7 +10,8 @@ namespace moe {
 struct ExpertRows {
     const int32_t *offsets;  // device, [E + 1]
     int E, L;                // experts, experts per rank
-    int64_t cap, rows_total;
+    int64_t cap, rows_total;  // rows of a region, of all of them
+    int64_t most;             // rows that one expert can have
 };
 
 cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, const void *x, const void *w, void *y,

@@ -39,7 +39,7 @@ struct ColumnMaps {
 struct Args {
     const int32_t *offsets;
     void *dw;
-    int64_t cap;
+    int64_t cap, most;
     int E, L, K, F;
 };
 
@@ -97,7 +97,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
     const int mt = (a.F + 2 * kM - 1) / (2 * kM), per = mt * ((a.K + kN - 1) / kN);  // tiles of an expert
-    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, [&](int) { return per; });  // syncs the block
+    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, a.most, [&](int) { return per; });  // syncs the block
     tc_fence_before();
     cluster_sync();  // barriers and TMEM of both blocks are ready
     tc_fence_after();
@@ -299,7 +299,7 @@ cudaError_t launch_expert_wgrad(const ExpertRows &r, int K, int F, const void *d
     ColumnMaps map_dy, map_x;
     if (!encode_columns(&map_dy, dy, F, r.rows_total, kM) || !encode_columns(&map_x, x, K, r.rows_total, kN / 2))
         return cudaErrorInvalidValue;
-    const Args a{r.offsets, dw, r.cap, r.E, r.L, K, F};
+    const Args a{r.offsets, dw, r.cap, r.most, r.E, r.L, K, F};
     return dw_f32 ? launch<true>(map_dy, map_x, a, stream) : launch<false>(map_dy, map_x, a, stream);
 }
 

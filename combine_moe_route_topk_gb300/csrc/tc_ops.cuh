@@ -175,7 +175,11 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *m, 
 // = 4096 took 274 us with boxes of 32 rows only, 212 with boxes of 64.)
 struct RowMaps {
     CUtensorMap m[4];
+    int first;  // the largest box that any tile of the batch can need; larger ones have no map
 };
+__device__ __forceinline__ void prefetch_maps(const RowMaps &maps) {
+    for (int i = maps.first; i < 4; ++i) tma_prefetch_map(&maps.m[i]);
+}
 __host__ __device__ constexpr int rows_loaded(int n) { return (n + 31) & ~31; }
 __device__ __forceinline__ void load_rows(uint32_t dst, const RowMaps &maps, uint32_t bar, int c0, int row, int n) {
     const int rows = rows_loaded(n);
@@ -282,7 +286,7 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap
 __device__ __forceinline__ void load_rows_pair(uint32_t dst, const RowMaps &maps, uint32_t bar, int c0, int row, int n) {
     const int rows = rows_loaded(n);
 #pragma unroll
-    for (int i = 1; i < 4; ++i) {  // half of at most 256
+    for (int i = 1; i < 4; ++i) {  // a half: at most 128
         const int box = 256 >> i;
         if (rows & box) {
             tma_load_2d_pair(dst, &maps.m[i], bar, c0, row);
@@ -361,12 +365,12 @@ struct Groups {
 __host__ __device__ constexpr int groups_bytes(int E) { return ((3 * E + 1) * 4 + 127) / 128 * 128; }
 
 // Fills the tables from expert_offsets; every thread of the block calls it.
-// tiles(count) is the number of tiles of a group.  Offsets that are not an
-// ascending sequence (no output of the count step) give groups that stay
-// inside the regions all the same.
+// tiles(count) is the number of tiles of a group.  Offsets that are no output of
+// the count step (not ascending, or more rows than `most` for an expert) give
+// groups that stay inside the regions and within `most` all the same.
 template <class Tiles>
 __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restrict__ offsets, int E, int L, int64_t cap,
-                                              Tiles tiles) {
+                                              int64_t most, Tiles tiles) {
     Groups g{mem, mem + E, mem + 2 * E};
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         const int d = e / L;
@@ -374,6 +378,7 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
         int64_t lo = (int64_t)__ldg(offsets + e) - base, hi = (int64_t)__ldg(offsets + e + 1) - base;
         lo = lo < 0 ? 0 : (lo < cap ? lo : cap);
         hi = hi < lo ? lo : (hi < cap ? hi : cap);
+        if (hi - lo > most) hi = lo + most;
         g.row[e] = (int)(d * cap + lo);
         g.count[e] = (int)(hi - lo);
     }
@@ -485,10 +490,12 @@ struct PairCache {
 bool encode_map(CUtensorMap *m, int fp8, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
                 const uint32_t *box);
 
-// The maps of load_rows over rows of `cols` elements (16-bit, or 8-bit: fp8).
-inline bool encode_rows(RowMaps *maps, int fp8, const void *base, int cols, int64_t rows) {
+// The maps of load_rows over rows of `cols` elements (16-bit, or 8-bit: fp8),
+// of which no tile takes more than `most` at once.
+inline bool encode_rows(RowMaps *maps, int fp8, const void *base, int cols, int64_t rows, int64_t most) {
     const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, stride = (uint64_t)cols * (fp8 ? 1 : 2);
-    for (int i = 0; i < 4; ++i) {
+    maps->first = most > 128 ? 0 : most > 64 ? 1 : most > 32 ? 2 : 3;  // by rows_loaded(most)
+    for (int i = maps->first; i < 4; ++i) {
         const uint32_t box[2] = {fp8 ? 128u : 64u, 256u >> i};
         if (!encode_map(&maps->m[i], fp8, 2, base, dims, &stride, box)) return false;
     }
