@@ -74,6 +74,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libmoe_route.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -168,23 +170,22 @@ def _stream(stream) -> int:
 
 def _ptr(t: torch.Tensor | None, nbytes: int, name: str, dtype=None, optional=False):
     """t's address, as an integer for a void* argument, once t is seen to fit."""
+    if (t is not None and t.is_cuda and t.get_device() == _current_device() and t.is_contiguous()
+            and (dtype is None or t.dtype is dtype) and t.nbytes >= nbytes):
+        return t.data_ptr()
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    dev = t.get_device()  # -1 on the CPU
-    if dev < 0:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    if dev != _current_device():
+    if t.get_device() != _current_device():
         raise ValueError(f"{name} is on {t.device}, not the current device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-    have = t.nbytes
-    if have < nbytes:
-        raise ValueError(f"{name} holds {have} bytes, needs {nbytes}")
-    return t.data_ptr()
+    raise ValueError(f"{name} holds {t.nbytes} bytes, needs {nbytes}")
 
 
 def route_topk(dims: MoeDims, logits, bias, score_fn, renormalize, topk_idx, topk_w, stream=None):
