@@ -207,8 +207,8 @@ int check_expert(const MoeDims *dims, int K, int F, bool gated, int elem, const 
         return set_error(MOE_ERR_UNSUPPORTED, "%s: a matrix of %lld x %d must stay below 2^40 bytes", what,
                          (long long)wide, K);
     const int64_t big = wide > K ? wide : K;
-    if ((v->pairs / 128 + dims->E) * ((big + 127) / 128) > kI32Max ||
-        (int64_t)dims->E * ((wide + 127) / 128) * (((int64_t)K + 127) / 128) > kI32Max)
+    if ((v->pairs / 128 + dims->E) * ((big + 127) / 128) > kI32Max - 65536 ||
+        (int64_t)dims->E * ((wide + 127) / 128) * (((int64_t)K + 127) / 128) > kI32Max - 65536)
         return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles (N*T*R=%lld, E=%d, K=%d, F=%d)", what,
                          (long long)v->pairs, dims->E, K, F);
     if (!offsets || !aligned(offsets, 4))

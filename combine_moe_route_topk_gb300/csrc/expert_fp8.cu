@@ -362,7 +362,10 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 s_amax[half][quarter * 32 + lane] = top;
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
                 top = fmaxf(top, s_amax[half ^ 1][quarter * 32 + lane]);
-                const float scale = __fdiv_rn(top, 448.f), inv = scale == 0.f ? 0.f : __fdiv_rn(1.f, scale);
+                // h / scale as (h up) (1 / (scale up)): the reciprocal of a
+                // scale below 2^-126 would overflow
+                const float scale = __fdiv_rn(top, 448.f), up = scale < 0x1p-100f ? 0x1p100f : 1.f;
+                const float inv = scale == 0.f ? 0.f : __fdiv_rn(1.f, scale * up);
                 if (mine) {
                     const int64_t row = w.row + quarter * 32 + lane;
                     uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.F + w.f0 + 64 * half;
@@ -372,7 +375,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float2 h0 = unpair(sum[0][i][2 * j]), h1 = unpair(sum[0][i][2 * j + 1]);
-                            p[j] = e4m3x2(h0.x * inv, h0.y * inv) | (e4m3x2(h1.x * inv, h1.y * inv) << 16);
+                            p[j] = e4m3x2(h0.x * up * inv, h0.y * up * inv) | (e4m3x2(h1.x * up * inv, h1.y * up * inv) << 16);
                         }
                         reinterpret_cast<uint4 *>(y)[i] = make_uint4(p[0], p[1], p[2], p[3]);
                     }

@@ -190,7 +190,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
             const Tile w = get_tile(g, a.E, e, t, kStep);
             e = w.e;
-            if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up)) break;
+            if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + steps * kStepPolls)) break;
             tc_fence_after();
             const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(warp * 32) << 16);
             for (int c0 = 0; c0 < w.n; c0 += 32) {

@@ -166,7 +166,8 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                 if (rank == 0) ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
                 if (left % 16 != 0 && ok) {
                     const uint32_t phase = end_phase >> r.slot & 1u;
-                    ok = mb_wait_warp(end_full + 8 * r.slot, phase, gave_up);
+                    // block 1 waits for nothing before: through the whole tile
+                    ok = mb_wait_warp(end_full + 8 * r.slot, phase, gave_up, kPolls + steps * kStepPolls);
                     const int words = (slices * 16 - left) * 8;  // 16-byte words of the lines behind the last row
                     for (int i = 0; i < (kM + kN / 2) / 64; ++i) {
                         uint4 *line = reinterpret_cast<uint4 *>(stages + r.slot * kStage + i * kCols + left * 128);
@@ -207,9 +208,10 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
         for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
             const int e = t / per;
             const Part p = get_part(a, mt, t % per);
-            const bool some = same(g.count[e]) > 0;
+            const int count = same(g.count[e]);
+            const bool some = count > 0;
             if (some) {
-                if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up)) break;
+                if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + (count / kP) * kStepPolls)) break;
                 tc_fence_after();
             }
             const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(warp * 32) << 16);

@@ -60,25 +60,28 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Every wait is bounded: after kPolls polls (each may suspend briefly), or
-// once another warp of the block has given up, it returns false and the
-// block's word `gave_up` is set; each role then leaves its loop, copies in
-// flight are waited for (again bounded), TMEM is freed and the kernel ends.
-constexpr int kPolls = 1 << 20;
-__device__ __forceinline__ bool mb_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
-    for (int i = 0; i < kPolls; ++i) {
+// Every wait is bounded: after `polls` polls (each may suspend briefly), or once
+// another warp of the block has given up, it returns false and the block's
+// word `gave_up` is set; each role then leaves its loop, copies in flight are
+// waited for (again bounded), TMEM is freed and the kernel ends.  A poll takes
+// no less than about 10 ns: kPolls are at least 10 ms, where a stage takes well
+// under 10 us; a wait for a whole tile adds kStepPolls for each of its stages.
+constexpr long long kPolls = 1 << 20, kStepPolls = 1 << 12;
+__device__ __forceinline__ bool mb_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, long long polls = kPolls) {
+    for (long long i = 0; i < polls; ++i) {
         if (mb_try(bar, parity)) return true;
         if ((i & 15) == 15 && *gave_up) return false;
     }
     *gave_up = 1;
     return false;
 }
-__device__ __forceinline__ bool mb_wait_warp(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+__device__ __forceinline__ bool mb_wait_warp(uint32_t bar, uint32_t parity, volatile int *gave_up,
+                                             long long polls = kPolls) {
     if (__all_sync(0xffffffffu, mb_try(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mb_wait(bar, parity, gave_up));
+    return __all_sync(0xffffffffu, mb_wait(bar, parity, gave_up, polls));
 }
 __device__ __forceinline__ void mb_drain(uint32_t bar, uint32_t parity) {  // bounded, result not needed
-    for (int i = 0; i < kPolls && !mb_try(bar, parity); ++i) {
+    for (long long i = 0; i < kPolls && !mb_try(bar, parity); ++i) {
     }
 }
 

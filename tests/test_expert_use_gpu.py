@@ -353,6 +353,27 @@ def test_scales_of_zero_and_zero_rows():
     assert bool((hs[:3, 0] > 0).all())
 
 
+def test_requantised_scales_below_the_normal_range():
+    """h near 1e-37: scales of 2^-129 to 2^-134, whose reciprocals overflow f32.
+    Beside expert_ref's terms, a denormal scale is rounded by up to 2^-150,
+    times a code of at most 448, and h itself by 2^-150."""
+    b = Batch(1, [40], 40)
+    K = F = 128
+    xq, xs = ref.quantise(b.randn(40, K))
+    wq = (torch.randn(1, 2 * F, K, generator=b.g, device="cuda") * 64).to(torch.float8_e4m3fn).view(torch.uint8)
+    ws = torch.empty(1, 2, 1, device="cuda")
+    ws[0, 0], ws[0, 1] = 2.0 ** -10, 2.0 ** -132
+    hq, hs = torch.zeros(40, F, dtype=torch.uint8, device="cuda"), b.out(1, torch.float32)
+    moe.expert_gemm_fp8(b.dims(), K, F, SWIGLU, xq, xs, wq, ws, b.offsets, hq, hs)
+    want, mag = ref.product(b, ref.dequant_rows(xq, xs), ref.dequant_matrix(wq, ws))
+    err = ref.sum_error(K, mag) + 2.0 ** -150 * K
+    h, eh = ref.swiglu(want[:, :F], want[:, F:], err[:, :F], err[:, F:])
+    s = hs.double()
+    assert bool((s < 2.0 ** -126).all()) and bool((s > 0).all())
+    lim = eh + E4M3_HALF * h.abs() + s * 2.0 ** -10 + 449 * 2.0 ** -150 + 4 * F32_HALF * h.abs()
+    assert bool(((ref.e4m3(hq) * s - h).abs() <= lim).all())
+
+
 def test_refusals_on_the_device():
     b = Batch(1, [4], 4)
     x, w, y = b.randn(4, 16), b.randn(1, 8, 16), b.out(8, torch.bfloat16)
