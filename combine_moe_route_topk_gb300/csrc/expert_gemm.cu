@@ -267,7 +267,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mb_arrive_remote(at_leader(tempty + 8 * acc.slot));
+            if (lane == 0) mb_arrive_remote_relaxed(at_leader(tempty + 8 * acc.slot));
             acc.next();
         }
     }

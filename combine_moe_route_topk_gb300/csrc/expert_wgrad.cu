@@ -7,9 +7,10 @@
 // dy (M) by 256 of x (N), each block holding 128 of both and 128 rows of the
 // result.  An expert's rows end anywhere; rows behind them belong to the next
 // expert or hold anything (NaN too), so they are zeroed in shared memory, up
-// to the next multiple of 16: each block's mma warp does so with its part of
-// the expert's last block of 64 rows, which is counted on a barrier of its
-// own, and tells the leader.
+// to the next multiple of 16: a warp of each block does so with its part of
+// the expert's last 64 rows, which are counted on barriers of their own, and
+// tells the leader.  (With the mma warp itself doing so, a tile of 512 rows
+// spent 2600 to 4000 of its 10000 cycles on it.)
 #include <cuda_bf16.h>
 
 #include "expert_internal.cuh"
@@ -26,7 +27,7 @@ constexpr int kCols = kP * 128;  // bytes of 64 columns of a stage
 constexpr int kStages = 6;
 constexpr int kStage = (kM + kN / 2) / 64 * kCols;
 constexpr int kBuf = 4096;  // each storing warp's: 128 bytes of its 32 rows
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;  // 4 warps store results, one loads, one issues mma, one zeroes
 constexpr int kSmem = 1024 + kStages * kStage + 4 * kBuf;
 
 // An operand's columns: whole blocks of 64 are the third dimension of `blocks`,
@@ -82,7 +83,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             mb_init(full + 8 * i, 1);
             mb_init(empty + 8 * i, 1);
             mb_init(end_full + 8 * i, 1);
-            mb_init(end_peer + 8 * i, 1);
+            mb_init(end_peer + 8 * i, 2);  // both blocks have zeroed
         }
         for (int i = 0; i < 2; ++i) {
             mb_init(tfull + 8 * i, 1);
@@ -146,42 +147,28 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
         }
         if (rank == 0) drain_loads(full, r);  // of both blocks
         for (int i = 0; i < kStages; ++i) mb_drain(end_full + 8 * i, (end_phase >> i & 1u) ^ 1u);
-    } else if (warp == 5) {  // zeroes, and the leader's mma
-        Ring<kStages> r;
-        Ring<2> acc;
-        uint32_t end_phase = 0;  // a bit per slot: the end barriers' next phases
-        bool ok = true;
-        for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
-            const int e = t / per;
-            const Part p = get_part(a, mt, t % per);
-            const int count = same(g.count[e]), steps = (count + kP - 1) / kP;
-            if (steps == 0) continue;  // nothing to sum: the results are zeros
-            const uint32_t desc = mma_desc(1, true, true, 2 * kM, p.n), d = tmem + acc.slot * kN;
-            if (rank == 0) {
+    } else if (warp == 5) {  // the leader's mma
+        if (rank == 0) {
+            Ring<kStages> r;
+            Ring<2> acc;
+            uint32_t end_phase = 0;
+            bool ok = true;
+            for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
+                const int e = t / per;
+                const Part p = get_part(a, mt, t % per);
+                const int count = same(g.count[e]), steps = (count + kP - 1) / kP;
+                if (steps == 0) continue;  // nothing to sum: the results are zeros
+                const uint32_t desc = mma_desc(1, true, true, 2 * kM, p.n), d = tmem + acc.slot * kN;
                 ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
                 tc_fence_after();
-            }
-            for (int k = 0; k < steps && ok; ++k) {
-                const int left = min(kP, count - k * kP), slices = (left + 15) / 16;
-                if (rank == 0) ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
-                if (left % 16 != 0 && ok) {
-                    const uint32_t phase = end_phase >> r.slot & 1u;
-                    // block 1 waits for nothing before: through the whole tile
-                    ok = mb_wait_warp(end_full + 8 * r.slot, phase, gave_up, kPolls + steps * kStepPolls);
-                    const int words = (slices * 16 - left) * 8;  // 16-byte words of the lines behind the last row
-                    for (int i = 0; i < (kM + kN / 2) / 64; ++i) {
-                        uint4 *line = reinterpret_cast<uint4 *>(stages + r.slot * kStage + i * kCols + left * 128);
-                        for (int j = lane; j < words; j += 32) line[j] = make_uint4(0u, 0u, 0u, 0u);
+                for (int k = 0; k < steps && ok; ++k) {
+                    const int left = min(kP, count - k * kP), slices = (left + 15) / 16;
+                    ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
+                    if (left % 16 != 0 && ok) {
+                        ok = mb_wait_warp(end_peer + 8 * r.slot, end_phase >> r.slot & 1u, gave_up);
+                        end_phase ^= 1u << r.slot;
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (rank == 0) ok = ok && mb_wait_warp(end_peer + 8 * r.slot, phase, gave_up);
-                    else if (lane == 0) mb_arrive_remote(at_leader(end_peer + 8 * r.slot));
-                    __syncwarp();
-                    end_phase ^= 1u << r.slot;
-                }
-                if (!ok) break;
-                if (rank == 0) {
+                    if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t sa = smem + r.slot * kStage;
@@ -191,17 +178,37 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                         tc_commit_pair(empty + 8 * r.slot);
                     }
                     __syncwarp();
+                    r.next();
                 }
-                r.next();
+                if (elect_one()) tc_commit_pair(tfull + 8 * acc.slot);
+                __syncwarp();
+                acc.next();
             }
-            if (rank == 0 && elect_one()) tc_commit_pair(tfull + 8 * acc.slot);
-            __syncwarp();
-            acc.next();
-        }
-        if (rank == 0) {
             if (elect_one()) tc_commit_pair(done);
             __syncwarp();
             mb_drain(done, 0);
+        }
+    } else if (warp == 6) {  // zeroes behind the experts' last rows
+        int slot = 0;
+        uint32_t end_phase = 0;
+        bool ok = true;
+        for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
+            const int count = same(g.count[t / per]), steps = (count + kP - 1) / kP, left = count % kP;
+            if (count % 16 != 0) {
+                const int last = (slot + steps - 1) % kStages;
+                // waits for nothing before: through the whole tile
+                ok = mb_wait_warp(end_full + 8 * last, end_phase >> last & 1u, gave_up, kPolls + steps * kStepPolls);
+                end_phase ^= 1u << last;
+                const int words = (((left + 15) & ~15) - left) * 8;  // 16-byte words of the lines behind the last row
+                for (int i = 0; i < (kM + kN / 2) / 64; ++i) {
+                    uint4 *line = reinterpret_cast<uint4 *>(stages + last * kStage + i * kCols + left * 128);
+                    for (int j = lane; j < words; j += 32) line[j] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mb_arrive_remote(at_leader(end_peer + 8 * last));
+            }
+            slot = (slot + steps) % kStages;
         }
     } else {  // results: warp w holds rows 32w.. of the block's half, one per lane
         Ring<2> acc;
@@ -257,7 +264,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             if (some) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mb_arrive_remote(at_leader(tempty + 8 * acc.slot));
+                if (lane == 0) mb_arrive_remote_relaxed(at_leader(tempty + 8 * acc.slot));
                 acc.next();
             }
         }

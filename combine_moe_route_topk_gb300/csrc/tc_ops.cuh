@@ -260,8 +260,16 @@ __device__ __forceinline__ uint32_t at_leader(uint32_t addr) {  // the same plac
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
     return r;
 }
-__device__ __forceinline__ void mb_arrive_remote(uint32_t bar) {  // bar from at_leader
+// Arrives at a barrier of the leader (bar from at_leader).  The released form
+// orders the thread's writes before it, for which it waits until its global
+// stores have reached L2: 2000 to 3400 cycles after a tile's results.  What
+// frees an accumulator only orders TMEM loads, which are complete (wait::ld,
+// then tc_fence_before): the relaxed form does.
+__device__ __forceinline__ void mb_arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mb_arrive_remote_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1) {
     asm volatile(
