@@ -14,6 +14,12 @@
 // Blocks work in pairs: one tcgen05.mma of the pair multiplies 256 matrix
 // rows by the tile's tokens, each block loading its 128 rows and half the
 // tokens, which halves what the tokens cost in L2 and shared memory.
+//
+// The tensor core cuts what it adds off below the accumulator's last place, so
+// a long sum comes out small: by 2.4e-7 of its value after 512 elements,
+// 3.5e-6 after 6144.  bf16 results (steps of 7.8e-3) do not show it.  For f32
+// results the sum is taken in parts of 512, which the storing warps add up in
+// registers, rounding to nearest.
 #include <cuda_bf16.h>
 
 #include "expert_internal.cuh"
@@ -26,14 +32,21 @@ namespace {
 constexpr int kM = 128;        // matrix rows of a block's half of a tile
 constexpr int kTok = 256;      // most tokens of a tile
 constexpr int kK = 64;         // reduction elements of a stage: one 128-byte line
-constexpr int kStages = 6;
 constexpr int kBytesA = kM * kK * 2;
 constexpr int kBytesB = kTok / 2 * kK * 2;
 constexpr int kStage = kBytesA + kBytesB;
 constexpr int kBuf = 4096;     // each storing warp's: 32 tokens' results, to be written as whole sectors
-constexpr int kThreads = 192;  // 4 warps store results, one loads, one issues mma
+constexpr int kPart = 512 / kK;  // stages of a part of an f32 sum
 
-constexpr int kSmem = 1024 + kStages * kStage + 4 * kBuf;
+// Warps: those that store results, one that loads, one that issues mma; for
+// f32 results two more that only give their registers away (384 threads are
+// launched with 168 each, the storing ones take 216, the others keep 72).
+template <bool kF32>
+struct Shape {
+    static constexpr int kStoreWarps = kF32 ? 8 : 4, kThreads = kF32 ? 384 : 192;
+    static constexpr int kStages = kF32 ? 5 : 6;
+    static constexpr int kSmem = 1024 + kStages * kStage + kStoreWarps * kBuf;
+};
 
 enum Form { kLinear, kGated, kDgrad };
 
@@ -70,22 +83,23 @@ __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, i
 }
 
 template <int kForm, bool kF32, bool kSave>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<kF32>::kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x, const Args a) {
+    constexpr int kStages = Shape<kF32>::kStages, kStoreWarps = Shape<kF32>::kStoreWarps;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t buf = smem + kStages * kStage + (warp & 3) * kBuf;
-    int *tables = reinterpret_cast<int *>(smem_raw + (smem - smem_u32(smem_raw)) + kStages * kStage + 4 * kBuf);
+    const uint32_t buf = smem + kStages * kStage + (warp & (kStoreWarps - 1)) * kBuf;
+    int *tables = reinterpret_cast<int *>(smem_raw + (smem - smem_u32(smem_raw)) + kStages * kStage + kStoreWarps * kBuf);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages,
                    tempty = tfull + 16, done = tempty + 16;
     volatile int *gave_up = &s_gave_up;
 
     const int rank = same((int)cluster_rank());
-    if (warp == 4) tmem_alloc_pair(smem_u32(&s_tmem), 512);
+    if (warp == kStoreWarps) tmem_alloc_pair(smem_u32(&s_tmem), 512);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mb_init(full + 8 * i, 1);
@@ -93,7 +107,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mb_init(tfull + 8 * i, 1);
-            mb_init(tempty + 8 * i, 8);  // the storing warps of both blocks
+            mb_init(tempty + 8 * i, 2 * kStoreWarps);  // the storing warps of both blocks
         }
         mb_init(done, 1);
         s_gave_up = 0;
@@ -114,7 +128,12 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     const uint32_t tmem = (uint32_t)same((int)s_tmem);
     const int tiles = same(g.prefix[a.E]), steps = (a.K + kK - 1) / kK;
 
-    if (warp == 4) {  // loads
+    const int part = kF32 ? kPart : steps;  // stages that are summed in TMEM
+    if constexpr (kF32) {
+        if (warp >= kStoreWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    }
+
+    if (warp == kStoreWarps) {  // loads
         Ring<kStages> r;
         int e = 0;
         bool ok = true;
@@ -144,7 +163,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             }
         }
         if (rank == 0) drain_loads(full, r);  // of both blocks
-    } else if (warp == 5) {  // mma
+    } else if (warp == kStoreWarps + 1) {  // mma
         if (rank == 0) {
             Ring<kStages> r;
             Ring<2> acc;
@@ -154,35 +173,95 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 const Tile w = get_tile(g, a.E, e, t, kStep);
                 e = w.e;
                 const uint32_t desc = mma_desc(1, kForm == kDgrad, false, 2 * kM, mma_tokens(w.n));
-                const uint32_t d = tmem + acc.slot * kTok;
-                ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
-                tc_fence_after();
-                for (int k = 0; k < steps && ok; ++k) {
-                    ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
-                    if (!ok) break;
+                for (int k0 = 0; k0 < steps && ok; k0 += part) {
+                    const uint32_t d = tmem + acc.slot * kTok;
+                    ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t sa = smem + r.slot * kStage;
-                        // reduction contiguous: 16 elements are 32 bytes of
-                        // the line; else they are 16 lines
-                        const uint64_t da = kForm == kDgrad ? smem_operand(sa, kBytesA / 2, 1024) : smem_operand(sa, 16, 1024);
-                        const uint64_t db = smem_operand(sa + kBytesA, 16, 1024);
-                        constexpr int kStepA = kForm == kDgrad ? 2048 / 16 : 32 / 16;
+                    for (int k = k0; k < min(k0 + part, steps) && ok; ++k) {
+                        ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t sa = smem + r.slot * kStage;
+                            // reduction contiguous: 16 elements are 32 bytes
+                            // of the line; else they are 16 lines
+                            const uint64_t da = kForm == kDgrad ? smem_operand(sa, kBytesA / 2, 1024)
+                                                                : smem_operand(sa, 16, 1024);
+                            const uint64_t db = smem_operand(sa + kBytesA, 16, 1024);
+                            constexpr int kStepA = kForm == kDgrad ? 2048 / 16 : 32 / 16;
 #pragma unroll
-                        for (int i = 0; i < kK / 16; ++i)
-                            mma_bf16_pair(d, da + i * kStepA, db + i * 2, desc, (k | i) != 0);
-                        tc_commit_pair(empty + 8 * r.slot);
+                            for (int i = 0; i < kK / 16; ++i)
+                                mma_bf16_pair(d, da + i * kStepA, db + i * 2, desc, k != k0 || i != 0);
+                            tc_commit_pair(empty + 8 * r.slot);
+                        }
+                        __syncwarp();
+                        r.next();
                     }
+                    if (elect_one()) tc_commit_pair(tfull + 8 * acc.slot);
                     __syncwarp();
-                    r.next();
+                    acc.next();
                 }
-                if (elect_one()) tc_commit_pair(tfull + 8 * acc.slot);
-                __syncwarp();
-                acc.next();
             }
             if (elect_one()) tc_commit_pair(done);
             __syncwarp();
             mb_drain(done, 0);
+        }
+    } else if constexpr (kF32) {
+        if (warp < kStoreWarps) {
+            // results: warp w holds matrix rows 32 (w % 4).. of the block's
+            // half, one per lane, and every other 32 tokens, 2 i + w / 4
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+            const int quarter = warp & 3, half = warp >> 2;
+            Ring<2> acc;
+            int e = 0;
+            bool ok = true;
+            for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
+                const Tile w = get_tile(g, a.E, e, t, kStep);
+                e = w.e;
+                float sum[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
+                for (int k0 = 0; k0 < steps; k0 += part) {
+                    ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + kPart * kStepPolls);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(quarter * 32) << 16) + 32 * half;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (64 * i + 32 * half < w.n) {
+                            uint32_t v[32];
+                            tmem_load32(src + 64 * i, v);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(v[j]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive_remote_relaxed(at_leader(tempty + 8 * acc.slot));
+                    acc.next();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c0 = 64 * i + 32 * half, left = w.n - c0;
+                    if (left > 0) {  // one token's 32 features are 128 bytes
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) st_shared32(buf + j * 128 + lane * 4, __float_as_uint(sum[i][j]));
+                        __syncwarp();
+                        const int f = w.m0 + rank * kHalf + quarter * 32 + lane % 8 * 4;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const int tok = q * 4 + lane / 8;
+                            const uint4 v = ld_shared128(buf + q * 512 + lane * 16);
+                            if (tok < left && f < a.F)
+                                *reinterpret_cast<uint4 *>(static_cast<float *>(a.y) + (int64_t)(w.row + c0 + tok) * a.F + f) = v;
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
         }
     } else {  // results: warp w holds matrix rows 32w.. of the tile, one per lane
         Ring<2> acc;
@@ -238,29 +317,22 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                                                        (int64_t)(w.row + c0 + tok) * a.F + f) = q;
                     }
                 } else {
-                    // one token's 32 features are 64 (f32: 128) bytes
-                    constexpr int kRow = kF32 ? 128 : 64, kElem = kF32 ? 4 : 2;
-                    if constexpr (kF32) {
+                    // one token's 32 features are 64 bytes
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) st_shared32(buf + j * kRow + lane * 4, v[j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const uint32_t two = bf16x2(v[j], v[j + 1]);
-                            st_shared16(buf + j * kRow + lane * 2, two);
-                            st_shared16(buf + (j + 1) * kRow + lane * 2, two >> 16);
-                        }
+                    for (int j = 0; j < 32; j += 2) {
+                        const uint32_t two = bf16x2(v[j], v[j + 1]);
+                        st_shared16(buf + j * 64 + lane * 2, two);
+                        st_shared16(buf + (j + 1) * 64 + lane * 2, two >> 16);
                     }
                     __syncwarp();
+                    const int f = w.m0 + rank * kHalf + warp * 32 + lane % 4 * 8;
 #pragma unroll
-                    for (int i = 0; i < kRow / 16; ++i) {
-                        constexpr int kPer = kRow / 16;  // lanes of a token
-                        const int tok = i * (32 / kPer) + lane / kPer;
-                        const int f = w.m0 + rank * kHalf + warp * 32 + lane % kPer * (16 / kElem);
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = i * 8 + lane / 4;
                         const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
                         if (tok < left && f < a.F)
-                            *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.y) +
-                                                       ((int64_t)(w.row + c0 + tok) * a.F + f) * kElem) = q;
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) +
+                                                       (int64_t)(w.row + c0 + tok) * a.F + f) = q;
                     }
                 }
                 __syncwarp();
@@ -276,18 +348,19 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     cluster_sync();  // neither block leaves, or frees TMEM, while the other may reach it
     tc_fence_after();
     if (tid == 0 && s_gave_up) record_timeout();
-    if (warp == 4) tmem_free_pair(tmem, 512);
+    if (warp == kStoreWarps) tmem_free_pair(tmem, 512);
 }
 
 template <int kForm, bool kF32, bool kSave>
 cudaError_t launch(const CUtensorMap &map_w, const RowMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_gemm_kernel<kForm, kF32, kSave>;
     static thread_local PairCache cache;
-    PairLaunch l(kThreads, kSmem + groups_bytes(1024), stream);
+    using S = Shape<kF32>;
+    PairLaunch l(S::kThreads, S::kSmem + groups_bytes(1024), stream);
     cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), l.cfg);
     if (e != cudaSuccess) return e;
     l.cfg.gridDim = dim3((unsigned)cache.blocks);
-    l.cfg.dynamicSmemBytes = kSmem + groups_bytes(a.E);
+    l.cfg.dynamicSmemBytes = S::kSmem + groups_bytes(a.E);
     return cudaLaunchKernelEx(&l.cfg, kern, map_w, map_x, a);
 }
 

@@ -11,6 +11,10 @@
 // the expert's last 64 rows, which are counted on barriers of their own, and
 // tells the leader.  (With the mma warp itself doing so, a tile of 512 rows
 // spent 2600 to 4000 of its 10000 cycles on it.)
+//
+// f32 results are summed in parts of 512 rows, added up in registers: the
+// tensor core's sums come out small, by 8e-7 of their value after 1024 rows,
+// 1.6e-5 after 16384 (expert_gemm.cu says why).
 #include <cuda_bf16.h>
 
 #include "expert_internal.cuh"
@@ -24,11 +28,20 @@ constexpr int kM = 128;  // columns of dy (rows of dw) of a block's half of a ti
 constexpr int kN = 256;  // columns of x of a tile
 constexpr int kP = 64;   // rows of a stage
 constexpr int kCols = kP * 128;  // bytes of 64 columns of a stage
-constexpr int kStages = 6;
 constexpr int kStage = (kM + kN / 2) / 64 * kCols;
 constexpr int kBuf = 4096;  // each storing warp's: 128 bytes of its 32 rows
-constexpr int kThreads = 224;  // 4 warps store results, one loads, one issues mma, one zeroes
-constexpr int kSmem = 1024 + kStages * kStage + 4 * kBuf;
+constexpr int kPart = 512 / kP;  // stages of a part of an f32 sum
+
+// Warps: those that store results, one that loads, one that issues mma, one
+// that zeroes; for f32 results one more that only gives its registers away
+// (384 threads are launched with 168 each, the storing ones take 216, the
+// others keep 72).
+template <bool kF32>
+struct Shape {
+    static constexpr int kStoreWarps = kF32 ? 8 : 4, kThreads = kF32 ? 384 : 224;
+    static constexpr int kStages = kF32 ? 5 : 6;
+    static constexpr int kSmem = 1024 + kStages * kStage + kStoreWarps * kBuf;
+};
 
 // An operand's columns: whole blocks of 64 are the third dimension of `blocks`,
 // so that one load takes all blocks of a tile; `cols` takes one block and
@@ -62,8 +75,9 @@ __device__ __forceinline__ Part get_part(const Args &a, int mt, int at) {
 }
 
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<kF32>::kThreads, 1)
 expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_constant__ ColumnMaps map_x, const Args a) {
+    constexpr int kStages = Shape<kF32>::kStages, kStoreWarps = Shape<kF32>::kStoreWarps;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[4 * kStages + 5];
     __shared__ uint32_t s_tmem;
@@ -71,13 +85,13 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32, rank = same((int)cluster_rank());
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *stages = smem_raw + (smem - smem_u32(smem_raw));
-    const uint32_t buf = smem + kStages * kStage + (warp & 3) * kBuf;
-    int *tables = reinterpret_cast<int *>(stages + kStages * kStage + 4 * kBuf);
+    const uint32_t buf = smem + kStages * kStage + (warp & (kStoreWarps - 1)) * kBuf;
+    int *tables = reinterpret_cast<int *>(stages + kStages * kStage + kStoreWarps * kBuf);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16,
                    done = tempty + 16, end_full = done + 8, end_peer = end_full + 8 * kStages;
     volatile int *gave_up = &s_gave_up;
 
-    if (warp == 4) tmem_alloc_pair(smem_u32(&s_tmem), 512);
+    if (warp == kStoreWarps) tmem_alloc_pair(smem_u32(&s_tmem), 512);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mb_init(full + 8 * i, 1);
@@ -87,7 +101,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             mb_init(tfull + 8 * i, 1);
-            mb_init(tempty + 8 * i, 8);  // the storing warps of both blocks
+            mb_init(tempty + 8 * i, 2 * kStoreWarps);  // the storing warps of both blocks
         }
         mb_init(done, 1);
         s_gave_up = 0;
@@ -105,7 +119,10 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     const uint32_t tmem = (uint32_t)same((int)s_tmem);
     const int tiles = a.E * per;
 
-    if (warp == 4) {  // loads
+    if constexpr (kF32) {
+        if (warp >= kStoreWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    }
+    if (warp == kStoreWarps) {  // loads
         Ring<kStages> r;
         uint32_t end_phase = 0;  // a bit per slot: the end barriers' next phases
         bool ok = true;
@@ -147,7 +164,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
         }
         if (rank == 0) drain_loads(full, r);  // of both blocks
         for (int i = 0; i < kStages; ++i) mb_drain(end_full + 8 * i, (end_phase >> i & 1u) ^ 1u);
-    } else if (warp == 5) {  // the leader's mma
+    } else if (warp == kStoreWarps + 1) {  // the leader's mma
         if (rank == 0) {
             Ring<kStages> r;
             Ring<2> acc;
@@ -158,37 +175,42 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                 const Part p = get_part(a, mt, t % per);
                 const int count = same(g.count[e]), steps = (count + kP - 1) / kP;
                 if (steps == 0) continue;  // nothing to sum: the results are zeros
-                const uint32_t desc = mma_desc(1, true, true, 2 * kM, p.n), d = tmem + acc.slot * kN;
-                ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
-                tc_fence_after();
-                for (int k = 0; k < steps && ok; ++k) {
-                    const int left = min(kP, count - k * kP), slices = (left + 15) / 16;
-                    ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
-                    if (left % 16 != 0 && ok) {
-                        ok = mb_wait_warp(end_peer + 8 * r.slot, end_phase >> r.slot & 1u, gave_up);
-                        end_phase ^= 1u << r.slot;
-                    }
-                    if (!ok) break;
+                const uint32_t desc = mma_desc(1, true, true, 2 * kM, p.n);
+                const int part = kF32 ? kPart : steps;  // stages that are summed in TMEM
+                for (int k0 = 0; k0 < steps && ok; k0 += part) {
+                    const uint32_t d = tmem + acc.slot * kN;
+                    ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t sa = smem + r.slot * kStage;
-                        const uint64_t da = smem_operand(sa, kCols, 1024), db = smem_operand(sa + kM / 64 * kCols, kCols, 1024);
-                        for (int i = 0; i < slices; ++i)  // 16 rows are 16 lines of 128 bytes
-                            mma_bf16_pair(d, da + i * 128, db + i * 128, desc, (k | i) != 0);
-                        tc_commit_pair(empty + 8 * r.slot);
+                    for (int k = k0; k < min(k0 + part, steps) && ok; ++k) {
+                        const int left = min(kP, count - k * kP), slices = (left + 15) / 16;
+                        ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
+                        if (left % 16 != 0 && ok) {
+                            ok = mb_wait_warp(end_peer + 8 * r.slot, end_phase >> r.slot & 1u, gave_up);
+                            end_phase ^= 1u << r.slot;
+                        }
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t sa = smem + r.slot * kStage;
+                            const uint64_t da = smem_operand(sa, kCols, 1024),
+                                           db = smem_operand(sa + kM / 64 * kCols, kCols, 1024);
+                            for (int i = 0; i < slices; ++i)  // 16 rows are 16 lines of 128 bytes
+                                mma_bf16_pair(d, da + i * 128, db + i * 128, desc, k != k0 || i != 0);
+                            tc_commit_pair(empty + 8 * r.slot);
+                        }
+                        __syncwarp();
+                        r.next();
                     }
+                    if (elect_one()) tc_commit_pair(tfull + 8 * acc.slot);
                     __syncwarp();
-                    r.next();
+                    acc.next();
                 }
-                if (elect_one()) tc_commit_pair(tfull + 8 * acc.slot);
-                __syncwarp();
-                acc.next();
             }
             if (elect_one()) tc_commit_pair(done);
             __syncwarp();
             mb_drain(done, 0);
         }
-    } else if (warp == 6) {  // zeroes behind the experts' last rows
+    } else if (warp == kStoreWarps + 2) {  // zeroes behind the experts' last rows
         int slot = 0;
         uint32_t end_phase = 0;
         bool ok = true;
@@ -210,6 +232,70 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             }
             slot = (slot + steps) % kStages;
         }
+    } else if constexpr (kF32) {
+        if (warp < kStoreWarps) {
+            // results: warp w holds rows 32 (w % 4).. of the block's half, one
+            // per lane, and every other 32 columns, 2 i + w / 4
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+            const int quarter = warp & 3, half = warp >> 2;
+            Ring<2> acc;
+            bool ok = true;
+            for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
+                const int e = t / per;
+                const Part p = get_part(a, mt, t % per);
+                const int steps = (same(g.count[e]) + kP - 1) / kP, n = min(kN, a.K - p.n0);
+                float sum[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
+                for (int k0 = 0; k0 < steps; k0 += kPart) {
+                    ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + kPart * kStepPolls);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(quarter * 32) << 16) + 32 * half;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (64 * i + 32 * half < n) {
+                            uint32_t v[32];
+                            tmem_load32(src + 64 * i, v);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(v[j]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive_remote_relaxed(at_leader(tempty + 8 * acc.slot));
+                    acc.next();
+                }
+                if (!ok) break;
+                // 128 bytes of each row at a time, turned in shared memory so
+                // that eight lanes write a row's 128 bytes (chunks of 16 bytes
+                // swapped by row against bank conflicts)
+                const int r0 = lane / 8, chunk = lane & 7, f0 = p.m0 + rank * kM + quarter * 32;
+                float *to = static_cast<float *>(a.dw) + ((int64_t)e * a.F + f0 + r0) * a.K + p.n0 + chunk * 4;
+                const int64_t step = (int64_t)4 * a.K;
+                const int rows = a.F - f0 - r0, cols = n - chunk * 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c0 = 64 * i + 32 * half;
+                    if (c0 < n) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            st_shared128(buf + lane * 128 + ((q ^ (lane & 7)) * 16),
+                                         make_uint4(__float_as_uint(sum[i][4 * q]), __float_as_uint(sum[i][4 * q + 1]),
+                                                    __float_as_uint(sum[i][4 * q + 2]), __float_as_uint(sum[i][4 * q + 3])));
+                        __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const uint4 v = ld_shared128(buf + (q * 4 + r0) * 128 + ((chunk ^ ((q * 4 + r0) & 7)) * 16));
+                            if (4 * q < rows && c0 < cols) *reinterpret_cast<uint4 *>(to + q * step + c0) = v;
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+        }
     } else {  // results: warp w holds rows 32w.. of the block's half, one per lane
         Ring<2> acc;
         for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
@@ -226,7 +312,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             // 128 bytes of each row at a time, turned in shared memory so that
             // eight lanes write a row's 128 bytes (chunks of 16 bytes swapped
             // by row against bank conflicts)
-            constexpr int kPass = kF32 ? 32 : 64, kElem = kF32 ? 4 : 2;
+            constexpr int kPass = 64, kElem = 2;
             const int r0 = lane / 8, chunk = lane & 7;
             unsigned char *to = static_cast<unsigned char *>(a.dw) +
                                 (((int64_t)e * a.F + f0 + r0) * a.K + p.n0 + chunk * (16 / kElem)) * kElem;
@@ -244,12 +330,8 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 16 / kElem) {
-                        uint4 q;
-                        if constexpr (kF32)
-                            q = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                        else
-                            q = make_uint4(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]),
-                                           bf16x2(v[j + 4], v[j + 5]), bf16x2(v[j + 6], v[j + 7]));
+                        const uint4 q = make_uint4(bf16x2(v[j], v[j + 1]), bf16x2(v[j + 2], v[j + 3]),
+                                                   bf16x2(v[j + 4], v[j + 5]), bf16x2(v[j + 6], v[j + 7]));
                         st_shared128(buf + lane * 128 + ((((32 * h + j) * kElem / 16) ^ (lane & 7)) * 16), q);
                     }
                 }
@@ -274,18 +356,19 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     cluster_sync();  // neither block leaves, or frees TMEM, while the other may reach it
     tc_fence_after();
     if (tid == 0 && s_gave_up) record_timeout();
-    if (warp == 4) tmem_free_pair(tmem, 512);
+    if (warp == kStoreWarps) tmem_free_pair(tmem, 512);
 }
 
 template <bool kF32>
 cudaError_t launch(const ColumnMaps &map_dy, const ColumnMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_wgrad_kernel<kF32>;
     static thread_local PairCache cache;
-    PairLaunch l(kThreads, kSmem + groups_bytes(1024), stream);
+    using S = Shape<kF32>;
+    PairLaunch l(S::kThreads, S::kSmem + groups_bytes(1024), stream);
     cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), l.cfg);
     if (e != cudaSuccess) return e;
     l.cfg.gridDim = dim3((unsigned)cache.blocks);
-    l.cfg.dynamicSmemBytes = kSmem + groups_bytes(a.E);
+    l.cfg.dynamicSmemBytes = S::kSmem + groups_bytes(a.E);
     return cudaLaunchKernelEx(&l.cfg, kern, map_dy, map_x, a);
 }
 
