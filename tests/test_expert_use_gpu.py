@@ -374,6 +374,30 @@ def test_requantised_scales_below_the_normal_range():
     assert bool(((ref.e4m3(hq) * s - h).abs() <= lim).all())
 
 
+def _off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+def test_f32_results_do_not_lose_with_length():
+    """A sum of 16384 is 32 sums of 512 joined in f32 registers.  Each part is as
+    far off as a sum of 512 is, and so is their sum; 32 additions rounded to
+    nearest add at most 32 2^-24 of it (the partial sums of independent values
+    are no larger than the result).  Summed in the tensor core's accumulator
+    alone, the result was 1.7e-5 off, eight times what is allowed here."""
+    off = {}
+    for n in (512, 16384):
+        b = Batch(1, [96], 96)
+        x, w, y = b.row_values(n), b.randn(1, 64, n), b.out(64, torch.float32)
+        moe.expert_gemm(b.dims(moe.MOE_F32), n, 64, LINEAR, x, w, b.offsets, y)
+        off["linear", n] = _off(y, x.double() @ w[0].double().t())
+        b = Batch(1, [n], n)
+        dy, x, dw = b.row_values(64), b.row_values(96), torch.empty(1, 64, 96, device="cuda")
+        moe.expert_gemm_wgrad(b.dims(), 96, 64, dy, x, b.offsets, dw)
+        off["wgrad", n] = _off(dw[0], dy.double().t() @ x.double())
+    for op in ("linear", "wgrad"):
+        assert off[op, 16384] <= off[op, 512] + 32 * F32_HALF, off
+
+
 def test_refusals_on_the_device():
     b = Batch(1, [4], 4)
     x, w, y = b.randn(4, 16), b.randn(1, 8, 16), b.out(8, torch.bfloat16)
