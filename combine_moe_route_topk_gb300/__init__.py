@@ -326,9 +326,21 @@ def dispatch_fused_quant(dims: MoeDims, logits, bias, score_fn, renormalize, x, 
         _stream(stream)))
 
 
-def _expert_rows(dims: MoeDims) -> int:
-    """Rows of the receive buffers (of every rank's region)."""
-    return dims.N * buffer_sizes(dims)["cap_rows"]
+def _expert_call(dims: MoeDims, stream):
+    """(rows of the receive buffers, current device, stream handle) of a call."""
+    try:
+        dev = _current_device()
+    except RuntimeError:  # no driver: every tensor is refused below
+        return dims.N * buffer_sizes(dims)["cap_rows"], None, None
+    return (dims.N * buffer_sizes(dims)["cap_rows"], dev,
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+
+
+def _on(dev, t, nbytes: int, name: str, dtype):
+    """_ptr for a call that has asked for its device once (0.4 us an argument instead of 0.6)."""
+    if t is not None and t.get_device() == dev and t.dtype is dtype and t.is_contiguous() and t.nbytes >= nbytes:
+        return t.data_ptr()
+    return _ptr(t, nbytes, name, dtype)
 
 
 def expert_gemm(dims: MoeDims, K: int, F: int, act: int, x, w, expert_offsets, y, pre=None,
@@ -336,49 +348,49 @@ def expert_gemm(dims: MoeDims, K: int, F: int, act: int, x, w, expert_offsets, y
     """Each expert's rows times its matrix in bf16: y = x w^T (MOE_EXPERT_LINEAR, y of
     dims.y_dtype) or silu(g) * u of the gate and up halves (MOE_EXPERT_SWIGLU, y bf16,
     g and u kept in `pre` where given)."""
-    rows, bf16 = _expert_rows(dims), torch.bfloat16
+    (rows, dev, st), bf16 = _expert_call(dims, stream), torch.bfloat16
     gated = int(act) == MOE_EXPERT_SWIGLU
     yt = bf16 if gated else _TORCH_DTYPE[dims.y_dtype]
     _check(lib().moe_expert_gemm(
-        ctypes.byref(dims), int(K), int(F), int(act), _ptr(x, rows * K * 2, "x", bf16),
-        _ptr(w, dims.E * F * K * (4 if gated else 2), "w", bf16),
-        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
-        _ptr(y, rows * F * yt.itemsize, "y", yt),
-        _ptr(pre, rows * F * 4, "pre", bf16, optional=True), _stream(stream)))
+        ctypes.byref(dims), int(K), int(F), int(act), _on(dev, x, rows * K * 2, "x", bf16),
+        _on(dev, w, dims.E * F * K * (4 if gated else 2), "w", bf16),
+        _on(dev, expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _on(dev, y, rows * F * yt.itemsize, "y", yt),
+        None if pre is None else _on(dev, pre, rows * F * 4, "pre", bf16), st))
 
 
 def expert_gemm_dgrad(dims: MoeDims, K: int, F: int, dy, w, expert_offsets, dx, stream=None):
     """dx = dy w of each expert's rows (bf16)."""
-    rows, bf16 = _expert_rows(dims), torch.bfloat16
+    (rows, dev, st), bf16 = _expert_call(dims, stream), torch.bfloat16
     _check(lib().moe_expert_gemm_dgrad(
-        ctypes.byref(dims), int(K), int(F), _ptr(dy, rows * F * 2, "dy", bf16),
-        _ptr(w, dims.E * F * K * 2, "w", bf16),
-        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
-        _ptr(dx, rows * K * 2, "dx", bf16), _stream(stream)))
+        ctypes.byref(dims), int(K), int(F), _on(dev, dy, rows * F * 2, "dy", bf16),
+        _on(dev, w, dims.E * F * K * 2, "w", bf16),
+        _on(dev, expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _on(dev, dx, rows * K * 2, "dx", bf16), st))
 
 
 def expert_gemm_wgrad(dims: MoeDims, K: int, F: int, dy, x, expert_offsets, dw, stream=None):
     """dw[e] = dy^T x over e's rows, 0 without any (dw bf16 or f32, written whole)."""
-    rows, bf16 = _expert_rows(dims), torch.bfloat16
+    (rows, dev, st), bf16 = _expert_call(dims, stream), torch.bfloat16
     if dw is not None and dw.dtype not in (bf16, torch.float32):
         raise ValueError(f"dw must be {bf16} or {torch.float32} (got {dw.dtype})")
     f32 = dw is not None and dw.dtype == torch.float32
     _check(lib().moe_expert_gemm_wgrad(
-        ctypes.byref(dims), int(K), int(F), _ptr(dy, rows * F * 2, "dy", bf16),
-        _ptr(x, rows * K * 2, "x", bf16),
-        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
-        _ptr(dw, dims.E * F * K * (4 if f32 else 2), "dw"), MOE_F32 if f32 else MOE_BF16,
-        _stream(stream)))
+        ctypes.byref(dims), int(K), int(F), _on(dev, dy, rows * F * 2, "dy", bf16),
+        _on(dev, x, rows * K * 2, "x", bf16),
+        _on(dev, expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _on(dev, dw, dims.E * F * K * (4 if f32 else 2), "dw", torch.float32 if f32 else bf16), MOE_F32 if f32 else MOE_BF16,
+        st))
 
 
 def expert_swiglu_grad(dims: MoeDims, F: int, pre, dh, expert_offsets, dpre, stream=None):
     """Gradient of silu(g) * u: dpre = (dg, du) from pre = (g, u) and dh (bf16)."""
-    rows, bf16 = _expert_rows(dims), torch.bfloat16
+    (rows, dev, st), bf16 = _expert_call(dims, stream), torch.bfloat16
     _check(lib().moe_expert_swiglu_grad(
-        ctypes.byref(dims), int(F), _ptr(pre, rows * F * 4, "pre", bf16),
-        _ptr(dh, rows * F * 2, "dh", bf16),
-        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
-        _ptr(dpre, rows * F * 4, "dpre", bf16), _stream(stream)))
+        ctypes.byref(dims), int(F), _on(dev, pre, rows * F * 4, "pre", bf16),
+        _on(dev, dh, rows * F * 2, "dh", bf16),
+        _on(dev, expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _on(dev, dpre, rows * F * 4, "dpre", bf16), st))
 
 
 def expert_gemm_fp8(dims: MoeDims, K: int, F: int, act: int, xq, x_scales, wq, w_scales,
@@ -386,17 +398,18 @@ def expert_gemm_fp8(dims: MoeDims, K: int, F: int, act: int, xq, x_scales, wq, w
     """Each expert's rows times its matrix in e4m3 with block scales (1 x 128 for the rows,
     128 x 128 for the matrices): y of dims.y_dtype (MOE_EXPERT_LINEAR), or silu(g) * u
     quantised again into codes y and scales y_scales (MOE_EXPERT_SWIGLU)."""
-    rows, f32, u8 = _expert_rows(dims), torch.float32, torch.uint8
+    (rows, dev, st), f32, u8 = _expert_call(dims, stream), torch.float32, torch.uint8
     gated = int(act) == MOE_EXPERT_SWIGLU
     W = F * (2 if gated else 1)
     yt = u8 if gated else _TORCH_DTYPE[dims.y_dtype]
     _check(lib().moe_expert_gemm_fp8(
-        ctypes.byref(dims), int(K), int(F), int(act), _ptr(xq, rows * K, "xq", u8),
-        _ptr(x_scales, rows * (K // 128) * 4, "x_scales", f32), _ptr(wq, dims.E * W * K, "wq", u8),
-        _ptr(w_scales, dims.E * -(-W // 128) * (K // 128) * 4, "w_scales", f32),
-        _ptr(expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
-        _ptr(y, rows * F * yt.itemsize, "y", yt),
-        _ptr(y_scales, rows * (F // 128) * 4, "y_scales", f32, optional=not gated), _stream(stream)))
+        ctypes.byref(dims), int(K), int(F), int(act), _on(dev, xq, rows * K, "xq", u8),
+        _on(dev, x_scales, rows * (K // 128) * 4, "x_scales", f32), _on(dev, wq, dims.E * W * K, "wq", u8),
+        _on(dev, w_scales, dims.E * -(-W // 128) * (K // 128) * 4, "w_scales", f32),
+        _on(dev, expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _on(dev, y, rows * F * yt.itemsize, "y", yt),
+        None if y_scales is None and not gated else
+        _on(dev, y_scales, rows * (F // 128) * 4, "y_scales", f32), st))
 
 
 def combine(dims: MoeDims, y, pos, topk_w, out, stream=None):
