@@ -57,6 +57,7 @@ struct Args {
     int E, L, K, F, w_rows;  // reduction length, result columns, matrix rows of an expert
 };
 
+__host__ __device__ inline int token_tiles(int count) { return (count + kTok - 1) / kTok; }
 
 struct Tile {
     int e, f0, row, n;  // group, first result column, first token row, tokens
@@ -64,8 +65,6 @@ struct Tile {
 
 // Token tiles of a group (of equal size) run fastest: blocks working at the
 // same time share the matrix rows through L2.
-__host__ __device__ inline int token_tiles(int count) { return (count + kTok - 1) / kTok; }
-
 __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, int f_step) {
     Tile r;
     r.e = same(find_group(g, E, e, t));
@@ -95,6 +94,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {  
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
+
 template <bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x, const Args a) {

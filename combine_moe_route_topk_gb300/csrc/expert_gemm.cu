@@ -127,7 +127,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     tc_fence_after();
     const uint32_t tmem = (uint32_t)same((int)s_tmem);
     const int tiles = same(g.prefix[a.E]), steps = (a.K + kK - 1) / kK;
-
     const int part = kF32 ? kPart : steps;  // stages that are summed in TMEM
     if constexpr (kF32) {
         if (warp >= kStoreWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");

@@ -163,32 +163,24 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
         "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1,
-                                            int c2, int c3, int c4) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, "
-        "%7}], [%2];" ::"r"(dst),
-        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-        : "memory");
-}
-
-// Rows of a row-major operand by boxes of 256, 128, 64 and 32 rows of 128
-// bytes: a tile's rows, rounded up to 32, in as few loads as its binary digits.
-// (A load costs the TMA about as much as 40 rows: 16384 tokens by K = 2048, F
-// = 4096 took 274 us with boxes of 32 rows only, 212 with boxes of 64.)
+// Rows of a row-major operand by boxes of 128, 64 and 32 rows of 128 bytes: a
+// block's rows of a tile, at most 128, rounded up to 32, in as few loads as
+// the number has binary digits.  (A load costs the TMA about as much as 40
+// rows: 16384 tokens by K = 2048, F = 4096 took 274 us with boxes of 32 rows
+// only, 212 with boxes of 64.)
 struct RowMaps {
-    CUtensorMap m[4];
+    CUtensorMap m[3];
     int first;  // the largest box that any tile of the batch can need; larger ones have no map
 };
 __device__ __forceinline__ void prefetch_maps(const RowMaps &maps) {
-    for (int i = maps.first; i < 4; ++i) tma_prefetch_map(&maps.m[i]);
+    for (int i = maps.first; i < 3; ++i) tma_prefetch_map(&maps.m[i]);
 }
 __host__ __device__ constexpr int rows_loaded(int n) { return (n + 31) & ~31; }
 __device__ __forceinline__ void load_rows(uint32_t dst, const RowMaps &maps, uint32_t bar, int c0, int row, int n) {
     const int rows = rows_loaded(n);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int box = 256 >> i;
+    for (int i = 0; i < 3; ++i) {
+        const int box = 128 >> i;
         if (rows & box) {
             tma_load_2d(dst, &maps.m[i], bar, c0, row);
             dst += box * 128;
@@ -297,8 +289,8 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap
 __device__ __forceinline__ void load_rows_pair(uint32_t dst, const RowMaps &maps, uint32_t bar, int c0, int row, int n) {
     const int rows = rows_loaded(n);
 #pragma unroll
-    for (int i = 1; i < 4; ++i) {  // a half: at most 128
-        const int box = 256 >> i;
+    for (int i = 0; i < 3; ++i) {
+        const int box = 128 >> i;
         if (rows & box) {
             tma_load_2d_pair(dst, &maps.m[i], bar, c0, row);
             dst += box * 128;
@@ -346,14 +338,6 @@ __host__ __device__ constexpr uint32_t mma_desc(int fmt, bool a_transposed, bool
            ((uint32_t)b_transposed << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
-        : "memory");
-}
 __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -505,9 +489,9 @@ bool encode_map(CUtensorMap *m, int fp8, int rank, const void *base, const uint6
 // of which no tile takes more than `most` at once.
 inline bool encode_rows(RowMaps *maps, int fp8, const void *base, int cols, int64_t rows, int64_t most) {
     const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, stride = (uint64_t)cols * (fp8 ? 1 : 2);
-    maps->first = most > 128 ? 0 : most > 64 ? 1 : most > 32 ? 2 : 3;  // by rows_loaded(most)
-    for (int i = maps->first; i < 4; ++i) {
-        const uint32_t box[2] = {fp8 ? 128u : 64u, 256u >> i};
+    maps->first = most > 96 ? 0 : most > 32 ? 1 : 2;  // by rows_loaded(most)
+    for (int i = maps->first; i < 3; ++i) {
+        const uint32_t box[2] = {fp8 ? 128u : 64u, 128u >> i};
         if (!encode_map(&maps->m[i], fp8, 2, base, dims, &stride, box)) return false;
     }
     return true;
