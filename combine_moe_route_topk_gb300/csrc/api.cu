@@ -230,6 +230,27 @@ bool bad_block_pointers(const void *a, const void *b, const void *c, const char 
     return false;
 }
 
+// An array that a call reads or writes.
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+bool overlap(const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+// The kernels read their inputs by blocks, in no order: results in the same
+// memory are refused.
+template <int kIn>
+bool overlap_any(const Span &out, const Span (&in)[kIn], const char *what, int *rc) {
+    for (const Span &i : in)
+        if (overlap(out, i)) {
+            *rc = set_error(MOE_ERR_INVALID_ARG, "%s: a result overlaps another array of the call", what);
+            return true;
+        }
+    return false;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -583,6 +604,11 @@ int moe_expert_gemm(const MoeDims *dims, int K, int F, int act, const void *x, c
         return set_error(MOE_ERR_INVALID_ARG, "%s: pre is an output of MOE_EXPERT_SWIGLU only", what);
     if (v.NT == 0) return MOE_OK;
     if (bad_block_pointers(x, w, y, what, &rc) || (pre && bad_block_pointers(pre, pre, pre, what, &rc))) return rc;
+    const int64_t wide = (act == MOE_EXPERT_SWIGLU ? 2 : 1) * (int64_t)F;
+    const int64_t y_elem = act == MOE_EXPERT_LINEAR && dims->y_dtype == MOE_F32 ? 4 : 2;
+    const Span out = {y, v.rows_total * F * y_elem}, kept = {pre, v.rows_total * wide * 2};
+    const Span in[] = {{x, v.rows_total * K * 2}, {w, dims->E * wide * K * 2}}, with_y[] = {in[0], in[1], out};
+    if (overlap_any(out, in, what, &rc) || overlap_any(kept, with_y, what, &rc)) return rc;
     return cuda_result(launch_expert_gemm(r, K, F, act == MOE_EXPERT_SWIGLU, x, w, y, dims->y_dtype == MOE_F32, pre,
                                           (cudaStream_t)stream),
                        what);
@@ -597,6 +623,8 @@ int moe_expert_gemm_dgrad(const MoeDims *dims, int K, int F, const void *dy, con
     if (rc != MOE_OK) return rc;
     if (v.NT == 0) return MOE_OK;
     if (bad_block_pointers(dy, w, dx, what, &rc)) return rc;
+    const Span in[] = {{dy, v.rows_total * F * 2}, {w, (int64_t)dims->E * F * K * 2}};
+    if (overlap_any({dx, v.rows_total * K * 2}, in, what, &rc)) return rc;
     return cuda_result(launch_expert_dgrad(r, K, F, dy, w, dx, (cudaStream_t)stream), what);
 }
 
@@ -616,6 +644,8 @@ int moe_expert_gemm_wgrad(const MoeDims *dims, int K, int F, const void *dy, con
                            what);
     }
     if (bad_block_pointers(dy, x, dw, what, &rc)) return rc;
+    const Span in[] = {{dy, v.rows_total * F * 2}, {x, v.rows_total * K * 2}};
+    if (overlap_any({dw, (int64_t)dims->E * F * K * (dw_dtype == MOE_F32 ? 4 : 2)}, in, what, &rc)) return rc;
     return cuda_result(launch_expert_wgrad(r, K, F, dy, x, dw, dw_dtype == MOE_F32, (cudaStream_t)stream), what);
 }
 
@@ -628,6 +658,8 @@ int moe_expert_swiglu_grad(const MoeDims *dims, int F, const void *pre, const vo
     if (rc != MOE_OK) return rc;
     if (v.NT == 0) return MOE_OK;
     if (bad_block_pointers(pre, dh, dpre, what, &rc)) return rc;
+    const Span in[] = {{pre, v.rows_total * F * 4}, {dh, v.rows_total * F * 2}};
+    if (overlap_any({dpre, v.rows_total * F * 4}, in, what, &rc)) return rc;
     return cuda_result(launch_expert_swiglu_grad(r, dims->N, F, pre, dh, dpre, (cudaStream_t)stream), what);
 }
 
@@ -652,6 +684,15 @@ int moe_expert_gemm_fp8(const MoeDims *dims, int K, int F, int act, const void *
         return set_error(MOE_ERR_INVALID_ARG, "%s: a required pointer is NULL", what);
     if (!aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(y_scales, 4))
         return set_error(MOE_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", what);
+    const int64_t wide = (gated ? 2 : 1) * (int64_t)F, blocks = K / 128;
+    const Span out = {y, v.rows_total * F * (gated ? 1 : dims->y_dtype == MOE_F32 ? 4 : 2)};
+    const Span in[] = {{xq, v.rows_total * K},
+                       {x_scales, v.rows_total * blocks * 4},
+                       {wq, dims->E * wide * K},
+                       {w_scales, dims->E * ((wide + 127) / 128) * blocks * 4}};
+    const Span with_y[] = {in[0], in[1], in[2], in[3], out};
+    if (overlap_any(out, in, what, &rc) || overlap_any({y_scales, v.rows_total * (F / 128) * 4}, with_y, what, &rc))
+        return rc;
     return cuda_result(launch_expert_gemm_fp8(r, K, F, gated, xq, x_scales, wq, w_scales, y, dims->y_dtype == MOE_F32,
                                               y_scales, (cudaStream_t)stream),
                        what);

@@ -24,7 +24,7 @@
  *     far as they lie in the rank's region (rows over capacity were
  *     dropped).  Only these rows of the outputs are written; what other
  *     rows of the inputs hold (NaN, say) has no influence.
- *   - Outputs must not overlap inputs.
+ *   - Outputs must not overlap inputs or each other (MOE_ERR_INVALID_ARG).
  *   - Array bases that a call reads by blocks must be 16-byte aligned (all
  *     but expert_offsets and the scales, which need 4).
  *   - Sums are f32; a result is rounded once, to nearest even.  Results do
@@ -97,7 +97,8 @@ int moe_expert_swiglu_grad(const MoeDims *dims, int F, const void *pre, const vo
  *            e4m3 of h * fl32(1/scale), to nearest even, saturated (amax = 0:
  *            scale 0, codes 0): y e4m3 [N*cap][F] and y_scales f32
  *            [N*cap][F/128], the layout moe_dispatch_pack_quant writes, ready
- *            to be the next product's rows.
+ *            to be the next product's rows.  Infinite or NaN sums give
+ *            unspecified codes.
  * Backward passes use the bf16 calls: the fp8 dispatch is a serving form. */
 int moe_expert_gemm_fp8(const MoeDims *dims, int K, int F, int act, const void *xq, const float *x_scales,
                         const void *wq, const float *w_scales, const int32_t *expert_offsets, void *y,

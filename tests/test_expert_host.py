@@ -103,6 +103,29 @@ def test_scales_are_required_and_aligned(lib):
         assert _call(lib, "fp8", **kw) == INVALID
 
 
+@pytest.mark.parametrize("name", EVERY)
+def test_results_over_another_array_are_refused(lib, name):
+    far = [ctypes.c_void_p(0x10000000 * i) for i in range(1, 7)]
+    a, b, s, t, out, extra = far
+    kw = dict(a=a, b=b, s=s, t=t, out=out)
+    for other in ("a", "b") + (("s", "t") if name == "fp8" else ()):
+        # the result begins in the last 16 bytes of another array, and the other way round
+        if name == "wgrad":
+            size = {"a": 32 * 128 * 2, "b": 32 * 128 * 2}[other]
+        else:
+            size = {"a": 32 * 128 * (1 if name == "fp8" else 4 if name == "swiglu_grad" else 2),
+                    "b": (4 * 128 * 128 * (1 if name == "fp8" else 2)) if name != "swiglu_grad" else 32 * 128 * 2,
+                    "s": 32 * 4, "t": 4 * 4}[other]
+        at = kw[other].value
+        for place in (at, at + size - 16, at - 16):
+            assert _call(lib, name, **{**kw, "out": ctypes.c_void_p(place)}) == INVALID, (other, place)
+            assert "overlaps" in lib.moe_last_error().decode()
+    if name in ("gemm", "fp8"):
+        for extra in (out, a, b):
+            assert _call(lib, name, act=SWIGLU, **kw, extra=extra) == INVALID
+            assert "overlaps" in lib.moe_last_error().decode()
+
+
 @pytest.mark.parametrize("dtype", [-1, 2, 7])
 def test_wgrad_refuses_other_result_types(lib, dtype):
     assert _call(lib, "wgrad", dtype=dtype) == INVALID and "dw_dtype" in lib.moe_last_error().decode()
