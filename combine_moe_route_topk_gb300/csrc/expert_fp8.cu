@@ -130,16 +130,16 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         tma_prefetch_map(&map_w);
         prefetch_maps(map_x);
     }
+    tc_fence_before();
+    __syncthreads();  // barriers and TMEM are ready
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)same((int)s_tmem);
     grid_dependency_wait();  // offsets, rows and scales come from earlier kernels
     grid_launch_dependents();
     constexpr int kStep = kGated ? kBlk : kN;  // result columns of a tile
     const int f_tiles = (a.F + kStep - 1) / kStep;
     const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, a.most,
                                  [&](int c) { return token_tiles(c) * f_tiles; });  // syncs the block
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = (uint32_t)same((int)s_tmem);
     const int tiles = same(g.prefix[a.E]), steps = a.K / kK;
     int e = 0;
 

@@ -115,6 +115,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         tma_prefetch_map(&map_w);
         prefetch_maps(map_x);
     }
+    tc_fence_before();
+    cluster_sync();  // barriers and TMEM of both blocks are ready
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)same((int)s_tmem);
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
     constexpr int kHalf = kForm == kGated ? kM / 2 : kM;  // result columns of a block
@@ -122,10 +126,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     const int m_tiles = (a.F + kStep - 1) / kStep;
     const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, a.most,
                                  [&](int c) { return token_tiles(c) * m_tiles; });  // syncs the block
-    tc_fence_before();
-    cluster_sync();  // barriers and TMEM of both blocks are ready
-    tc_fence_after();
-    const uint32_t tmem = (uint32_t)same((int)s_tmem);
     const int tiles = same(g.prefix[a.E]), steps = (a.K + kK - 1) / kK;
     const int part = kF32 ? kPart : steps;  // stages that are summed in TMEM
     if constexpr (kF32) {

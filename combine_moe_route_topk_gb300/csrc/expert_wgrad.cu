@@ -109,14 +109,14 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
         tma_prefetch_map(&map_dy.blocks);
         tma_prefetch_map(&map_x.blocks);
     }
-    grid_dependency_wait();  // offsets and rows come from earlier kernels
-    grid_launch_dependents();
-    const int mt = (a.F + 2 * kM - 1) / (2 * kM), per = mt * ((a.K + kN - 1) / kN);  // tiles of an expert
-    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, a.most, [&](int) { return per; });  // syncs the block
     tc_fence_before();
     cluster_sync();  // barriers and TMEM of both blocks are ready
     tc_fence_after();
     const uint32_t tmem = (uint32_t)same((int)s_tmem);
+    grid_dependency_wait();  // offsets and rows come from earlier kernels
+    grid_launch_dependents();
+    const int mt = (a.F + 2 * kM - 1) / (2 * kM), per = mt * ((a.K + kN - 1) / kN);  // tiles of an expert
+    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, a.most, [&](int) { return per; });  // syncs the block
     const int tiles = a.E * per;
 
     if constexpr (kF32) {
