@@ -35,7 +35,7 @@ constexpr int kK = 64;         // reduction elements of a stage: one 128-byte li
 constexpr int kBytesA = kM * kK * 2;
 constexpr int kBytesB = kTok / 2 * kK * 2;
 constexpr int kStage = kBytesA + kBytesB;
-constexpr int kBuf = 4096;     // each storing warp's: 32 tokens' results, to be written as whole sectors
+constexpr int kStoreWarps = 8;
 constexpr int kPart = 512 / kK;  // stages of a part of an f32 sum
 
 // Warps: those that store results, one that loads, one that issues mma; for
@@ -43,8 +43,8 @@ constexpr int kPart = 512 / kK;  // stages of a part of an f32 sum
 // launched with 168 each, the storing ones take 216, the others keep 72).
 template <bool kF32>
 struct Shape {
-    static constexpr int kStoreWarps = kF32 ? 8 : 4, kThreads = kF32 ? 384 : 192;
-    static constexpr int kStages = kF32 ? 5 : 6;
+    static constexpr int kThreads = 32 * (kStoreWarps + (kF32 ? 4 : 2)), kStages = kF32 ? 5 : 6;
+    static constexpr int kBuf = kF32 ? 4096 : 2048;  // each storing warp's: 32 tokens' results, to be written as whole sectors
     static constexpr int kSmem = 1024 + kStages * kStage + kStoreWarps * kBuf;
 };
 
@@ -85,7 +85,7 @@ __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, i
 template <int kForm, bool kF32, bool kSave>
 __global__ void __launch_bounds__(Shape<kF32>::kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x, const Args a) {
-    constexpr int kStages = Shape<kF32>::kStages, kStoreWarps = Shape<kF32>::kStoreWarps;
+    constexpr int kStages = Shape<kF32>::kStages, kBuf = Shape<kF32>::kBuf;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
     __shared__ uint32_t s_tmem;
@@ -262,7 +262,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 }
             }
         }
-    } else {  // results: warp w holds matrix rows 32w.. of the tile, one per lane
+    } else {
+        // results: rows as above, straight from TMEM, 32 tokens at a time of
+        // every other 32.  (Four warps, each with all tokens, took 8.7 us for
+        // 222 rows of K = 1000, F = 776 with pre kept, eight take 8.4.)
+        const int quarter = warp & 3, half = warp >> 2;
         Ring<2> acc;
         int e = 0;
         for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
@@ -270,8 +274,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             e = w.e;
             if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + steps * kStepPolls)) break;
             tc_fence_after();
-            const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(warp * 32) << 16);
-            for (int c0 = 0; c0 < w.n; c0 += 32) {
+            const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(quarter * 32) << 16);
+            for (int c0 = 32 * half; c0 < w.n; c0 += 64) {
                 uint32_t v[32];
                 tmem_load32(src + c0, v);
                 const int left = w.n - c0;
@@ -280,7 +284,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     // up rows of the same features; of a pair of tokens each
                     // half of the lanes finishes one
                     const int fl = (lane >> 4) * 8 + (lane & 7), up = (lane >> 3) & 1;
-                    const int f0 = w.m0 + rank * kHalf + warp * 16;
+                    const int f0 = w.m0 + rank * kHalf + quarter * 16;
                     if constexpr (kSave) {
                         const uint32_t to = buf + up * 32 + fl * 2;
 #pragma unroll
@@ -292,10 +296,10 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int tok = i * 8 + lane / 4, half = (lane >> 1) & 1, f = f0 + (lane & 1) * 8;
+                            const int tok = i * 8 + lane / 4, which = (lane >> 1) & 1, f = f0 + (lane & 1) * 8;
                             const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
                             if (tok < left && f < a.F)
-                                *reinterpret_cast<uint4 *>(a.pre + ((int64_t)(w.row + c0 + tok) * 2 + half) * a.F + f) = q;
+                                *reinterpret_cast<uint4 *>(a.pre + ((int64_t)(w.row + c0 + tok) * 2 + which) * a.F + f) = q;
                         }
                         __syncwarp();
                     }
@@ -324,7 +328,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                         st_shared16(buf + (j + 1) * 64 + lane * 2, two >> 16);
                     }
                     __syncwarp();
-                    const int f = w.m0 + rank * kHalf + warp * 32 + lane % 4 * 8;
+                    const int f = w.m0 + rank * kHalf + quarter * 32 + lane % 4 * 8;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int tok = i * 8 + lane / 4;
