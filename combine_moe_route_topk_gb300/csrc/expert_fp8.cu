@@ -138,8 +138,8 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     grid_launch_dependents();
     constexpr int kStep = kGated ? kBlk : kN;  // result columns of a tile
     const int f_tiles = (a.F + kStep - 1) / kStep;
-    const Groups g = make_groups(tables, a.offsets, a.E, a.L, a.cap, a.most,
-                                 [&](int c) { return token_tiles(c) * f_tiles; });  // syncs the block
+    const Groups g = make_groups<0, 0>(tables, a.offsets, a.E, a.L, a.cap, a.most, 0,
+                                       [&](int c, int) { return token_tiles(c) * f_tiles; });  // syncs the block
     const int tiles = same(g.prefix[a.E]), steps = a.K / kK;
     int e = 0;
 

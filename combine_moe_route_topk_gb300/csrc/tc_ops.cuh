@@ -356,17 +356,22 @@ struct Groups {
     int *row;     // [E]
     int *count;   // [E]
     int *prefix;  // [E + 1]
+    int shift;    // log2 of the most rows of a tile
 };
 __host__ __device__ constexpr int groups_bytes(int E) { return ((3 * E + 1) * 4 + 127) / 128 * 128; }
 
 // Fills the tables from expert_offsets; every thread of the block calls it.
-// tiles(count) is the number of tiles of a group.  Offsets that are no output of
-// the count step (not ascending, or more rows than `most` for an expert) give
-// groups that stay inside the regions and within `most` all the same.
-template <class Tiles>
+// tiles(count, shift) is the number of tiles of a group when a tile takes at
+// most 2^shift rows.  The shift is kMost, made less (down to kLeast) as long
+// as all tiles then still run at once in the `units` of the grid: tiles that
+// leave some idle are made shorter.  Offsets that are no output of the count
+// step (not ascending, or more rows than `most` for an expert) give groups
+// that stay inside the regions and within `most` all the same.
+template <int kMost, int kLeast, class Tiles>
 __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restrict__ offsets, int E, int L, int64_t cap,
-                                              int64_t most, Tiles tiles) {
-    Groups g{mem, mem + E, mem + 2 * E};
+                                              int64_t most, int units, Tiles tiles) {
+    __shared__ int s_shift;
+    Groups g{mem, mem + E, mem + 2 * E, kMost};
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         const int d = e / L;
         const int64_t base = __ldg(offsets + d * L);
@@ -379,9 +384,24 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
     }
     __syncthreads();
     if (threadIdx.x < 32) {
+        constexpr int kTries = kMost - kLeast + 1;
         const int lane = threadIdx.x, per = (E + 31) / 32, e0 = lane * per, e1 = min(E, e0 + per);
-        int sum = 0;
-        for (int e = e0; e < e1; ++e) sum += tiles(g.count[e]);
+        int sums[kTries] = {}, shift = kMost;
+        for (int e = e0; e < e1; ++e) {
+            const int c = g.count[e];
+#pragma unroll
+            for (int i = 0; i < kTries; ++i) sums[i] += tiles(c, kMost - i);
+        }
+        int sum = sums[0];
+        if constexpr (kTries > 1) {
+            int all[kTries];  // does not get less with the shift
+#pragma unroll
+            for (int i = 1; i < kTries; ++i) all[i] = __reduce_add_sync(0xffffffffu, sums[i]);
+#pragma unroll
+            for (int i = 1; i < kTries; ++i) {
+                if (all[i] <= units) shift = kMost - i, sum = sums[i];
+            }
+        }
         int before = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -389,13 +409,15 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
             if (lane >= o) before += v;
         }
         if (lane == 31) g.prefix[E] = before;
+        if (lane == 0) s_shift = shift;
         before -= sum;
         for (int e = e0; e < e1; ++e) {
             g.prefix[e] = before;
-            before += tiles(g.count[e]);
+            before += tiles(g.count[e], shift);
         }
     }
     __syncthreads();
+    if constexpr (kLeast < kMost) g.shift = same(s_shift);
     return g;
 }
 

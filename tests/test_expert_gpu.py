@@ -83,6 +83,43 @@ def test_dgrad(N, counts, cap, K, F):
     ref.check_untouched(b, dx)
 
 
+def _matrix_tiles(b, shift):
+    """Least number of tiles of matrix rows with which token tiles of 2^shift rows are the longest that are needed."""
+    def tiles(k):
+        return sum(-(-(b.span(e).stop - b.span(e).start) // 2 ** k) for e in range(b.E))
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    return 1 if shift == 6 else pairs // tiles(shift - 1) + 1
+
+
+@pytest.mark.parametrize("form", ["linear", "f32", "gated", "dgrad"])
+@pytest.mark.parametrize("shift", [6, 7, 8])
+@pytest.mark.parametrize("N,counts,cap", [r for r in ROWS if max(r[1]) > 64], ids=_ids)
+def test_token_tiles(N, counts, cap, shift, form):
+    """Small batches are cut into tiles of 64 or 128 tokens so that all pairs of blocks get one: each size, by the
+    number of columns."""
+    b = Batch(N, counts, cap)
+    step = 128 if form == "gated" else 256
+    F, K = _matrix_tiles(b, shift) * step - 40, 72
+    x = b.row_values(K)
+    if form == "dgrad":
+        w = b.randn(b.E, K, F, scale=K ** -0.5)
+        y = b.out(F, torch.bfloat16)
+        moe.expert_gemm_dgrad(b.dims(), F, K, x, w, b.offsets, y)
+        want, mag = ref.product(b, x, w.transpose(1, 2))
+        err = ref.sum_error(K, mag)
+    else:
+        w = b.randn(b.E, 2 * F if form == "gated" else F, K, scale=K ** -0.5)
+        y = b.out(F, torch.float32 if form == "f32" else torch.bfloat16)
+        moe.expert_gemm(b.dims(moe.MOE_F32 if form == "f32" else moe.MOE_BF16), K, F,
+                        moe.MOE_EXPERT_SWIGLU if form == "gated" else moe.MOE_EXPERT_LINEAR, x, w, b.offsets, y)
+        want, mag = ref.product(b, x, w)
+        err = ref.sum_error(K, mag)
+        if form == "gated":
+            want, err = ref.swiglu(want[:, :F], want[:, F:], err[:, :F], err[:, F:])
+    ref.check(y[b.valid], want[b.valid], err[b.valid], F32_HALF if form == "f32" else BF16_HALF, "y")
+    ref.check_untouched(b, y)
+
+
 @pytest.mark.parametrize("K,F", SIZES, ids=_ids)
 @pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
 @pytest.mark.parametrize("f32", [False, True])
