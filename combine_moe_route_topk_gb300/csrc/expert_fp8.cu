@@ -136,10 +136,12 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     const uint32_t tmem = (uint32_t)same((int)s_tmem);
     grid_dependency_wait();  // offsets, rows and scales come from earlier kernels
     grid_launch_dependents();
-    constexpr int kStep = kGated ? kBlk : kN;  // result columns of a tile
-    const int f_tiles = (a.F + kStep - 1) / kStep;
-    const Groups g = make_groups<0, 0>(tables, a.offsets, a.E, a.L, a.cap, a.most, 0,
-                                       [&](int c, int) { return token_tiles(c) * f_tiles; });  // syncs the block
+    // Result columns of a tile: 256, or 128 where all tiles then still run at
+    // once (8 experts of 128 rows, K = 7168, F = 2048: 27.3 us against 30.0).
+    const Groups g = make_groups<kGated ? 7 : 8, 7>(
+        tables, a.offsets, a.E, a.L, a.cap, a.most, gridDim.x,
+        [&](int c, int shift) { return token_tiles(c) * ((a.F + (1 << shift) - 1) >> shift); });  // syncs the block
+    const int width = 1 << g.shift;
     const int tiles = same(g.prefix[a.E]), steps = a.K / kK;
     int e = 0;
 
@@ -148,9 +150,9 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         Ring<kStages> r;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile w = get_tile(g, a.E, e, t, kStep);
+            const Tile w = get_tile(g, a.E, e, t, width);
             e = w.e;
-            const bool two = kGated || w.f0 + kBlk < a.F;  // the second block of matrix rows exists
+            const bool two = kGated || (width == kN && w.f0 + kBlk < a.F);  // the second block of matrix rows exists
             const int second = w.f0 + (kGated ? a.F : kBlk);
             for (int k = 0; k < steps; ++k) {
                 ok = mb_wait_warp(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
@@ -172,9 +174,9 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         Ring<2> acc;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile w = get_tile(g, a.E, e, t, kStep);
+            const Tile w = get_tile(g, a.E, e, t, width);
             e = w.e;
-            const uint32_t desc = mma_desc(0, false, false, kTok, kGated ? kN : min(kN, (a.F - w.f0 + 15) & ~15));
+            const uint32_t desc = mma_desc(0, false, false, kTok, kGated ? kN : min(width, (a.F - w.f0 + 15) & ~15));
             for (int k = 0; k < steps; ++k) {
                 ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up) &&
                      mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
@@ -206,9 +208,9 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         Ring<2> acc;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile w = get_tile(g, a.E, e, t, kStep);
+            const Tile w = get_tile(g, a.E, e, t, width);
             e = w.e;
-            const bool in0 = t0 < w.n, in1 = t0 + 32 < w.n, two = kGated || w.f0 + kBlk < a.F;
+            const bool in0 = t0 < w.n, in1 = t0 + 32 < w.n, two = kGated || (width == kN && w.f0 + kBlk < a.F);
             const float *sx = a.x_scales + (int64_t)(w.row + t0) * steps, *sx1 = sx + (int64_t)32 * steps;
             const float *sw0 = a.w_scales + ((int64_t)w.e * fb + w.f0 / kBlk) * steps;
             const float *sw1 = sw0 + (kGated ? (int64_t)(a.F / kBlk) * steps : steps);
@@ -253,7 +255,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         Ring<2> acc;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile w = get_tile(g, a.E, e, t, kStep);
+            const Tile w = get_tile(g, a.E, e, t, width);
             e = w.e;
             const bool some = quarter * 32 < w.n, mine = quarter * 32 + lane < w.n;
             uint64_t sum[2][4][8];  // [block][16 columns][pair]
@@ -315,6 +317,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 const uint32_t put = buf + lane * 64, get = buf + t0 * 64 + (((lane & 3) ^ ((t0 >> 1) & 3)) * 16);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
+                    if (b == 1 && width < kN) break;
 #pragma unroll
                     for (int c0 = 0; c0 < 64; c0 += kCols) {
 #pragma unroll

@@ -180,6 +180,23 @@ def test_fp8_linear(N, counts, cap, K, F, f32):
     ref.check_untouched(b, y)
 
 
+@pytest.mark.parametrize("last", [8, 136], ids=["one_block_last", "two_blocks_last"])
+@pytest.mark.parametrize("N,counts,cap", [r for r in ROWS if sum(r[1]) > 0], ids=_ids)
+@pytest.mark.parametrize("f32", [False, True])
+def test_fp8_wide(N, counts, cap, last, f32):
+    """So many columns that the tiles of 128 do not run at once and tiles of 256 are taken."""
+    b = Batch(N, counts, cap)
+    tiles = sum(-(-(b.span(e).stop - b.span(e).start) // 128) for e in range(b.E))
+    K, F = 256, torch.cuda.get_device_properties(0).multi_processor_count // tiles // 2 * 256 + 256 + last
+    xq, xs, wq, ws = _fp8_operands(b, K, F)
+    y = b.out(F, torch.float32 if f32 else torch.bfloat16)
+    moe.expert_gemm_fp8(b.dims(moe.MOE_F32 if f32 else moe.MOE_BF16), K, F, moe.MOE_EXPERT_LINEAR, xq, xs, wq, ws,
+                        b.offsets, y)
+    want, mag = ref.product(b, ref.dequant_rows(xq, xs), ref.dequant_matrix(wq, ws))
+    ref.check(y[b.valid], want[b.valid], ref.sum_error(K, mag)[b.valid], F32_HALF if f32 else BF16_HALF, "y")
+    ref.check_untouched(b, y)
+
+
 @pytest.mark.parametrize("K,F", [(128, 128), (384, 256), (1152, 384), (640, 640)], ids=_ids)
 @pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
 def test_fp8_gated(N, counts, cap, K, F):
