@@ -138,9 +138,10 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     grid_launch_dependents();
     // Result columns of a tile: 256, or 128 where all tiles then still run at
     // once (8 experts of 128 rows, K = 7168, F = 2048: 27.3 us against 30.0).
-    const Groups g = make_groups<kGated ? 7 : 8, 7>(
+    const Groups g = make_groups<kGated ? 7 : 8, 7, 1>(
         tables, a.offsets, a.E, a.L, a.cap, a.most, gridDim.x,
-        [&](int c, int shift) { return token_tiles(c) * ((a.F + (1 << shift) - 1) >> shift); });  // syncs the block
+        [&](int c, int shift) { return token_tiles(c) * ((a.F + (1 << shift) - 1) >> shift); },
+        [](int) { return 0; });  // syncs the block
     const int width = 1 << g.shift;
     const int tiles = same(g.prefix[a.E]), steps = a.K / kK;
     int e = 0;

@@ -116,8 +116,8 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
     const int mt = (a.F + 2 * kM - 1) / (2 * kM), per = mt * ((a.K + kN - 1) / kN);  // tiles of an expert
-    const Groups g = make_groups<0, 0>(tables, a.offsets, a.E, a.L, a.cap, a.most, 0,
-                                       [&](int, int) { return per; });  // syncs the block
+    const Groups g = make_groups<0, 0, 1>(tables, a.offsets, a.E, a.L, a.cap, a.most, 0,
+                                       [&](int, int) { return per; }, [](int) { return 0; });  // syncs the block
     const int tiles = a.E * per;
 
     if constexpr (kF32) {

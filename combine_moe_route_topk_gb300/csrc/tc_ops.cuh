@@ -355,23 +355,41 @@ __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint
 struct Groups {
     int *row;     // [E]
     int *count;   // [E]
-    int *prefix;  // [E + 1]
-    int shift;    // log2 of the most rows of a tile
+    int *prefix;  // [E + 1], in the order in which the tiles are taken
+    int *order;   // [E], the experts in that order
+    int shift;    // log2 of the most rows (or columns) of a tile
+    int sorted;   // `order` is not the experts' own
 };
-__host__ __device__ constexpr int groups_bytes(int E) { return ((3 * E + 1) * 4 + 127) / 128 * 128; }
+__host__ __device__ constexpr int groups_bytes(int E, bool ordered = false) {
+    return (((ordered ? 4 : 3) * E + 1) * 4 + 127) / 128 * 128;
+}
+
+__device__ __forceinline__ int scan(int v, int lane) {  // sum over the lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
 
 // Fills the tables from expert_offsets; every thread of the block calls it.
 // tiles(count, shift) is the number of tiles of a group when a tile takes at
 // most 2^shift rows.  The shift is kMost, made less (down to kLeast) as long
 // as all tiles then still run at once in the `units` of the grid: tiles that
-// leave some idle are made shorter.  Offsets that are no output of the count
-// step (not ascending, or more rows than `most` for an expert) give groups
-// that stay inside the regions and within `most` all the same.
-template <int kMost, int kLeast, class Tiles>
+// leave some idle are made shorter.  Where they take more than kRounds rounds
+// (fewer gain less than the sorting takes), and kRanks > 1, the groups are
+// taken in the order of rank(count), 0 to kRanks - 1 (for groups without
+// rows), so that the tiles of a round are alike.  Offsets that are no output of
+// the count step (not ascending, or more rows than `most` for an expert) give
+// groups that stay inside the regions and within `most` all the same.
+constexpr int kRounds = 4;
+template <int kMost, int kLeast, int kRanks, class Tiles, class Rank>
 __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restrict__ offsets, int E, int L, int64_t cap,
-                                              int64_t most, int units, Tiles tiles) {
-    __shared__ int s_shift;
-    Groups g{mem, mem + E, mem + 2 * E, kMost};
+                                              int64_t most, int units, Tiles tiles, Rank rank) {
+    constexpr bool kSort = kRanks > 1;
+    __shared__ int s_shift, s_sorted;
+    Groups g{mem, mem + E, mem + 2 * E, mem + 3 * E + 1, kMost, 0};
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         const int d = e / L;
         const int64_t base = __ldg(offsets + d * L);
@@ -381,12 +399,13 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
         if (hi - lo > most) hi = lo + most;
         g.row[e] = (int)(d * cap + lo);
         g.count[e] = (int)(hi - lo);
+        if constexpr (kSort) g.order[e] = e;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
         constexpr int kTries = kMost - kLeast + 1;
         const int lane = threadIdx.x, per = (E + 31) / 32, e0 = lane * per, e1 = min(E, e0 + per);
-        int sums[kTries] = {}, shift = kMost;
+        int sums[kTries] = {}, shift = kMost, sorted = 0;
         for (int e = e0; e < e1; ++e) {
             const int c = g.count[e];
 #pragma unroll
@@ -402,6 +421,40 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
                 if (all[i] <= units) shift = kMost - i, sum = sums[i];
             }
         }
+        if constexpr (kSort) {
+            if (__reduce_add_sync(0xffffffffu, sum) > kRounds * units) {
+                int at[kRanks] = {}, first = 0, kinds = 0;  // groups of a rank, then the next one's place
+                for (int c0 = 0; c0 < E; c0 += 32) {
+                    int r = -1;
+                    if (c0 + lane < E) g.prefix[c0 + lane] = r = rank(g.count[c0 + lane]);
+#pragma unroll
+                    for (int i = 0; i < kRanks; ++i) at[i] += __popc(__ballot_sync(0xffffffffu, r == i));
+                }
+#pragma unroll
+                for (int i = 0; i < kRanks; ++i) {
+                    const int n = at[i];
+                    at[i] = first;
+                    first += n;
+                    kinds += i < kRanks - 1 && n > 0;
+                }
+                if (kinds > 1) {
+                    sorted = 1;
+                    for (int c0 = 0; c0 < E; c0 += 32) {
+                        const int r = c0 + lane < E ? g.prefix[c0 + lane] : -1;
+#pragma unroll
+                        for (int i = 0; i < kRanks; ++i) {
+                            const uint32_t alike = __ballot_sync(0xffffffffu, r == i);
+                            if (r == i) g.order[at[i] + __popc(alike & ((1u << lane) - 1))] = c0 + lane;
+                            at[i] += __popc(alike);
+                        }
+                    }
+                    __syncwarp();  // the order is complete
+                    sum = 0;
+                    for (int i = e0; i < e1; ++i) sum += tiles(g.count[g.order[i]], shift);
+                }
+                __syncwarp();  // prefix is written again
+            }
+        }
         int before = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -409,15 +462,16 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
             if (lane >= o) before += v;
         }
         if (lane == 31) g.prefix[E] = before;
-        if (lane == 0) s_shift = shift;
+        if (lane == 0) s_shift = shift, s_sorted = sorted;
         before -= sum;
-        for (int e = e0; e < e1; ++e) {
-            g.prefix[e] = before;
-            before += tiles(g.count[e], shift);
+        for (int i = e0; i < e1; ++i) {
+            g.prefix[i] = before;
+            before += tiles(g.count[kSort ? g.order[i] : i], shift);
         }
     }
     __syncthreads();
     if constexpr (kLeast < kMost) g.shift = same(s_shift);
+    if constexpr (kSort) g.sorted = same(s_sorted);
     return g;
 }
 

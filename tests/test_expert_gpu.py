@@ -84,15 +84,16 @@ def test_dgrad(N, counts, cap, K, F):
 
 
 def _matrix_tiles(b, shift):
-    """Least number of tiles of matrix rows with which token tiles of 2^shift rows are the longest that are needed."""
+    """Least number of tiles of matrix rows with which token tiles of 2^shift rows are the longest that are needed
+    (9: tiles of 256 rows take more than four rounds and are sorted by size)."""
     def tiles(k):
         return sum(-(-(b.span(e).stop - b.span(e).start) // 2 ** k) for e in range(b.E))
     pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
-    return 1 if shift == 6 else pairs // tiles(shift - 1) + 1
+    return 1 if shift == 6 else (4 if shift == 9 else 1) * pairs // tiles(shift - 1) + 1
 
 
 @pytest.mark.parametrize("form", ["linear", "f32", "gated", "dgrad"])
-@pytest.mark.parametrize("shift", [6, 7, 8])
+@pytest.mark.parametrize("shift", [6, 7, 8, 9])
 @pytest.mark.parametrize("N,counts,cap", [r for r in ROWS if max(r[1]) > 64], ids=_ids)
 def test_token_tiles(N, counts, cap, shift, form):
     """Small batches are cut into tiles of 64 or 128 tokens so that all pairs of blocks get one: each size, by the
@@ -117,6 +118,28 @@ def test_token_tiles(N, counts, cap, shift, form):
         if form == "gated":
             want, err = ref.swiglu(want[:, :F], want[:, F:], err[:, :F], err[:, F:])
     ref.check(y[b.valid], want[b.valid], err[b.valid], F32_HALF if form == "f32" else BF16_HALF, "y")
+    ref.check_untouched(b, y)
+
+
+@pytest.mark.parametrize("form", ["linear", "dgrad"])
+@pytest.mark.parametrize("N,E,most,F", [(1, 33, 520, 2056), (2, 70, 300, 1288), (4, 1024, 40, 264)])
+def test_many_experts(N, E, most, F, form):
+    """Experts of mixed sizes, some of them empty, in more tiles than four rounds: sorted by the size of their tiles."""
+    g = torch.Generator().manual_seed(E)
+    counts = (torch.rand(E, generator=g) * 1.2 * most - 0.2 * most).clamp(min=0).int().tolist()
+    b = Batch(N, counts, max(sum(counts[r * E // N:(r + 1) * E // N]) for r in range(N)))
+    K = 72
+    x = b.row_values(K)
+    y = b.out(F, torch.bfloat16)
+    if form == "linear":
+        w = b.randn(E, F, K, scale=K ** -0.5)
+        moe.expert_gemm(b.dims(), K, F, moe.MOE_EXPERT_LINEAR, x, w, b.offsets, y)
+    else:
+        w = b.randn(E, K, F, scale=K ** -0.5)
+        moe.expert_gemm_dgrad(b.dims(), F, K, x, w, b.offsets, y)
+        w = w.transpose(1, 2)
+    want, mag = ref.product(b, x, w)
+    ref.check(y[b.valid], want[b.valid], ref.sum_error(K, mag)[b.valid], BF16_HALF, "y")
     ref.check_untouched(b, y)
 
 
