@@ -25,7 +25,7 @@ namespace moe {
 namespace {
 
 constexpr int kM = 128;  // columns of dy (rows of dw) of a block's half of a tile
-constexpr int kN = 256;  // columns of x of a tile
+constexpr int kN = 256;  // most columns of x of a tile
 constexpr int kP = 64;   // rows of a stage
 constexpr int kCols = kP * 128;  // bytes of 64 columns of a stage
 constexpr int kStage = (kM + kN / 2) / 64 * kCols;
@@ -55,6 +55,7 @@ struct Args {
     void *dw;
     int64_t cap, most;
     int E, L, K, F;
+    int width;  // columns of x of a tile
 };
 
 // Tile `at` of an expert, and what block `rank` of the pair has of it.
@@ -66,8 +67,8 @@ struct Part {
 __device__ __forceinline__ Part get_part(const Args &a, int mt, int at) {
     Part p;
     p.m0 = at % mt * 2 * kM;
-    p.n0 = at / mt * kN;
-    p.n = min(kN, (a.K - p.n0 + 31) & ~31);  // a pair's N is a multiple of 32
+    p.n0 = at / mt * a.width;
+    p.n = min(a.width, (a.K - p.n0 + 31) & ~31);  // a pair's N is a multiple of 32
     p.m_cols0 = min(2, (a.F - p.m0 + 63) / 64);
     p.m_cols1 = max(0, min(2, (a.F - p.m0 - kM + 63) / 64));
     p.n_cols = (p.n / 2 + 63) / 64;
@@ -115,7 +116,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     const uint32_t tmem = (uint32_t)same((int)s_tmem);
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
-    const int mt = (a.F + 2 * kM - 1) / (2 * kM), per = mt * ((a.K + kN - 1) / kN);  // tiles of an expert
+    const int mt = (a.F + 2 * kM - 1) / (2 * kM), per = mt * ((a.K + a.width - 1) / a.width);  // tiles of an expert
     const Groups g = make_groups<0, 0, 1>(tables, a.offsets, a.E, a.L, a.cap, a.most, 0,
                                        [&](int, int) { return per; }, [](int) { return 0; });  // syncs the block
     const int tiles = a.E * per;
@@ -132,7 +133,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             const Part p = get_part(a, mt, t % per);
             const int row = same(g.row[e]), count = same(g.count[e]), steps = (count + kP - 1) / kP;
             const int m0 = p.m0 + rank * kM, n0 = p.n0 + rank * (p.n / 2), m_cols = rank == 0 ? p.m_cols0 : p.m_cols1;
-            const bool whole_m = m0 + kM <= a.F, whole_n = p.n0 + kN <= a.K;
+            const bool whole_m = m0 + kM <= a.F, whole_n = a.width == kN && p.n0 + kN <= a.K;
             for (int k = 0; k < steps; ++k) {
                 ok = mb_wait_warp(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
                 if (!ok) break;
@@ -244,7 +245,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
                 const int e = t / per;
                 const Part p = get_part(a, mt, t % per);
-                const int steps = (same(g.count[e]) + kP - 1) / kP, n = min(kN, a.K - p.n0);
+                const int steps = (same(g.count[e]) + kP - 1) / kP, n = min(a.width, a.K - p.n0);
                 float sum[4][32];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -314,7 +315,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                 tc_fence_after();
             }
             const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(warp * 32) << 16);
-            const int f0 = p.m0 + rank * kM + warp * 32, n = min(kN, a.K - p.n0);
+            const int f0 = p.m0 + rank * kM + warp * 32, n = min(a.width, a.K - p.n0);
             // 128 bytes of each row at a time, turned in shared memory so that
             // eight lanes write a row's 128 bytes (chunks of 16 bytes swapped
             // by row against bank conflicts)
@@ -366,7 +367,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
 }
 
 template <bool kF32>
-cudaError_t launch(const ColumnMaps &map_dy, const ColumnMaps &map_x, const Args &a, cudaStream_t stream) {
+cudaError_t launch(const ColumnMaps &map_dy, const ColumnMaps &map_x, Args a, cudaStream_t stream) {
     auto kern = expert_wgrad_kernel<kF32>;
     static thread_local PairCache cache;
     using S = Shape<kF32>;
@@ -374,6 +375,10 @@ cudaError_t launch(const ColumnMaps &map_dy, const ColumnMaps &map_x, const Args
     cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), l.cfg);
     if (e != cudaSuccess) return e;
     l.cfg.gridDim = dim3((unsigned)cache.blocks);
+    // 128 columns where all tiles then still run at once: one expert of 8192
+    // rows, K = F = 1024, f32, takes 36 us against 41; 64 gain no more
+    const int64_t narrow = (int64_t)a.E * ((a.F + 2 * kM - 1) / (2 * kM)) * ((a.K + kN / 2 - 1) / (kN / 2));
+    a.width = narrow <= cache.blocks / 2 ? kN / 2 : kN;
     l.cfg.dynamicSmemBytes = S::kSmem + groups_bytes(a.E);
     return cudaLaunchKernelEx(&l.cfg, kern, map_dy, map_x, a);
 }
@@ -397,7 +402,7 @@ cudaError_t launch_expert_wgrad(const ExpertRows &r, int K, int F, const void *d
     ColumnMaps map_dy, map_x;
     if (!encode_columns(&map_dy, dy, F, r.rows_total, kM) || !encode_columns(&map_x, x, K, r.rows_total, kN / 2))
         return cudaErrorInvalidValue;
-    const Args a{r.offsets, dw, r.cap, r.most, r.E, r.L, K, F};
+    const Args a{r.offsets, dw, r.cap, r.most, r.E, r.L, K, F, kN};
     return dw_f32 ? launch<true>(map_dy, map_x, a, stream) : launch<false>(map_dy, map_x, a, stream);
 }
 

@@ -158,6 +158,13 @@ def test_wgrad(N, counts, cap, K, F, f32):
                   F32_HALF if f32 else BF16_HALF, f"dw[{e}]")
 
 
+@pytest.mark.parametrize("N,counts,cap", [r for r in ROWS if sum(r[1]) > 0], ids=_ids)
+@pytest.mark.parametrize("f32", [False, True])
+def test_wgrad_wide(N, counts, cap, f32):
+    """So many columns that tiles of 128 do not run at once, for one expert either, and tiles of 256 are taken."""
+    test_wgrad(N, counts, cap, 2056, 2568, f32)
+
+
 @pytest.mark.parametrize("F", [8, 136, 264, 2048, 2056])
 @pytest.mark.parametrize("N,counts,cap", ROWS, ids=_ids)
 def test_swiglu_grad(N, counts, cap, F):
