@@ -660,7 +660,7 @@ int moe_expert_swiglu_grad(const MoeDims *dims, int F, const void *pre, const vo
     if (bad_block_pointers(pre, dh, dpre, what, &rc)) return rc;
     const Span in[] = {{pre, v.rows_total * F * 4}, {dh, v.rows_total * F * 2}};
     if (overlap_any({dpre, v.rows_total * F * 4}, in, what, &rc)) return rc;
-    return cuda_result(launch_expert_swiglu_grad(r, dims->N, F, pre, dh, dpre, (cudaStream_t)stream), what);
+    return cuda_result(launch_expert_swiglu_grad(r, dims->N, v.pairs, F, pre, dh, dpre, (cudaStream_t)stream), what);
 }
 
 int moe_expert_gemm_fp8(const MoeDims *dims, int K, int F, int act, const void *xq, const float *x_scales,

@@ -20,8 +20,8 @@ cudaError_t launch_expert_dgrad(const ExpertRows &r, int K, int F, const void *d
                                 cudaStream_t stream);
 cudaError_t launch_expert_wgrad(const ExpertRows &r, int K, int F, const void *dy, const void *x, void *dw, int dw_f32,
                                 cudaStream_t stream);
-cudaError_t launch_expert_swiglu_grad(const ExpertRows &r, int N, int F, const void *pre, const void *dh, void *dpre,
-                                      cudaStream_t stream);
+cudaError_t launch_expert_swiglu_grad(const ExpertRows &r, int N, int64_t pairs, int F, const void *pre, const void *dh,
+                                      void *dpre, cudaStream_t stream);
 cudaError_t launch_expert_gemm_fp8(const ExpertRows &r, int K, int F, int gated, const void *xq, const float *x_scales,
                                    const void *wq, const float *w_scales, void *y, int y_f32, float *y_scales,
                                    cudaStream_t stream);

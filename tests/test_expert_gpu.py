@@ -185,6 +185,23 @@ def test_swiglu_grad(N, counts, cap, F):
     ref.check_untouched(b, dpre)
 
 
+@pytest.mark.parametrize("N,E,cap", [(2, 2, 1), (31, 31, 9), (33, 66, 5), (70, 70, 12), (256, 512, 7), (1024, 1024, 4)])
+def test_swiglu_grad_ranks(N, E, cap):
+    """Many ranks, some without rows and some whose region overflows."""
+    g = torch.Generator().manual_seed(N)
+    counts = (torch.rand(E, generator=g) * 16 - 4).clamp(min=0).int().tolist()
+    b = Batch(N, counts, cap, seed=N)
+    F = 136
+    pre, dh = b.row_values(2 * F, scale=3.0), b.row_values(F)
+    dpre = b.out(2 * F, torch.bfloat16)
+    moe.expert_swiglu_grad(b.dims(), F, pre, dh, b.offsets, dpre)
+    g, u, d = pre[b.valid, :F].double(), pre[b.valid, F:].double(), dh[b.valid].double()
+    s, t = torch.special.expit(g), torch.special.expit(-g)
+    ref.check(dpre[b.valid, :F], d * u * s * (1 + g * t), 16 * F32_HALF * (d * u * s).abs() * (1 + g.abs()), BF16_HALF, "dg")
+    ref.check(dpre[b.valid, F:], d * g * s, 16 * F32_HALF * (d * g * s).abs(), BF16_HALF, "du")
+    ref.check_untouched(b, dpre)
+
+
 def _fp8_operands(b, K, W):
     x = b.row_values(K)
     x[~b.valid] = 0
