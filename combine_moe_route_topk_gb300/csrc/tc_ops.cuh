@@ -409,7 +409,10 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
         for (int e = e0; e < e1; ++e) {
             const int c = g.count[e];
 #pragma unroll
-            for (int i = 0; i < kTries; ++i) sums[i] += tiles(c, kMost - i);
+            for (int i = 0; i < kTries; ++i) {
+                sums[i] += tiles(c, kMost - i);
+                if (i > 0) sums[i] = min(sums[i], 1 << 25);  // too many anyway; 32 lanes' do not overflow
+            }
         }
         int sum = sums[0];
         if constexpr (kTries > 1) {
