@@ -169,7 +169,9 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 r.next();
             }
         }
-        drain_loads(full, r);
+        drain_ring(full, r);
+        drain_ring(empty, r);
+        mb_drain(done, 0);
     } else if (warp == kSumWarps + 1) {  // mma
         Ring<kStages> r;
         Ring<2> acc;
@@ -199,7 +201,6 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         }
         if (elect_one()) tc_commit(done);
         __syncwarp();
-        mb_drain(done, 0);
     } else if (warp >= kSumWarps + 2) {
         // scales: each of two warps takes 64 tokens, two a lane; the next
         // blocks' are on their way while these wait for their accumulator

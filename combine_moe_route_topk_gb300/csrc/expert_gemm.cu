@@ -192,7 +192,9 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 r.next();
             }
         }
-        if (rank == 0) drain_loads(full, r);  // of both blocks
+        if (rank == 0) drain_ring(full, r);  // of both blocks
+        drain_ring(empty, r);  // in each block: its loads, and the leader's arrivals, the last of them `done`
+        mb_drain(done, 0);
     } else if (warp == kStoreWarps + 1) {  // mma
         if (rank == 0) {
             Ring<kStages> r;
@@ -234,7 +236,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             }
             if (elect_one()) tc_commit_pair(done);
             __syncwarp();
-            mb_drain(done, 0);
         }
     } else if constexpr (kF32) {
         if (warp < kStoreWarps) {

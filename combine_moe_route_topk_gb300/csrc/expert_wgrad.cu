@@ -164,7 +164,9 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                 r.next();
             }
         }
-        if (rank == 0) drain_loads(full, r);  // of both blocks
+        if (rank == 0) drain_ring(full, r);  // of both blocks
+        drain_ring(empty, r);  // in each block: its loads, and the leader's arrivals, the last of them `done`
+        mb_drain(done, 0);
         for (int i = 0; i < kStages; ++i) mb_drain(end_full + 8 * i, (end_phase >> i & 1u) ^ 1u);
     } else if (warp == kStoreWarps + 1) {  // the leader's mma
         if (rank == 0) {
@@ -210,7 +212,6 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             }
             if (elect_one()) tc_commit_pair(done);
             __syncwarp();
-            mb_drain(done, 0);
         }
     } else if (warp == kStoreWarps + 2) {  // zeroes behind the experts' last rows
         int slot = 0;

@@ -127,13 +127,19 @@ struct Ring {
     }
 };
 
-// Waits (bounded) for the last loads into every slot of a ring: r is the
-// producer's position after its last load.  Nothing may still be landing in
-// shared memory when the block ends.
+// Waits (bounded, all slots together) for the last use of every slot of a
+// ring: r is the producer's position after its last load.  Nothing may still be
+// landing in shared memory, loads or arrivals at a barrier, when the block ends.
+// On `full` barriers the last loads have landed, on `empty` ones mma has read
+// them too.  A pair's loads are counted on the leader's `full` barriers alone,
+// and after a wait that gave up the two producers may be at different places:
+// each block knows about its own loads, and about the arrivals that the leader's
+// commits send it, by its own `empty` barriers.
 template <int kSlots>
-__device__ __forceinline__ void drain_loads(uint32_t full, Ring<kSlots> r) {
+__device__ __forceinline__ void drain_ring(uint32_t bars, Ring<kSlots> r) {
+    long long left = kPolls;
     for (int i = 0; i < kSlots; ++i) {
-        mb_drain(full + 8 * r.slot, r.phase ^ 1u);
+        while (!mb_try(bars + 8 * r.slot, r.phase ^ 1u) && left > 0) --left;
         r.next();
     }
 }

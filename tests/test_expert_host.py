@@ -155,3 +155,28 @@ def test_binding_refuses_cpu_tensors_and_other_types():
     with pytest.raises(ValueError, match="CUDA tensor"):
         moe.expert_gemm_fp8(d, 128, 8, LINEAR, torch.zeros(32, 128, **u8), torch.zeros(32, 1, **f32),
                             torch.zeros(4, 8, 128, **u8), torch.zeros(4, 1, 1, **f32), off, y)
+
+
+def _enclosing(text, needle):
+    """The heads of the blocks around `needle` (which stands once in the source)."""
+    text = re.sub(r"//[^\n]*", "", text)
+    assert text.count(needle) == 1, needle
+    heads, at = [], 0
+    for i, c in enumerate(text[:text.index(needle)]):
+        if c in "{};":
+            if c == "{":
+                heads.append(text[at:i].strip())
+            elif c == "}":
+                heads.pop()
+            at = i + 1
+    return heads + [text[at:text.index(needle)].strip()]
+
+
+@pytest.mark.parametrize("name", ["expert_gemm.cu", "expert_wgrad.cu"])
+@pytest.mark.parametrize("needle", ["drain_ring(empty", "mb_drain(done"])
+def test_both_blocks_of_a_pair_wait_for_the_leaders_commits(name, needle):
+    """The leader's commits arrive in both blocks' shared memory: each block waits for its own last arrivals
+    before the closing barrier, which orders threads, not arrivals under way."""
+    text = open(os.path.join(_build.CSRC, name)).read()
+    assert text.index(needle) < text.rindex("cluster_sync()")
+    assert not any("rank" in h.split(")")[0] for h in _enclosing(text, needle) if h.startswith(("if", "else")))
