@@ -99,10 +99,10 @@ template <bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x, const Args a) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[2 * kStages + 7];
+    __shared__ __align__(8) unsigned long long bars[2 * kStages + 11];
     __shared__ float s_x[2][kTok];     // the tokens' scales of a block, per accumulator
     __shared__ float2 s_w[2];          // the two blocks of matrix rows' scales
-    __shared__ float s_amax[2][kTok];  // largest |h| of a token in each half of the features
+    __shared__ float s_amax[2][2][kTok];  // largest |h| of a token in each half of the features, for two tiles by turns
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
@@ -110,7 +110,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     const uint32_t buf = smem + kStages * kStage + (warp & (kSumWarps - 1)) * kBuf;
     int *tables = reinterpret_cast<int *>(smem_raw + (smem - smem_u32(smem_raw)) + kStages * kStage + kSumWarps * kBuf);
     const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16,
-                   sempty = tempty + 16, done = sempty + 16;
+                   sempty = tempty + 16, done = sempty + 16, met = done + 8;
     volatile int *gave_up = &s_gave_up;
 
     if (warp == kSumWarps) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -125,6 +125,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             mb_init(sempty + 8 * i, kSumWarps);
         }
         mb_init(done, 1);
+        for (int i = 0; i < 4; ++i) mb_init(met + 8 * i, 2);  // the two warps that share 32 tokens
         s_gave_up = 0;
         mb_init_fence();
         tma_prefetch_map(&map_w);
@@ -255,6 +256,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         // and 64 columns of both blocks, 64 (w / 4)..
         const int quarter = warp & 3, half = warp >> 2;
         Ring<2> acc;
+        int turn = 0;  // of the meetings at `met`
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             const Tile w = get_tile(g, a.E, e, t, width);
@@ -364,9 +366,17 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                         sum[0][i][j] = pair(__float_as_uint(h0), __float_as_uint(h1));
                         top = fmaxf(top, fmaxf(fabsf(h0), fabsf(h1)));
                     }
-                s_amax[half][quarter * 32 + lane] = top;
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                top = fmaxf(top, s_amax[half ^ 1][quarter * 32 + lane]);
+                // (a wait like the others: the other warp may have given
+                // up.  One meeting a tile: what is written here is written
+                // again after the next one, which the other warp reaches
+                // after reading it.)
+                s_amax[turn][half][quarter * 32 + lane] = top;
+                __syncwarp();
+                if (lane == 0) mb_arrive(met + 8 * quarter);
+                ok = mb_wait_warp(met + 8 * quarter, turn, gave_up);
+                if (!ok) break;
+                top = fmaxf(top, s_amax[turn][half ^ 1][quarter * 32 + lane]);
+                turn ^= 1;
                 // h / scale as (h up) (1 / (scale up)): the reciprocal of a
                 // scale below 2^-126 would overflow
                 const float scale = __fdiv_rn(top, 448.f), up = scale < 0x1p-100f ? 0x1p100f : 1.f;
@@ -386,7 +396,6 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                     }
                     if (half == 0) a.y_scales[row * (a.F / kBlk) + w.f0 / kBlk] = scale;
                 }
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");  // s_amax is written again
             }
         }
     }

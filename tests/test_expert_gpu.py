@@ -263,3 +263,25 @@ def test_fp8_gated(N, counts, cap, K, F):
     ref.check(got, h, eh + got_s * 2.0 ** -10 + 4 * F32_HALF * h.abs(), E4M3_HALF, "codes")
     ref.check_untouched(b, ys)
     assert bool((y[~b.valid] == 0xA5).all())
+
+
+def test_fp8_gated_many_tiles():
+    """Several tiles for each block, in a row: the tokens' largest values of one tile and the next stay apart.  The
+    tokens' scales lie 2^-12 to 2^12 apart from tile to tile, so a value of another tile would show."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    K, F, rows = 128, 256, 128 * sms * 2 + 77
+    b = Batch(1, [rows], rows)
+    xq, xs, wq, ws = _fp8_operands(b, K, 2 * F)
+    xs *= torch.exp2(((torch.arange(rows, device="cuda") // 61) % 25 - 12).float()).unsqueeze(1)
+    y = torch.full((rows, F), 0xA5, dtype=torch.uint8, device="cuda")
+    ys = b.out(F // 128, torch.float32)
+    moe.expert_gemm_fp8(b.dims(), K, F, moe.MOE_EXPERT_SWIGLU, xq, xs, wq, ws, b.offsets, y, ys)
+    want, mag = ref.product(b, ref.dequant_rows(xq, xs), ref.dequant_matrix(wq, ws))
+    err = ref.sum_error(K, mag)
+    h, eh = ref.swiglu(want[:, :F], want[:, F:], err[:, :F], err[:, F:])
+    h, eh = h.unflatten(1, (-1, 128)), eh.unflatten(1, (-1, 128))
+    # the scale's own division: half a unit, and 2^-150 where it is below the normal range
+    ref.check(ys, h.abs().amax(2) / 448, eh.amax(2) / 448 + 2.0 ** -149, 2 * F32_HALF, "scales")
+    got_s = ys.double().unsqueeze(2)
+    ref.check(ref.e4m3(y).unflatten(1, (-1, 128)) * got_s, h, eh + got_s * 2.0 ** -10 + 4 * F32_HALF * h.abs(), E4M3_HALF,
+              "codes")

@@ -180,3 +180,11 @@ def test_both_blocks_of_a_pair_wait_for_the_leaders_commits(name, needle):
     text = open(os.path.join(_build.CSRC, name)).read()
     assert text.index(needle) < text.rindex("cluster_sync()")
     assert not any("rank" in h.split(")")[0] for h in _enclosing(text, needle) if h.startswith(("if", "else")))
+
+
+@pytest.mark.parametrize("name", ["expert_gemm.cu", "expert_wgrad.cu", "expert_fp8.cu", "tc_ops.cuh"])
+def test_warps_meet_at_bounded_waits_only(name):
+    """A named barrier of some warps would wait for ever for one that has given up.  Whole blocks and clusters meet
+    before the roles part and after they are all done."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, name)).read())
+    assert not re.search(r"\bbar\.|\bbarrier\.(?!cluster)|__syncthreads_|cooperative_groups", text)
