@@ -239,6 +239,7 @@ bool overlap(const Span &a, const Span &b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
     return a.p && b.p && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
 }
+Span offsets_span(const ExpertRows &r) { return {r.offsets, ((int64_t)r.E + 1) * 4}; }
 // The kernels read their inputs by blocks, in no order: results in the same
 // memory are refused.
 template <int kIn>
@@ -607,7 +608,8 @@ int moe_expert_gemm(const MoeDims *dims, int K, int F, int act, const void *x, c
     const int64_t wide = (act == MOE_EXPERT_SWIGLU ? 2 : 1) * (int64_t)F;
     const int64_t y_elem = act == MOE_EXPERT_LINEAR && dims->y_dtype == MOE_F32 ? 4 : 2;
     const Span out = {y, v.rows_total * F * y_elem}, kept = {pre, v.rows_total * wide * 2};
-    const Span in[] = {{x, v.rows_total * K * 2}, {w, dims->E * wide * K * 2}}, with_y[] = {in[0], in[1], out};
+    const Span in[] = {{x, v.rows_total * K * 2}, {w, dims->E * wide * K * 2}, offsets_span(r)};
+    const Span with_y[] = {in[0], in[1], in[2], out};
     if (overlap_any(out, in, what, &rc) || overlap_any(kept, with_y, what, &rc)) return rc;
     return cuda_result(launch_expert_gemm(r, K, F, act == MOE_EXPERT_SWIGLU, x, w, y, dims->y_dtype == MOE_F32, pre,
                                           (cudaStream_t)stream),
@@ -623,7 +625,7 @@ int moe_expert_gemm_dgrad(const MoeDims *dims, int K, int F, const void *dy, con
     if (rc != MOE_OK) return rc;
     if (v.NT == 0) return MOE_OK;
     if (bad_block_pointers(dy, w, dx, what, &rc)) return rc;
-    const Span in[] = {{dy, v.rows_total * F * 2}, {w, (int64_t)dims->E * F * K * 2}};
+    const Span in[] = {{dy, v.rows_total * F * 2}, {w, (int64_t)dims->E * F * K * 2}, offsets_span(r)};
     if (overlap_any({dx, v.rows_total * K * 2}, in, what, &rc)) return rc;
     return cuda_result(launch_expert_dgrad(r, K, F, dy, w, dx, (cudaStream_t)stream), what);
 }
@@ -637,15 +639,15 @@ int moe_expert_gemm_wgrad(const MoeDims *dims, int K, int F, const void *dy, con
     if (rc != MOE_OK) return rc;
     if (dw_dtype != MOE_BF16 && dw_dtype != MOE_F32)
         return set_error(MOE_ERR_INVALID_ARG, "%s: dw_dtype must be MOE_BF16 or MOE_F32 (got %d)", what, dw_dtype);
+    const Span out = {dw, (int64_t)dims->E * F * K * (dw_dtype == MOE_F32 ? 4 : 2)};
     if (v.NT == 0) {  // no rows anywhere: every sum is empty
-        if (bad_block_pointers(dw, dw, dw, what, &rc)) return rc;
-        return cuda_result(cudaMemsetAsync(dw, 0, (size_t)dims->E * F * K * (dw_dtype == MOE_F32 ? 4 : 2),
-                                           (cudaStream_t)stream),
-                           what);
+        const Span in[] = {offsets_span(r)};
+        if (bad_block_pointers(dw, dw, dw, what, &rc) || overlap_any(out, in, what, &rc)) return rc;
+        return cuda_result(cudaMemsetAsync(dw, 0, (size_t)out.bytes, (cudaStream_t)stream), what);
     }
     if (bad_block_pointers(dy, x, dw, what, &rc)) return rc;
-    const Span in[] = {{dy, v.rows_total * F * 2}, {x, v.rows_total * K * 2}};
-    if (overlap_any({dw, (int64_t)dims->E * F * K * (dw_dtype == MOE_F32 ? 4 : 2)}, in, what, &rc)) return rc;
+    const Span in[] = {{dy, v.rows_total * F * 2}, {x, v.rows_total * K * 2}, offsets_span(r)};
+    if (overlap_any(out, in, what, &rc)) return rc;
     return cuda_result(launch_expert_wgrad(r, K, F, dy, x, dw, dw_dtype == MOE_F32, (cudaStream_t)stream), what);
 }
 
@@ -658,7 +660,7 @@ int moe_expert_swiglu_grad(const MoeDims *dims, int F, const void *pre, const vo
     if (rc != MOE_OK) return rc;
     if (v.NT == 0) return MOE_OK;
     if (bad_block_pointers(pre, dh, dpre, what, &rc)) return rc;
-    const Span in[] = {{pre, v.rows_total * F * 4}, {dh, v.rows_total * F * 2}};
+    const Span in[] = {{pre, v.rows_total * F * 4}, {dh, v.rows_total * F * 2}, offsets_span(r)};
     if (overlap_any({dpre, v.rows_total * F * 4}, in, what, &rc)) return rc;
     return cuda_result(launch_expert_swiglu_grad(r, dims->N, v.pairs, F, pre, dh, dpre, (cudaStream_t)stream), what);
 }
@@ -689,8 +691,9 @@ int moe_expert_gemm_fp8(const MoeDims *dims, int K, int F, int act, const void *
     const Span in[] = {{xq, v.rows_total * K},
                        {x_scales, v.rows_total * blocks * 4},
                        {wq, dims->E * wide * K},
-                       {w_scales, dims->E * ((wide + 127) / 128) * blocks * 4}};
-    const Span with_y[] = {in[0], in[1], in[2], in[3], out};
+                       {w_scales, dims->E * ((wide + 127) / 128) * blocks * 4},
+                       offsets_span(r)};
+    const Span with_y[] = {in[0], in[1], in[2], in[3], in[4], out};
     if (overlap_any(out, in, what, &rc) || overlap_any({y_scales, v.rows_total * (F / 128) * 4}, with_y, what, &rc))
         return rc;
     return cuda_result(launch_expert_gemm_fp8(r, K, F, gated, xq, x_scales, wq, w_scales, y, dims->y_dtype == MOE_F32,

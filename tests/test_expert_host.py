@@ -188,3 +188,19 @@ def test_warps_meet_at_bounded_waits_only(name):
     before the roles part and after they are all done."""
     text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, name)).read())
     assert not re.search(r"\bbar\.|\bbarrier\.(?!cluster)|__syncthreads_|cooperative_groups", text)
+
+
+@pytest.mark.parametrize("name", EVERY)
+def test_results_over_the_offsets_are_refused(lib, name):
+    """Blocks read expert_offsets when they start, others may be storing by then."""
+    a, b, s, t, out, extra, off = (ctypes.c_void_p(0x10000000 * i) for i in range(1, 8))
+    kw = dict(a=a, b=b, s=s, t=t, off=off)
+    for at in (off.value - 16, off.value, off.value + 16):  # 5 offsets: 20 bytes
+        assert _call(lib, name, out=ctypes.c_void_p(at), **kw) == INVALID, hex(at)
+        assert "overlaps" in lib.moe_last_error().decode()
+        if name in ("gemm", "fp8"):
+            assert _call(lib, name, act=SWIGLU, out=out, extra=ctypes.c_void_p(at), **kw) == INVALID, hex(at)
+            assert "overlaps" in lib.moe_last_error().decode()
+    if name == "wgrad":
+        assert _call(lib, name, d=_dims(T=0), a=None, b=None, out=off, off=off) == INVALID
+        assert "overlaps" in lib.moe_last_error().decode()
