@@ -127,6 +127,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     if (warp == kStoreWarps) {  // loads
         Ring<kStages> r;
         uint32_t end_phase = 0;  // a bit per slot: the end barriers' next phases
+        WaitLimit limit;
         bool ok = true;
         for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
             const int e = t / per;
@@ -134,9 +135,11 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             const int row = same(g.row[e]), count = same(g.count[e]), steps = (count + kP - 1) / kP;
             const int m0 = p.m0 + rank * kM, n0 = p.n0 + rank * (p.n / 2), m_cols = rank == 0 ? p.m_cols0 : p.m_cols1;
             const bool whole_m = m0 + kM <= a.F, whole_n = a.width == kN && p.n0 + kN <= a.K;
+            limit.tile(steps);
             for (int k = 0; k < steps; ++k) {
-                ok = mb_wait_warp(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                ok = mb_wait_warp(empty + 8 * r.slot, r.phase ^ 1u, gave_up, limit.polls());
                 if (!ok) break;
+                limit.waited();
                 const bool ends = k + 1 == steps && count % 16 != 0;  // rows to be zeroed
                 if (elect_one()) {
                     const uint32_t sa = smem + r.slot * kStage, sb = sa + kM / 64 * kCols;
@@ -165,7 +168,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             }
         }
         if (rank == 0) drain_ring(full, r);  // of both blocks
-        drain_ring(empty, r);  // in each block: its loads, and the leader's arrivals, the last of them `done`
+        drain_ring(empty, r, limit.polls());  // in each block: its loads, and the leader's arrivals, the last of them `done`
         mb_drain(done, 0);
         for (int i = 0; i < kStages; ++i) mb_drain(end_full + 8 * i, (end_phase >> i & 1u) ^ 1u);
     } else if (warp == kStoreWarps + 1) {  // the leader's mma
@@ -173,23 +176,26 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             Ring<kStages> r;
             Ring<2> acc;
             uint32_t end_phase = 0;
+            WaitLimit limit;
             bool ok = true;
             for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
                 const int e = t / per;
                 const Part p = get_part(a, mt, t % per);
                 const int count = same(g.count[e]), steps = (count + kP - 1) / kP;
+                limit.tile(steps);
                 if (steps == 0) continue;  // nothing to sum: the results are zeros
                 const uint32_t desc = mma_desc(1, true, true, 2 * kM, p.n);
                 const int part = kF32 ? kPart : steps;  // stages that are summed in TMEM
                 for (int k0 = 0; k0 < steps && ok; k0 += part) {
                     const uint32_t d = tmem + acc.slot * kN;
-                    ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
+                    ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up, limit.polls());
                     tc_fence_after();
+                    limit.waited();
                     for (int k = k0; k < min(k0 + part, steps) && ok; ++k) {
                         const int left = min(kP, count - k * kP), slices = (left + 15) / 16;
-                        ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up);
+                        ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up, limit.polls());
                         if (left % 16 != 0 && ok) {
-                            ok = mb_wait_warp(end_peer + 8 * r.slot, end_phase >> r.slot & 1u, gave_up);
+                            ok = mb_wait_warp(end_peer + 8 * r.slot, end_phase >> r.slot & 1u, gave_up, limit.polls());
                             end_phase ^= 1u << r.slot;
                         }
                         if (!ok) break;
@@ -216,13 +222,16 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     } else if (warp == kStoreWarps + 2) {  // zeroes behind the experts' last rows
         int slot = 0;
         uint32_t end_phase = 0;
+        WaitLimit limit;
         bool ok = true;
         for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
             const int count = same(g.count[t / per]), steps = (count + kP - 1) / kP, left = count % kP;
+            limit.tile(steps);
             if (count % 16 != 0) {
                 const int last = (slot + steps - 1) % kStages;
-                // waits for nothing before: through the whole tile
-                ok = mb_wait_warp(end_full + 8 * last, end_phase >> last & 1u, gave_up, kPolls + steps * kStepPolls);
+                // the first wait since the last such tile
+                ok = mb_wait_warp(end_full + 8 * last, end_phase >> last & 1u, gave_up, limit.polls());
+                limit.waited();
                 end_phase ^= 1u << last;
                 const int words = (((left + 15) & ~15) - left) * 8;  // 16-byte words of the lines behind the last row
                 for (int i = 0; i < (kM + kN / 2) / 64; ++i) {
@@ -242,18 +251,20 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
             const int quarter = warp & 3, half = warp >> 2;
             Ring<2> acc;
+            WaitLimit limit;
             bool ok = true;
             for (int t = blockIdx.x / 2; t < tiles && ok; t += gridDim.x / 2) {
                 const int e = t / per;
                 const Part p = get_part(a, mt, t % per);
                 const int steps = (same(g.count[e]) + kP - 1) / kP, n = min(a.width, a.K - p.n0);
+                limit.tile(min(steps, kPart));
                 float sum[4][32];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
                 for (int k0 = 0; k0 < steps; k0 += kPart) {
-                    ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + kPart * kStepPolls);
+                    ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, limit.polls());
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(quarter * 32) << 16) + 32 * half;
@@ -272,6 +283,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                     acc.next();
                 }
                 if (!ok) break;
+                limit.waited();
                 // 64 bytes of each row at a time, turned in shared memory so
                 // that four lanes write them (chunks of 16 bytes swapped by
                 // row against bank conflicts).  With 128 bytes at a time the
@@ -306,14 +318,17 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
         }
     } else {  // results: warp w holds rows 32w.. of the block's half, one per lane
         Ring<2> acc;
+        WaitLimit limit;
         for (int t = blockIdx.x / 2; t < tiles; t += gridDim.x / 2) {
             const int e = t / per;
             const Part p = get_part(a, mt, t % per);
-            const int count = same(g.count[e]);
-            const bool some = count > 0;
+            const int steps = (same(g.count[e]) + kP - 1) / kP;
+            const bool some = steps > 0;
+            limit.tile(steps);
             if (some) {
-                if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + (count / kP) * kStepPolls)) break;
+                if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, limit.polls())) break;
                 tc_fence_after();
+                limit.waited();
             }
             const uint32_t src = tmem + acc.slot * kN + ((uint32_t)(warp * 32) << 16);
             const int f0 = p.m0 + rank * kM + warp * 32, n = min(a.width, a.K - p.n0);

@@ -65,8 +65,23 @@ __device__ __forceinline__ bool elect_one() {
 // word `gave_up` is set; each role then leaves its loop, copies in flight are
 // waited for (again bounded), TMEM is freed and the kernel ends.  A poll takes
 // no less than about 10 ns: kPolls are at least 10 ms, where a stage takes well
-// under 10 us; a wait for a whole tile adds kStepPolls for each of its stages.
+// under 10 us; a wait that spans more adds kStepPolls for each stage.
 constexpr long long kPolls = 1 << 20, kStepPolls = 1 << 12;
+
+// The limit of a role's waits where they may span whole tiles, some of which
+// have no stages but results to be written (zeros, 256 KB a pair: 3 us at the
+// rate of HBM, less than the 40 us of kStepPolls).  Roles run ahead of
+// one another through such tiles without waiting, so all that came before count
+// for every later wait, of tiles with stages those since the last wait.
+struct WaitLimit {
+    long long stages = 0, empty_tiles = 0;
+    __host__ __device__ void tile(int steps) {  // each tile, as the role comes to it
+        if (steps > 0) stages += steps;
+        else ++empty_tiles;
+    }
+    __host__ __device__ void waited() { stages = 0; }
+    __host__ __device__ long long polls() const { return kPolls + (stages + empty_tiles) * kStepPolls; }
+};
 __device__ __forceinline__ bool mb_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, long long polls = kPolls) {
     for (long long i = 0; i < polls; ++i) {
         if (mb_try(bar, parity)) return true;
@@ -136,8 +151,7 @@ struct Ring {
 // each block knows about its own loads, and about the arrivals that the leader's
 // commits send it, by its own `empty` barriers.
 template <int kSlots>
-__device__ __forceinline__ void drain_ring(uint32_t bars, Ring<kSlots> r) {
-    long long left = kPolls;
+__device__ __forceinline__ void drain_ring(uint32_t bars, Ring<kSlots> r, long long left = kPolls) {
     for (int i = 0; i < kSlots; ++i) {
         while (!mb_try(bars + 8 * r.slot, r.phase ^ 1u) && left > 0) --left;
         r.next();

@@ -285,3 +285,26 @@ def test_fp8_gated_many_tiles():
     got_s = ys.double().unsqueeze(2)
     ref.check(ref.e4m3(y).unflatten(1, (-1, 128)) * got_s, h, eh + got_s * 2.0 ** -10 + 4 * F32_HALF * h.abs(), E4M3_HALF,
               "codes")
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("K,F", [(264, 520), (1024, 1024)], ids=_ids)
+@pytest.mark.parametrize("kind", ["whole", "empty", "mixed"])
+def test_wgrad_ragged_expert_behind_many_others(kind, K, F, f32):
+    """A ragged expert behind some hundred whole (multiples of 16) or empty ones: roles that pass those by wait long."""
+    E = 500
+    g = torch.Generator().manual_seed(3)
+    pick = torch.randint(0, 4, (E,), generator=g).tolist()
+    counts = [{"whole": 64, "empty": 0, "mixed": [0, 16, 0, 80][p]}[kind] for p in pick] + [7, 0, 33]
+    b = Batch(1, counts, sum(counts))
+    dy, x = b.row_values(F), b.row_values(K)
+    dw = torch.full((b.E, F, K), ref.SENTINEL, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    moe.expert_gemm_wgrad(b.dims(), K, F, dy, x, b.offsets, dw)
+    for e in list(range(0, E, 41)) + [E, E + 1, E + 2]:
+        r = b.span(e)
+        d, v = dy[r].double(), x[r].double()
+        ref.check(dw[e], d.t() @ v, ref.sum_error(r.stop - r.start, d.abs().t() @ v.abs()),
+                  F32_HALF if f32 else BF16_HALF, f"dw[{e}]")
+    empty = torch.tensor([c == 0 for c in counts], device="cuda")
+    assert int(dw[empty].count_nonzero()) == 0
+    assert moe.take_device_error() == moe.MOE_OK

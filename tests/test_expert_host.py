@@ -2,6 +2,7 @@
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -204,3 +205,47 @@ def test_results_over_the_offsets_are_refused(lib, name):
     if name == "wgrad":
         assert _call(lib, name, d=_dims(T=0), a=None, b=None, out=off, off=off) == INVALID
         assert "overlaps" in lib.moe_last_error().decode()
+
+
+LIMITS = r'''
+#include <stdio.h>
+#include <stdlib.h>
+#include "tc_ops.cuh"
+int main() {  // "w": a wait is over; a number: the steps of the next tile, and the limit then is printed
+    moe::WaitLimit limit;
+    char word[32];
+    printf("%lld %lld\n", moe::kPolls, moe::kStepPolls);
+    while (scanf("%31s", word) == 1) {
+        if (word[0] == 'w') { limit.waited(); continue; }
+        limit.tile(atoi(word));
+        printf("%lld\n", limit.polls());
+    }
+}
+'''
+
+
+def test_limits_of_waits_cover_the_tiles_since_the_last_one(tmp_path):
+    """What a role may have to wait for: the stages of all tiles since its last wait (the zeroing warp waits at ragged
+    tiles only), and the zeros of every empty tile so far (loads and mma pass them by, storing warps do not)."""
+    src = tmp_path / "limits.cu"
+    src.write_text(LIMITS)
+    subprocess.run([_build.nvcc(), *_build.ARCH, *_build.NVCC_FLAGS, "-o", str(tmp_path / "limits"), str(src)], check=True,
+                   capture_output=True)
+
+    def run(words):
+        out = subprocess.run([str(tmp_path / "limits")], input=" ".join(map(str, words)), capture_output=True, text=True,
+                             check=True).stdout.split()
+        base, step, *limits = map(int, out)
+        return [(v - base) / step for v in limits]  # in stages
+
+    assert run([4, 4, 1]) == [4, 8, 9]                        # whole tiles, then a ragged one
+    assert run([4, "w", 1, "w", 2]) == [4, 1, 2]              # nothing left over after a wait
+    assert run([0] * 1000 + [2, "w", 3])[-2:] == [1002, 1003]  # a thousand matrices of zeros first
+    assert run([1 << 24] * 300)[-1] == 300 << 24              # no overflow
+
+
+def test_every_wait_across_tiles_has_a_limit_of_its_tiles():
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, "expert_wgrad.cu")).read())
+    waits = re.findall(r"mb_wait_warp\(([^;]*)\)\s*(?:;|&&|\))", text)
+    assert len(waits) == 7
+    assert all("limit.polls()" in w for w in waits), waits
