@@ -195,7 +195,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                         const int left = min(kP, count - k * kP), slices = (left + 15) / 16;
                         ok = mb_wait_warp(full + 8 * r.slot, r.phase, gave_up, limit.polls());
                         if (left % 16 != 0 && ok) {
-                            ok = mb_wait_warp(end_peer + 8 * r.slot, end_phase >> r.slot & 1u, gave_up, limit.polls());
+                            ok = mb_wait_warp_pair(end_peer + 8 * r.slot, end_phase >> r.slot & 1u, gave_up, limit.polls());
                             end_phase ^= 1u << r.slot;
                         }
                         if (!ok) break;

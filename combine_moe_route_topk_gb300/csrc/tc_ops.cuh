@@ -40,6 +40,20 @@ __device__ __forceinline__ bool mb_try(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+// The same where the other block of a pair may have arrived after writing what
+// is read next: the wait acquires for the cluster, not for the block alone.
+__device__ __forceinline__ bool mb_try_pair(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // A value that every lane of a converged warp holds: the compiler then knows
 // that it is the same in all of them, keeps it in uniform registers and takes
 // branches on it without considering divergence.
@@ -94,6 +108,10 @@ __device__ __forceinline__ bool mb_wait_warp(uint32_t bar, uint32_t parity, vola
                                              long long polls = kPolls) {
     if (__all_sync(0xffffffffu, mb_try(bar, parity))) return true;
     return __all_sync(0xffffffffu, mb_wait(bar, parity, gave_up, polls));
+}
+__device__ __forceinline__ bool mb_wait_warp_pair(uint32_t bar, uint32_t parity, volatile int *gave_up, long long polls) {
+    const bool ok = mb_wait_warp(bar, parity, gave_up, polls);
+    return ok && __all_sync(0xffffffffu, mb_try_pair(bar, parity));  // complete: acquires, does not wait
 }
 __device__ __forceinline__ void mb_drain(uint32_t bar, uint32_t parity) {  // bounded, result not needed
     for (long long i = 0; i < kPolls && !mb_try(bar, parity); ++i) {

@@ -246,6 +246,16 @@ def test_limits_of_waits_cover_the_tiles_since_the_last_one(tmp_path):
 
 def test_every_wait_across_tiles_has_a_limit_of_its_tiles():
     text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, "expert_wgrad.cu")).read())
-    waits = re.findall(r"mb_wait_warp\(([^;]*)\)\s*(?:;|&&|\))", text)
+    waits = re.findall(r"mb_wait_warp(?:_pair)?\(([^;]*)\)\s*(?:;|&&|\))", text)
     assert len(waits) == 7
     assert all("limit.polls()" in w for w in waits), waits
+
+
+def test_waits_for_the_other_blocks_writes_acquire_for_the_cluster():
+    """Zeros that block 1 wrote in its shared memory are read by the leader's mma: released for the cluster, they
+    have to be acquired for it too (a wait's default is the block)."""
+    wgrad, ops = (re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, n)).read()) for n in ("expert_wgrad.cu", "tc_ops.cuh"))
+    waits = re.findall(r"(\w+)\(end_peer \+", wgrad)
+    waits.remove("at_leader")  # the arrival
+    assert [w for w in waits if w != "mb_init"] == ["mb_wait_warp_pair"]
+    assert "mbarrier.arrive.release.cluster" in ops and "mbarrier.try_wait.parity.acquire.cluster" in ops
