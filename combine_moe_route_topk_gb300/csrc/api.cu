@@ -214,7 +214,8 @@ int check_expert(const MoeDims *dims, int K, int F, bool gated, int elem, const 
     if (!offsets || !aligned(offsets, 4))
         return set_error(MOE_ERR_INVALID_ARG, "%s: expert_offsets must be a 4-byte aligned pointer", what);
     // a token takes an expert once, and what does not fit the region is dropped
-    *r = ExpertRows{offsets, dims->E, dims->E / dims->N, v->cap, v->rows_total, v->NT < v->cap ? v->NT : v->cap};
+    *r = ExpertRows{offsets, dims->E, dims->E / dims->N, v->cap, v->rows_total, v->NT < v->cap ? v->NT : v->cap,
+                    v->pairs};
     return MOE_OK;
 }
 

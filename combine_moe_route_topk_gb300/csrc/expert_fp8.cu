@@ -53,7 +53,7 @@ struct Args {
     const float *x_scales, *w_scales;
     void *y;
     float *y_scales;
-    int64_t cap, most;
+    int64_t cap, most, pairs;
     int E, L, K, F, w_rows;  // reduction length, result columns, matrix rows of an expert
 };
 
@@ -140,7 +140,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     // Result columns of a tile: 256, or 128 where all tiles then still run at
     // once (8 experts of 128 rows, K = 7168, F = 2048: 27.3 us against 30.0).
     const Groups g = make_groups<kGated ? 7 : 8, 7, 1>(
-        tables, a.offsets, a.E, a.L, a.cap, a.most, gridDim.x,
+        tables, a.offsets, a.E, a.L, a.cap, a.most, a.pairs, gridDim.x,
         [&](int c, int shift) { return token_tiles(c) * ((a.F + (1 << shift) - 1) >> shift); },
         [](int) { return 0; });  // syncs the block
     const int width = 1 << g.shift;
@@ -437,7 +437,7 @@ cudaError_t launch_expert_gemm_fp8(const ExpertRows &r, int K, int F, int gated,
     const uint32_t wbox[3] = {kK, kBlk, 1};
     if (!encode_map(&map_w, 1, 3, wq, wdims, strides, wbox)) return cudaErrorInvalidValue;
     if (!encode_rows(&map_x, 1, xq, K, r.rows_total, r.most < kTok ? r.most : kTok)) return cudaErrorInvalidValue;
-    const Args a{r.offsets, x_scales, w_scales, y, y_scales, r.cap, r.most, r.E, r.L, K, F, w_rows};
+    const Args a{r.offsets, x_scales, w_scales, y, y_scales, r.cap, r.most, r.pairs, r.E, r.L, K, F, w_rows};
     if (gated) return launch<true, false>(map_w, map_x, a, stream);
     return y_f32 ? launch<false, true>(map_w, map_x, a, stream) : launch<false, false>(map_w, map_x, a, stream);
 }

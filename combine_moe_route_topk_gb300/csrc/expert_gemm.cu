@@ -57,7 +57,7 @@ struct Args {
     const int32_t *offsets;
     void *y;
     __nv_bfloat16 *pre;
-    int64_t cap, most;
+    int64_t cap, most, pairs;
     int E, L, K, F;  // reduction length, result columns
 };
 
@@ -154,7 +154,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     constexpr int kStep = 2 * kHalf;
     const int m_tiles = (a.F + kStep - 1) / kStep;
     const Groups g = make_groups<kTokShift, kLeastShift, kTok / 32 + 1>(
-        tables, a.offsets, a.E, a.L, a.cap, a.most, gridDim.x / 2,
+        tables, a.offsets, a.E, a.L, a.cap, a.most, a.pairs, gridDim.x / 2,
         [&](int c, int shift) { return token_tiles(c, shift) * m_tiles; },
         [](int c) { return c == 0 ? kTok / 32 : (kTok - tile_tokens(c, kTokShift)) / 32; });  // syncs the block
     const int tiles = same(g.prefix[a.E]), steps = (a.K + kK - 1) / kK;
@@ -421,7 +421,7 @@ cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, con
         if (!encode_map(&map_w, 0, 3, w, dims, strides, box)) return cudaErrorInvalidValue;
     }
     if (!encode_rows(&map_x, 0, x, K, r.rows_total, half_tile(r))) return cudaErrorInvalidValue;
-    const Args a{r.offsets, y, static_cast<__nv_bfloat16 *>(pre), r.cap, r.most, r.E, r.L, K, F};
+    const Args a{r.offsets, y, static_cast<__nv_bfloat16 *>(pre), r.cap, r.most, r.pairs, r.E, r.L, K, F};
     if (gated) return pre ? launch<kGated, false, true>(map_w, map_x, a, stream)
                           : launch<kGated, false, false>(map_w, map_x, a, stream);
     return y_f32 ? launch<kLinear, true, false>(map_w, map_x, a, stream)
@@ -437,7 +437,7 @@ cudaError_t launch_expert_dgrad(const ExpertRows &r, int K, int F, const void *d
     const uint32_t wbox[3] = {64, kK, 1};
     if (!encode_map(&map_w, 0, 3, w, wdims, strides, wbox)) return cudaErrorInvalidValue;
     if (!encode_rows(&map_x, 0, dy, F, r.rows_total, half_tile(r))) return cudaErrorInvalidValue;
-    const Args a{r.offsets, dx, nullptr, r.cap, r.most, r.E, r.L, F, K};
+    const Args a{r.offsets, dx, nullptr, r.cap, r.most, r.pairs, r.E, r.L, F, K};
     return launch<kDgrad, false, false>(map_w, map_x, a, stream);
 }
 

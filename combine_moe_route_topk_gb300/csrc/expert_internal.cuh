@@ -11,7 +11,7 @@ struct ExpertRows {
     const int32_t *offsets;  // device, [E + 1]
     int E, L;                // experts, experts per rank
     int64_t cap, rows_total;  // rows of a region, of all of them
-    int64_t most;             // rows that one expert can have
+    int64_t most, pairs;      // rows that one expert can have, that all of them can
 };
 
 cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, const void *x, const void *w, void *y,

@@ -53,7 +53,7 @@ struct ColumnMaps {
 struct Args {
     const int32_t *offsets;
     void *dw;
-    int64_t cap, most;
+    int64_t cap, most, pairs;
     int E, L, K, F;
     int width;  // columns of x of a tile
 };
@@ -117,7 +117,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
     const int mt = (a.F + 2 * kM - 1) / (2 * kM), per = mt * ((a.K + a.width - 1) / a.width);  // tiles of an expert
-    const Groups g = make_groups<0, 0, 1>(tables, a.offsets, a.E, a.L, a.cap, a.most, 0,
+    const Groups g = make_groups<0, 0, 1>(tables, a.offsets, a.E, a.L, a.cap, a.most, a.pairs, 0,
                                        [&](int, int) { return per; }, [](int) { return 0; });  // syncs the block
     const int tiles = a.E * per;
 
@@ -418,7 +418,7 @@ cudaError_t launch_expert_wgrad(const ExpertRows &r, int K, int F, const void *d
     ColumnMaps map_dy, map_x;
     if (!encode_columns(&map_dy, dy, F, r.rows_total, kM) || !encode_columns(&map_x, x, K, r.rows_total, kN / 2))
         return cudaErrorInvalidValue;
-    const Args a{r.offsets, dw, r.cap, r.most, r.E, r.L, K, F, kN};
+    const Args a{r.offsets, dw, r.cap, r.most, r.pairs, r.E, r.L, K, F, kN};
     return dw_f32 ? launch<true>(map_dy, map_x, a, stream) : launch<false>(map_dy, map_x, a, stream);
 }
 

@@ -418,25 +418,28 @@ __device__ __forceinline__ int scan(int v, int lane) {  // sum over the lanes up
 // leave some idle are made shorter.  Where they take more than kRounds rounds
 // (fewer gain less than the sorting takes), and kRanks > 1, the groups are
 // taken in the order of rank(count), 0 to kRanks - 1 (for groups without
-// rows), so that the tiles of a round are alike.  Offsets that are no output of
-// the count step (not ascending, or more rows than `most` for an expert) give
-// groups that stay inside the regions and within `most` all the same.
+// rows), so that the tiles of a round are alike.  Groups stay inside the regions
+// and within `most` rows whatever the offsets are; offsets that no batch of
+// `pairs` rows has (they descend, or span more) stand for no rows at all: the
+// number of tiles, checked by the host for `pairs` rows, could pass 32 bits.
 constexpr int kRounds = 4;
 template <int kMost, int kLeast, int kRanks, class Tiles, class Rank>
 __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restrict__ offsets, int E, int L, int64_t cap,
-                                              int64_t most, int units, Tiles tiles, Rank rank) {
+                                              int64_t most, int64_t pairs, int units, Tiles tiles, Rank rank) {
     constexpr bool kSort = kRanks > 1;
     __shared__ int s_shift, s_sorted;
     Groups g{mem, mem + E, mem + 2 * E, mem + 3 * E + 1, kMost, 0};
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         const int d = e / L;
-        const int64_t base = __ldg(offsets + d * L);
+        // four loads at once: one behind the others costs 0.3 us a call
+        const int64_t first = __ldg(offsets), base = __ldg(offsets + d * L);
         int64_t lo = (int64_t)__ldg(offsets + e) - base, hi = (int64_t)__ldg(offsets + e + 1) - base;
+        const bool descends = (hi < lo) | (base + hi - first > pairs);
         lo = lo < 0 ? 0 : (lo < cap ? lo : cap);
         hi = hi < lo ? lo : (hi < cap ? hi : cap);
         if (hi - lo > most) hi = lo + most;
         g.row[e] = (int)(d * cap + lo);
-        g.count[e] = (int)(hi - lo);
+        g.count[e] = descends ? -1 : (int)(hi - lo);
         if constexpr (kSort) g.order[e] = e;
     }
     __syncthreads();
@@ -444,13 +447,21 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
         constexpr int kTries = kMost - kLeast + 1;
         const int lane = threadIdx.x, per = (E + 31) / 32, e0 = lane * per, e1 = min(E, e0 + per);
         int sums[kTries] = {}, shift = kMost, sorted = 0;
+        int signs = 0;
         for (int e = e0; e < e1; ++e) {
             const int c = g.count[e];
+            signs |= c;
 #pragma unroll
             for (int i = 0; i < kTries; ++i) {
                 sums[i] += tiles(c, kMost - i);
                 if (i > 0) sums[i] = min(sums[i], 1 << 25);  // too many anyway; 32 lanes' do not overflow
             }
+        }
+        if (__any_sync(0xffffffffu, signs < 0)) {  // no rows
+            for (int e = e0; e < e1; ++e) g.count[e] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kTries; ++i) sums[i] = max(0, e1 - e0) * tiles(0, kMost - i);
         }
         int sum = sums[0];
         if constexpr (kTries > 1) {

@@ -24,6 +24,8 @@
  *     far as they lie in the rank's region (rows over capacity were
  *     dropped).  Only these rows of the outputs are written; what other
  *     rows of the inputs hold (NaN, say) has no influence.
+ *     Other contents lead to no access outside the arrays; for the products,
+ *     offsets that descend or span more than N*T*R rows stand for no rows.
  *   - Outputs must not overlap inputs or each other (MOE_ERR_INVALID_ARG).
  *   - Array bases that a call reads by blocks must be 16-byte aligned (all
  *     but expert_offsets and the scales, which need 4).

@@ -434,3 +434,21 @@ def test_pairs_without_tiles_and_the_kernels_behind_them():
             call()
     for (_, outs), bits in zip(calls, want):
         assert _same(_bits(outs), bits)
+
+
+@pytest.mark.parametrize("offsets", [[0, 8, 0, 8, 0, 8, 8], [0, 8, 16, 15, 20, 24, 24], [0, 1, 2, 3, 4, 5, 200], [3, 2, 2, 2, 2, 2, 2]])
+def test_offsets_of_no_batch_stand_for_no_rows(offsets):
+    """Offsets that descend, or span more rows than the batch routes, are no output of the count step; read as they
+    are, every expert could seem to have all rows, and the number of tiles pass 32 bits."""
+    b = Batch(2, [8, 8, 8, 0, 0, 0], 24)
+    for i, (call, outs) in enumerate(_calls(b)):
+        if i == 4:  # the activation's gradient takes ranks' regions whole
+            continue
+        b.offsets.copy_(torch.tensor(offsets, dtype=torch.int32))
+        _clear(outs)
+        call()
+        for t in outs:
+            if i == 3:
+                assert int(t.count_nonzero()) == 0  # dw: no rows, zeros
+            else:
+                assert bool((t.view(torch.uint8) == 0x5A).all())
