@@ -16,10 +16,13 @@
 // tokens, which halves what the tokens cost in L2 and shared memory.
 //
 // The tensor core cuts what it adds off below the accumulator's last place, so
-// a long sum comes out small: by 2.4e-7 of its value after 512 elements,
-// 3.5e-6 after 6144.  bf16 results (steps of 7.8e-3) do not show it.  For f32
-// results the sum is taken in parts of 512, which the storing warps add up in
-// registers, rounding to nearest.
+// a long sum comes out small, the more the longer it is.  For f32 results the sum
+// is taken in parts of 512, which the storing warps add up in registers,
+// rounding to nearest: 3e-7 off for any length where one accumulator was 3.5e-6
+// off after 6144 elements.  bf16 results, which are off by up to 3.9e-3 from
+// their rounding alone, are summed in one go up to kWhole elements and in parts
+// of 2048 beyond (K = 28672, 4096 rows: 1145 us either way; 512 cost the gated
+// form 4 %).
 #include <cuda_bf16.h>
 
 #include "expert_internal.cuh"
@@ -39,14 +42,16 @@ constexpr int kBytesA = kM * kK * 2;
 constexpr int kBytesB = kTok / 2 * kK * 2;
 constexpr int kStage = kBytesA + kBytesB;
 constexpr int kStoreWarps = 8;
-constexpr int kPart = 512 / kK;  // stages of a part of an f32 sum
+// Stages of a part of a sum: 512 elements for f32 results, 2048 for bf16.
+constexpr int part_stages(bool f32) { return (f32 ? 512 : 2048) / kK; }
 
 // Warps: those that store results, one that loads, one that issues mma; for
-// f32 results two more that only give their registers away (384 threads are
+// sums in parts two more that only give their registers away (384 threads are
 // launched with 168 each, the storing ones take 216, the others keep 72).
-template <bool kF32>
+template <bool kParts, bool kF32>
 struct Shape {
-    static constexpr int kThreads = 32 * (kStoreWarps + (kF32 ? 4 : 2)), kStages = kF32 ? 5 : 6;
+    static_assert(kParts || !kF32, "f32 results are summed in parts");
+    static constexpr int kThreads = 32 * (kStoreWarps + (kParts ? 4 : 2)), kStages = kF32 ? 5 : 6;
     static constexpr int kBuf = kF32 ? 4096 : 2048;  // each storing warp's: 32 tokens' results, to be written as whole sectors
     static constexpr int kSmem = 1024 + kStages * kStage + kStoreWarps * kBuf;
 };
@@ -111,10 +116,10 @@ __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int i, int t, i
     return r;
 }
 
-template <int kForm, bool kF32, bool kSave>
-__global__ void __launch_bounds__(Shape<kF32>::kThreads, 1)
+template <int kForm, bool kParts, bool kF32, bool kSave>
+__global__ void __launch_bounds__(Shape<kParts, kF32>::kThreads, 1)
 expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_x, const Args a) {
-    constexpr int kStages = Shape<kF32>::kStages, kBuf = Shape<kF32>::kBuf;
+    constexpr int kStages = Shape<kParts, kF32>::kStages, kBuf = Shape<kParts, kF32>::kBuf;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[2 * kStages + 5];
     __shared__ uint32_t s_tmem;
@@ -158,8 +163,8 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         [&](int c, int shift) { return token_tiles(c, shift) * m_tiles; },
         [](int c) { return c == 0 ? kTok / 32 : (kTok - tile_tokens(c, kTokShift)) / 32; });  // syncs the block
     const int tiles = same(g.prefix[a.E]), steps = (a.K + kK - 1) / kK;
-    const int part = kF32 ? kPart : steps;  // stages that are summed in TMEM
-    if constexpr (kF32) {
+    const int part = kParts ? part_stages(kF32) : steps;  // stages that are summed in TMEM
+    if constexpr (kParts) {
         if (warp >= kStoreWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
 
@@ -237,25 +242,101 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             if (elect_one()) tc_commit_pair(done);
             __syncwarp();
         }
-    } else if constexpr (kF32) {
-        if (warp < kStoreWarps) {
-            // results: warp w holds matrix rows 32 (w % 4).. of the block's
-            // half, one per lane, and every other 32 tokens, 2 i + w / 4
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-            const int quarter = warp & 3, half = warp >> 2;
-            Ring<2> acc;
-            int i = 0;
-            bool ok = true;
-            for (Turns t(g); t < tiles && ok; t.next()) {
-                const Tile w = get_tile(g, a.E, i, t, kStep);
-                i = w.i;
+    } else if (warp < kStoreWarps) {
+        // results: warp w holds matrix rows 32 (w % 4).. of the block's half,
+        // one per lane, and every other 32 tokens, 2 i + w / 4.  (Four warps,
+        // each with all tokens, took 8.7 us for 222 rows of K = 1000, F = 776
+        // with pre kept, eight take 8.4.)
+        if constexpr (kParts) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int quarter = warp & 3, half = warp >> 2;
+        // The lane's sums of tokens c0.. of a tile, v(0) to v(31) as bits, are
+        // finished, turned in shared memory and stored.
+        auto store = [&](const Tile &w, int c0, auto v) {
+            const int left = w.n - c0;
+            if constexpr (kF32) {  // one token's 32 features are 128 bytes
+#pragma unroll
+                for (int j = 0; j < 32; ++j) st_shared32(buf + j * 128 + lane * 4, v(j));
+                __syncwarp();
+                const int f = w.m0 + rank * kHalf + quarter * 32 + lane % 8 * 4;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int tok = q * 4 + lane / 8;
+                    const uint4 r = ld_shared128(buf + q * 512 + lane * 16);
+                    if (tok < left && f < a.F)
+                        *reinterpret_cast<uint4 *>(static_cast<float *>(a.y) + (int64_t)(w.row + c0 + tok) * a.F + f) = r;
+                }
+            } else if constexpr (kForm == kGated) {
+                // lanes with bit 3 clear hold gate rows, the others the
+                // up rows of the same features; of a pair of tokens each
+                // half of the lanes finishes one
+                const int fl = (lane >> 4) * 8 + (lane & 7), up = (lane >> 3) & 1;
+                const int f0 = w.m0 + rank * kHalf + quarter * 16;
+                if constexpr (kSave) {
+                    const uint32_t to = buf + up * 32 + fl * 2;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const uint32_t two = bf16x2(v(j), v(j + 1));
+                        st_shared16(to + j * 64, two);
+                        st_shared16(to + j * 64 + 64, two >> 16);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = i * 8 + lane / 4, which = (lane >> 1) & 1, f = f0 + (lane & 1) * 8;
+                        const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
+                        if (tok < left && f < a.F)
+                            *reinterpret_cast<uint4 *>(a.pre + ((int64_t)(w.row + c0 + tok) * 2 + which) * a.F + f) = q;
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v(j) : v(j + 1), 8);
+                    const float gate = __uint_as_float(up ? got : v(j)), lin = __uint_as_float(up ? v(j + 1) : got);
+                    const float h = silu_mul(gate, lin);
+                    st_shared16(buf + (j + up) * 32 + fl * 2, bf16x2(__float_as_uint(h), 0u));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = i * 16 + lane / 2, f = f0 + (lane & 1) * 8;
+                    const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
+                    if (tok < left && f < a.F)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + (int64_t)(w.row + c0 + tok) * a.F + f) = q;
+                }
+            } else {  // one token's 32 features are 64 bytes
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const uint32_t two = bf16x2(v(j), v(j + 1));
+                    st_shared16(buf + j * 64 + lane * 2, two);
+                    st_shared16(buf + (j + 1) * 64 + lane * 2, two >> 16);
+                }
+                __syncwarp();
+                const int f = w.m0 + rank * kHalf + quarter * 32 + lane % 4 * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = i * 8 + lane / 4;
+                    const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
+                    if (tok < left && f < a.F)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + (int64_t)(w.row + c0 + tok) * a.F + f) = q;
+                }
+            }
+            __syncwarp();
+        };
+        Ring<2> acc;
+        int i = 0;
+        bool ok = true;
+        for (Turns t(g); t < tiles && ok; t.next()) {
+            const Tile w = get_tile(g, a.E, i, t, kStep);
+            i = w.i;
+            if constexpr (kParts) {
                 float sum[4][32];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
                 for (int k0 = 0; k0 < steps; k0 += part) {
-                    ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + kPart * kStepPolls);
+                    ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + part * kStepPolls);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(quarter * 32) << 16) + 32 * half;
@@ -276,106 +357,24 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int c0 = 64 * i + 32 * half, left = w.n - c0;
-                    if (left > 0) {  // one token's 32 features are 128 bytes
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) st_shared32(buf + j * 128 + lane * 4, __float_as_uint(sum[i][j]));
-                        __syncwarp();
-                        const int f = w.m0 + rank * kHalf + quarter * 32 + lane % 8 * 4;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const int tok = q * 4 + lane / 8;
-                            const uint4 v = ld_shared128(buf + q * 512 + lane * 16);
-                            if (tok < left && f < a.F)
-                                *reinterpret_cast<uint4 *>(static_cast<float *>(a.y) + (int64_t)(w.row + c0 + tok) * a.F + f) = v;
-                        }
-                        __syncwarp();
-                    }
+                    if (64 * i + 32 * half < w.n)
+                        store(w, 64 * i + 32 * half, [&](int j) { return __float_as_uint(sum[i][j]); });
                 }
-            }
-        }
-    } else {
-        // results: rows as above, straight from TMEM, 32 tokens at a time of
-        // every other 32.  (Four warps, each with all tokens, took 8.7 us for
-        // 222 rows of K = 1000, F = 776 with pre kept, eight take 8.4.)
-        const int quarter = warp & 3, half = warp >> 2;
-        Ring<2> acc;
-        int i = 0;
-        for (Turns t(g); t < tiles; t.next()) {
-            const Tile w = get_tile(g, a.E, i, t, kStep);
-            i = w.i;
-            if (!mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + steps * kStepPolls)) break;
-            tc_fence_after();
-            const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(quarter * 32) << 16);
-            for (int c0 = 32 * half; c0 < w.n; c0 += 64) {
-                uint32_t v[32];
-                tmem_load32(src + c0, v);
-                const int left = w.n - c0;
-                if constexpr (kForm == kGated) {
-                    // lanes with bit 3 clear hold gate rows, the others the
-                    // up rows of the same features; of a pair of tokens each
-                    // half of the lanes finishes one
-                    const int fl = (lane >> 4) * 8 + (lane & 7), up = (lane >> 3) & 1;
-                    const int f0 = w.m0 + rank * kHalf + quarter * 16;
-                    if constexpr (kSave) {
-                        const uint32_t to = buf + up * 32 + fl * 2;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const uint32_t two = bf16x2(v[j], v[j + 1]);
-                            st_shared16(to + j * 64, two);
-                            st_shared16(to + j * 64 + 64, two >> 16);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int tok = i * 8 + lane / 4, which = (lane >> 1) & 1, f = f0 + (lane & 1) * 8;
-                            const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
-                            if (tok < left && f < a.F)
-                                *reinterpret_cast<uint4 *>(a.pre + ((int64_t)(w.row + c0 + tok) * 2 + which) * a.F + f) = q;
-                        }
-                        __syncwarp();
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 8);
-                        const float gate = __uint_as_float(up ? got : v[j]), lin = __uint_as_float(up ? v[j + 1] : got);
-                        const float h = silu_mul(gate, lin);
-                        st_shared16(buf + (j + up) * 32 + fl * 2, bf16x2(__float_as_uint(h), 0u));
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int tok = i * 16 + lane / 2, f = f0 + (lane & 1) * 8;
-                        const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
-                        if (tok < left && f < a.F)
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) +
-                                                       (int64_t)(w.row + c0 + tok) * a.F + f) = q;
-                    }
-                } else {
-                    // one token's 32 features are 64 bytes
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const uint32_t two = bf16x2(v[j], v[j + 1]);
-                        st_shared16(buf + j * 64 + lane * 2, two);
-                        st_shared16(buf + (j + 1) * 64 + lane * 2, two >> 16);
-                    }
-                    __syncwarp();
-                    const int f = w.m0 + rank * kHalf + quarter * 32 + lane % 4 * 8;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tok = i * 8 + lane / 4;
-                        const uint4 q = ld_shared128(buf + i * 512 + lane * 16);
-                        if (tok < left && f < a.F)
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) +
-                                                       (int64_t)(w.row + c0 + tok) * a.F + f) = q;
-                    }
+            } else {  // straight from TMEM
+                ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + steps * kStepPolls);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t src = tmem + acc.slot * kTok + ((uint32_t)(quarter * 32) << 16);
+                for (int c0 = 32 * half; c0 < w.n; c0 += 64) {
+                    uint32_t v[32];
+                    tmem_load32(src + c0, v);
+                    store(w, c0, [&](int j) { return v[j]; });
                 }
+                tc_fence_before();
                 __syncwarp();
+                if (lane == 0) mb_arrive_remote_relaxed(at_leader(tempty + 8 * acc.slot));
+                acc.next();
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mb_arrive_remote_relaxed(at_leader(tempty + 8 * acc.slot));
-            acc.next();
         }
     }
     __syncwarp();
@@ -386,11 +385,11 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     if (warp == kStoreWarps) tmem_free_pair(tmem, 512);
 }
 
-template <int kForm, bool kF32, bool kSave>
+template <int kForm, bool kParts, bool kF32 = false, bool kSave = false>
 cudaError_t launch(const CUtensorMap &map_w, const RowMaps &map_x, const Args &a, cudaStream_t stream) {
-    auto kern = expert_gemm_kernel<kForm, kF32, kSave>;
+    auto kern = expert_gemm_kernel<kForm, kParts, kF32, kSave>;
     static thread_local PairCache cache;
-    using S = Shape<kF32>;
+    using S = Shape<kParts, kF32>;
     PairLaunch l(S::kThreads, S::kSmem + groups_bytes(1024, true), stream);
     cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), l.cfg);
     if (e != cudaSuccess) return e;
@@ -422,10 +421,12 @@ cudaError_t launch_expert_gemm(const ExpertRows &r, int K, int F, int gated, con
     }
     if (!encode_rows(&map_x, 0, x, K, r.rows_total, half_tile(r))) return cudaErrorInvalidValue;
     const Args a{r.offsets, y, static_cast<__nv_bfloat16 *>(pre), r.cap, r.most, r.pairs, r.E, r.L, K, F};
-    if (gated) return pre ? launch<kGated, false, true>(map_w, map_x, a, stream)
-                          : launch<kGated, false, false>(map_w, map_x, a, stream);
-    return y_f32 ? launch<kLinear, true, false>(map_w, map_x, a, stream)
-                 : launch<kLinear, false, false>(map_w, map_x, a, stream);
+    const bool parts = K > kWhole;
+    if (gated && pre) return parts ? launch<kGated, true, false, true>(map_w, map_x, a, stream)
+                                   : launch<kGated, false, false, true>(map_w, map_x, a, stream);
+    if (gated) return parts ? launch<kGated, true>(map_w, map_x, a, stream) : launch<kGated, false>(map_w, map_x, a, stream);
+    if (y_f32) return launch<kLinear, true, true>(map_w, map_x, a, stream);
+    return parts ? launch<kLinear, true>(map_w, map_x, a, stream) : launch<kLinear, false>(map_w, map_x, a, stream);
 }
 
 cudaError_t launch_expert_dgrad(const ExpertRows &r, int K, int F, const void *dy, const void *w, void *dx,
@@ -438,7 +439,7 @@ cudaError_t launch_expert_dgrad(const ExpertRows &r, int K, int F, const void *d
     if (!encode_map(&map_w, 0, 3, w, wdims, strides, wbox)) return cudaErrorInvalidValue;
     if (!encode_rows(&map_x, 0, dy, F, r.rows_total, half_tile(r))) return cudaErrorInvalidValue;
     const Args a{r.offsets, dx, nullptr, r.cap, r.most, r.pairs, r.E, r.L, F, K};
-    return launch<kDgrad, false, false>(map_w, map_x, a, stream);
+    return F > kWhole ? launch<kDgrad, true>(map_w, map_x, a, stream) : launch<kDgrad, false>(map_w, map_x, a, stream);
 }
 
 cudaError_t take_expert_gemm_error(int *err) { return take_tc_error(err); }

@@ -14,8 +14,13 @@
 //
 // f32 results are summed in parts of 512 rows, added up in registers: the
 // tensor core's sums come out small, by 8e-7 of their value after 1024 rows,
-// 1.6e-5 after 16384 (expert_gemm.cu says why).
+// 1.6e-5 after 16384 (expert_gemm.cu says why).  So are bf16 ones, in parts of
+// 2048, where an expert can have more than kWhole rows (at most 1.5 % slower; with
+// parts of 512 one expert of 65536 rows, K = F = 1024, took 248 us instead of 236,
+// now 239).
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "expert_internal.cuh"
 #include "pdl.cuh"
@@ -30,16 +35,17 @@ constexpr int kP = 64;   // rows of a stage
 constexpr int kCols = kP * 128;  // bytes of 64 columns of a stage
 constexpr int kStage = (kM + kN / 2) / 64 * kCols;
 constexpr int kStages = 6;
-constexpr int kPart = 512 / kP;  // stages of a part of an f32 sum
+// Stages of a part of a sum: 512 rows for f32 results, 2048 for bf16.
+constexpr int part_stages(bool f32) { return (f32 ? 512 : 2048) / kP; }
 
 // Warps: those that store results, one that loads, one that issues mma, one
-// that zeroes; for f32 results one more that only gives its registers away
+// that zeroes; for sums in parts one more that only gives its registers away
 // (384 threads are launched with 168 each, the storing ones take 216, the
 // others keep 72).
-template <bool kF32>
+template <bool kParts>
 struct Shape {
-    static constexpr int kStoreWarps = kF32 ? 8 : 4, kThreads = kF32 ? 384 : 224;
-    static constexpr int kBuf = kF32 ? 2048 : 4096;  // each storing warp's: 64 (bf16: 128) bytes of its 32 rows
+    static constexpr int kStoreWarps = kParts ? 8 : 4, kThreads = kParts ? 384 : 224;
+    static constexpr int kBuf = kParts ? 2048 : 4096;  // each storing warp's: 64 (or 128) bytes of its 32 rows
     static constexpr int kSmem = 1024 + kStages * kStage + kStoreWarps * kBuf;
 };
 
@@ -75,10 +81,11 @@ __device__ __forceinline__ Part get_part(const Args &a, int mt, int at) {
     return p;
 }
 
-template <bool kF32>
-__global__ void __launch_bounds__(Shape<kF32>::kThreads, 1)
+template <bool kParts, bool kF32>
+__global__ void __launch_bounds__(Shape<kParts>::kThreads, 1)
 expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_constant__ ColumnMaps map_x, const Args a) {
-    constexpr int kStoreWarps = Shape<kF32>::kStoreWarps, kBuf = Shape<kF32>::kBuf;
+    static_assert(kParts || !kF32, "f32 results are summed in parts");
+    constexpr int kStoreWarps = Shape<kParts>::kStoreWarps, kBuf = Shape<kParts>::kBuf;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[4 * kStages + 5];
     __shared__ uint32_t s_tmem;
@@ -121,7 +128,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                                        [&](int, int) { return per; }, [](int) { return 0; });  // syncs the block
     const int tiles = a.E * per;
 
-    if constexpr (kF32) {
+    if constexpr (kParts) {
         if (warp >= kStoreWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
     if (warp == kStoreWarps) {  // loads
@@ -185,7 +192,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                 limit.tile(steps);
                 if (steps == 0) continue;  // nothing to sum: the results are zeros
                 const uint32_t desc = mma_desc(1, true, true, 2 * kM, p.n);
-                const int part = kF32 ? kPart : steps;  // stages that are summed in TMEM
+                const int part = kParts ? part_stages(kF32) : steps;  // stages that are summed in TMEM
                 for (int k0 = 0; k0 < steps && ok; k0 += part) {
                     const uint32_t d = tmem + acc.slot * kN;
                     ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up, limit.polls());
@@ -244,7 +251,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             }
             slot = (slot + steps) % kStages;
         }
-    } else if constexpr (kF32) {
+    } else if constexpr (kParts) {
         if (warp < kStoreWarps) {
             // results: warp w holds rows 32 (w % 4).. of the block's half, one
             // per lane, and every other 32 columns, 2 i + w / 4
@@ -257,6 +264,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                 const int e = t / per;
                 const Part p = get_part(a, mt, t % per);
                 const int steps = (same(g.count[e]) + kP - 1) / kP, n = min(a.width, a.K - p.n0);
+                constexpr int kPart = part_stages(kF32);
                 limit.tile(min(steps, kPart));
                 float sum[4][32];
 #pragma unroll
@@ -289,21 +297,31 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
                 // row against bank conflicts).  With 128 bytes at a time the
                 // buffers take a stage's place: 324 us instead of 312 for 1 GB
                 // of results.
+                using Elem = std::conditional_t<kF32, float, __nv_bfloat16>;
+                constexpr int kVec = 16 / sizeof(Elem), kPass = 64 / sizeof(Elem);
                 const int r0 = lane / 4, chunk = lane & 3, f0 = p.m0 + rank * kM + quarter * 32;
-                float *to = static_cast<float *>(a.dw) + ((int64_t)e * a.F + f0 + r0) * a.K + p.n0 + chunk * 4;
+                Elem *to = static_cast<Elem *>(a.dw) + ((int64_t)e * a.F + f0 + r0) * a.K + p.n0 + chunk * kVec;
                 const int64_t step = (int64_t)8 * a.K;
-                const int rows = a.F - f0 - r0, cols = n - chunk * 4;
+                const int rows = a.F - f0 - r0, cols = n - chunk * kVec;
                 const uint32_t put = buf + lane * 64, get = buf + r0 * 64 + ((chunk ^ ((r0 >> 1) & 3)) * 16);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c0 = 64 * (i / 2) + 32 * half + 16 * (i % 2);
+                for (int i = 0; i < 128 / kPass; ++i) {
+                    const int at = i * kPass, c0 = 64 * (at / 32) + 32 * half + at % 32;
                     if (c0 < n) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float *v = &sum[i / 2][16 * (i % 2) + 4 * q];
-                            st_shared128(put + ((q ^ ((lane >> 1) & 3)) * 16),
-                                         make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                                    __float_as_uint(v[3])));
+                            const float *v = &sum[at / 32][at % 32 + kVec * q];
+                            uint4 four;
+                            if constexpr (kF32) {
+                                four = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                  __float_as_uint(v[3]));
+                            } else {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) w[j] = bf16x2(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]));
+                                four = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                            st_shared128(put + ((q ^ ((lane >> 1) & 3)) * 16), four);
                         }
                         __syncwarp();
 #pragma unroll
@@ -382,11 +400,11 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
     if (warp == kStoreWarps) tmem_free_pair(tmem, 512);
 }
 
-template <bool kF32>
+template <bool kParts, bool kF32>
 cudaError_t launch(const ColumnMaps &map_dy, const ColumnMaps &map_x, Args a, cudaStream_t stream) {
-    auto kern = expert_wgrad_kernel<kF32>;
+    auto kern = expert_wgrad_kernel<kParts, kF32>;
     static thread_local PairCache cache;
-    using S = Shape<kF32>;
+    using S = Shape<kParts>;
     PairLaunch l(S::kThreads, S::kSmem + groups_bytes(1024), stream);
     cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), l.cfg);
     if (e != cudaSuccess) return e;
@@ -419,7 +437,8 @@ cudaError_t launch_expert_wgrad(const ExpertRows &r, int K, int F, const void *d
     if (!encode_columns(&map_dy, dy, F, r.rows_total, kM) || !encode_columns(&map_x, x, K, r.rows_total, kN / 2))
         return cudaErrorInvalidValue;
     const Args a{r.offsets, dw, r.cap, r.most, r.pairs, r.E, r.L, K, F, kN};
-    return dw_f32 ? launch<true>(map_dy, map_x, a, stream) : launch<false>(map_dy, map_x, a, stream);
+    if (dw_f32) return launch<true, true>(map_dy, map_x, a, stream);
+    return r.most > kWhole ? launch<true, false>(map_dy, map_x, a, stream) : launch<false, false>(map_dy, map_x, a, stream);
 }
 
 cudaError_t take_expert_wgrad_error(int *err) { return take_tc_error(err); }

@@ -269,6 +269,12 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t *r) {
         : "memory");
 }
 
+// Most elements of a sum that bf16 results take in one accumulator.  The tensor
+// core cuts off what it adds: a sum of n terms comes out small by about 1e-9 n of
+// itself, 5e-9 n where all terms have one sign.  After these many that is 8e-5,
+// a fiftieth of what the rounding to bf16 alone may be off by (2^-8).
+constexpr int kWhole = 1 << 14;
+
 // ---- pairs of blocks (clusters of two; cta_group::2) --------------------------
 //
 // One tcgen05.mma spans the two SMs of a cluster: each block holds half of A
