@@ -22,10 +22,13 @@ constexpr int kActBlocks = 24;  // per SM at most: of these rows' time 8 cost 9 
 __device__ __forceinline__ float lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+// The factors with s come first: s (1 + g (1 - s)) is at most 1.1 and |g s| at most
+// |g|, and both are 0 where g is the type's lowest value; dh g or dh u could pass
+// the range before s = 0 takes it back (infinity times 0).
 __device__ __forceinline__ void grad(float g, float u, float dh, float *dg, float *du) {
     const float s = 1.f / (1.f + expf(-g));
-    *dg = dh * u * s * (1.f + g * (1.f - s));
-    *du = dh * g * s;
+    *dg = s * (1.f + g * (1.f - s)) * u * dh;
+    *du = g * s * dh;
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {

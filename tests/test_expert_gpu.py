@@ -308,3 +308,31 @@ def test_wgrad_ragged_expert_behind_many_others(kind, K, F, f32):
     empty = torch.tensor([c == 0 for c in counts], device="cuda")
     assert int(dw[empty].count_nonzero()) == 0
     assert moe.take_device_error() == moe.MOE_OK
+
+
+def test_swiglu_grad_at_the_ends_of_the_range():
+    """g or u the lowest or highest value of the type, or so low that the sigmoid is 0: gradients are finite, and as the
+    formula gives them in f32 range, though dh g and dh u are not."""
+    low = torch.finfo(torch.bfloat16).min
+    g = [low, low, low / 2, -200.0, -200.0, -89.0, -120.0, 200.0, 5.0]
+    u = [1.0, -low, 3.0, -low, low, -low, 1e30, 2.0, 1e30]
+    d = [4.0, 2.0, -3e38, 3e38, 4.0, -2.0, 3e38, 1e30, 1e7]
+    F = 16
+    b = Batch(1, [1], 1)
+    pre, dh = torch.zeros(1, 2 * F, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, F, dtype=torch.bfloat16, device="cuda")
+    for t, at in ((pre[0, :F], g), (pre[0, F:], u), (dh[0], d)):
+        t[:len(at)] = torch.tensor(at, dtype=torch.bfloat16)
+    dpre = b.out(2 * F, torch.bfloat16)
+    moe.expert_swiglu_grad(b.dims(), F, pre, dh, b.offsets, dpre)
+    g, u, d = pre[:, :F].double(), pre[:, F:].double(), dh.double()
+    s, t = torch.special.expit(g), torch.special.expit(-g)
+    # f32 operations as in test_swiglu_grad; a sigmoid below 2^-126 has no more than 2^-149 as its step
+    small = 2.0 ** -149
+    dg_err = 16 * F32_HALF * (d * u * s).abs() * (1 + g.abs()) + small * (d * u).abs() * (1 + g.abs())
+    du_err = 16 * F32_HALF * (d * g * s).abs() + small * (d * g).abs()
+    # where exp(-g) passes the range of f32 (g below -88.73) s is 0, and so is the gradient
+    zero = g < -88.73
+    for got, want, err in ((dpre[:, :F], d * u * s * (1 + g * t), dg_err), (dpre[:, F:], d * g * s, du_err)):
+        assert bool(torch.isfinite(got.float()).all())
+        assert int(got[zero].count_nonzero()) == 0
+        ref.check(got[~zero], want[~zero], err[~zero], BF16_HALF, "gradient")
