@@ -4,8 +4,8 @@
 One step is one pass of the whole routing path over one batch of the
 DeepSeek-V3-shaped decode workload (N=32 ranks x T=128 tokens, E=256, R=8,
 H=7168 bf16), with the inputs already in HBM.  The expert op between pack
-and combine stands in for the grouped expert GEMM and is not timed; in its
-place the L2 is flushed (a GPU-side read of 2x the L2 size), as it is
+and combine stands in for the experts' products (moe_expert.h, measured by
+perf/operators.py) and is not timed; in its place the L2 is flushed (a GPU-side read of 2x the L2 size), as it is
 before every step, so no kernel reads data a previous kernel left in L2.
 
 Prints one JSON line (rank 0).  `--impl reference` times the CPU oracle on
@@ -300,7 +300,7 @@ def workload_config(w):
             "cap_rows_per_rank": W.default_cap(w),
             "l2": "flushed before every step and between pack and combine by reading a 2x L2 "
                   "buffer (untimed; evicts everything, leaves clean lines)",
-            "expert_op": "not timed (stands in for the grouped expert GEMM)",
+            "expert_op": "not timed (stands in for the experts' products)",
             "parallelism": "replicas"}
 
 
@@ -343,7 +343,7 @@ def mean_interval(pairs):
 class PathRunner:
     """One workload on one GPU: its seeded inputs in HBM, its buffers, and the
     four calls of the path.  The expert op between pack and combine stands in
-    for the grouped expert GEMM and is not run: combine reads y as pack left
+    for the experts' products and is not run: combine reads y as pack left
     it (identity) or as it was zeroed once (a separate y)."""
 
     def __init__(self, moe, W, w, dev, stream, flush):

@@ -144,7 +144,8 @@ __device__ __forceinline__ uint32_t bf16x2(uint32_t first, uint32_t second) {
 }
 
 // silu(g) u; exp within 2 units in the last place, the fast division too.
-// exp(-g) = infinity (g < -88) gives 0, and NaN for g = -infinity.
+// A divisor above 2^126 (g below -87.3; exp(-g) = infinity too) gives 0, and NaN for
+// g = -infinity.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
 
 // Position in a ring of kSlots slots: the slot and the parity of its use.
@@ -245,8 +246,8 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
                  : "memory");
 }
 
-// 32 lanes x 16 columns of 32 bits, complete on return; a warp reaches the
-// 32 lanes of its place in its group of four.
+// Loads of 32 lanes x 32 columns of 32 bits; a warp reaches the 32 lanes of its
+// place in its group of four.
 // The load alone: its registers may be read after tmem_wait32 on them.
 __device__ __forceinline__ void tmem_load32_async(uint32_t addr, uint32_t *r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -260,7 +261,7 @@ __device__ __forceinline__ void tmem_wait32(uint32_t *r) {  // waits for every l
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t *r) {
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t *r) {  // complete on return
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
@@ -513,12 +514,7 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
                 __syncwarp();  // prefix is written again
             }
         }
-        int before = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += v;
-        }
+        int before = scan(sum, lane);
         if (lane == 31) g.prefix[E] = before;
         if (lane == 0) s_shift = shift, s_sorted = sorted;
         before -= sum;

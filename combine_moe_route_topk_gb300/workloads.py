@@ -32,7 +32,8 @@ SOFTMAX = 0
 SIGMOID = 1
 
 # expert op used by the harness between pack and combine (stands in for the
-# grouped expert GEMM, which needs trained weights and is not on this path)
+# experts' products, which the library has in moe_expert.h: these workloads
+# are of the routing steps alone)
 EXPERT_IDENTITY = "identity"
 EXPERT_SCALE = "scale"
 EXPERT_DEQUANT = "dequant"
