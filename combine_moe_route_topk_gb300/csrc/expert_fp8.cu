@@ -202,6 +202,7 @@ expert_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         }
         if (elect_one()) tc_commit(done);
         __syncwarp();
+        mb_drain(done, 0);
     } else if (warp >= kSumWarps + 2) {
         // scales: each of two warps takes 64 tokens, two a lane; the next
         // blocks' are on their way while these wait for their accumulator

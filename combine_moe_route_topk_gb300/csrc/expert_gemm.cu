@@ -241,6 +241,7 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             }
             if (elect_one()) tc_commit_pair(done);
             __syncwarp();
+            mb_drain(done, 0);
         }
     } else if (warp < kStoreWarps) {
         // results: warp w holds matrix rows 32 (w % 4).. of the block's half,

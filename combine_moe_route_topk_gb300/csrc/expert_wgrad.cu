@@ -225,6 +225,7 @@ expert_wgrad_kernel(const __grid_constant__ ColumnMaps map_dy, const __grid_cons
             }
             if (elect_one()) tc_commit_pair(done);
             __syncwarp();
+            mb_drain(done, 0);
         }
     } else if (warp == kStoreWarps + 2) {  // zeroes behind the experts' last rows
         int slot = 0;

@@ -158,19 +158,17 @@ def test_binding_refuses_cpu_tensors_and_other_types():
                             torch.zeros(4, 8, 128, **u8), torch.zeros(4, 1, 1, **f32), off, y)
 
 
-def _enclosing(text, needle):
-    """The heads of the blocks around `needle` (which stands once in the source)."""
-    text = re.sub(r"//[^\n]*", "", text)
-    assert text.count(needle) == 1, needle
-    heads, at = [], 0
-    for i, c in enumerate(text[:text.index(needle)]):
+def _enclosing(text, at):
+    """The heads of the blocks around a place of a source without comments."""
+    heads, begin = [], 0
+    for i, c in enumerate(text[:at]):
         if c in "{};":
             if c == "{":
-                heads.append(text[at:i].strip())
+                heads.append(text[begin:i].strip())
             elif c == "}":
                 heads.pop()
-            at = i + 1
-    return heads + [text[at:text.index(needle)].strip()]
+            begin = i + 1
+    return heads + [text[begin:at].strip()]
 
 
 @pytest.mark.parametrize("name", ["expert_gemm.cu", "expert_wgrad.cu"])
@@ -178,9 +176,16 @@ def _enclosing(text, needle):
 def test_both_blocks_of_a_pair_wait_for_the_leaders_commits(name, needle):
     """The leader's commits arrive in both blocks' shared memory: each block waits for its own last arrivals
     before the closing barrier, which orders threads, not arrivals under way."""
-    text = open(os.path.join(_build.CSRC, name)).read()
-    assert text.index(needle) < text.rindex("cluster_sync()")
-    assert not any("rank" in h.split(")")[0] for h in _enclosing(text, needle) if h.startswith(("if", "else")))
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, name)).read())
+
+    def of_the_leader(at):
+        return any("rank" in h.split(")")[0] for h in _enclosing(text, at) if h.startswith(("if", "else", "}")))
+
+    places = [m.start() for m in re.finditer(re.escape(needle), text)]
+    assert places and max(places) < text.rindex("cluster_sync()")
+    assert not all(of_the_leader(p) for p in places)
+    if "done" in needle:  # and the issuing warp, however late it comes to it, before the block frees TMEM
+        assert any(of_the_leader(p) for p in places)
 
 
 @pytest.mark.parametrize("name", ["expert_gemm.cu", "expert_wgrad.cu", "expert_fp8.cu", "tc_ops.cuh"])
