@@ -77,14 +77,15 @@ __device__ __forceinline__ bool elect_one() {
 // Every wait is bounded: after `polls` polls (each may suspend briefly), or once
 // another warp of the block has given up, it returns false and the block's
 // word `gave_up` is set; each role then leaves its loop, copies in flight are
-// waited for (again bounded), TMEM is freed and the kernel ends.  A poll takes
-// no less than about 10 ns: kPolls are at least 10 ms, where a stage takes well
-// under 10 us; a wait that spans more adds kStepPolls for each stage.
+// waited for (again bounded), TMEM is freed and the kernel ends.  A failing poll is
+// suspended for 3.9 us on GB300, which nothing promises: kPolls are 4 s, and
+// 10 ms if polls took as little as 10 ns, where a stage takes well under 10 us; a
+// wait that spans more adds kStepPolls (16 ms, or 40 us) for each stage.
 constexpr long long kPolls = 1 << 20, kStepPolls = 1 << 12;
 
 // The limit of a role's waits where they may span whole tiles, some of which
 // have no stages but results to be written (zeros, 256 KB a pair: 3 us at the
-// rate of HBM, less than the 40 us of kStepPolls).  Roles run ahead of
+// rate of HBM, a stage's allowance again).  Roles run ahead of
 // one another through such tiles without waiting, so all that came before count
 // for every later wait, of tiles with stages those since the last wait.
 struct WaitLimit {
