@@ -452,3 +452,59 @@ def test_offsets_of_no_batch_stand_for_no_rows(offsets):
                 assert int(t.count_nonzero()) == 0  # dw: no rows, zeros
             else:
                 assert bool((t.view(torch.uint8) == 0x5A).all())
+
+
+def test_captured_calls_of_two_graphs_at_the_same_time(batch):
+    """Two graphs that hold every call, replayed on two streams at once: no call keeps anything another one uses."""
+    one, two = _calls(batch), _calls(Batch(3, [65, 0, 200, 9, 300, 1], 320, seed=9))
+    want, graphs = [], []
+    for calls in (one, two):
+        for call, outs in calls:
+            _clear(outs)
+            call()
+            want.append(_bits(outs))
+            _clear(outs)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(3):
+                for call, _ in calls:
+                    call()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, outs), bits in zip(one + two, want):
+        assert _same(_bits(outs), bits)
+
+
+def test_calls_from_two_threads():
+    """What the library keeps per thread is set up by the first calls of each, at the same time."""
+    import threading
+    failed = []
+
+    def work(seed):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                calls = _calls(Batch(2, [100, 3, 0, 290, 17, 64], 400, seed=seed))
+                for i in range(20):
+                    for call, outs in calls:
+                        call()
+                        if i == 0:
+                            stream.synchronize()
+                            outs.append(_bits(outs))
+                stream.synchronize()
+                for call, (*outs, bits) in calls:
+                    assert _same(_bits(outs), bits)
+        except BaseException as e:  # reported by the test's own thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in (1, 2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
