@@ -202,6 +202,8 @@ int check_expert(const MoeDims *dims, int K, int F, bool gated, int elem, const 
         return set_error(MOE_ERR_INVALID_ARG, "%s: K=%d and F=%d must be positive multiples of 8", what, K, F);
     if (K > (1 << 24) || F > (1 << 24))
         return set_error(MOE_ERR_UNSUPPORTED, "%s: this build supports K, F <= 2^24 (got K=%d F=%d)", what, K, F);
+    if (v->rows_total > kI32Max - 65536)  // a block's last load begins up to a tile behind the last row
+        return set_error(MOE_ERR_UNSUPPORTED, "%s: N*cap=%lld must stay below 2^31 - 65536", what, (long long)v->rows_total);
     const int64_t wide = gated ? 2 * (int64_t)F : F;
     if (wide * K * elem >= (int64_t)1 << 40)  // the stride of a tensor map
         return set_error(MOE_ERR_UNSUPPORTED, "%s: a matrix of %lld x %d must stay below 2^40 bytes", what,

@@ -69,7 +69,7 @@ __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, i
     Tile r;
     r.e = same(find_group(g, E, e, t));
     const int c = same(g.count[r.e]), nt = token_tiles(c), at = t - same(g.prefix[r.e]);
-    const int size = (c + nt - 1) / nt, tt = at % nt;
+    const int size = tile_rows(c, nt), tt = at % nt;
     r.f0 = at / nt * f_step;
     r.row = same(g.row[r.e]) + tt * size;
     r.n = min(size, c - tt * size);

@@ -72,8 +72,7 @@ __device__ __forceinline__ int token_tiles(int count, int shift) { return (count
 __host__ __device__ inline int mma_tokens(int n) { return (n + 31) & ~31; }
 
 __device__ __forceinline__ int tile_tokens(int count, int shift) {
-    const int nt = token_tiles(count, shift);
-    return mma_tokens((count + nt - 1) / nt);
+    return mma_tokens(tile_rows(count, token_tiles(count, shift)));
 }
 
 // Larger tiles come first (make_groups sorts by the size), so that a round's

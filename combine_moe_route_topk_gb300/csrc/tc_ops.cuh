@@ -530,6 +530,10 @@ __device__ __forceinline__ Groups make_groups(int *mem, const int32_t *__restric
     return g;
 }
 
+// Rows of each of a group's `tiles` equal tiles (count > 0): count + tiles - 1 need
+// not fit 32 bits.
+__host__ __device__ constexpr int tile_rows(int count, int tiles) { return (count - 1) / tiles + 1; }
+
 // The group that holds tile t (prefix[e] <= t < prefix[e + 1]), searched
 // from group e on: tiles are taken in ascending order, so e only grows.
 __device__ __forceinline__ int find_group(const Groups &g, int E, int e, int t) {

@@ -17,7 +17,8 @@
  * before anything is enqueued.  More precisely:
  *   - dims gives N, T, E, R and cap_rows of the batch; H, x_dtype are not
  *     used, y_dtype where stated.  K and F are the product's own sizes:
- *     8 <= K, F <= 2^24, multiples of 8 (128 where stated).
+ *     8 <= K, F <= 2^24, multiples of 8 (128 where stated).  N*cap stays below
+ *     2^31 - 65536.
  *   - expert_offsets i32 [E+1] is moe_dispatch_count's output.  The rows of
  *     expert e on rank d = e / (E/N) are p = d*cap + (expert_offsets[e] -
  *     expert_offsets[d*E/N]) and the expert_counts[e] - 1 rows behind it, as

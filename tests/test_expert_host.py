@@ -264,3 +264,45 @@ def test_waits_for_the_other_blocks_writes_acquire_for_the_cluster():
     waits.remove("at_leader")  # the arrival
     assert [w for w in waits if w != "mb_init"] == ["mb_wait_warp_pair"]
     assert "mbarrier.arrive.release.cluster" in ops and "mbarrier.try_wait.parity.acquire.cluster" in ops
+
+
+TILES = r'''
+#include <stdio.h>
+#include "tc_ops.cuh"
+int main() {
+    int count, most;
+    while (scanf("%d %d", &count, &most) == 2) {
+        const int tiles = (count + most - 1) / most, rows = moe::tile_rows(count, tiles);
+        printf("%d %d\n", tiles, rows);
+    }
+}
+'''
+
+
+def test_tiles_of_the_longest_groups(tmp_path):
+    """A group has up to 2^31 - 65537 rows (what the library accepts); its rows and its tiles added up pass 32 bits."""
+    src = tmp_path / "tiles.cu"
+    src.write_text(TILES)
+    subprocess.run([_build.nvcc(), *_build.ARCH, *_build.NVCC_FLAGS, "-o", str(tmp_path / "tiles"), str(src)], check=True,
+                   capture_output=True)
+    top = (1 << 31) - 1 - 65536
+    counts = [1, 2, 63, 64, 65, 255, 256, 257, 511, 513, 10 ** 6, top // 2, top - 1000003, top - 1, top]
+    cases = [(n, most) for n in counts for most in (64, 128, 256)]
+    out = subprocess.run([str(tmp_path / "tiles")], input=" ".join(f"{n} {m}" for n, m in cases), capture_output=True,
+                         text=True, check=True).stdout.split()
+    for (n, most), tiles, rows in zip(cases, map(int, out[::2]), map(int, out[1::2])):
+        assert tiles == -(-n // most) and rows == -(-n // tiles), (n, most)
+        assert 0 < rows <= most and rows * (tiles - 1) < n <= rows * tiles
+    # every place that cuts a group into tiles uses it
+    for name in ("expert_gemm.cu", "expert_fp8.cu"):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, name)).read())
+        assert "tile_rows(" in text and not re.search(r"\+ nt - 1", text)
+
+
+@pytest.mark.parametrize("name", EVERY)
+def test_rows_at_the_end_of_32_bits_are_refused(lib, name):
+    """The last load of a region may begin a tile behind its last row."""
+    top = (1 << 31) - 1 - 65536
+    assert _call(lib, name, d=_dims(N=1, T=8, E=4, R=2, cap_rows=top + 1)) == UNSUPPORTED
+    assert "N*cap" in lib.moe_last_error().decode()
+    assert _call(lib, name, d=_dims(N=1, T=8, E=4, R=2, cap_rows=top), a=None) == INVALID  # gets as far as the pointers

@@ -142,3 +142,27 @@ def test_wgrad_of_a_batch_that_could_be_long(K, F):
         r = b.span(e)
         p, q = dy[r].double(), x[r].double()
         ref.check(dw[e], p.t() @ q, ref.sum_error(r.stop - r.start, p.abs().t() @ q.abs()), BF16_HALF, f"dw[{e}]")
+
+
+def test_the_most_rows():
+    """An expert of almost 2^31 rows: its rows and the number of its tiles added up pass 32 bits."""
+    rows, first, K, F = (1 << 31) - 1 - 65536, 1000003, 8, 8
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("rows and results take 70 GB")
+    d = moe.make_dims(1, rows, 2, 1, 8, cap_rows=rows)
+    off = torch.tensor([0, first, rows], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x, y = (torch.empty(rows, n, dtype=torch.bfloat16, device="cuda") for n in (K, F))
+    step = 1 << 25
+    for i in range(0, rows, step):
+        x[i:i + step].normal_(generator=g)
+        y[i:i + step].fill_(ref.SENTINEL)
+    w = torch.randn(2, F, K, generator=g, device="cuda").to(torch.bfloat16)
+    moe.expert_gemm(d, K, F, LINEAR, x, w, off, y)
+    for i in range(0, rows, step):
+        for e, lo, hi in ((0, i, min(i + step, first)), (1, max(i, first), min(i + step, rows))):
+            if lo < hi:
+                a, m = x[lo:hi].double(), w[e].double().t()
+                ref.check(y[lo:hi], a @ m, ref.sum_error(K, a.abs() @ m.abs()), BF16_HALF, f"rows {lo} to {hi}")
