@@ -106,6 +106,10 @@ def lib() -> ctypes.CDLL:
             L.moe_expert_gemm_wgrad.argtypes = [D, i32, i32, P, P, P, P, i32, P]
             L.moe_expert_swiglu_grad.argtypes = [D, i32, P, P, P, P, P]
             L.moe_expert_gemm_fp8.argtypes = [D, i32, i32, i32, P, P, P, P, P, P, P, P]
+            L.moe_expert_gemm_w4.argtypes = [D, i32, i32, i32, i32, P, P, P, P, P, P, P]
+            L.moe_combine_grad.argtypes = [D, P, P, P, P, P, P, P]
+            L.moe_dispatch_grad.argtypes = [D, P, P, P, P, P]
+            L.moe_route_grad.argtypes = [D, P, P, i32, i32, P, P, P, P, P, P]
             L.moe_read_status.argtypes = [P, P]
             L.moe_take_device_error.argtypes = [P]
             L.moe_selftest_bounded_wait.argtypes = [P, ctypes.c_int64, P]
@@ -118,6 +122,7 @@ def lib() -> ctypes.CDLL:
                        "moe_combine", "moe_combine_rank", "moe_combine_partials",
                        "moe_combine_reduce_partials", "moe_expert_gemm", "moe_expert_gemm_dgrad",
                        "moe_expert_gemm_wgrad", "moe_expert_swiglu_grad", "moe_expert_gemm_fp8",
+                       "moe_expert_gemm_w4", "moe_combine_grad", "moe_dispatch_grad", "moe_route_grad",
                        "moe_read_status",
                        "moe_take_device_error", "moe_selftest_bounded_wait"):
                 getattr(L, fn).restype = i32
@@ -410,6 +415,101 @@ def expert_gemm_fp8(dims: MoeDims, K: int, F: int, act: int, xq, x_scales, wq, w
         _on(dev, y, rows * F * yt.itemsize, "y", yt),
         None if y_scales is None and not gated else
         _on(dev, y_scales, rows * (F // 128) * 4, "y_scales", f32), st))
+
+
+def pack_w4(q: torch.Tensor) -> torch.Tensor:
+    """Whole numbers in [-8, 7] (integers [..., K], K % 8 == 0) as expert_gemm_w4's words, int32
+    [..., K/8]: element 2j of eight at bit 4j, element 2j + 1 at bit 16 + 4j.  On q's device."""
+    if q.shape[-1] % 8 != 0 or q.dtype.is_floating_point:
+        raise ValueError(f"q must be integers, a multiple of 8 in a row (got {q.dtype} {tuple(q.shape)})")
+    if q.numel() and (int(q.min()) < -8 or int(q.max()) > 7):
+        raise ValueError("q must lie in [-8, 7]")
+    q = q.unflatten(-1, (-1, 8))
+    words = torch.zeros(q.shape[:-1], dtype=torch.int32, device=q.device)
+    for i in range(8):
+        words |= (q[..., i].to(torch.int32) & 15) << (4 * (i // 2) + 16 * (i % 2))
+    return words
+
+
+def quantize_w4(w: torch.Tensor, group: int):
+    """Matrices [E][W][K] (of finite values) in expert_gemm_w4's form: (wq int32 [E][W][K/8],
+    group_scales e4m3 as uint8 [E][K/group][W], row_scales f32 [E][W]).  A group's scale makes its
+    largest magnitude 7; the row's scale makes the largest group's 448, e4m3's largest."""
+    if w.dim() != 3 or group not in (32, 64, 128) or w.shape[-1] % group != 0:
+        raise ValueError(f"w must be [E][W][K] with K a multiple of group 32, 64 or 128 (got {tuple(w.shape)}, {group})")
+    E, W, K = w.shape
+    wq = torch.empty(E, W, K // 8, dtype=torch.int32, device=w.device)
+    group_scales = torch.empty(E, K // group, W, dtype=torch.uint8, device=w.device)
+    row_scales = torch.empty(E, W, dtype=torch.float32, device=w.device)
+    for e in range(E):  # one matrix at a time: what it needs on the way is four times its size
+        m = w[e].float().view(W, K // group, group)
+        want = m.abs().amax(dim=2) / 7.0
+        row = want.amax(dim=1) / 448.0
+        row = torch.where(row > 0, row, torch.ones_like(row))
+        s = (want / row.unsqueeze(1)).clamp(max=448.0).to(torch.float8_e4m3fn)
+        step = s.float() * row.unsqueeze(1)
+        q = (m / torch.where(step > 0, step, torch.ones_like(step)).unsqueeze(2)).round_().clamp_(-8.0, 7.0)
+        wq[e] = pack_w4(torch.where((step > 0).unsqueeze(2), q, 0.0).to(torch.int8).view(W, K))
+        group_scales[e] = s.t().contiguous().view(torch.uint8)
+        row_scales[e] = row
+    return wq, group_scales, row_scales
+
+
+def expert_gemm_w4(dims: MoeDims, K: int, F: int, act: int, group: int, x, wq, group_scales, row_scales,
+                   expert_offsets, y, stream=None):
+    """Each expert's rows (bf16) times its matrix of 4-bit weights with group scales: y of
+    dims.y_dtype (MOE_EXPERT_LINEAR), or silu(g) * u of the gate and up halves (MOE_EXPERT_SWIGLU,
+    y bf16).  Weights as from quantize_w4; group_scales may be uint8 or float8_e4m3fn."""
+    (rows, dev, st), f32 = _expert_call(dims, stream), torch.float32
+    gated = int(act) == MOE_EXPERT_SWIGLU
+    W = F * (2 if gated else 1)
+    yt = torch.bfloat16 if gated else _TORCH_DTYPE[dims.y_dtype]
+    st8 = torch.float8_e4m3fn if group_scales is not None and group_scales.dtype is torch.float8_e4m3fn else torch.uint8
+    _check(lib().moe_expert_gemm_w4(
+        ctypes.byref(dims), int(K), int(F), int(act), int(group), _on(dev, x, rows * K * 2, "x", torch.bfloat16),
+        _on(dev, wq, dims.E * W * K // 2, "wq", torch.int32),
+        _on(dev, group_scales, dims.E * W * K // group if group in (32, 64, 128) else 0, "group_scales", st8),
+        _on(dev, row_scales, dims.E * W * 4, "row_scales", f32),
+        _on(dev, expert_offsets, (dims.E + 1) * 4, "expert_offsets", torch.int32),
+        _on(dev, y, rows * F * yt.itemsize, "y", yt), st))
+
+
+def combine_grad(dims: MoeDims, dout, y, pos, topk_w, dy, dtopk_w, stream=None):
+    """Gradient of combine: rows dy[pos] = topk_w * dout and dtopk_w = <dout, y[pos]>."""
+    s = buffer_sizes(dims)
+    yt = _TORCH_DTYPE[dims.y_dtype]
+    (_, dev, st), f32 = _expert_call(dims, stream), torch.float32
+    _check(lib().moe_combine_grad(
+        ctypes.byref(dims), _on(dev, dout, s["out_bytes"], "dout", yt), _on(dev, y, s["y_bytes"], "y", yt),
+        _on(dev, pos, s["pos_bytes"], "pos", torch.int32), _on(dev, topk_w, s["topk_w_bytes"], "topk_w", f32),
+        _on(dev, dy, s["y_bytes"], "dy", yt), _on(dev, dtopk_w, s["topk_w_bytes"], "dtopk_w", f32), st))
+
+
+def dispatch_grad(dims: MoeDims, dpacked, pos, dx, add=None, stream=None):
+    """Gradient of dispatch_pack: dx = add + the sum of a token's rows of dpacked (add may be
+    None, or dx itself)."""
+    s = buffer_sizes(dims)
+    xt = _TORCH_DTYPE[dims.x_dtype]
+    _, dev, st = _expert_call(dims, stream)
+    _check(lib().moe_dispatch_grad(
+        ctypes.byref(dims), _on(dev, dpacked, s["packed_x_bytes"], "dpacked", xt),
+        _on(dev, pos, s["pos_bytes"], "pos", torch.int32),
+        None if add is None else _on(dev, add, s["x_bytes"], "add", xt), _on(dev, dx, s["x_bytes"], "dx", xt), st))
+
+
+def route_grad(dims: MoeDims, logits, bias, score_fn, renormalize, topk_idx, topk_w, dtopk_w, dlogits,
+               dbias=None, stream=None):
+    """Gradient of route_topk's weights: dlogits, and their sum over the tokens as the gradient of
+    a bias that is added to the logits."""
+    s = buffer_sizes(dims)
+    (_, dev, st), f32 = _expert_call(dims, stream), torch.float32
+    _check(lib().moe_route_grad(
+        ctypes.byref(dims), _on(dev, logits, s["logits_bytes"], "logits", f32),
+        None if bias is None else _on(dev, bias, dims.E * 4, "bias", f32), int(score_fn), int(bool(renormalize)),
+        _on(dev, topk_idx, s["topk_idx_bytes"], "topk_idx", torch.int32),
+        _on(dev, topk_w, s["topk_w_bytes"], "topk_w", f32), _on(dev, dtopk_w, s["topk_w_bytes"], "dtopk_w", f32),
+        _on(dev, dlogits, s["logits_bytes"], "dlogits", f32),
+        None if dbias is None else _on(dev, dbias, dims.E * 4, "dbias", f32), st))
 
 
 def combine(dims: MoeDims, y, pos, topk_w, out, stream=None):

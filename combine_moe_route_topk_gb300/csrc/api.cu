@@ -8,6 +8,8 @@
 #include <cuda.h>  // types only: the driver calls are fetched at run time
 
 #include "expert_internal.cuh"
+#include "expert_w4_internal.cuh"
+#include "grad_internal.cuh"
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -715,6 +717,108 @@ int moe_expert_gemm_fp8(const MoeDims *dims, int K, int F, int act, const void *
                        what);
 }
 
+int moe_expert_gemm_w4(const MoeDims *dims, int K, int F, int act, int group, const void *x, const int32_t *wq,
+                       const void *group_scales, const float *row_scales, const int32_t *expert_offsets, void *y,
+                       void *stream) {
+    const char *what = "moe_expert_gemm_w4";
+    Derived v;
+    ExpertRows r;
+    const bool gated = act == MOE_EXPERT_SWIGLU;
+    int rc = check_expert(dims, K, F, gated, 1, expert_offsets, &v, &r, what);
+    if (rc != MOE_OK) return rc;
+    if (act != MOE_EXPERT_LINEAR && !gated) return set_error(MOE_ERR_INVALID_ARG, "%s: unknown act %d", what, act);
+    if (group != 32 && group != 64 && group != 128)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: group must be 32, 64 or 128 (got %d)", what, group);
+    if (K % group != 0)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: K=%d must be a multiple of group=%d", what, K, group);
+    if (v.NT == 0) return MOE_OK;
+    if (bad_block_pointers(x, wq, y, what, &rc)) return rc;
+    if (!group_scales || !row_scales) return set_error(MOE_ERR_INVALID_ARG, "%s: a required pointer is NULL", what);
+    if (!aligned(group_scales, 4) || !aligned(row_scales, 4))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", what);
+    const int64_t wide = (gated ? 2 : 1) * (int64_t)F;
+    const Span out = {y, v.rows_total * F * (!gated && dims->y_dtype == MOE_F32 ? 4 : 2)};
+    const Span in[] = {{x, v.rows_total * K * 2},
+                       {wq, dims->E * wide * (K / 2)},
+                       {group_scales, dims->E * wide * (K / group)},
+                       {row_scales, dims->E * wide * 4},
+                       offsets_span(r)};
+    if (overlap_any(out, in, what, &rc)) return rc;
+    return cuda_result(launch_expert_gemm_w4(r, K, F, gated, group, x, wq, group_scales, row_scales, y,
+                                             dims->y_dtype == MOE_F32, (cudaStream_t)stream),
+                       what);
+}
+
+int moe_combine_grad(const MoeDims *dims, const void *dout, const void *y, const int32_t *pos, const float *topk_w,
+                     void *dy, float *dtopk_w, void *stream) {
+    const char *what = "moe_combine_grad";
+    Derived v;
+    int rc = check_dims(dims, &v, what);
+    if (rc != MOE_OK) return rc;
+    if (v.NT == 0) return MOE_OK;
+    if (!dout || !y || !pos || !topk_w || !dy || !dtopk_w)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: a required pointer is NULL", what);
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: dout, y and dy must be 16-byte aligned", what);
+    if (!aligned(pos, 4) || !aligned(topk_w, 4) || !aligned(dtopk_w, 4))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: pos, topk_w and dtopk_w must be 4-byte aligned", what);
+    const Span rows = {dy, v.rows_total * v.y_row_bytes}, weights = {dtopk_w, v.pairs * 4};
+    const Span in[] = {{dout, v.NT * v.y_row_bytes}, {y, rows.bytes}, {pos, v.pairs * 4}, {topk_w, v.pairs * 4}};
+    const Span with_rows[] = {in[0], in[1], in[2], in[3], rows};
+    if (overlap_any(rows, in, what, &rc) || overlap_any(weights, with_rows, what, &rc)) return rc;
+    return cuda_result(launch_combine_grad(dout, y, dims->y_dtype, pos, topk_w, v.NT, dims->R, dims->H, v.rows_total, dy,
+                                           dtopk_w, (cudaStream_t)stream),
+                       what);
+}
+
+int moe_dispatch_grad(const MoeDims *dims, const void *dpacked, const int32_t *pos, const void *add, void *dx,
+                      void *stream) {
+    const char *what = "moe_dispatch_grad";
+    Derived v;
+    int rc = check_dims(dims, &v, what);
+    if (rc != MOE_OK) return rc;
+    if (dims->x_dtype != MOE_BF16 && dims->x_dtype != MOE_F32)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: x_dtype must be MOE_BF16 or MOE_F32 (got %d)", what, dims->x_dtype);
+    if (v.NT == 0) return MOE_OK;
+    if (!dpacked || !pos || !dx) return set_error(MOE_ERR_INVALID_ARG, "%s: a required pointer is NULL", what);
+    if (!aligned(dpacked, 16) || !aligned(add, 16) || !aligned(dx, 16))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: dpacked, add and dx must be 16-byte aligned", what);
+    if (!aligned(pos, 4)) return set_error(MOE_ERR_INVALID_ARG, "%s: pos must be 4-byte aligned", what);
+    const Span out = {dx, v.NT * v.x_row_bytes};
+    const Span in[] = {{dpacked, v.rows_total * v.x_row_bytes}, {pos, v.pairs * 4}, {add == dx ? nullptr : add, out.bytes}};
+    if (overlap_any(out, in, what, &rc)) return rc;
+    return cuda_result(launch_dispatch_grad(dpacked, dims->x_dtype, pos, add, v.NT, dims->R, dims->H, v.rows_total, dx,
+                                            (cudaStream_t)stream),
+                       what);
+}
+
+int moe_route_grad(const MoeDims *dims, const float *logits, const float *bias, int score_fn, int renormalize,
+                   const int32_t *topk_idx, const float *topk_w, const float *dtopk_w, float *dlogits, float *dbias,
+                   void *stream) {
+    const char *what = "moe_route_grad";
+    Derived v;
+    int rc = check_dims(dims, &v, what);
+    if (rc != MOE_OK) return rc;
+    if (!valid_score_fn(score_fn)) return set_error(MOE_ERR_INVALID_ARG, "%s: unknown score_fn %d", what, score_fn);
+    if ((score_fn & MOE_BIAS_SELECT_ONLY) && dbias)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: a bias for the selection alone has no gradient: dbias must be NULL", what);
+    if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
+        !aligned(dtopk_w, 4) || !aligned(dlogits, 4) || !aligned(dbias, 4))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: pointers must be 4-byte aligned", what);
+    if (v.NT == 0)  // no tokens: an empty sum
+        return dbias ? cuda_result(cudaMemsetAsync(dbias, 0, (size_t)dims->E * 4, (cudaStream_t)stream), what) : MOE_OK;
+    if (!logits || !topk_idx || !topk_w || !dtopk_w || !dlogits)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: a required pointer is NULL", what);
+    const int64_t all = v.NT * dims->E * 4;
+    const Span out = {dlogits, all}, sums = {dbias, (int64_t)dims->E * 4};
+    const Span in[] = {{logits, all}, {bias, sums.bytes}, {topk_idx, v.pairs * 4}, {topk_w, v.pairs * 4}, {dtopk_w, v.pairs * 4}};
+    const Span with_out[] = {in[0], in[1], in[2], in[3], in[4], out};
+    if (overlap_any(out, in, what, &rc) || overlap_any(sums, with_out, what, &rc)) return rc;
+    return cuda_result(launch_route_grad(logits, bias, v.NT, dims->E, dims->R, score_fn, renormalize ? 1 : 0, topk_idx,
+                                         topk_w, dtopk_w, dlogits, dbias, (cudaStream_t)stream),
+                       what);
+}
+
 int moe_selftest_bounded_wait(int32_t *status, int64_t polls, void *stream) {
     g_err[0] = '\0';
     if (!status || !aligned(status, 4))
@@ -730,7 +834,8 @@ int moe_take_device_error(void *stream) {
     g_err[0] = '\0';
     int err = 0;
     cudaError_t e = take_device_error(&err, (cudaStream_t)stream);
-    cudaError_t (*const more[])(int *) = {take_expert_gemm_error, take_expert_wgrad_error, take_expert_fp8_error};
+    cudaError_t (*const more[])(int *) = {take_expert_gemm_error, take_expert_wgrad_error, take_expert_fp8_error,
+                                        take_expert_w4_error};
     for (auto take : more) {  // the stream has been waited for
         int one = 0;
         if (e == cudaSuccess) e = take(&one);

@@ -1,0 +1,510 @@
+// Product of the experts' rows with matrices of 4-bit weights, on the layout
+// that dispatch writes:
+//
+//   y[p][f] = r[e][f] sum_k x[p][k] (s[e][k/group][f] q[e][f][k])
+//
+// q has 4 bits, s (e4m3) four significant ones: q s has at most seven and is
+// exact in bf16, which has eight.  So the weights become bf16 on the way and
+// the tensor core multiplies them exactly; r multiplies the f32 sum.
+//
+// The matrix is the operand with 128 rows of tcgen05.mma (M), read from TMEM;
+// the expert's tokens are its columns (N).  A block's warps: one loads codes
+// (TMA) and group scales, one loads the tokens (TMA), one issues mma, eight turn
+// codes into bf16 (a thread has one matrix row) and write them to TMEM, eight
+// store results.  Dequantised weights never see shared memory: there they
+// would cost 2 x 2 bytes a weight for writing and reading where the codes
+// come in at 47 a cycle from HBM, 188 bytes a cycle of the 128 it has.
+//
+// Codes to bf16: a nibble of two's complement with its top bit flipped is
+// q + 8; put under the exponent of 128 it is the bf16 number 128 + (q + 8); and
+// (128 + q + 8) s - 136 s in one multiply-add is q s exactly (136 s = 17 * 8 s
+// fits eight bits).  The elements of a word lie so that a shift and one
+// logic operation give two of them in the halves of a register: 11
+// instructions for eight weights.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "expert_w4_internal.cuh"
+#include "pdl.cuh"
+#include "tc_ops.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kM = 128;            // matrix rows of a tile
+constexpr int kTokShift = 7, kTok = 1 << kTokShift;  // most tokens of a tile
+constexpr int kK = 64;             // reduction elements of a unit: what one slot of TMEM and of token rows holds
+constexpr int kUnits = 4;          // units of a stage of codes: 256 codes, one 128-byte line of a row
+constexpr int kCodeStages = 5, kUnitSlots = 6;
+constexpr int kCodes = kM * 128, kScales = 8 * kM, kRows = kTok * 128;  // bytes of a slot
+constexpr int kDequantWarps = 8, kStoreWarps = 8;
+constexpr int kThreads = 32 * (kDequantWarps + kStoreWarps + 3);
+constexpr int kPartUnits = 512 / kK;  // units of a part of an f32 result's sum
+
+template <bool kF32>
+struct Shape {
+    static constexpr int kBuf = kF32 ? 4096 : 2048;  // a storing warp's: 32 tokens' results, to be written as whole sectors
+    static constexpr int kSmem = 1024 + kCodeStages * (kCodes + kScales) + kUnitSlots * kRows + kStoreWarps * kBuf;
+};
+
+// Token rows by boxes of 128, 64, 32 and 16 rows of 128 bytes.
+struct TokenMaps {
+    CUtensorMap m[4];
+    int first;  // the largest box that any tile of the batch can need
+};
+
+struct Args {
+    const int32_t *offsets;
+    const uint8_t *group_scales;
+    const float *row_scales;
+    void *y;
+    int64_t cap, most, pairs;
+    int E, L, K, F, wide, groups, group_shift;
+};
+
+__host__ __device__ constexpr int mma_tokens(int n) { return (n + 15) & ~15; }
+__device__ __forceinline__ int token_tiles(int count, int shift) { return (count + (1 << shift) - 1) >> shift; }
+
+struct Tile {
+    int e, m0, row, n;  // group, first matrix row (or feature), first token row, tokens
+};
+
+// Tiles of a group: its token tiles (of equal size) run fastest, so that
+// blocks working at the same time share the matrix rows through L2.
+__device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, int m_step) {
+    Tile r;
+    r.e = same(find_group(g, E, e, t));
+    const int c = same(g.count[r.e]), nt = token_tiles(c, g.shift), at = t - same(g.prefix[r.e]);
+    const int size = mma_tokens(tile_rows(c, nt));
+    const int tt = at % nt;
+    r.m0 = at / nt * m_step;
+    r.row = same(g.row[r.e]) + tt * size;
+    r.n = min(size, c - tt * size);
+    return r;
+}
+
+// 4 bytes from global to shared memory without a register; `bytes` of them are read, the others are zeros.
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Arrives on `bar` (whose count includes it) once this thread's copies so far are done.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t *r) {  // complete on return
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// D += A B, A in TMEM: lane i holds row i, a column two elements of the reduction.
+__device__ __forceinline__ void mma_bf16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// An e4m3 scale twice, as bf16 (exact).
+__device__ __forceinline__ __nv_bfloat162 scale_bf16x2(uint32_t code) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
+    const float f = __half2float(__half(h));
+    return __floats2bfloat162_rn(f, f);
+}
+
+// Eight codes as bf16 times their scale: (128 + q + 8) s - 136 s.
+__device__ __forceinline__ void dequant8(uint32_t word, __nv_bfloat162 s, __nv_bfloat162 minus, uint32_t *out) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t bits = ((word >> (4 * j)) & 0x000f000fu) ^ 0x43084308u;
+        const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&bits), s, minus);
+        out[j] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+template <bool kGated, bool kParts, bool kF32>
+__global__ void __launch_bounds__(kThreads, 1)
+expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x, const Args a) {
+    constexpr int kBuf = Shape<kF32>::kBuf;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) unsigned long long bars[2 * kCodeStages + 3 * kUnitSlots + 5];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_gave_up;
+    const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t rows_at = smem + kCodeStages * kCodes, scales_at = rows_at + kUnitSlots * kRows,
+                   bufs_at = scales_at + kCodeStages * kScales, tables_at = bufs_at + kStoreWarps * kBuf;
+    int *tables = reinterpret_cast<int *>(smem_raw + (tables_at - smem_u32(smem_raw)));
+    const uint32_t cfull = smem_u32(bars), cempty = cfull + 8 * kCodeStages, xfull = cempty + 8 * kCodeStages,
+                   afull = xfull + 8 * kUnitSlots, uempty = afull + 8 * kUnitSlots, tfull = uempty + 8 * kUnitSlots,
+                   tempty = tfull + 16, done = tempty + 16;
+    volatile int *gave_up = &s_gave_up;
+    constexpr int kStoreFirst = kDequantWarps, kCodeWarp = kDequantWarps + kStoreWarps, kRowWarp = kCodeWarp + 1,
+                  kMmaWarp = kCodeWarp + 2;
+
+    if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
+    if (tid == 0) {
+        for (int i = 0; i < kCodeStages; ++i) {
+            mb_init(cfull + 8 * i, 1 + 32);  // the loads' bytes, and the lanes that copy scales
+            mb_init(cempty + 8 * i, kDequantWarps);
+        }
+        for (int i = 0; i < kUnitSlots; ++i) {
+            mb_init(xfull + 8 * i, 1);
+            mb_init(afull + 8 * i, 4);
+            mb_init(uempty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mb_init(tfull + 8 * i, 1);
+            mb_init(tempty + 8 * i, kStoreWarps);
+        }
+        mb_init(done, 1);
+        s_gave_up = 0;
+        mb_init_fence();
+        tma_prefetch_map(&map_w);
+        for (int i = map_x.first; i < 4; ++i) tma_prefetch_map(&map_x.m[i]);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)same((int)s_tmem), a_at = tmem + 2 * kTok;
+    grid_dependency_wait();  // offsets and rows come from earlier kernels
+    grid_launch_dependents();
+    constexpr int kStep = kGated ? kM / 2 : kM;  // result columns of a tile
+    const int m_tiles = (a.F + kStep - 1) / kStep;
+    const Groups g = make_groups<kTokShift, kTokShift, 1>(
+        tables, a.offsets, a.E, a.L, a.cap, a.most, a.pairs, gridDim.x,
+        [&](int c, int shift) { return token_tiles(c, shift) * m_tiles; }, [](int) { return 0; });  // syncs the block
+    const int tiles = same(g.prefix[a.E]), units = (a.K + kK - 1) / kK;
+    const int part = kParts ? kPartUnits : units;  // units that are summed in TMEM
+
+    if (warp == kCodeWarp) {
+        Ring<kCodeStages> r;
+        int e = 0;
+        bool ok = true;
+        const int per_stage = 256 >> a.group_shift;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
+            // lanes copy the scales of four matrix rows each
+            int f = w.m0 + lane * 4;
+            bool inside = f < a.F;
+            if constexpr (kGated) {  // rows run in groups of 8 gate rows and their 8 up rows
+                f = w.m0 + lane / 4 * 8 + lane % 2 * 4;
+                inside = f < a.F;
+                f += (lane & 2) ? a.F : 0;
+            }
+            const uint8_t *scales = a.group_scales + (int64_t)w.e * a.groups * a.wide + (inside ? f : 0);
+            for (int u = 0, b = 0; u < units; u += kUnits) {
+                ok = mb_wait_warp(cempty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                if (!ok) break;
+                const uint32_t bar = cfull + 8 * r.slot;
+                if (elect_one()) {
+                    mb_expect_tx(bar, kCodes);
+                    if constexpr (kGated)
+                        tma_load_5d(smem + r.slot * kCodes, &map_w, bar, u * (kK / 2), 0, 0, w.m0 / 8, w.e);
+                    else
+                        tma_load_3d(smem + r.slot * kCodes, &map_w, bar, u * (kK / 2), w.m0, w.e);
+                }
+                __syncwarp();
+                const uint32_t to = scales_at + r.slot * kScales + lane * 4;
+                for (int i = 0; i < per_stage; ++i, ++b) {
+                    const bool there = inside && b < a.groups;
+                    copy4(to + i * kM, scales + (there ? (int64_t)b * a.wide : 0), there ? 4 : 0);
+                }
+                copy_arrive(bar);
+                r.next();
+            }
+        }
+        drain_ring(cfull, r);  // nothing may still be landing here when the block ends
+    } else if (warp == kRowWarp) {
+        Ring<kUnitSlots> r;
+        int e = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
+            const int n = mma_tokens(w.n);
+            for (int u = 0; u < units; ++u) {
+                ok = mb_wait_warp(uempty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t bar = xfull + 8 * r.slot;
+                    mb_expect_tx(bar, n * 128);
+                    uint32_t dst = rows_at + r.slot * kRows;
+                    int row = w.row;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int box = 128 >> i;
+                        if (n & box) {
+                            tma_load_2d(dst, &map_x.m[i], bar, u * kK, row);
+                            dst += box * 128;
+                            row += box;
+                        }
+                    }
+                }
+                __syncwarp();
+                r.next();
+            }
+        }
+        drain_ring(xfull, r);
+    } else if (warp == kMmaWarp) {
+        Ring<kUnitSlots> r;
+        Ring<2> acc;
+        int e = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
+            const uint32_t desc = mma_desc(1, false, false, kM, mma_tokens(w.n));
+            for (int u0 = 0; u0 < units && ok; u0 += part) {
+                const uint32_t d = tmem + acc.slot * kTok;
+                ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
+                for (int u = u0; u < min(u0 + part, units) && ok; ++u) {
+                    ok = mb_wait_warp(xfull + 8 * r.slot, r.phase, gave_up) &&
+                         mb_wait_warp(afull + 8 * r.slot, r.phase, gave_up);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t db = smem_operand(rows_at + r.slot * kRows, 16, 1024);
+                        const uint32_t da = a_at + r.slot * (kK / 2);
+#pragma unroll
+                        for (int i = 0; i < kK / 16; ++i)
+                            mma_bf16_tmem(d, da + i * 8, db + i * 2, desc, u != u0 || i != 0);
+                        tc_commit(uempty + 8 * r.slot);
+                    }
+                    __syncwarp();
+                    r.next();
+                }
+                if (elect_one()) tc_commit(tfull + 8 * acc.slot);
+                __syncwarp();
+                acc.next();
+            }
+        }
+        if (elect_one()) tc_commit(done);  // after every arrival before it
+        __syncwarp();
+        mb_drain(done, 0);
+    } else if (warp < kDequantWarps) {
+        // A thread has one matrix row; the two sets of four warps take units by turns.
+        const int quarter = warp & 3, set = warp >> 2, row = quarter * 32 + lane;
+        const uint32_t line = smem + row * 128, at = a_at + ((uint32_t)(quarter * 32) << 16);
+        Ring<kCodeStages> c;
+        Ring<kUnitSlots> r;
+        bool ok = true;
+        int turn = 0;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int u0 = 0; u0 < units && ok; u0 += kUnits) {
+                ok = mb_wait_warp(cfull + 8 * c.slot, c.phase, gave_up);
+                if (!ok) break;
+                const uint32_t codes = line + c.slot * kCodes, scales = scales_at + c.slot * kScales + row;
+                const int n = min(kUnits, units - u0);
+                for (int i = 0; i < n; ++i, turn ^= 1, r.next()) {
+                    if (turn != set) continue;
+                    uint32_t out[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // 32 codes: 16 bytes, one group's
+                        const int chunk = 2 * i + h;
+                        const uint4 q = ld_shared128(codes + ((chunk ^ (row & 7)) << 4));
+                        const __nv_bfloat162 s = scale_bf16x2(ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM));
+                        const __nv_bfloat162 minus = __hmul2(s, __floats2bfloat162_rn(-136.f, -136.f));
+                        dequant8(q.x, s, minus, out + 16 * h);
+                        dequant8(q.y, s, minus, out + 16 * h + 4);
+                        dequant8(q.z, s, minus, out + 16 * h + 8);
+                        dequant8(q.w, s, minus, out + 16 * h + 12);
+                    }
+                    ok = mb_wait_warp(uempty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                    if (!ok) break;
+                    tc_fence_after();
+                    tmem_store32(at + r.slot * (kK / 2), out);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(afull + 8 * r.slot);
+                }
+                __syncwarp();
+                if (lane == 0) mb_arrive(cempty + 8 * c.slot);
+                c.next();
+            }
+        }
+    } else {
+        // Results: warp w holds matrix rows 32 (w % 4).. of the tile, one per lane, and every other 32 tokens.
+        const int quarter = warp & 3, half = (warp - kStoreFirst) >> 2;
+        const uint32_t buf = bufs_at + (warp - kStoreFirst) * kBuf;
+        const int fl = kGated ? (lane >> 4) * 8 + (lane & 7) : lane, up = (lane >> 3) & 1;
+        auto store = [&](const Tile &w, int c0, float scale, auto v) {
+            const int left = w.n - c0;
+            if constexpr (kF32) {  // one token's 32 features are 128 bytes
+#pragma unroll
+                for (int j = 0; j < 32; ++j) st_shared32(buf + j * 128 + lane * 4, __float_as_uint(v(j) * scale));
+                __syncwarp();
+                const int f = w.m0 + quarter * 32 + lane % 8 * 4;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int tok = q * 4 + lane / 8;
+                    const uint4 o = ld_shared128(buf + q * 512 + lane * 16);
+                    if (tok < left && f < a.F)
+                        *reinterpret_cast<uint4 *>(static_cast<float *>(a.y) + (int64_t)(w.row + c0 + tok) * a.F + f) = o;
+                }
+            } else if constexpr (kGated) {
+                // lanes with bit 3 clear hold gate rows, the others the up
+                // rows of the same features; of a pair of tokens each half of
+                // the lanes finishes one
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float first = v(j) * scale, second = v(j + 1) * scale;
+                    const float got = __shfl_xor_sync(0xffffffffu, up ? first : second, 8);
+                    const float h = silu_mul(up ? got : first, up ? second : got);
+                    st_shared16(buf + (j + up) * 32 + fl * 2, bf16x2(__float_as_uint(h), 0u));
+                }
+                __syncwarp();
+                const int f = w.m0 + quarter * 16 + (lane & 1) * 8;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = i * 16 + lane / 2;
+                    const uint4 o = ld_shared128(buf + i * 512 + lane * 16);
+                    if (tok < left && f < a.F)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + (int64_t)(w.row + c0 + tok) * a.F + f) = o;
+                }
+            } else {  // one token's 32 features are 64 bytes
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const uint32_t two = bf16x2(__float_as_uint(v(j) * scale), __float_as_uint(v(j + 1) * scale));
+                    st_shared16(buf + j * 64 + lane * 2, two);
+                    st_shared16(buf + (j + 1) * 64 + lane * 2, two >> 16);
+                }
+                __syncwarp();
+                const int f = w.m0 + quarter * 32 + lane % 4 * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = i * 8 + lane / 4;
+                    const uint4 o = ld_shared128(buf + i * 512 + lane * 16);
+                    if (tok < left && f < a.F)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + (int64_t)(w.row + c0 + tok) * a.F + f) = o;
+                }
+            }
+            __syncwarp();
+        };
+        Ring<2> acc;
+        int e = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const Tile w = get_tile(g, a.E, e, t, kStep);
+            e = w.e;
+            const int f = w.m0 + quarter * (kGated ? 16 : 32) + fl;
+            const float scale =
+                f < a.F ? __ldg(a.row_scales + (int64_t)w.e * a.wide + f + (kGated && up ? a.F : 0)) : 0.f;
+            const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + 32 * half;
+            if constexpr (kParts) {
+                float sum[2][32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
+                for (int u0 = 0; u0 < units; u0 += part) {
+                    ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + part * kStepPolls);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (64 * i + 32 * half < w.n) {
+                            uint32_t v[32];
+                            tmem_load32(src + acc.slot * kTok + 64 * i, v);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(v[j]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(tempty + 8 * acc.slot);
+                    acc.next();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (64 * i + 32 * half < w.n) store(w, 64 * i + 32 * half, scale, [&](int j) { return sum[i][j]; });
+                }
+            } else {  // straight from TMEM
+                ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + units * kStepPolls);
+                if (!ok) break;
+                tc_fence_after();
+                for (int c0 = 0; 32 * half + c0 < w.n; c0 += 64) {
+                    uint32_t v[32];
+                    tmem_load32(src + acc.slot * kTok + c0, v);
+                    store(w, c0 + 32 * half, scale, [&](int j) { return __uint_as_float(v[j]); });
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mb_arrive(tempty + 8 * acc.slot);
+                acc.next();
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && s_gave_up) record_timeout();
+    if (warp == kMmaWarp) tmem_free(tmem, 512);
+}
+
+template <bool kGated, bool kParts, bool kF32>
+cudaError_t launch(const CUtensorMap &map_w, const TokenMaps &map_x, const Args &a, cudaStream_t stream) {
+    auto kern = expert_w4_kernel<kGated, kParts, kF32>;
+    static thread_local AttrCache attr;
+    cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), Shape<kF32>::kSmem + groups_bytes(1024));
+    if (e != cudaSuccess) return e;
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    cudaLaunchAttribute pdl[1] = {pdl_attribute()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Shape<kF32>::kSmem + groups_bytes(a.E);
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, a);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, int group, const void *x,
+                                  const void *wq, const void *group_scales, const float *row_scales, void *y, int y_f32,
+                                  cudaStream_t stream) {
+    CUtensorMap map_w;
+    TokenMaps map_x;
+    const uint64_t line = (uint64_t)K / 2;  // bytes of a matrix row's codes
+    if (gated) {  // per feature block of 8: 8 gate rows, then its 8 up rows
+        const uint64_t dims[5] = {line, 8, 2, (uint64_t)F / 8, (uint64_t)r.E};
+        const uint64_t strides[4] = {line, line * F, line * 8, line * F * 2};
+        const uint32_t box[5] = {128, 8, 2, kM / 16, 1};
+        if (!encode_map(&map_w, 1, 5, wq, dims, strides, box)) return cudaErrorInvalidValue;
+    } else {
+        const uint64_t dims[3] = {line, (uint64_t)F, (uint64_t)r.E};
+        const uint64_t strides[2] = {line, line * F};
+        const uint32_t box[3] = {128, kM, 1};
+        if (!encode_map(&map_w, 1, 3, wq, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    const int64_t tok = r.most < kTok ? mma_tokens((int)r.most) : kTok;
+    map_x.first = tok > 112 ? 0 : tok > 48 ? 1 : tok > 16 ? 2 : 3;
+    const uint64_t dims[2] = {(uint64_t)K, (uint64_t)r.rows_total}, stride = (uint64_t)K * 2;
+    for (int i = map_x.first; i < 4; ++i) {
+        const uint32_t box[2] = {kK, 128u >> i};
+        if (!encode_map(&map_x.m[i], 0, 2, x, dims, &stride, box)) return cudaErrorInvalidValue;
+    }
+    int shift = 5;
+    while ((1 << shift) < group) ++shift;
+    const Args a{r.offsets, static_cast<const uint8_t *>(group_scales), row_scales, y, r.cap, r.most, r.pairs,
+                 r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift};
+    const bool parts = K > kWhole;
+    if (gated) return parts ? launch<true, true, false>(map_w, map_x, a, stream) : launch<true, false, false>(map_w, map_x, a, stream);
+    if (y_f32) return launch<false, true, true>(map_w, map_x, a, stream);
+    return parts ? launch<false, true, false>(map_w, map_x, a, stream) : launch<false, false, false>(map_w, map_x, a, stream);
+}
+
+cudaError_t take_expert_w4_error(int *err) { return take_tc_error(err); }
+
+}  // namespace moe

@@ -1,0 +1,268 @@
+// Gradient of the router's weights with respect to its logits, one warp per
+// token, and the sum over the tokens that a bias gets.
+//
+// With h the gradient of the weights w and d = sum_k h_k w_k:
+//   softmax                dz_e = p_e (h_e - d): every logit is read
+//   softmax, renormalised  the weights are a softmax of the chosen logits alone,
+//                          so dz_e = w_k (h_k - d) and no logit is read
+//   sigmoid                ds/dz = s (1 - s), 1 - s = 1 / (1 + exp(z)) without
+//                          cancellation; renormalised, the other chosen scores
+//                          take d off: dz_e = w_k (1 - s_e) (h_k - d)
+// All but the first have at most R entries a row: the warp writes the row's
+// zeros, then (ordered by __syncwarp) its lanes k < R write their entries, both
+// into lines that are still in L2.
+#include <math.h>
+
+#include "grad_internal.cuh"
+#include "mem_ops.cuh"
+#include "pdl.cuh"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kThreads = 256;  // 8 tokens per block
+constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+// What lane k < R knows of the token's k-th expert.
+struct Choice {
+    int e;       // -1: no part
+    float w, h;  // weight and its gradient, 0 without a part
+    float d;     // sum of h w over the token
+};
+__device__ __forceinline__ Choice load_choice(const int32_t *__restrict__ idx, const float *__restrict__ w,
+                                              const float *__restrict__ dw, int64_t g, int E, int R, int lane) {
+    Choice c{-1, 0.f, 0.f, 0.f};
+    if (lane < R) {
+        const int e = __ldg(idx + g * R + lane);
+        if (e >= 0 && e < E) {
+            c.e = e;
+            c.w = __ldg(w + g * R + lane);
+            c.h = __ldg(dw + g * R + lane);
+        }
+    }
+    c.d = warp_sum(c.h * c.w);
+    return c;
+}
+
+// Sum of v over the lanes that name the same expert, in every one of them, in
+// lane order; without repeated experts (as the router chooses them) v itself.
+__device__ __forceinline__ float sum_same(int e, float v, int lane) {
+    const unsigned alike = __match_any_sync(kFull, e < 0 ? -1 - lane : e);
+    if (__any_sync(kFull, (alike & (alike - 1)) != 0)) {
+        float s = 0.f;
+        for (int k = 0; k < 32; ++k) {
+            const float o = __shfl_sync(kFull, v, k);
+            if ((alike >> k) & 1u) s += o;
+        }
+        v = s;
+    }
+    return v;
+}
+
+// Entries at the chosen experts only.
+template <bool kVec4>
+__global__ void __launch_bounds__(kThreads)
+route_grad_chosen_kernel(const float *__restrict__ logits, const float *__restrict__ bias, int64_t NT, int E, int R,
+                         int sigmoid, int renormalize, const int32_t *__restrict__ idx, const float *__restrict__ w,
+                         const float *__restrict__ dw, float *__restrict__ dlogits) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t g = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (g >= NT) return;  // uniform per warp
+    const Choice c = load_choice(idx, w, dw, g, E, R, lane);
+    float at = c.w * (renormalize ? c.h - c.d : c.h);
+    if (sigmoid && c.e >= 0) {
+        float z = __ldg(logits + g * E + c.e);
+        if (bias != nullptr) z = __fadd_rn(z, __ldg(bias + c.e));
+        at = at / (1.0f + expf(z));
+    }
+    at = sum_same(c.e, at, lane);
+    float *row = dlogits + g * E;
+    if (kVec4) {
+        for (int e = lane * 4; e < E; e += 128) *reinterpret_cast<float4 *>(row + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+        for (int e = lane; e < E; e += 32) row[e] = 0.f;
+    }
+    __syncwarp();
+    if (c.e >= 0) row[c.e] = at;
+}
+
+// Softmax over all experts: lane l holds J of them, four in a row at a time.
+template <int J, bool kVec4>
+__global__ void __launch_bounds__(kThreads)
+route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restrict__ bias, int64_t NT, int E, int R,
+                          const int32_t *__restrict__ idx, const float *__restrict__ w, const float *__restrict__ dw,
+                          float *__restrict__ dlogits) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t g = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (g >= NT) return;  // uniform per warp
+    const float *row = logits + g * E;
+    constexpr int kRun = kVec4 ? 4 : 1;
+    auto expert = [&](int j) { return (j / kRun * 32 + lane) * kRun + j % kRun; };
+    float z[J];
+#pragma unroll
+    for (int j = 0; j < J; j += kRun) {
+        const int e = expert(j);
+        if constexpr (kVec4) {
+            const float4 v = e < E ? __ldg(reinterpret_cast<const float4 *>(row + e))
+                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            z[j] = v.x, z[j + 1] = v.y, z[j + 2] = v.z, z[j + 3] = v.w;
+        } else {
+            z[j] = e < E ? __ldg(row + e) : -INFINITY;
+        }
+    }
+    const Choice c = load_choice(idx, w, dw, g, E, R, lane);
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        if (bias != nullptr && expert(j) < E) z[j] = __fadd_rn(z[j], __ldg(bias + expert(j)));
+        top = fmaxf(top, z[j]);
+    }
+    top = warp_max(top);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        z[j] = expf(__fsub_rn(z[j], top));
+        sum += expert(j) < E ? z[j] : 0.f;
+    }
+    sum = warp_sum(sum);
+    const bool none = top == -INFINITY;  // nothing to choose from: zeros
+    const float scale = none ? 0.f : 1.0f / sum, d = none ? 0.f : c.d;
+    float *out = dlogits + g * E;
+#pragma unroll
+    for (int j = 0; j < J; j += kRun) {
+        const int e = expert(j);
+        if (e >= E) continue;
+        if constexpr (kVec4) {
+            float4 v = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+            v.x = none ? 0.f : -(v.x * scale * d), v.y = none ? 0.f : -(v.y * scale * d);
+            v.z = none ? 0.f : -(v.z * scale * d), v.w = none ? 0.f : -(v.w * scale * d);
+            *reinterpret_cast<float4 *>(out + e) = v;
+        } else {
+            out[e] = none ? 0.f : -(z[j] * scale * d);
+        }
+    }
+    const float h = sum_same(c.e, c.h, lane);
+    __syncwarp();
+    if (c.e >= 0 && !none) {
+        float zc = __ldg(row + c.e);
+        if (bias != nullptr) zc = __fadd_rn(zc, __ldg(bias + c.e));
+        out[c.e] = expf(__fsub_rn(zc, top)) * scale * (h - d);
+    }
+}
+
+// ---- bias ------------------------------------------------------------------
+
+// dbias[e] = sum over the tokens of dlogits[g][e]: a cluster of kCluster blocks
+// takes 32 columns, its rows dealt out to the blocks' warps; a thread adds
+// kRun values in f32, those sums in 64 bits, and the first block adds the
+// others' in their order.
+constexpr int kCluster = 8;
+constexpr int kRunRows = 16;
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+column_sum_kernel(const float *__restrict__ d, int64_t NT, int E, float *__restrict__ dbias) {
+    __shared__ double part[kWarps][32];
+    __shared__ double total[32];
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = (int)(blockIdx.x / kCluster) * 32 + lane;
+    grid_dependency_wait();  // d comes from the kernel before
+    grid_launch_dependents();
+    double sum = 0.0;
+    if (e < E) {
+        const int64_t step = kCluster * kWarps;
+        for (int64_t g = rank * kWarps + warp; g < NT; g += step * kRunRows) {
+            float run = 0.f;
+#pragma unroll
+            for (int i = 0; i < kRunRows; ++i) {
+                const int64_t r = g + i * step;
+                run += r < NT ? __ldg(d + r * E + e) : 0.f;
+            }
+            sum += run;
+        }
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        double t = 0.0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) t += part[i][lane];
+        total[lane] = t;
+    }
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    if (rank == 0 && warp == 0) {
+        double t = 0.0;
+        const uint32_t here = (uint32_t)__cvta_generic_to_shared(&total[lane]);
+        for (int i = 0; i < kCluster; ++i) {
+            uint32_t there;
+            double v;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(i));
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(there) : "memory");
+            t += v;
+        }
+        if (e < E) dbias[e] = (float)t;
+    }
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");  // totals are read
+}
+
+struct Launch {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = {};
+    Launch(int64_t blocks, cudaStream_t stream) {
+        attr[0] = pdl_attribute();
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    Launch(const Launch &) = delete;
+};
+
+}  // namespace
+
+cudaError_t launch_route_grad(const float *logits, const float *bias, int64_t NT, int E, int R, int score_fn,
+                              int renormalize, const int32_t *topk_idx, const float *topk_w, const float *dtopk_w,
+                              float *dlogits, float *dbias, cudaStream_t stream) {
+    const bool softmax = (score_fn & ~MOE_BIAS_SELECT_ONLY) == MOE_SOFTMAX;
+    if (score_fn & MOE_BIAS_SELECT_ONLY) bias = nullptr;  // the scores are the raw logits'
+    auto at16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    Launch l((NT + kWarps - 1) / kWarps, stream);
+    cudaError_t e = cudaSuccess;
+    if (softmax && !renormalize) {
+        const bool vec = E % 4 == 0 && at16(logits) && at16(dlogits);
+        const int need = (E + 31) / 32;
+        auto launch = [&](auto kern) {
+            return cudaLaunchKernelEx(&l.cfg, kern, logits, bias, NT, E, R, topk_idx, topk_w, dtopk_w, dlogits);
+        };
+#define MOE_CASE(J) need <= J ? launch(vec ? route_grad_softmax_kernel<J, true> : route_grad_softmax_kernel<J, false>)
+        e = MOE_CASE(4) : MOE_CASE(8) : MOE_CASE(16) : MOE_CASE(32) : cudaErrorInvalidValue;
+#undef MOE_CASE
+    } else {
+        const bool vec = E % 4 == 0 && at16(dlogits);
+        e = cudaLaunchKernelEx(&l.cfg, vec ? route_grad_chosen_kernel<true> : route_grad_chosen_kernel<false>, logits, bias,
+                               NT, E, R, softmax ? 0 : 1, renormalize, topk_idx, topk_w, dtopk_w, dlogits);
+    }
+    if (e != cudaSuccess || dbias == nullptr) return e;
+    Launch s((E + 31) / 32 * kCluster, stream);
+    return cudaLaunchKernelEx(&s.cfg, column_sum_kernel, static_cast<const float *>(dlogits), NT, E, dbias);
+}
+
+}  // namespace moe

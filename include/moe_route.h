@@ -408,9 +408,11 @@ const char *moe_last_error(void);
  * zero-filled once by the caller (no clearing inside the call) and may be
  * NULL for an empty batch; R up to 32 in the fused dispatch.
  * 1.3: the experts' products (moe_expert.h).
+ * 1.4: the routing steps' gradients (moe_grad.h), the experts' product with
+ * 4-bit weights (moe_expert_w4.h).
  * A caller can compare MOE_VERSION (the header it was built against) with
  * moe_version() (the library it loaded). */
-#define MOE_VERSION 10300
+#define MOE_VERSION 10400
 int moe_version(void);
 
 #ifdef __cplusplus

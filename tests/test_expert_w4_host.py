@@ -1,0 +1,129 @@
+"""Host-side checks of the experts' product with 4-bit weights: exports, refusals, the weights' form.  Nothing is launched."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import combine_moe_route_topk_gb300 as moe
+from combine_moe_route_topk_gb300 import _build
+from conftest import ROOT
+
+INVALID, UNSUPPORTED = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED
+LINEAR, SWIGLU = moe.MOE_EXPERT_LINEAR, moe.MOE_EXPERT_SWIGLU
+NAMES = ["x", "wq", "group_scales", "row_scales", "expert_offsets", "y"]
+
+
+def at(i, off=0):  # apart from each other, never dereferenced on the host
+    return ctypes.c_void_p(0x10000000 * (i + 1) + off)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return moe.lib()
+
+
+def _dims(**kw):
+    return moe.make_dims(**{**dict(N=2, T=8, E=4, R=2, H=8, cap_rows=16), **kw})
+
+
+def _call(lib, d=None, K=128, F=128, act=LINEAR, group=32, **kw):
+    p = [kw.get(n, at(i)) for i, n in enumerate(NAMES)]
+    return lib.moe_expert_gemm_w4(ctypes.byref(d if d is not None else _dims()), K, F, act, group, *p, None)
+
+
+def test_library_exports_every_declared_symbol(lib):
+    text = open(os.path.join(ROOT, "include", "moe_expert_w4.h")).read()
+    names = set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", re.sub(r"/\*.*?\*/", "", text, flags=re.S)))
+    assert names == {"moe_expert_gemm_w4"} and hasattr(lib, "moe_expert_gemm_w4")
+
+
+@pytest.mark.parametrize("act", [LINEAR, SWIGLU])
+def test_bad_arguments_are_refused(lib, act):
+    for kw, code, msg in [
+            (dict(F=0), INVALID, "multiples of 8"), (dict(F=132), INVALID, "multiples of 8"),
+            (dict(K=0), INVALID, "multiples of 8"), (dict(K=48), INVALID, "multiple of group"),
+            (dict(K=192, group=128), INVALID, "multiple of group"), (dict(group=0), INVALID, "group must be"),
+            (dict(group=-32), INVALID, "group must be"), (dict(group=16), INVALID, "group must be"),
+            (dict(group=256, K=256), INVALID, "group must be"), (dict(F=(1 << 24) + 8), UNSUPPORTED, "2^24"),
+            (dict(K=(1 << 24) + 32), UNSUPPORTED, "2^24"), (dict(d=_dims(E=5)), INVALID, "multiple of N"),
+            (dict(d=_dims(N=1, cap_rows=(1 << 31) - 65536)), UNSUPPORTED, "65536")]:
+        assert _call(lib, act=act, **kw) == code, kw
+        assert msg in lib.moe_last_error().decode(), kw
+    assert _call(lib, act=2) == INVALID and "act" in lib.moe_last_error().decode()
+
+
+def test_missing_misaligned_and_overlapping_arrays_are_refused(lib):
+    for i, n in enumerate(NAMES):
+        assert _call(lib, **{n: None}) == INVALID, n
+        off = 8 if n in ("x", "wq", "y") else 2
+        assert _call(lib, **{n: at(i, off)}) == INVALID, n
+        assert "aligned" in lib.moe_last_error().decode()
+        if n != "y":
+            for o in (0, 16):
+                for act in (LINEAR, SWIGLU):
+                    assert _call(lib, act=act, y=at(i, o)) == INVALID, n
+                    assert "overlaps" in lib.moe_last_error().decode()
+
+
+def test_an_empty_batch_is_accepted_without_buffers(lib):
+    for act in (LINEAR, SWIGLU):
+        assert _call(lib, d=_dims(T=0), act=act, x=None, wq=None, group_scales=None, row_scales=None, y=None) == moe.MOE_OK
+
+
+def test_binding_refuses_cpu_tensors_and_other_types():
+    d = moe.make_dims(1, 1, 1, 1, 8)
+    with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+        moe.expert_gemm_w4(d, 32, 8, LINEAR, 32, torch.zeros(1, 32, dtype=torch.bfloat16), None, None, None, None, None)
+
+
+def unpack(words):
+    """The header's layout, word by word."""
+    out = []
+    for word in words.flatten().tolist():
+        for i in range(8):
+            v = (word >> (4 * (i // 2) + 16 * (i % 2))) & 15
+            out.append(v - 16 if v > 7 else v)
+    return torch.tensor(out).view(*words.shape[:-1], -1)
+
+
+def test_words_hold_their_elements():
+    g = torch.Generator()
+    g.manual_seed(1)
+    q = torch.randint(-8, 8, (3, 5, 64), generator=g, dtype=torch.int8)
+    words = moe.pack_w4(q)
+    assert words.dtype == torch.int32 and words.shape == (3, 5, 8)
+    assert torch.equal(unpack(words), q.long())
+    one = torch.zeros(8, dtype=torch.int32)
+    one[5] = -1  # element 2j + 1, j = 2: bit 16 + 8
+    assert int(moe.pack_w4(one)) & 0xFFFFFFFF == 0xF << 24
+    for bad in (q.float(), q[..., :12], q.to(torch.int32) + 8):
+        with pytest.raises(ValueError):
+            moe.pack_w4(bad)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_quantised_weights_are_near(group):
+    g = torch.Generator()
+    g.manual_seed(2)
+    w = torch.randn(2, 24, 256, generator=g) * torch.rand(2, 24, 1, generator=g)
+    w[0, 3] = 0  # a row of zeros, a group of zeros, one that is tiny beside the others
+    w[1, 5, :group] = 0
+    w[1, 6, :group] *= 1e-9
+    wq, gs, rs = moe.quantize_w4(w.to(torch.bfloat16), group)
+    assert wq.shape == (2, 24, 32) and gs.shape == (2, 256 // group, 24) and rs.shape == (2, 24)
+    step = gs.view(torch.float8_e4m3fn).double().transpose(1, 2) * rs.double().unsqueeze(2)  # [E][W][groups]
+    got = unpack(wq).double().view(2, 24, -1, group) * step.unsqueeze(3)
+    w = w.to(torch.bfloat16).double().view(2, 24, -1, group)
+    amax = w.abs().amax(3, keepdim=True)
+    assert torch.isfinite(got).all() and bool((got[0, 3] == 0).all()) and bool((got[1, 5, 0] == 0).all())
+    # half a step, or what the clamp at -8 and 7 takes off: a scale rounded down by 2^-4 leaves 7 / (1 - 2^-4) = 7.47,
+    # cut to 7; a scale below the smallest one is zero or up to twice too large
+    lim = torch.maximum(0.5 * step, amax.squeeze(3) / 14.9) * (1 + 1e-5)
+    lim[1, 6, 0] = amax[1, 6, 0, 0]
+    assert bool(((got - w).abs() <= lim.unsqueeze(3)).all())
+    for bad in (w[0, 0], torch.zeros(1, 8, 48)):
+        with pytest.raises(ValueError):
+            moe.quantize_w4(bad, group)
