@@ -33,16 +33,21 @@ namespace {
 
 constexpr int kM = 128;            // matrix rows of a tile
 constexpr int kTokShift = 7, kTok = 1 << kTokShift;  // most tokens of a tile
-constexpr int kK = 64;             // reduction elements of a unit: what one slot of TMEM and of token rows holds
-constexpr int kUnits = 4;          // units of a stage of codes: 256 codes, one 128-byte line of a row
-constexpr int kCodeStages = 5, kUnitSlots = 6;
-constexpr int kCodes = kM * 128, kScales = 8 * kM, kRows = kTok * 128;  // bytes of a slot
-constexpr int kDequantWarps = 8, kStoreWarps = 8;
-constexpr int kThreads = 32 * (kDequantWarps + kStoreWarps + 3);
+constexpr int kK = 128;            // reduction elements of a unit: what one slot of TMEM and of token rows holds
+constexpr int kUnits = 2;          // units of a stage of codes: 256 codes, one 128-byte line of a row
+constexpr int kUnitSlots = 4;
+constexpr int kCodes = kM * 128, kScales = 8 * kM, kHalfRows = kTok * 128, kRows = 2 * kHalfRows;  // bytes of a slot
+constexpr int kStoreWarps = 8;
 constexpr int kPartUnits = 512 / kK;  // units of a part of an f32 result's sum
 
-template <bool kF32>
+// For sums in parts the storing warps hold them in registers: 768 threads are
+// launched with 80 each, the storing ones take 120, the dequantising ones keep 64,
+// the others (with an idle warp, so that they are four) 40.
+template <bool kParts, bool kF32>
 struct Shape {
+    static constexpr int kSets = kParts ? 3 : 4, kDequantWarps = 4 * kSets;  // sets of four warps that dequantise units by turns
+    static constexpr int kThreads = 32 * (kDequantWarps + kStoreWarps + (kParts ? 4 : 3));
+    static constexpr int kCodeStages = kF32 ? 3 : 4;
     static constexpr int kBuf = kF32 ? 4096 : 2048;  // a storing warp's: 32 tokens' results, to be written as whole sectors
     static constexpr int kSmem = 1024 + kCodeStages * (kCodes + kScales) + kUnitSlots * kRows + kStoreWarps * kBuf;
 };
@@ -92,13 +97,16 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t *r) {  // complete on return
+// 32 lanes x 16 columns of 32 bits; done after tmem_store_wait.
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t *r) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D += A B, A in TMEM: lane i holds row i, a column two elements of the reduction.
 __device__ __forceinline__ void mma_bf16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool accumulate) {
@@ -128,9 +136,10 @@ __device__ __forceinline__ void dequant8(uint32_t word, __nv_bfloat162 s, __nv_b
 }
 
 template <bool kGated, bool kParts, bool kF32>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<kParts, kF32>::kThreads, 1)
 expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x, const Args a) {
-    constexpr int kBuf = Shape<kF32>::kBuf;
+    using S = Shape<kParts, kF32>;
+    constexpr int kBuf = S::kBuf, kCodeStages = S::kCodeStages, kDequantWarps = S::kDequantWarps;
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) unsigned long long bars[2 * kCodeStages + 3 * kUnitSlots + 5];
     __shared__ uint32_t s_tmem;
@@ -181,6 +190,11 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         [&](int c, int shift) { return token_tiles(c, shift) * m_tiles; }, [](int) { return 0; });  // syncs the block
     const int tiles = same(g.prefix[a.E]), units = (a.K + kK - 1) / kK;
     const int part = kParts ? kPartUnits : units;  // units that are summed in TMEM
+
+    if constexpr (kParts) {
+        if (warp < kDequantWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else if (warp >= kCodeWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    }
 
     if (warp == kCodeWarp) {
         Ring<kCodeStages> r;
@@ -234,7 +248,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t bar = xfull + 8 * r.slot;
-                    mb_expect_tx(bar, n * 128);
+                    mb_expect_tx(bar, 2 * n * 128);
                     uint32_t dst = rows_at + r.slot * kRows;
                     int row = w.row;
 #pragma unroll
@@ -242,6 +256,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                         const int box = 128 >> i;
                         if (n & box) {
                             tma_load_2d(dst, &map_x.m[i], bar, u * kK, row);
+                            tma_load_2d(dst + kHalfRows, &map_x.m[i], bar, u * kK + kK / 2, row);
                             dst += box * 128;
                             row += box;
                         }
@@ -274,7 +289,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                         const uint32_t da = a_at + r.slot * (kK / 2);
 #pragma unroll
                         for (int i = 0; i < kK / 16; ++i)
-                            mma_bf16_tmem(d, da + i * 8, db + i * 2, desc, u != u0 || i != 0);
+                            mma_bf16_tmem(d, da + i * 8, db + (i / 4 * (kHalfRows / 16) + i % 4 * 2), desc, u != u0 || i != 0);
                         tc_commit(uempty + 8 * r.slot);
                     }
                     __syncwarp();
@@ -289,7 +304,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         __syncwarp();
         mb_drain(done, 0);
     } else if (warp < kDequantWarps) {
-        // A thread has one matrix row; the two sets of four warps take units by turns.
+        // A thread has one matrix row; the sets of four warps take units by turns.
         const int quarter = warp & 3, set = warp >> 2, row = quarter * 32 + lane;
         const uint32_t line = smem + row * 128, at = a_at + ((uint32_t)(quarter * 32) << 16);
         Ring<kCodeStages> c;
@@ -298,39 +313,53 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         int turn = 0;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             for (int u0 = 0; u0 < units && ok; u0 += kUnits) {
+                const int n = min(kUnits, units - u0);
+                int mine = set - turn;  // this set's unit of the stage, if it has one
+                mine += mine < 0 ? S::kSets : 0;
+                turn = (turn + n) % S::kSets;
+                // a set without a unit waits as well: its arrival must not run ahead into the slot's next use
                 ok = mb_wait_warp(cfull + 8 * c.slot, c.phase, gave_up);
                 if (!ok) break;
-                const uint32_t codes = line + c.slot * kCodes, scales = scales_at + c.slot * kScales + row;
-                const int n = min(kUnits, units - u0);
-                for (int i = 0; i < n; ++i, turn ^= 1, r.next()) {
-                    if (turn != set) continue;
-                    uint32_t out[32];
+                if (mine < n) {
+                    for (int i = 0; i < mine; ++i) r.next();
+                    const uint32_t codes = line + c.slot * kCodes, scales = scales_at + c.slot * kScales + row;
+                    const uint32_t to = at + r.slot * (kK / 2);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // 32 codes: 16 bytes, one group's
-                        const int chunk = 2 * i + h;
+                    for (int h = 0; h < kK / 32; ++h) {  // 32 codes: 16 bytes, of one group
+                        const int chunk = mine * (kK / 32) + h;
                         const uint4 q = ld_shared128(codes + ((chunk ^ (row & 7)) << 4));
                         const __nv_bfloat162 s = scale_bf16x2(ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM));
                         const __nv_bfloat162 minus = __hmul2(s, __floats2bfloat162_rn(-136.f, -136.f));
-                        dequant8(q.x, s, minus, out + 16 * h);
-                        dequant8(q.y, s, minus, out + 16 * h + 4);
-                        dequant8(q.z, s, minus, out + 16 * h + 8);
-                        dequant8(q.w, s, minus, out + 16 * h + 12);
+                        uint32_t out[16];
+                        dequant8(q.x, s, minus, out);
+                        dequant8(q.y, s, minus, out + 4);
+                        dequant8(q.z, s, minus, out + 8);
+                        dequant8(q.w, s, minus, out + 12);
+                        if (h == 0) {
+                            ok = mb_wait_warp(uempty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        tmem_store16(to + h * 16, out);
                     }
-                    ok = mb_wait_warp(uempty + 8 * r.slot, r.phase ^ 1u, gave_up);
                     if (!ok) break;
-                    tc_fence_after();
-                    tmem_store32(at + r.slot * (kK / 2), out);
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(cempty + 8 * c.slot);  // the codes are in registers or TMEM
+                    tmem_store_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mb_arrive(afull + 8 * r.slot);
+                    for (int i = mine; i < n; ++i) r.next();
+                } else {
+                    for (int i = 0; i < n; ++i) r.next();
+                    if (lane == 0) mb_arrive(cempty + 8 * c.slot);
                 }
-                __syncwarp();
-                if (lane == 0) mb_arrive(cempty + 8 * c.slot);
                 c.next();
             }
         }
-    } else {
+    } else if (warp < kCodeWarp) {
         // Results: warp w holds matrix rows 32 (w % 4).. of the tile, one per lane, and every other 32 tokens.
+        if constexpr (kParts) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int quarter = warp & 3, half = (warp - kStoreFirst) >> 2;
         const uint32_t buf = bufs_at + (warp - kStoreFirst) * kBuf;
         const int fl = kGated ? (lane >> 4) * 8 + (lane & 7) : lane, up = (lane >> 3) & 1;
@@ -454,15 +483,15 @@ template <bool kGated, bool kParts, bool kF32>
 cudaError_t launch(const CUtensorMap &map_w, const TokenMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_w4_kernel<kGated, kParts, kF32>;
     static thread_local AttrCache attr;
-    cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), Shape<kF32>::kSmem + groups_bytes(1024));
+    cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), Shape<kParts, kF32>::kSmem + groups_bytes(1024));
     if (e != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
     cudaLaunchAttribute pdl[1] = {pdl_attribute()};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Shape<kF32>::kSmem + groups_bytes(a.E);
+    cfg.blockDim = dim3(Shape<kParts, kF32>::kThreads);
+    cfg.dynamicSmemBytes = Shape<kParts, kF32>::kSmem + groups_bytes(a.E);
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
@@ -492,7 +521,7 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
     map_x.first = tok > 112 ? 0 : tok > 48 ? 1 : tok > 16 ? 2 : 3;
     const uint64_t dims[2] = {(uint64_t)K, (uint64_t)r.rows_total}, stride = (uint64_t)K * 2;
     for (int i = map_x.first; i < 4; ++i) {
-        const uint32_t box[2] = {kK, 128u >> i};
+        const uint32_t box[2] = {kK / 2, 128u >> i};
         if (!encode_map(&map_x.m[i], 0, 2, x, dims, &stride, box)) return cudaErrorInvalidValue;
     }
     int shift = 5;

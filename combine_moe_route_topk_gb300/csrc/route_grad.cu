@@ -24,42 +24,44 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;  // 8 tokens per block
 constexpr int kWarps = kThreads / 32;
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
-}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
     return v;
 }
+// Sum over the lanes of each aligned run of P.
+template <int P>
+__device__ __forceinline__ float run_sum(float v) {
+#pragma unroll
+    for (int o = P / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
 
-// What lane k < R knows of the token's k-th expert.
+// What lane k of a run of P >= R lanes knows of its token's k-th expert.
 struct Choice {
     int e;       // -1: no part
     float w, h;  // weight and its gradient, 0 without a part
     float d;     // sum of h w over the token
 };
+template <int P>
 __device__ __forceinline__ Choice load_choice(const int32_t *__restrict__ idx, const float *__restrict__ w,
-                                              const float *__restrict__ dw, int64_t g, int E, int R, int lane) {
+                                              const float *__restrict__ dw, int64_t g, bool inside, int E, int R, int k) {
     Choice c{-1, 0.f, 0.f, 0.f};
-    if (lane < R) {
-        const int e = __ldg(idx + g * R + lane);
-        if (e >= 0 && e < E) {
-            c.e = e;
-            c.w = __ldg(w + g * R + lane);
-            c.h = __ldg(dw + g * R + lane);
-        }
+    if (inside && k < R) {
+        const int e = __ldg(idx + g * R + k);
+        const float wk = __ldg(w + g * R + k), hk = __ldg(dw + g * R + k);
+        if (e >= 0 && e < E) c.e = e, c.w = wk, c.h = hk;
     }
-    c.d = warp_sum(c.h * c.w);
+    c.d = run_sum<P>(c.h * c.w);
     return c;
 }
 
-// Sum of v over the lanes that name the same expert, in every one of them, in
-// lane order; without repeated experts (as the router chooses them) v itself.
+// Sum of v over the lanes of a run that name the same expert, in every one of
+// them, in lane order; without repeated experts (as the router chooses them) v
+// itself.
+template <int P>
 __device__ __forceinline__ float sum_same(int e, float v, int lane) {
-    const unsigned alike = __match_any_sync(kFull, e < 0 ? -1 - lane : e);
+    const unsigned alike = __match_any_sync(kFull, e < 0 ? -1 - lane : e * 32 + lane / P);
     if (__any_sync(kFull, (alike & (alike - 1)) != 0)) {
         float s = 0.f;
         for (int k = 0; k < 32; ++k) {
@@ -71,8 +73,10 @@ __device__ __forceinline__ float sum_same(int e, float v, int lane) {
     return v;
 }
 
-// Entries at the chosen experts only.
-template <bool kVec4>
+// Entries at the chosen experts only.  A warp takes 32 / P tokens at once, P the
+// power of two that holds their R experts: its loads are whole lines and it
+// has 32 gathers of logits under way.
+template <int P, bool kVec4>
 __global__ void __launch_bounds__(kThreads)
 route_grad_chosen_kernel(const float *__restrict__ logits, const float *__restrict__ bias, int64_t NT, int E, int R,
                          int sigmoid, int renormalize, const int32_t *__restrict__ idx, const float *__restrict__ w,
@@ -80,24 +84,27 @@ route_grad_chosen_kernel(const float *__restrict__ logits, const float *__restri
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t g = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (g >= NT) return;  // uniform per warp
-    const Choice c = load_choice(idx, w, dw, g, E, R, lane);
-    float at = c.w * (renormalize ? c.h - c.d : c.h);
+    const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (32 / P);
+    if (first >= NT) return;  // uniform per warp
+    const int64_t g = first + lane / P;
+    const Choice c = load_choice<P>(idx, w, dw, g, g < NT, E, R, lane % P);
+    float z = 0.f;
     if (sigmoid && c.e >= 0) {
-        float z = __ldg(logits + g * E + c.e);
+        z = __ldg(logits + g * E + c.e);
         if (bias != nullptr) z = __fadd_rn(z, __ldg(bias + c.e));
-        at = at / (1.0f + expf(z));
     }
-    at = sum_same(c.e, at, lane);
-    float *row = dlogits + g * E;
+    const int64_t end = (min(first + 32 / P, NT) - first) * E;  // the tokens' rows are one run of memory
+    float *rows = dlogits + first * E;
     if (kVec4) {
-        for (int e = lane * 4; e < E; e += 128) *reinterpret_cast<float4 *>(row + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int64_t i = lane * 4; i < end; i += 128) *reinterpret_cast<float4 *>(rows + i) = make_float4(0.f, 0.f, 0.f, 0.f);
     } else {
-        for (int e = lane; e < E; e += 32) row[e] = 0.f;
+        for (int64_t i = lane; i < end; i += 32) rows[i] = 0.f;
     }
+    float at = c.w * (renormalize ? c.h - c.d : c.h);
+    if (sigmoid) at = at / (1.0f + expf(z));
+    at = sum_same<P>(c.e, at, lane);
     __syncwarp();
-    if (c.e >= 0) row[c.e] = at;
+    if (c.e >= 0) dlogits[g * E + c.e] = at;
 }
 
 // Softmax over all experts: lane l holds J of them, four in a row at a time.
@@ -126,7 +133,7 @@ route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restr
             z[j] = e < E ? __ldg(row + e) : -INFINITY;
         }
     }
-    const Choice c = load_choice(idx, w, dw, g, E, R, lane);
+    const Choice c = load_choice<32>(idx, w, dw, g, true, E, R, lane);
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -140,7 +147,7 @@ route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restr
         z[j] = expf(__fsub_rn(z[j], top));
         sum += expert(j) < E ? z[j] : 0.f;
     }
-    sum = warp_sum(sum);
+    sum = run_sum<32>(sum);
     const bool none = top == -INFINITY;  // nothing to choose from: zeros
     const float scale = none ? 0.f : 1.0f / sum, d = none ? 0.f : c.d;
     float *out = dlogits + g * E;
@@ -157,7 +164,7 @@ route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restr
             out[e] = none ? 0.f : -(z[j] * scale * d);
         }
     }
-    const float h = sum_same(c.e, c.h, lane);
+    const float h = sum_same<32>(c.e, c.h, lane);
     __syncwarp();
     if (c.e >= 0 && !none) {
         float zc = __ldg(row + c.e);
@@ -244,21 +251,27 @@ cudaError_t launch_route_grad(const float *logits, const float *bias, int64_t NT
     const bool softmax = (score_fn & ~MOE_BIAS_SELECT_ONLY) == MOE_SOFTMAX;
     if (score_fn & MOE_BIAS_SELECT_ONLY) bias = nullptr;  // the scores are the raw logits'
     auto at16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-    Launch l((NT + kWarps - 1) / kWarps, stream);
-    cudaError_t e = cudaSuccess;
+    auto blocks = [&](int tokens) { return (NT + tokens * kWarps - 1) / (tokens * kWarps); };
+    cudaError_t e = cudaErrorInvalidValue;
     if (softmax && !renormalize) {
         const bool vec = E % 4 == 0 && at16(logits) && at16(dlogits);
-        const int need = (E + 31) / 32;
+        Launch l(blocks(1), stream);
         auto launch = [&](auto kern) {
             return cudaLaunchKernelEx(&l.cfg, kern, logits, bias, NT, E, R, topk_idx, topk_w, dtopk_w, dlogits);
         };
-#define MOE_CASE(J) need <= J ? launch(vec ? route_grad_softmax_kernel<J, true> : route_grad_softmax_kernel<J, false>)
-        e = MOE_CASE(4) : MOE_CASE(8) : MOE_CASE(16) : MOE_CASE(32) : cudaErrorInvalidValue;
+#define MOE_CASE(J) E <= 32 * J ? launch(vec ? route_grad_softmax_kernel<J, true> : route_grad_softmax_kernel<J, false>)
+        e = MOE_CASE(4) : MOE_CASE(8) : MOE_CASE(16) : launch(vec ? route_grad_softmax_kernel<32, true> : route_grad_softmax_kernel<32, false>);
 #undef MOE_CASE
     } else {
         const bool vec = E % 4 == 0 && at16(dlogits);
-        e = cudaLaunchKernelEx(&l.cfg, vec ? route_grad_chosen_kernel<true> : route_grad_chosen_kernel<false>, logits, bias,
-                               NT, E, R, softmax ? 0 : 1, renormalize, topk_idx, topk_w, dtopk_w, dlogits);
+        auto launch = [&](int tokens, auto kern) {
+            Launch l(blocks(tokens), stream);
+            return cudaLaunchKernelEx(&l.cfg, kern, logits, bias, NT, E, R, softmax ? 0 : 1, renormalize, topk_idx, topk_w,
+                                      dtopk_w, dlogits);
+        };
+#define MOE_CASE(P) R <= P ? launch(32 / P, vec ? route_grad_chosen_kernel<P, true> : route_grad_chosen_kernel<P, false>)
+        e = MOE_CASE(2) : MOE_CASE(4) : MOE_CASE(8) : MOE_CASE(16) : launch(1, vec ? route_grad_chosen_kernel<32, true> : route_grad_chosen_kernel<32, false>);
+#undef MOE_CASE
     }
     if (e != cudaSuccess || dbias == nullptr) return e;
     Launch s((E + 31) / 32 * kCluster, stream);
