@@ -14,19 +14,12 @@
 // store results.  Dequantised weights never see shared memory: there they
 // would cost 2 x 2 bytes a weight for writing and reading where the codes
 // come in at 47 a cycle from HBM, 188 bytes a cycle of the 128 it has.
-//
-// Codes to bf16: a nibble of two's complement with its top bit flipped is
-// q + 8; put under the exponent of 128 it is the bf16 number 128 + (q + 8); and
-// (128 + q + 8) s - 136 s in one multiply-add is q s exactly (136 s = 17 * 8 s
-// fits eight bits).  The elements of a word lie so that a shift and one
-// logic operation give two of them in the halves of a register: 11
-// instructions for eight weights.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "expert_w4_internal.cuh"
 #include "pdl.cuh"
 #include "tc_ops.cuh"
+#include "w4_ops.cuh"
 
 namespace moe {
 namespace {
@@ -116,23 +109,6 @@ __device__ __forceinline__ void mma_bf16_tmem(uint32_t d, uint32_t a, uint64_t b
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(desc), "r"((uint32_t)accumulate)
         : "memory");
-}
-
-// An e4m3 scale twice, as bf16 (exact).
-__device__ __forceinline__ __nv_bfloat162 scale_bf16x2(uint32_t code) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
-    const float f = __half2float(__half(h));
-    return __floats2bfloat162_rn(f, f);
-}
-
-// Eight codes as bf16 times their scale: (128 + q + 8) s - 136 s.
-__device__ __forceinline__ void dequant8(uint32_t word, __nv_bfloat162 s, __nv_bfloat162 minus, uint32_t *out) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t bits = ((word >> (4 * j)) & 0x000f000fu) ^ 0x43084308u;
-        const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&bits), s, minus);
-        out[j] = *reinterpret_cast<const uint32_t *>(&v);
-    }
 }
 
 template <bool kGated, bool kParts, bool kF32>
@@ -328,13 +304,12 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                     for (int h = 0; h < kK / 32; ++h) {  // 32 codes: 16 bytes, of one group
                         const int chunk = mine * (kK / 32) + h;
                         const uint4 q = ld_shared128(codes + ((chunk ^ (row & 7)) << 4));
-                        const __nv_bfloat162 s = scale_bf16x2(ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM));
-                        const __nv_bfloat162 minus = __hmul2(s, __floats2bfloat162_rn(-136.f, -136.f));
+                        const W4Scale s(ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM));
                         uint32_t out[16];
-                        dequant8(q.x, s, minus, out);
-                        dequant8(q.y, s, minus, out + 4);
-                        dequant8(q.z, s, minus, out + 8);
-                        dequant8(q.w, s, minus, out + 12);
+                        dequant8(q.x, s, out);
+                        dequant8(q.y, s, out + 4);
+                        dequant8(q.z, s, out + 8);
+                        dequant8(q.w, s, out + 12);
                         if (h == 0) {
                             ok = mb_wait_warp(uempty + 8 * r.slot, r.phase ^ 1u, gave_up);
                             if (!ok) break;
@@ -503,6 +478,8 @@ cudaError_t launch(const CUtensorMap &map_w, const TokenMaps &map_x, const Args 
 cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, int group, const void *x,
                                   const void *wq, const void *group_scales, const float *row_scales, void *y, int y_f32,
                                   cudaStream_t stream) {
+    if (expert_w4_few(r, K, F, gated))
+        return launch_expert_w4_few(r, K, F, gated, group, x, wq, group_scales, row_scales, y, y_f32, stream);
     CUtensorMap map_w;
     TokenMaps map_x;
     const uint64_t line = (uint64_t)K / 2;  // bytes of a matrix row's codes

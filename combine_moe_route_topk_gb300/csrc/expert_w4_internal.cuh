@@ -11,4 +11,11 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
                                   cudaStream_t stream);
 cudaError_t take_expert_w4_error(int *err);
 
+// The form for experts with few rows: whether it takes a batch, and its launch.
+bool expert_w4_few(const ExpertRows &r, int K, int F, int gated);
+cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, int group, const void *x, const void *wq,
+                                 const void *group_scales, const float *row_scales, void *y, int y_f32,
+                                 cudaStream_t stream);
+constexpr int kMostSharedW4 = 227 * 1024 - 256;  // dynamic shared memory of a block, beside the few static words
+
 }  // namespace moe

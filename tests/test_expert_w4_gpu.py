@@ -56,12 +56,21 @@ ROWS = [
     (4, [3, 0, 0, 2, 0, 0, 7, 1], 12),
     (1, [48, 112, 49, 113], 400),
 ]
+# at most four rows an expert on average: one tile of eight tokens, edges of it, several tiles, no rows at all
+FEW = [
+    (1, [8, 0, 1, 7], 40),
+    (1, [9, 0, 0, 0, 3], 12),
+    (2, [20, 0, 0, 0, 0, 0, 4, 0], 17),   # three tiles, the last cut by the region's end
+    (4, [2, 0, 0, 0, 3, 1, 8, 0], 9),
+    (1, [0, 0, 0, 17, 0, 0, 0], 64),
+    (1, [4], 4),
+]
 SIZES = [(32, 8, 32), (64, 72, 64), (96, 136, 32), (256, 128, 128), (288, 264, 32), (512, 96, 64), (1152, 200, 128),
-         (1056, 64, 32)]
+         (1056, 64, 32), (2304, 520, 32)]
 
 
 @pytest.mark.parametrize("K,F,group", SIZES, ids=str)
-@pytest.mark.parametrize("N,counts,cap", ROWS, ids=str)
+@pytest.mark.parametrize("N,counts,cap", ROWS + FEW, ids=str)
 @pytest.mark.parametrize("form", ["bf16", "f32", "gated"])
 def test_product(N, counts, cap, K, F, group, form):
     b = Batch(N, counts, cap)
@@ -79,9 +88,10 @@ def test_product(N, counts, cap, K, F, group, form):
     ref.check_untouched(b, y)
 
 
-def test_many_experts():
+@pytest.mark.parametrize("counts", [[(7 * e * e) % 200 if e % 3 == 0 else 0 for e in range(240)],
+                                    [e % 11 if e % 3 == 0 else 0 for e in range(240)]], ids=["many", "few"])
+def test_many_experts(counts):
     """More tiles than blocks, tiles of every size, most experts without rows."""
-    counts = [(7 * e * e) % 200 if e % 3 == 0 else 0 for e in range(240)]
     b = Batch(4, counts, 4000)
     K, F = 320, 392
     x, w = b.row_values(K), Weights(b, F, K, 32)
@@ -93,18 +103,20 @@ def test_many_experts():
     ref.check_untouched(b, y)
 
 
+@pytest.mark.parametrize("counts,K", [([70, 3], 17408), ([3, 1], 10240), ([3, 1], 17408)], ids=str)
 @pytest.mark.parametrize("form", ["bf16", "f32", "gated"])
-def test_long_sums_are_taken_in_parts(form):
-    """K = 17408: f32 results in parts of 512, bf16 ones beyond 16384 likewise.  Within a part an addition is off by
+def test_long_sums_are_taken_in_parts(form, counts, K):
+    """Sums of f32 results in parts of 512, those of bf16 ones beyond 16384 likewise.  Within a part an addition is off by
     at most a unit (2^-23) of what the part holds, and the parts are added rounding to nearest."""
-    b = Batch(1, [70, 3], 80)
-    K, F = 17408, 136
+    b = Batch(1, counts, 80)
+    F = 136
     x, w = b.row_values(K), Weights(b, 2 * F if form == "gated" else F, K, 128)
     y = b.out(F, torch.float32 if form == "f32" else torch.bfloat16)
     call(b, K, F, SWIGLU if form == "gated" else LINEAR, 128, x, w, y, form == "f32")
     want, mag = ref.product(b, x, w.w)
     v = b.valid
-    err = ((512 + 4) * 2.0 ** -23 * mag + K / 512 * F32_HALF * mag + F32_HALF * want.abs())[v]
+    part = 512 if form == "f32" or K > 16384 else K
+    err = ((part + 4) * 2.0 ** -23 * mag + K / part * F32_HALF * mag + F32_HALF * want.abs())[v]
     if form == "gated":
         want, err = ref.swiglu(want[v, :F], want[v, F:], err[:, :F], err[:, F:])
         ref.check(y[v], want, err, BF16_HALF, "y")
@@ -112,12 +124,13 @@ def test_long_sums_are_taken_in_parts(form):
         ref.check(y[v], want[v], err, F32_HALF if form == "f32" else BF16_HALF, "y")
 
 
-def test_exact_sums():
+@pytest.mark.parametrize("rows", [3, 40])
+def test_exact_sums(rows):
     """Whole numbers whose sums fit 24 bits come out exactly: no weight and no product is rounded."""
-    b = Batch(1, [40], 40)
+    b = Batch(1, [rows], rows)
     K, F = 512, 128
     kw = dict(generator=b.g, device="cuda")
-    x = torch.randint(-16, 17, (40, K), **kw).to(torch.bfloat16)
+    x = torch.randint(-16, 17, (rows, K), **kw).to(torch.bfloat16)
     w = Weights(b, F, K, 32)
     q = torch.randint(-8, 8, (1, F, K), dtype=torch.int8, **kw)
     s = torch.randint(1, 16, (1, K // 32, F), **kw).float()
@@ -183,9 +196,10 @@ def test_layer_between_dispatch_and_combine():
     ref.check(b.out, (rows * t).sum(1), ref.sum_error(R, (rows.abs() * t).sum(1)), BF16_HALF, "out")
 
 
-def test_what_stands_in_other_rows_and_weights_has_no_influence():
+@pytest.mark.parametrize("counts", [[20, 0, 5], [8, 0, 2]])
+def test_what_stands_in_other_rows_and_weights_has_no_influence(counts):
     """NaN in rows without a token and in the scales of experts without rows; NaN of one expert's rows stays there."""
-    b = Batch(1, [20, 0, 5], 64)
+    b = Batch(1, counts, 64)
     K, F = 96, 72
     x, w = b.row_values(K), Weights(b, F, K, 32)
     x[b.span(0)][7] = float("nan")
@@ -197,9 +211,10 @@ def test_what_stands_in_other_rows_and_weights_has_no_influence():
     ref.check_untouched(b, y)
 
 
-def test_offsets_of_no_batch_stand_for_no_rows():
-    for off in ([0, 5, 3, 8], [0, 4, 8, 1 << 30], [8, 0, 0, 0]):
-        b = Batch(1, [3, 3, 2], 20)
+@pytest.mark.parametrize("counts", [[3, 3, 2], [30, 30, 20]])
+def test_offsets_of_no_batch_stand_for_no_rows(counts):
+    for off in ([0, 5, 3, 8], [0, 4, 8, 1 << 30], [8, 0, 0, 0], [0, -5, 1, 2]):
+        b = Batch(1, counts, 90)
         x, w = b.randn(b.rows, 64), Weights(b, 40, 64, 32)
         b.offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
         y = b.out(40, torch.bfloat16)
@@ -207,8 +222,9 @@ def test_offsets_of_no_batch_stand_for_no_rows():
         assert bool((y == SENTINEL).all()), off
 
 
-def test_same_bits_in_graphs_on_streams_and_from_threads():
-    b = Batch(2, [30, 0, 129, 7, 1, 64], 200)
+@pytest.mark.parametrize("counts", [[30, 0, 129, 7, 1, 64], [3, 0, 12, 7, 1, 0]])
+def test_same_bits_in_graphs_on_streams_and_from_threads(counts):
+    b = Batch(2, counts, 200)
     K, F = 544, 264
     x, w1 = b.row_values(K), Weights(b, 2 * F, K, 32)
     want = b.out(F, torch.bfloat16)
@@ -244,9 +260,10 @@ def test_same_bits_in_graphs_on_streams_and_from_threads():
         assert torch.equal(y.view(torch.int16), want.view(torch.int16))
 
 
-def test_captured_call_follows_new_routing():
-    b, c = Batch(2, [30, 0, 9, 7], 60), Batch(2, [1, 40, 0, 0], 60, seed=1)
-    b.T = c.T = 60
+@pytest.mark.parametrize("old,new,T", [([30, 0, 9, 7], [1, 40, 0, 0], 60), ([3, 0, 2, 1], [0, 8, 0, 0], 8)])
+def test_captured_call_follows_new_routing(old, new, T):
+    b, c = Batch(2, old, 60), Batch(2, new, 60, seed=1)
+    b.T = c.T = T
     K, F = 128, 136
     x, w = b.randn(b.rows, K), Weights(b, F, K, 64)
     y = b.out(F, torch.float32)
