@@ -835,7 +835,7 @@ int moe_take_device_error(void *stream) {
     int err = 0;
     cudaError_t e = take_device_error(&err, (cudaStream_t)stream);
     cudaError_t (*const more[])(int *) = {take_expert_gemm_error, take_expert_wgrad_error, take_expert_fp8_error,
-                                        take_expert_w4_error};
+                                        take_expert_w4_error, take_expert_w4_few_error};
     for (auto take : more) {  // the stream has been waited for
         int one = 0;
         if (e == cudaSuccess) e = take(&one);

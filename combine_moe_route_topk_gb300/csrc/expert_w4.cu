@@ -81,15 +81,6 @@ __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, i
     return r;
 }
 
-// 4 bytes from global to shared memory without a register; `bytes` of them are read, the others are zeros.
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// Arrives on `bar` (whose count includes it) once this thread's copies so far are done.
-__device__ __forceinline__ void copy_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 // 32 lanes x 16 columns of 32 bits; done after tmem_store_wait.
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t *r) {
     asm volatile(
@@ -204,7 +195,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 const uint32_t to = scales_at + r.slot * kScales + lane * 4;
                 for (int i = 0; i < per_stage; ++i, ++b) {
                     const bool there = inside && b < a.groups;
-                    copy4(to + i * kM, scales + (there ? (int64_t)b * a.wide : 0), there ? 4 : 0);
+                    copy_async<4>(to + i * kM, scales + (there ? (int64_t)b * a.wide : 0), there ? 4 : 0);
                 }
                 copy_arrive(bar);
                 r.next();
@@ -282,7 +273,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     } else if (warp < kDequantWarps) {
         // A thread has one matrix row; the sets of four warps take units by turns.
         const int quarter = warp & 3, set = warp >> 2, row = quarter * 32 + lane;
-        const uint32_t line = smem + row * 128, at = a_at + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t magic = w4_magic(), line = smem + row * 128, at = a_at + ((uint32_t)(quarter * 32) << 16);
         Ring<kCodeStages> c;
         Ring<kUnitSlots> r;
         bool ok = true;
@@ -306,10 +297,10 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                         const uint4 q = ld_shared128(codes + ((chunk ^ (row & 7)) << 4));
                         const W4Scale s(ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM));
                         uint32_t out[16];
-                        dequant8(q.x, s, out);
-                        dequant8(q.y, s, out + 4);
-                        dequant8(q.z, s, out + 8);
-                        dequant8(q.w, s, out + 12);
+                        dequant8(q.x, s, magic, out);
+                        dequant8(q.y, s, magic, out + 4);
+                        dequant8(q.z, s, magic, out + 8);
+                        dequant8(q.w, s, magic, out + 12);
                         if (h == 0) {
                             ok = mb_wait_warp(uempty + 8 * r.slot, r.phase ^ 1u, gave_up);
                             if (!ok) break;
@@ -482,18 +473,7 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
         return launch_expert_w4_few(r, K, F, gated, group, x, wq, group_scales, row_scales, y, y_f32, stream);
     CUtensorMap map_w;
     TokenMaps map_x;
-    const uint64_t line = (uint64_t)K / 2;  // bytes of a matrix row's codes
-    if (gated) {  // per feature block of 8: 8 gate rows, then its 8 up rows
-        const uint64_t dims[5] = {line, 8, 2, (uint64_t)F / 8, (uint64_t)r.E};
-        const uint64_t strides[4] = {line, line * F, line * 8, line * F * 2};
-        const uint32_t box[5] = {128, 8, 2, kM / 16, 1};
-        if (!encode_map(&map_w, 1, 5, wq, dims, strides, box)) return cudaErrorInvalidValue;
-    } else {
-        const uint64_t dims[3] = {line, (uint64_t)F, (uint64_t)r.E};
-        const uint64_t strides[2] = {line, line * F};
-        const uint32_t box[3] = {128, kM, 1};
-        if (!encode_map(&map_w, 1, 3, wq, dims, strides, box)) return cudaErrorInvalidValue;
-    }
+    if (!encode_w4(&map_w, wq, r.E, K, F, gated, kM)) return cudaErrorInvalidValue;
     const int64_t tok = r.most < kTok ? mma_tokens((int)r.most) : kTok;
     map_x.first = tok > 112 ? 0 : tok > 48 ? 1 : tok > 16 ? 2 : 3;
     const uint64_t dims[2] = {(uint64_t)K, (uint64_t)r.rows_total}, stride = (uint64_t)K * 2;

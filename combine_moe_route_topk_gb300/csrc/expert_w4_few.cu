@@ -3,20 +3,23 @@
 //
 //   y[p][f] = r[e][f] sum_k x[p][k] (s[e][k/group][f] q[e][f][k])
 //
-// Codes go from memory to registers (16 bytes a lane, three steps ahead), become
-// bf16 there (w4_ops.cuh) and are the A fragments of mma.sync as they are: a
-// lane's word of eight consecutive elements serves two products of 16, the
-// order of the reduction being free as long as the tokens' fragments have
-// the same one.  tcgen05 would have to read them from TMEM, 128 rows by 16
-// elements at a time, which takes it 64 to 70 cycles whatever the number of
-// tokens: 32 weights a cycle where HBM brings 47.  mma.sync takes 2 cycles for
-// 16 x 16 weights and eight tokens (measured), 128 weights a cycle.
+// Codes come to shared memory by TMA, become bf16 in registers (w4_ops.cuh) and
+// are the A fragments of mma.sync as they are: a lane's word of eight
+// consecutive elements serves two products of 16, the order of the reduction
+// being free as long as the tokens' fragments have the same one.  tcgen05 would
+// read them from TMEM, 128 rows by 16 elements at a time, which takes it 64 to 70
+// cycles whatever the number of tokens: 32 weights a cycle where HBM brings 47.
+// mma.sync takes 2 cycles for 16 x 16 weights and eight tokens (measured), 128
+// weights a cycle.  What is left to bound it are integer instructions: 7 for eight
+// weights, of which an SM executes two warps' a cycle, 73 weights.
 //
 // A block holds one expert's tokens, at most eight, in shared memory, in the
-// order in which lanes read them, and walks through a run of the matrix's
-// rows, 32 a warp at a time.  kSplit warps take the same rows and share their
-// reduction by blocks of 128; the sums are added up in shared memory in the
-// warps' order.
+// order in which lanes read them, and walks through a run of the matrices'
+// rows, in granules of 32, its share of all there are.  A unit is up to
+// 16 / split granules; the `split` warps of a granule share its reduction by
+// blocks of 128, and their sums are added up in shared memory in the warps'
+// order.  Two more warps load, one of them the groups' scales, whose copies in
+// the same warp as the codes' loads held those up.
 #include "expert_w4_internal.cuh"
 #include "mem_ops.cuh"
 #include "pdl.cuh"
@@ -26,22 +29,27 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kWarps = 16, kThreads = 32 * (kWarps + 2);
 constexpr int kTokShift = 3, kTok = 1 << kTokShift;
-constexpr int kRows = 32;        // matrix rows of a warp's step: two of mma's 16
-constexpr int kK = 128;          // its reduction elements: 16 bytes of codes a lane and row
+constexpr int kRows = 32;        // matrix rows of a granule, which a warp takes: two of mma's 16
+constexpr int kK = 128;          // reduction elements of its step: 16 bytes of codes a lane and row
 constexpr int kPartSteps = 4;    // steps of a part of a sum: 512 elements
+constexpr int kCodes = kWarps * kRows * kK / 2, kScales = kWarps * kRows * kK / 32;  // bytes of a stage: a step of every warp
+constexpr int kMostStages = 6;
 constexpr int kSums = kRows * kTok;
-constexpr int kRed = 2 * kWarps * kSums * 4;  // bytes of the warps' sums, twice
+constexpr int kSumLine = kSums;
+constexpr int kRed = 2 * kWarps * (kSumLine + kRows) * 4;  // bytes of the warps' sums and of the rows' scales, twice
+constexpr int kZeros = 256;           // bytes that stand for the tokens of a fragment that are not there
 
 struct Args {
     const int32_t *offsets;
-    const uint8_t *x, *wq, *group_scales;
+    const uint8_t *x, *group_scales;
     const float *row_scales;
     void *y;
     int64_t cap, most, pairs;
     int E, L, K, F, wide, groups, group_shift;
-    int split_shift, units;  // log2 of the warps that share rows; units of (16 / split) * 32 rows in a matrix
+    int split_shift, granules;  // log2 of the warps that share a granule, granules of a matrix
+    int stages, lines;       // stages of codes, lines of tokens in shared memory
 };
 
 // Bytes of a token's line in shared memory: two lines that are read together start 64 bytes apart.
@@ -49,202 +57,284 @@ __host__ __device__ constexpr int line_bytes(int K) { return (K + kK - 1) / kK *
 
 __device__ __forceinline__ void mma_m16n8k16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
         "%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-struct Unit {
-    int i, tt, m;    // group, token tile, first row (or feature) of this warp's rows
-    int row, n;      // first token row, tokens
+// Rows of codes by boxes of 128, 64 and 32.
+struct CodeMaps {
+    CUtensorMap m[3];
 };
 
-__device__ __forceinline__ Unit get_unit(const Groups &g, int E, int i, int u, int units) {
+struct Unit {
+    int i, tt;     // group, token tile
+    int m, count;  // first granule in the matrix, granules
+    int row, n;    // first token row, tokens
+};
+
+// The unit at place p of all granules, of which the block's end at hi.
+__device__ __forceinline__ Unit get_unit(const Groups &g, int E, int i, int p, int hi, int most, int granules) {
     Unit r;
-    r.i = same(find_group(g, E, i, u));
-    const int at = u - same(g.prefix[r.i]), c = same(g.count[r.i]);
-    r.tt = at / units;
-    r.m = at - r.tt * units;
+    r.i = same(find_group(g, E, i, p));
+    const int at = p - same(g.prefix[r.i]), c = same(g.count[r.i]);
+    r.tt = at / granules;
+    r.m = at - r.tt * granules;
+    r.count = min(min(most, granules - r.m), hi - p);
     r.row = same(g.row[r.i]) + (r.tt << kTokShift);
     r.n = min(kTok, c - (r.tt << kTokShift));
     return r;
 }
 
-// A warp's step: what a lane loads for it.
-struct Step {
-    uint4 codes[4];
-    uint32_t scales[4];
-};
-
 template <bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
-expert_w4_few_kernel(const Args a) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
+expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) unsigned long long bars[2 * kMostStages + 2];
+    __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
     const int line = line_bytes(a.K);
-    float *red = reinterpret_cast<float *>(smem_raw);
-    unsigned char *tokens = smem_raw + kRed;
-    int *tables = reinterpret_cast<int *>(tokens + kTok * line);
+    const uint32_t codes = (smem_u32(smem_raw) + 1023u) & ~1023u, scales_at = codes + a.stages * kCodes;
+    unsigned char *behind = smem_raw + (scales_at + a.stages * kScales - smem_u32(smem_raw));
+    float *red = reinterpret_cast<float *>(behind);
+    unsigned char *tokens = behind + kRed + kZeros;
+    int *tables = reinterpret_cast<int *>(tokens + a.lines * line);
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kMostStages, summed = empty + 8 * kMostStages,
+                   placed = summed + 8;
+    volatile int *gave_up = &s_gave_up;
+    if (tid == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+            mb_init(full + 8 * i, 1 + 32);  // the codes' bytes, and the lanes that copy scales
+            mb_init(empty + 8 * i, kWarps);
+        }
+        mb_init(summed, kWarps);
+        mb_init(placed, kWarps);
+        s_gave_up = 0;
+        mb_init_fence();
+        for (int i = 0; i < 3; ++i) tma_prefetch_map(&maps.m[i]);
+    }
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
+    if (tid < kZeros / 4) reinterpret_cast<int *>(behind + kRed)[tid] = 0;
     const Groups g = make_groups<kTokShift, kTokShift, 1>(
         tables, a.offsets, a.E, a.L, a.cap, a.most, a.pairs, gridDim.x,
-        [&](int c, int shift) { return ((c + (1 << shift) - 1) >> shift) * a.units; }, [](int) { return 0; });
+        [&](int c, int shift) { return ((c + (1 << shift) - 1) >> shift) * a.granules; }, [](int) { return 0; });
+    // A block's granules are a run of all of them: it rarely changes the expert.
     const int total = same(g.prefix[a.E]);
     const int lo = (int)((int64_t)total * blockIdx.x / gridDim.x), hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
     if (lo == hi) return;  // the whole block
 
-    const int split = 1 << a.split_shift, part = warp & (split - 1), sub = warp >> a.split_shift;
-    const int per_unit = (kWarps >> a.split_shift) * (kGated ? kRows / 2 : kRows);  // rows (or features) of a unit
-    const int blocks = (a.K + kK - 1) / kK, rest = blocks & (split - 1);
-    const int gr = lane >> 2, t = lane & 3;  // row of a fragment's eight, place in the four lanes of a row
-    const int64_t pitch = a.K / 2;           // bytes of a row's codes
+    const int split = 1 << a.split_shift, most = kWarps >> a.split_shift, unit_rows = most * kRows;
+    constexpr int kCols = kGated ? kRows / 2 : kRows;  // result columns of a granule
+    const int blocks = (a.K + kK - 1) / kK, rounds = (blocks + split - 1) >> a.split_shift;
+    auto advance = [&](Unit &w, int p) {  // to the unit at p, the one behind it
+        w.m += w.count;
+        if (w.m == a.granules) w = get_unit(g, a.E, w.i, p, hi, most, a.granules);
+        else w.count = min(min(most, a.granules - w.m), hi - p);
+    };
+    Unit w = get_unit(g, a.E, 0, lo, hi, most, a.granules);
+    int slot = 0;
+    uint32_t phase = 0;
+    auto next_slot = [&] {
+        if (++slot == a.stages) slot = 0, phase ^= 1u;
+    };
 
-    // The warp's steps, in order: blocks part', part' + split, ... of every unit, part' turned from unit to unit
-    // so that all warps get the same number in the long run.
-    struct Cursor {
-        int u, kb;
-    };
-    auto first_block = [&](int u) { return (int)((uint32_t)part + (uint32_t)u * (uint32_t)rest) & (split - 1); };
-    Cursor next{lo, first_block(lo)};
-    int next_group = 0;
-    const uint8_t *base = nullptr, *sbase = nullptr;  // of the lane's first row
-    uint32_t rows_ok = 0;                             // which of its four rows there are
-    auto open = [&] {  // the unit of `next`
-        const Unit w = get_unit(g, a.E, next_group, next.u, a.units);
-        next_group = w.i;
-        const int f = w.m * per_unit + sub * (kGated ? kRows / 2 : kRows) + gr;
-        base = a.wq + ((int64_t)w.i * a.wide + f) * pitch + t * 16;
-        sbase = a.group_scales + (int64_t)w.i * a.groups * a.wide + f;
-        rows_ok = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rows_ok |= (uint32_t)(f + (kGated ? (i & 1) * 8 : i * 8) < a.F) << i;
-    };
-    auto fetch = [&](Step &s) {
-        if (next.u < hi) {
-            const int k = next.kb * kK + t * 32;
-            const int64_t group = (int64_t)(k >> a.group_shift) * a.wide;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t row = kGated ? (i & 1) * 8 + (i >> 1) * (int64_t)a.F : i * 8;
-                const bool there = ((rows_ok >> i) & 1u) && k < a.K;
-                s.codes[i] = there ? ld_stream(reinterpret_cast<const uint4 *>(base + row * pitch + next.kb * (kK / 2)))
-                                   : make_uint4(0u, 0u, 0u, 0u);
-                s.scales[i] = there ? __ldg(sbase + group + row) : 0u;
+    if (warp >= kWarps) {  // loads
+        const bool scales = warp > kWarps;
+        // A lane copies eight rows' scales of every 32 / (unit_rows / 8)-th group.
+        const int q = lane & (unit_rows / 8 - 1), first = lane / (unit_rows / 8), step = 32 / (unit_rows / 8);
+        const int groups = (split * kK) >> a.group_shift;  // of a stage
+        bool ok = true;
+        for (int p = lo; p < hi && ok;) {
+            const int f0 = w.m * kCols, f = kGated ? f0 + (q >> 1) * 8 : f0 + q * 8;
+            const uint8_t *from = a.group_scales + (int64_t)w.i * a.groups * a.wide + (int64_t)first * a.wide;
+            if (f < a.F) from += f + (kGated && (q & 1) ? a.F : 0);
+            for (int r = 0; r < rounds; ++r) {
+                ok = mb_wait_warp(empty + 8 * slot, phase ^ 1u, gave_up);
+                if (!ok) break;
+                const uint32_t bar = full + 8 * slot;
+                if (scales) {
+                    const int left = a.groups - r * groups;
+                    uint32_t to = scales_at + slot * kScales + first * unit_rows + q * 8;
+                    for (int b = first; b < groups; b += step, to += step * unit_rows, from += (int64_t)step * a.wide) {
+                        const bool there = f < a.F && b < left;
+                        copy_async<8>(to, there ? from : a.group_scales, there ? 8 : 0);
+                    }
+                    copy_arrive(bar);
+                } else if (elect_one()) {
+                    // boxes of 256 elements (a line of 128 bytes) by up to 128 rows
+                    const int b0 = r * split / 2, b1 = min(b0 + split / 2, (blocks + 1) / 2);
+                    mb_expect_tx(bar, (b1 - b0) * w.count * kRows * 128);
+                    for (int b = b0; b < b1; ++b) {
+                        const uint32_t dst = codes + slot * kCodes + (b - b0) * unit_rows * 128;
+                        for (int q = 0; q < w.count * kRows;) {
+                            const int left = w.count * kRows - q, i = left >= 128 ? 0 : left >= 64 ? 1 : 2;
+                            if constexpr (kGated) tma_load_5d(dst + q * 128, &maps.m[i], bar, b * 128, 0, 0, (f0 + q / 2) / 8, w.i);
+                            else tma_load_3d(dst + q * 128, &maps.m[i], bar, b * 128, f0 + q, w.i);
+                            q += 128 >> i;
+                        }
+                    }
+                }
+                __syncwarp();
+                next_slot();
             }
-            next.kb += split;
-            if (next.kb >= blocks) {
-                ++next.u;
-                next.kb = first_block(next.u);
-                if (next.u < hi) open();
-            }
+            p += w.count;
+            if (p < hi) advance(w, p);
         }
-    };
-    open();
-    Step s0, s1, s2;
-    fetch(s0);
-    fetch(s1);
-    fetch(s2);
+        // nothing may still be landing here when the block ends
+        long long left = kPolls;
+        for (int i = 0; i < a.stages; ++i, next_slot()) {
+            while (!mb_try(full + 8 * slot, phase ^ 1u) && left > 0) --left;
+        }
+    } else {
+        const int part = warp & (split - 1), sub = warp >> a.split_shift;
+        const int gr = lane >> 2, t = lane & 3;  // row of a fragment's eight, place in the four lanes of a row
+        // A lane's four rows (of two fragments, eight rows apart in each) are four that follow one another in the
+        // matrix: their scales are one word, and lanes that read codes at once read different places of the
+        // swizzled lines.
+        const uint32_t magic = w4_magic(), zeros = smem_u32(behind + kRed) + t * 16, held_at = smem_u32(tokens) + gr * line + t * 16;
+        const int ch = ((part & 1) * 4 + t) ^ ((gr & 1) * 4);  // the lane's chunk of its first row's line
+        uint32_t codes_at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            codes_at[i] = codes + (part >> 1) * unit_rows * 128 + (sub * kRows + 4 * gr + i) * 128 + ((ch ^ i) << 4);
+        const uint32_t scale_at = scales_at + ((part * kK + t * 32) >> a.group_shift) * unit_rows + sub * kRows + 4 * gr;
+        float acc[8], sum[8];
+        int held_i = -1, held_tt = -1, buf = 0;
+        uint32_t x_at = zeros, x_step = 0, summed_phase = 0, placed_phase = 0;  // the lane's token, from block to block
+        Unit done = w;
+        bool pending = false, ok = true;  // pending: `done` has sums that are not added up yet
 
-    float acc[8], sum[8];
-    int u = lo, kb = first_block(lo), steps = 0, held_i = -1, held_tt = -1, buf = 0;
-    Unit w = get_unit(g, a.E, 0, lo, a.units);
-    // Sums of the finished unit: element j of a warp's 256 lies at (j / 32: fragment register, j % 32: lane).
-    auto row_of = [&](int j) { return ((j >> 5 & 4) << 2) + ((j & 31) >> 2) + ((j >> 5 & 2) << 2); };
-    auto begin = [&] {
-        if (w.i != held_i || w.tt != held_tt) {  // other tokens
-            __syncthreads();                     // nobody reads the old ones any more
-            held_i = w.i, held_tt = w.tt;
-            const int chunks = blocks * (kK / 8);
-            for (int j = tid; j < kTok * chunks; j += kThreads) {
-                const int tok = j / chunks, q = j - tok * chunks;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (tok < w.n && q * 8 < a.K)
-                    v = __ldg(reinterpret_cast<const uint4 *>(a.x + ((int64_t)(w.row + tok) * a.K + q * 8) * 2));
-                // lane t reads chunk 4 t + i of a block of 16 in its i-th turn: stored in that order
-                *reinterpret_cast<uint4 *>(tokens + tok * line + (q >> 4) * 256 + (q & 3) * 64 + (q >> 2 & 3) * 16) = v;
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = sum[i] = 0.f;
-    };
-    begin();
-    const uint32_t mine = smem_u32(tokens) + gr * line + t * 16;
-    bool more = true;
-    auto step = [&](Step &s) {
-        const W4Scale sc[4] = {W4Scale(s.scales[0]), W4Scale(s.scales[1]), W4Scale(s.scales[2]), W4Scale(s.scales[3])};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint4 b = ld_shared128(mine + kb * 256 + j * 64);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                auto word = [&](const uint4 &v) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; };
-                uint32_t p[4], q[4];
-                dequant8(word(s.codes[2 * m]), sc[2 * m], p);
-                dequant8(word(s.codes[2 * m + 1]), sc[2 * m + 1], q);
-                mma_m16n8k16(acc + 4 * m, p[0], q[0], p[1], q[1], b.x, b.y);
-                mma_m16n8k16(acc + 4 * m, p[2], q[2], p[3], q[3], b.z, b.w);
-            }
-        }
-        fetch(s);
-        kb += split;
-        if (++steps == kPartSteps || kb >= blocks) {
-            steps = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += acc[i], acc[i] = 0.f;
-        }
-        if (kb < blocks) return;
-        // the unit is done: the warps' sums, in their order
-        float *to = red + buf * (kWarps * kSums);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) to[warp * kSums + i * 32 + lane] = sum[i];
-        __syncthreads();
-        constexpr int kOut = kGated ? kSums / 2 : kSums;
-        for (int j = tid; j < (kWarps >> a.split_shift) * kOut; j += kThreads) {
-            const int which = j / kOut, jj = j % kOut;
-            const int f = w.m * per_unit + which * (kGated ? kRows / 2 : kRows) + row_of(jj);
-            const int tok = 2 * (jj & 3) + (jj >> 5 & 1);
-            if (tok >= w.n || f >= a.F) continue;
-            const float *from = to + (which << a.split_shift) * kSums + jj;
-            const float *rs = a.row_scales + (int64_t)w.i * a.wide + f;
-            float v = 0.f;
-            for (int i = 0; i < split; ++i) v += from[i * kSums];
-            v *= __ldg(rs);
-            const int64_t at = (int64_t)(w.row + tok) * a.F + f;
-            if constexpr (kGated) {
+        // The unit `done`: its warps' sums are added up in their order.  Element j of a warp's 256 lies at (j / 32: fragment register, j % 32: lane).
+        auto finish = [&] {
+            pending = false;
+            ok = mb_wait_warp(summed, summed_phase, gave_up, kPolls + rounds * kStepPolls);
+            summed_phase ^= 1u;
+            if (!ok) return;
+            const float *from = red + (buf ^ 1) * (kWarps * (kSumLine + kRows)), *scales = from + kWarps * kSumLine;
+            for (int j = tid; j < most * kSums; j += 32 * kWarps) {
+                int e = j;
+                if constexpr (kGated) e = (e & ~15) + (e & 1) * 8 + (e >> 1 & 7);  // gate and up in neighbouring lanes
+                const int which = e >> 8, i = e >> 5 & 7, l = e & 31;
+                const float *at = from + (which << a.split_shift) * kSumLine + (e & 255);
+                float v = 0.f;
+                for (int k = 0; k < split; k += 2) v = v + at[k * kSumLine] + at[(k + 1) * kSumLine];
+                // the row of the granule; of a gated one's, 8 are gate rows and the next 8 the same features' up rows
+                const int row = 4 * (l >> 2) + (i >> 2) * 2 + (i >> 1 & 1);
+                const int r = which * kCols + (kGated ? (row >> 4) * 8 + (row & 7) : row);
+                const bool is_up = kGated && (row & 8);
+                v *= scales[r + (is_up ? most * kCols : 0)];
                 float up = 0.f;
-                for (int i = 0; i < split; ++i) up += from[i * kSums + kSums / 2];
-                static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(silu_mul(v, up * __ldg(rs + a.F)));
-            } else if constexpr (kF32) {
-                static_cast<float *>(a.y)[at] = v;
-            } else {
-                static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(v);
+                if constexpr (kGated) up = __shfl_xor_sync(0xffffffffu, v, 1);
+                const int f = done.m * kCols + r, tok = 2 * (l & 3) + (i & 1);
+                if (which >= done.count || tok >= done.n || f >= a.F || is_up) continue;
+                const int64_t to = (int64_t)(done.row + tok) * a.F + f;
+                if constexpr (kGated) static_cast<__nv_bfloat16 *>(a.y)[to] = __float2bfloat16_rn(silu_mul(v, up));
+                else if constexpr (kF32) static_cast<float *>(a.y)[to] = v;
+                else static_cast<__nv_bfloat16 *>(a.y)[to] = __float2bfloat16_rn(v);
             }
+        };
+
+        for (int p = lo; p < hi && ok;) {
+            if (w.i != held_i || w.tt != held_tt) {  // other tokens
+                if (pending) finish();               // nobody reads the old ones any more
+                if (!ok) break;
+                held_i = w.i, held_tt = w.tt;
+                const int chunks = blocks * (kK / 8);
+                for (int tok = 0; tok < w.n; ++tok) {
+                    for (int q = tid; q < chunks; q += 32 * kWarps) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (q * 8 < a.K) v = __ldg(reinterpret_cast<const uint4 *>(a.x + ((int64_t)(w.row + tok) * a.K + q * 8) * 2));
+                        // lane t reads chunk 4 t + i of a block of 16 in its i-th turn: stored in that order
+                        *reinterpret_cast<uint4 *>(tokens + tok * line + (q >> 4) * 256 + (q & 3) * 64 + (q >> 2 & 3) * 16) = v;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mb_arrive(placed);
+                ok = mb_wait_warp(placed, placed_phase, gave_up);
+                if (!ok) break;
+                placed_phase ^= 1u;
+                x_at = gr < w.n ? held_at : zeros;
+                x_step = gr < w.n ? 2 * kK : 0;
+            }
+            float scale = 0.f;  // of the thread's row of the unit, gate rows first
+            {
+                const int r = kGated && tid >= most * kCols ? tid - most * kCols : tid, f = w.m * kCols + r;
+                if (r < w.count * kCols && f < a.F) scale = __ldg(a.row_scales + (int64_t)w.i * a.wide + f + (r != tid ? a.F : 0));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = sum[i] = 0.f;
+            const int mine = sub < w.count ? (blocks - part + split - 1) >> a.split_shift : 0;  // blocks of this warp
+            uint32_t x = x_at + part * x_step;
+            for (int r = 0; r < rounds; ++r, x += x_step << a.split_shift) {
+                ok = mb_wait_warp(full + 8 * slot, phase, gave_up);
+                if (!ok) break;
+                if (r >= mine) {
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(empty + 8 * slot);
+                    next_slot();
+                    continue;
+                }
+                uint4 c[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[i] = ld_shared128(codes_at[i] + slot * kCodes);
+                const uint32_t sc = ld_shared32(scale_at + slot * kScales);
+                __syncwarp();
+                if (lane == 0) mb_arrive(empty + 8 * slot);  // all of it is in registers
+                next_slot();
+                const W4Scale s[4] = {W4Scale(sc & 0xff), W4Scale(sc >> 8 & 0xff), W4Scale(sc >> 16 & 0xff), W4Scale(sc >> 24)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 b = ld_shared128(x + j * 64);
+                    auto word = [&](const uint4 &v) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; };
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t top[4], low[4];  // the lane's row of the fragment's first eight, of its second
+                        dequant8(word(c[2 * m]), s[2 * m], magic, top);
+                        dequant8(word(c[2 * m + 1]), s[2 * m + 1], magic, low);
+                        mma_m16n8k16(acc + 4 * m, top[0], low[0], top[1], low[1], b.x, b.y);
+                        mma_m16n8k16(acc + 4 * m, top[2], low[2], top[3], low[3], b.z, b.w);
+                    }
+                }
+                if ((r & (kPartSteps - 1)) == kPartSteps - 1 || r == mine - 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[i] += acc[i], acc[i] = 0.f;
+                }
+            }
+            // The unit before is finished only now: warps that got a block more or less than others need not wait.
+            if (ok && pending) finish();
+            if (!ok) break;
+            float *to = red + buf * (kWarps * (kSumLine + kRows));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to[warp * kSumLine + i * 32 + lane] = sum[i];
+            to[kWarps * kSumLine + tid] = scale;
+            __syncwarp();
+            if (lane == 0) mb_arrive(summed);
+            buf ^= 1;
+            pending = true;
+            done = w;
+            p += w.count;
+            if (p < hi) advance(w, p);
         }
-        buf ^= 1;
-        if (++u == hi) {
-            more = false;
-            return;
-        }
-        kb = first_block(u);
-        w = get_unit(g, a.E, w.i, u, a.units);
-        begin();
-    };
-    while (more) {
-        step(s0);
-        if (more) step(s1);
-        if (more) step(s2);
+        if (ok && pending) finish();
     }
+    __syncthreads();
+    if (tid == 0 && s_gave_up) record_timeout();
 }
 
+// Stages of codes that fit beside the tokens (fewer than two: the kernel does not take the batch).
+int stages_of(const ExpertRows &r, int K, int lines) {
+    const int left = kMostSharedW4 - 1024 - kRed - kZeros - groups_bytes(r.E) - lines * line_bytes(K);
+    const int n = left / (kCodes + kScales);
+    return n < kMostStages ? n : kMostStages;
+}
+int lines_of(const ExpertRows &r) { return r.most < kTok ? (int)r.most : kTok; }
+
 template <bool kGated, bool kF32>
-cudaError_t launch(const Args &a, cudaStream_t stream) {
+cudaError_t launch(const CodeMaps &maps, const Args &a, cudaStream_t stream) {
     auto kern = expert_w4_few_kernel<kGated, kF32>;
     static thread_local AttrCache attr;
-    const int smem = kRed + kTok * line_bytes(a.K) + groups_bytes(a.E);
     cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), kMostSharedW4);
     if (e != cudaSuccess) return e;
     const int sms = sm_count();
@@ -253,18 +343,18 @@ cudaError_t launch(const Args &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = 1024 + a.stages * (kCodes + kScales) + kRed + kZeros + a.lines * line_bytes(a.K) + groups_bytes(a.E);
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, kern, maps, a);
 }
 
 }  // namespace
 
 bool expert_w4_few(const ExpertRows &r, int K, int F, int gated) {
     const int64_t wide = gated ? 2 * (int64_t)F : F;
-    return r.pairs <= 4 * (int64_t)r.E && kRed + kTok * line_bytes(K) + groups_bytes(r.E) <= kMostSharedW4 &&
+    return r.pairs <= 4 * (int64_t)r.E && K <= (1 << 16) && stages_of(r, K, lines_of(r)) >= 2 &&
            (r.E + r.pairs / kTok) * (wide / kRows + 1) < (1 << 30);  // units are counted in 32 bits
 }
 
@@ -272,16 +362,27 @@ cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, i
                                  const void *group_scales, const float *row_scales, void *y, int y_f32,
                                  cudaStream_t stream) {
     const int blocks = (K + kK - 1) / kK;
-    int split = 0;
-    while (split < 4 && (2 << split) <= blocks) ++split;
-    const int per_unit = (kWarps >> split) * (gated ? kRows / 2 : kRows);
+    const int cols = gated ? kRows / 2 : kRows, granules = (F + cols - 1) / cols;
+    // Four warps share a granule, so that a block's units are 128 rows: whole
+    // boxes and lines of scales.  More, where a block has less than that to do
+    // (one matrix of 4096 x 7168: 15 us with 16 warps a granule, 17 with four).
+    const int64_t active = r.pairs < r.E ? r.pairs : r.E, sms = sm_count();
+    const int64_t share = sms > 0 ? (active * granules + sms - 1) / sms : 1;
+    int split = blocks > 2 ? 2 : 1;  // two at least: a line of shared memory has two blocks
+    while (split < 4 && (share << (split + 1)) <= kWarps && (2 << split) <= blocks) ++split;
+    CodeMaps maps;
+    for (int i = 0; i < 3; ++i)
+        if (!encode_w4(&maps.m[i], wq, r.E, K, F, gated, 128 >> i)) return cudaErrorInvalidValue;
     int shift = 5;
     while ((1 << shift) < group) ++shift;
-    const Args a{r.offsets, static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(wq),
-                 static_cast<const uint8_t *>(group_scales), row_scales, y, r.cap, r.most, r.pairs,
-                 r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift, split, (F + per_unit - 1) / per_unit};
-    if (gated) return launch<true, false>(a, stream);
-    return y_f32 ? launch<false, true>(a, stream) : launch<false, false>(a, stream);
+    const int lines = lines_of(r);
+    const Args a{r.offsets, static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(group_scales), row_scales, y,
+                 r.cap, r.most, r.pairs, r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift, split,
+                 granules, stages_of(r, K, lines), lines};
+    if (gated) return launch<true, false>(maps, a, stream);
+    return y_f32 ? launch<false, true>(maps, a, stream) : launch<false, false>(maps, a, stream);
 }
+
+cudaError_t take_expert_w4_few_error(int *err) { return take_tc_error(err); }
 
 }  // namespace moe

@@ -16,6 +16,7 @@ bool expert_w4_few(const ExpertRows &r, int K, int F, int gated);
 cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, int group, const void *x, const void *wq,
                                  const void *group_scales, const float *row_scales, void *y, int y_f32,
                                  cudaStream_t stream);
+cudaError_t take_expert_w4_few_error(int *err);
 constexpr int kMostSharedW4 = 227 * 1024 - 256;  // dynamic shared memory of a block, beside the few static words
 
 }  // namespace moe

@@ -142,6 +142,11 @@ __device__ __forceinline__ uint32_t ld_shared8(uint32_t addr) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t ld_shared32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 // Two f32 (bits) rounded to bf16, the first in the low half.
 __device__ __forceinline__ uint32_t bf16x2(uint32_t first, uint32_t second) {
     uint32_t r;
@@ -632,6 +637,21 @@ struct PairCache {
 // strides in bytes for dimensions 1.. (false: the driver refused it).
 bool encode_map(CUtensorMap *m, int fp8, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
                 const uint32_t *box);
+
+// The map of matrices of 4-bit codes, boxes of 256 elements (a line of 128 bytes)
+// by `rows` rows; of a gated product's, blocks of 8 gate rows and the up rows of
+// the same 8 features follow one another.
+inline bool encode_w4(CUtensorMap *m, const void *wq, int E, int K, int F, int gated, int rows) {
+    const uint64_t line = (uint64_t)K / 2, f = (uint64_t)F, e = (uint64_t)E;
+    if (gated) {
+        const uint64_t dims[5] = {line, 8, 2, f / 8, e}, strides[4] = {line, line * f, line * 8, line * f * 2};
+        const uint32_t box[5] = {128, 8, 2, (uint32_t)rows / 16, 1};
+        return encode_map(m, 1, 5, wq, dims, strides, box);
+    }
+    const uint64_t dims[3] = {line, f, e}, strides[2] = {line, line * f};
+    const uint32_t box[3] = {128, (uint32_t)rows, 1};
+    return encode_map(m, 1, 3, wq, dims, strides, box);
+}
 
 // The maps of load_rows over rows of `cols` elements (16-bit, or 8-bit: fp8),
 // of which no tile takes more than `most` at once.

@@ -1,5 +1,5 @@
-// 4-bit codes to bf16, shared by the kernels of the experts' product with
-// 4-bit weights.
+// 4-bit codes to bf16, and what the kernels of the experts' product with
+// 4-bit weights share besides.
 //
 // A nibble of two's complement with its top bit flipped is q + 8; put under the
 // exponent of 128 it is the bf16 number 128 + (q + 8); and (128 + q + 8) s - 136 s
@@ -26,14 +26,33 @@ struct W4Scale {
     }
 };
 
+// The constant of dequant8, from a register: as a literal next to the mask, which is
+// one too, it cost an instruction for every pair.
+__device__ __forceinline__ uint32_t w4_magic() {
+    uint32_t r;
+    asm volatile("mov.b32 %0, 0x43084308;" : "=r"(r));
+    return r;
+}
+
 // The eight elements of a word, two a register, in their order.
-__device__ __forceinline__ void dequant8(uint32_t word, const W4Scale &w, uint32_t *out) {
+__device__ __forceinline__ void dequant8(uint32_t word, const W4Scale &w, uint32_t magic, uint32_t *out) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const uint32_t bits = ((word >> (4 * j)) & 0x000f000fu) ^ 0x43084308u;
+        uint32_t bits;  // (word >> 4 j) & 0x000f000f ^ magic
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(bits) : "r"(word >> (4 * j)), "r"(0x000f000fu), "r"(magic));
         const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&bits), w.s, w.minus);
         out[j] = *reinterpret_cast<const uint32_t *>(&v);
     }
+}
+
+// `kBytes` from global to shared memory without a register; `bytes` of them are read, the others are zeros.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(bytes) : "memory");
+}
+// Arrives on `bar` (whose count includes it) once this thread's copies so far are done.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 }  // namespace moe
