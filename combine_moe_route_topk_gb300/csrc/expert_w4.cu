@@ -25,24 +25,34 @@ namespace moe {
 namespace {
 
 constexpr int kM = 128;            // matrix rows of a tile
-constexpr int kTokShift = 7, kTok = 1 << kTokShift;  // most tokens of a tile
-constexpr int kK = 128;            // reduction elements of a unit: what one slot of TMEM and of token rows holds
+constexpr int kK = 128;            // reduction elements of a unit: what one slot of TMEM and one of token rows hold
 constexpr int kUnits = 2;          // units of a stage of codes: 256 codes, one 128-byte line of a row
-constexpr int kUnitSlots = 4;
-constexpr int kCodes = kM * 128, kScales = 8 * kM, kHalfRows = kTok * 128, kRows = 2 * kHalfRows;  // bytes of a slot
+constexpr int kCodes = kM * 128, kScales = 8 * kM;  // bytes of a stage
+constexpr int kDequantWarps = 16;  // in sets, which turn units into bf16 by turns
 constexpr int kStoreWarps = 8;
 constexpr int kPartUnits = 512 / kK;  // units of a part of an f32 result's sum
 
-// For sums in parts the storing warps hold them in registers: 768 threads are
-// launched with 80 each, the storing ones take 120, the dequantising ones keep 64,
-// the others (with an idle warp, so that they are four) 40.
-template <bool kParts, bool kF32>
+// TMEM holds two accumulators of kTok columns, so that a tile's results leave
+// while the next one is computed, and kSlots slots of 64 columns for weights.
+// For sums in parts the storing warps hold kTok / 2 sums a thread in registers:
+// 896 threads are launched with 72 each, the storing ones take 104 or 120, the
+// dequantising ones keep 64 or 56, the others (with an idle warp, so that they
+// are four) 40.
+template <int kTok, bool kParts, bool kF32>
 struct Shape {
-    static constexpr int kSets = kParts ? 3 : 4, kDequantWarps = 4 * kSets;  // sets of four warps that dequantise units by turns
+    static constexpr int kSlots = (512 - 2 * kTok) / (kK / 2);
+    // No more sets than slots: a set that came to a slot's use after the next would take
+    // the barrier's phase for the one before.
+    static constexpr int kSets = kTok == 64 ? 4 : 2, kShare = 4 / kSets;  // sets; fours of warps of one, which share a unit
+    static_assert(kSets <= kSlots);
+    static constexpr int kHalf = kTok * 128, kRows = 2 * kHalf;  // bytes of half a unit's token rows, of a slot of them
+    static constexpr int kRowSlots = kTok == 192 ? 3 : kTok == 128 ? 4 : 6;
+    static constexpr int kCodeStages = kTok == 64 ? 5 : 3;
     static constexpr int kThreads = 32 * (kDequantWarps + kStoreWarps + (kParts ? 4 : 3));
-    static constexpr int kCodeStages = kF32 ? 3 : 4;
+    static constexpr int kStoreRegs = kTok == 64 ? 104 : 120, kDequantRegs = kTok == 64 ? 64 : 56;
+    static_assert(!kParts || 32 * (kStoreWarps * kStoreRegs + kDequantWarps * kDequantRegs + 4 * 40) <= kThreads * 72);
     static constexpr int kBuf = kF32 ? 4096 : 2048;  // a storing warp's: 32 tokens' results, to be written as whole sectors
-    static constexpr int kSmem = 1024 + kCodeStages * (kCodes + kScales) + kUnitSlots * kRows + kStoreWarps * kBuf;
+    static constexpr int kSmem = 1024 + kCodeStages * (kCodes + kScales) + kRowSlots * kRows + kStoreWarps * kBuf;
 };
 
 // Token rows by boxes of 128, 64, 32 and 16 rows of 128 bytes.
@@ -61,7 +71,10 @@ struct Args {
 };
 
 __host__ __device__ constexpr int mma_tokens(int n) { return (n + 15) & ~15; }
-__device__ __forceinline__ int token_tiles(int count, int shift) { return (count + (1 << shift) - 1) >> shift; }
+template <int kTok>
+__device__ __forceinline__ int token_tiles(int count) {
+    return count > 0 ? (count - 1) / kTok + 1 : 0;  // count + kTok need not fit 32 bits
+}
 
 struct Tile {
     int e, m0, row, n;  // group, first matrix row (or feature), first token row, tokens
@@ -69,10 +82,11 @@ struct Tile {
 
 // Tiles of a group: its token tiles (of equal size) run fastest, so that
 // blocks working at the same time share the matrix rows through L2.
+template <int kTok>
 __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, int m_step) {
     Tile r;
     r.e = same(find_group(g, E, e, t));
-    const int c = same(g.count[r.e]), nt = token_tiles(c, g.shift), at = t - same(g.prefix[r.e]);
+    const int c = same(g.count[r.e]), nt = token_tiles<kTok>(c), at = t - same(g.prefix[r.e]);
     const int size = mma_tokens(tile_rows(c, nt));
     const int tt = at % nt;
     r.m0 = at / nt * m_step;
@@ -102,23 +116,23 @@ __device__ __forceinline__ void mma_bf16_tmem(uint32_t d, uint32_t a, uint64_t b
         : "memory");
 }
 
-template <bool kGated, bool kParts, bool kF32>
-__global__ void __launch_bounds__(Shape<kParts, kF32>::kThreads, 1)
+template <int kTok, bool kGated, bool kParts, bool kF32>
+__global__ void __launch_bounds__(Shape<kTok, kParts, kF32>::kThreads, 1)
 expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x, const Args a) {
-    using S = Shape<kParts, kF32>;
-    constexpr int kBuf = S::kBuf, kCodeStages = S::kCodeStages, kDequantWarps = S::kDequantWarps;
+    using S = Shape<kTok, kParts, kF32>;
+    constexpr int kSlots = S::kSlots, kRows = S::kRows, kRowSlots = S::kRowSlots, kCodeStages = S::kCodeStages, kBuf = S::kBuf;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[2 * kCodeStages + 3 * kUnitSlots + 5];
+    __shared__ __align__(8) unsigned long long bars[2 * kCodeStages + 2 * kRowSlots + 2 * kSlots + 5];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t rows_at = smem + kCodeStages * kCodes, scales_at = rows_at + kUnitSlots * kRows,
+    const uint32_t rows_at = smem + kCodeStages * kCodes, scales_at = rows_at + kRowSlots * kRows,
                    bufs_at = scales_at + kCodeStages * kScales, tables_at = bufs_at + kStoreWarps * kBuf;
     int *tables = reinterpret_cast<int *>(smem_raw + (tables_at - smem_u32(smem_raw)));
     const uint32_t cfull = smem_u32(bars), cempty = cfull + 8 * kCodeStages, xfull = cempty + 8 * kCodeStages,
-                   afull = xfull + 8 * kUnitSlots, uempty = afull + 8 * kUnitSlots, tfull = uempty + 8 * kUnitSlots,
-                   tempty = tfull + 16, done = tempty + 16;
+                   xempty = xfull + 8 * kRowSlots, afull = xempty + 8 * kRowSlots, aempty = afull + 8 * kSlots,
+                   tfull = aempty + 8 * kSlots, tempty = tfull + 16, done = tempty + 16;
     volatile int *gave_up = &s_gave_up;
     constexpr int kStoreFirst = kDequantWarps, kCodeWarp = kDequantWarps + kStoreWarps, kRowWarp = kCodeWarp + 1,
                   kMmaWarp = kCodeWarp + 2;
@@ -129,10 +143,13 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
             mb_init(cfull + 8 * i, 1 + 32);  // the loads' bytes, and the lanes that copy scales
             mb_init(cempty + 8 * i, kDequantWarps);
         }
-        for (int i = 0; i < kUnitSlots; ++i) {
+        for (int i = 0; i < kRowSlots; ++i) {
             mb_init(xfull + 8 * i, 1);
-            mb_init(afull + 8 * i, 4);
-            mb_init(uempty + 8 * i, 1);
+            mb_init(xempty + 8 * i, 1);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            mb_init(afull + 8 * i, 4 * S::kShare);
+            mb_init(aempty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mb_init(tfull + 8 * i, 1);
@@ -152,14 +169,14 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     grid_launch_dependents();
     constexpr int kStep = kGated ? kM / 2 : kM;  // result columns of a tile
     const int m_tiles = (a.F + kStep - 1) / kStep;
-    const Groups g = make_groups<kTokShift, kTokShift, 1>(
+    const Groups g = make_groups<0, 0, 1>(
         tables, a.offsets, a.E, a.L, a.cap, a.most, a.pairs, gridDim.x,
-        [&](int c, int shift) { return token_tiles(c, shift) * m_tiles; }, [](int) { return 0; });  // syncs the block
+        [&](int c, int) { return token_tiles<kTok>(c) * m_tiles; }, [](int) { return 0; });  // syncs the block
     const int tiles = same(g.prefix[a.E]), units = (a.K + kK - 1) / kK;
     const int part = kParts ? kPartUnits : units;  // units that are summed in TMEM
 
     if constexpr (kParts) {
-        if (warp < kDequantWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp < kDequantWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kDequantRegs));
         else if (warp >= kCodeWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     }
 
@@ -169,7 +186,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         bool ok = true;
         const int per_stage = 256 >> a.group_shift;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile w = get_tile(g, a.E, e, t, kStep);
+            const Tile w = get_tile<kTok>(g, a.E, e, t, kStep);
             e = w.e;
             // lanes copy the scales of four matrix rows each
             int f = w.m0 + lane * 4;
@@ -203,15 +220,15 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         }
         drain_ring(cfull, r);  // nothing may still be landing here when the block ends
     } else if (warp == kRowWarp) {
-        Ring<kUnitSlots> r;
+        Ring<kRowSlots> r;
         int e = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile w = get_tile(g, a.E, e, t, kStep);
+            const Tile w = get_tile<kTok>(g, a.E, e, t, kStep);
             e = w.e;
             const int n = mma_tokens(w.n);
             for (int u = 0; u < units; ++u) {
-                ok = mb_wait_warp(uempty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                ok = mb_wait_warp(xempty + 8 * r.slot, r.phase ^ 1u, gave_up);
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t bar = xfull + 8 * r.slot;
@@ -223,7 +240,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                         const int box = 128 >> i;
                         if (n & box) {
                             tma_load_2d(dst, &map_x.m[i], bar, u * kK, row);
-                            tma_load_2d(dst + kHalfRows, &map_x.m[i], bar, u * kK + kK / 2, row);
+                            tma_load_2d(dst + S::kHalf, &map_x.m[i], bar, u * kK + kK / 2, row);
                             dst += box * 128;
                             row += box;
                         }
@@ -235,32 +252,36 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         }
         drain_ring(xfull, r);
     } else if (warp == kMmaWarp) {
-        Ring<kUnitSlots> r;
+        // An mma of few tokens takes 33 cycles, a commit 87 to issue and a wait some 60: what is
+        // between the eight mma of a unit is kept short.
+        Ring<kSlots> r;
+        Ring<kRowSlots> x;
         Ring<2> acc;
         int e = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile w = get_tile(g, a.E, e, t, kStep);
+            const Tile w = get_tile<kTok>(g, a.E, e, t, kStep);
             e = w.e;
             const uint32_t desc = mma_desc(1, false, false, kM, mma_tokens(w.n));
             for (int u0 = 0; u0 < units && ok; u0 += part) {
                 const uint32_t d = tmem + acc.slot * kTok;
                 ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
                 for (int u = u0; u < min(u0 + part, units) && ok; ++u) {
-                    ok = mb_wait_warp(xfull + 8 * r.slot, r.phase, gave_up) &&
-                         mb_wait_warp(afull + 8 * r.slot, r.phase, gave_up);
+                    ok = mb_wait_warp2(xfull + 8 * x.slot, x.phase, afull + 8 * r.slot, r.phase, gave_up);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t db = smem_operand(rows_at + r.slot * kRows, 16, 1024);
+                        const uint64_t db = smem_operand(rows_at + x.slot * kRows, 16, 1024);
                         const uint32_t da = a_at + r.slot * (kK / 2);
 #pragma unroll
                         for (int i = 0; i < kK / 16; ++i)
-                            mma_bf16_tmem(d, da + i * 8, db + (i / 4 * (kHalfRows / 16) + i % 4 * 2), desc, u != u0 || i != 0);
-                        tc_commit(uempty + 8 * r.slot);
+                            mma_bf16_tmem(d, da + i * 8, db + (i / 4 * (S::kHalf / 16) + i % 4 * 2), desc, u != u0 || i != 0);
+                        tc_commit(aempty + 8 * r.slot);
+                        tc_commit(xempty + 8 * x.slot);
                     }
                     __syncwarp();
                     r.next();
+                    x.next();
                 }
                 if (elect_one()) tc_commit(tfull + 8 * acc.slot);
                 __syncwarp();
@@ -271,61 +292,69 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         __syncwarp();
         mb_drain(done, 0);
     } else if (warp < kDequantWarps) {
-        // A thread has one matrix row; the sets of four warps take units by turns.
-        const int quarter = warp & 3, set = warp >> 2, row = quarter * 32 + lane;
+        // A thread has one matrix row and, of a unit, all or a half; the sets take units by turns.
+        constexpr int kSets = S::kSets, kChunks = kK / 32 / S::kShare;
+        const int quarter = warp & 3, set = (warp >> 2) / S::kShare, share = (warp >> 2) % S::kShare, row = quarter * 32 + lane;
         const uint32_t magic = w4_magic(), line = smem + row * 128, at = a_at + ((uint32_t)(quarter * 32) << 16);
         Ring<kCodeStages> c;
-        Ring<kUnitSlots> r;
+        Ring<kSlots> r;  // of the next unit
         bool ok = true;
-        int turn = 0;
+        int turn = 0;    // the set that takes it
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             for (int u0 = 0; u0 < units && ok; u0 += kUnits) {
                 const int n = min(kUnits, units - u0);
-                int mine = set - turn;  // this set's unit of the stage, if it has one
-                mine += mine < 0 ? S::kSets : 0;
-                turn = (turn + n) % S::kSets;
+                const int mine = (set - turn) & (kSets - 1);  // this set's unit of the stage, if below n
+                turn = (turn + n) & (kSets - 1);
                 // a set without a unit waits as well: its arrival must not run ahead into the slot's next use
                 ok = mb_wait_warp(cfull + 8 * c.slot, c.phase, gave_up);
                 if (!ok) break;
                 if (mine < n) {
-                    for (int i = 0; i < mine; ++i) r.next();
+                    if (mine) r.next();
                     const uint32_t codes = line + c.slot * kCodes, scales = scales_at + c.slot * kScales + row;
-                    const uint32_t to = at + r.slot * (kK / 2);
+                    const uint32_t to = at + r.slot * (kK / 2) + share * (kChunks * 16);
+                    uint4 q[kChunks];
+                    uint32_t code[kChunks];
 #pragma unroll
-                    for (int h = 0; h < kK / 32; ++h) {  // 32 codes: 16 bytes, of one group
-                        const int chunk = mine * (kK / 32) + h;
-                        const uint4 q = ld_shared128(codes + ((chunk ^ (row & 7)) << 4));
-                        const W4Scale s(ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM));
+                    for (int h = 0; h < kChunks; ++h) {  // 32 codes: 16 bytes, of one group
+                        const int chunk = mine * (kK / 32) + share * kChunks + h;
+                        q[h] = ld_shared128(codes + ((chunk ^ (row & 7)) << 4));
+                        code[h] = ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(cempty + 8 * c.slot);  // all of it is in registers
+#pragma unroll
+                    for (int h = 0; h < kChunks; ++h) {
+                        const W4Scale s(code[h]);
                         uint32_t out[16];
-                        dequant8(q.x, s, magic, out);
-                        dequant8(q.y, s, magic, out + 4);
-                        dequant8(q.z, s, magic, out + 8);
-                        dequant8(q.w, s, magic, out + 12);
+                        dequant8(q[h].x, s, magic, out);
+                        dequant8(q[h].y, s, magic, out + 4);
+                        dequant8(q[h].z, s, magic, out + 8);
+                        dequant8(q[h].w, s, magic, out + 12);
                         if (h == 0) {
-                            ok = mb_wait_warp(uempty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                            ok = mb_wait_warp(aempty + 8 * r.slot, r.phase ^ 1u, gave_up);
                             if (!ok) break;
                             tc_fence_after();
                         }
                         tmem_store16(to + h * 16, out);
                     }
                     if (!ok) break;
-                    __syncwarp();
-                    if (lane == 0) mb_arrive(cempty + 8 * c.slot);  // the codes are in registers or TMEM
                     tmem_store_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mb_arrive(afull + 8 * r.slot);
-                    for (int i = mine; i < n; ++i) r.next();
+                    if (mine == 0 && n == 2) r.next();
+                    r.next();
                 } else {
-                    for (int i = 0; i < n; ++i) r.next();
                     if (lane == 0) mb_arrive(cempty + 8 * c.slot);
+                    if (n == 2) r.next();
+                    r.next();
                 }
                 c.next();
             }
         }
     } else if (warp < kCodeWarp) {
         // Results: warp w holds matrix rows 32 (w % 4).. of the tile, one per lane, and every other 32 tokens.
-        if constexpr (kParts) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+        if constexpr (kParts) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kStoreRegs));
         const int quarter = warp & 3, half = (warp - kStoreFirst) >> 2;
         const uint32_t buf = bufs_at + (warp - kStoreFirst) * kBuf;
         const int fl = kGated ? (lane >> 4) * 8 + (lane & 7) : lane, up = (lane >> 3) & 1;
@@ -386,16 +415,16 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         int e = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const Tile w = get_tile(g, a.E, e, t, kStep);
+            const Tile w = get_tile<kTok>(g, a.E, e, t, kStep);
             e = w.e;
             const int f = w.m0 + quarter * (kGated ? 16 : 32) + fl;
             const float scale =
                 f < a.F ? __ldg(a.row_scales + (int64_t)w.e * a.wide + f + (kGated && up ? a.F : 0)) : 0.f;
             const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + 32 * half;
             if constexpr (kParts) {
-                float sum[2][32];
+                float sum[kTok / 64][32];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < kTok / 64; ++i)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
                 for (int u0 = 0; u0 < units; u0 += part) {
@@ -403,7 +432,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < kTok / 64; ++i) {
                         if (64 * i + 32 * half < w.n) {
                             uint32_t v[32];
                             tmem_load32(src + acc.slot * kTok + 64 * i, v);
@@ -418,7 +447,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < kTok / 64; ++i) {
                     if (64 * i + 32 * half < w.n) store(w, 64 * i + 32 * half, scale, [&](int j) { return sum[i][j]; });
                 }
             } else {  // straight from TMEM
@@ -445,19 +474,21 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
-template <bool kGated, bool kParts, bool kF32>
+template <int kTok, bool kGated, bool kParts, bool kF32>
 cudaError_t launch(const CUtensorMap &map_w, const TokenMaps &map_x, const Args &a, cudaStream_t stream) {
-    auto kern = expert_w4_kernel<kGated, kParts, kF32>;
+    auto kern = expert_w4_kernel<kTok, kGated, kParts, kF32>;
+    using S = Shape<kTok, kParts, kF32>;
+    static_assert(S::kSmem + groups_bytes(1024) <= kMostSharedW4);
     static thread_local AttrCache attr;
-    cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), Shape<kParts, kF32>::kSmem + groups_bytes(1024));
+    cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), S::kSmem + groups_bytes(1024));
     if (e != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
     cudaLaunchAttribute pdl[1] = {pdl_attribute()};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
-    cfg.blockDim = dim3(Shape<kParts, kF32>::kThreads);
-    cfg.dynamicSmemBytes = Shape<kParts, kF32>::kSmem + groups_bytes(a.E);
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem + groups_bytes(a.E);
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
@@ -471,11 +502,13 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
                                   cudaStream_t stream) {
     if (expert_w4_few(r, K, F, gated))
         return launch_expert_w4_few(r, K, F, gated, group, x, wq, group_scales, row_scales, y, y_f32, stream);
+    const bool parts = K > kWhole || (y_f32 && !gated), small = r.pairs <= 32 * (int64_t)r.E;
+    const int most = small ? 64 : parts ? 128 : 192;
     CUtensorMap map_w;
     TokenMaps map_x;
     if (!encode_w4(&map_w, wq, r.E, K, F, gated, kM)) return cudaErrorInvalidValue;
-    const int64_t tok = r.most < kTok ? mma_tokens((int)r.most) : kTok;
-    map_x.first = tok > 112 ? 0 : tok > 48 ? 1 : tok > 16 ? 2 : 3;
+    const int64_t tok = r.most < most ? mma_tokens((int)r.most) : most;
+    map_x.first = tok >= 128 ? 0 : tok >= 64 ? 1 : tok >= 32 ? 2 : 3;
     const uint64_t dims[2] = {(uint64_t)K, (uint64_t)r.rows_total}, stride = (uint64_t)K * 2;
     for (int i = map_x.first; i < 4; ++i) {
         const uint32_t box[2] = {kK / 2, 128u >> i};
@@ -485,10 +518,13 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
     while ((1 << shift) < group) ++shift;
     const Args a{r.offsets, static_cast<const uint8_t *>(group_scales), row_scales, y, r.cap, r.most, r.pairs,
                  r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift};
-    const bool parts = K > kWhole;
-    if (gated) return parts ? launch<true, true, false>(map_w, map_x, a, stream) : launch<true, false, false>(map_w, map_x, a, stream);
-    if (y_f32) return launch<false, true, true>(map_w, map_x, a, stream);
-    return parts ? launch<false, true, false>(map_w, map_x, a, stream) : launch<false, false, false>(map_w, map_x, a, stream);
+    if (gated) {
+        if (parts) return small ? launch<64, true, true, false>(map_w, map_x, a, stream) : launch<128, true, true, false>(map_w, map_x, a, stream);
+        return small ? launch<64, true, false, false>(map_w, map_x, a, stream) : launch<192, true, false, false>(map_w, map_x, a, stream);
+    }
+    if (y_f32) return small ? launch<64, false, true, true>(map_w, map_x, a, stream) : launch<128, false, true, true>(map_w, map_x, a, stream);
+    if (parts) return small ? launch<64, false, true, false>(map_w, map_x, a, stream) : launch<128, false, true, false>(map_w, map_x, a, stream);
+    return small ? launch<64, false, false, false>(map_w, map_x, a, stream) : launch<192, false, false, false>(map_w, map_x, a, stream);
 }
 
 cudaError_t take_expert_w4_error(int *err) { return take_tc_error(err); }

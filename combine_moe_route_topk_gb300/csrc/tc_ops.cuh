@@ -114,6 +114,13 @@ __device__ __forceinline__ bool mb_wait_warp_pair(uint32_t bar, uint32_t parity,
     const bool ok = mb_wait_warp(bar, parity, gave_up, polls);
     return ok && __all_sync(0xffffffffu, mb_try_pair(bar, parity));  // complete: acquires, does not wait
 }
+// Two barriers with one vote where both are complete already.
+__device__ __forceinline__ bool mb_wait_warp2(uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2,
+                                              volatile int *gave_up) {
+    const bool first = mb_try(bar, parity), second = mb_try(bar2, parity2);
+    if (__all_sync(0xffffffffu, first && second)) return true;
+    return mb_wait_warp(bar, parity, gave_up) && mb_wait_warp(bar2, parity2, gave_up);
+}
 __device__ __forceinline__ void mb_drain(uint32_t bar, uint32_t parity) {  // bounded, result not needed
     for (long long i = 0; i < kPolls && !mb_try(bar, parity); ++i) {
     }
