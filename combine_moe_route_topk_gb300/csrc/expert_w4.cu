@@ -9,11 +9,21 @@
 //
 // The matrix is the operand with 128 rows of tcgen05.mma (M), read from TMEM;
 // the expert's tokens are its columns (N).  A block's warps: one loads codes
-// (TMA) and group scales, one loads the tokens (TMA), one issues mma, eight turn
+// (TMA) and group scales, one loads the tokens (TMA), one issues mma, 16 turn
 // codes into bf16 (a thread has one matrix row) and write them to TMEM, eight
 // store results.  Dequantised weights never see shared memory: there they
 // would cost 2 x 2 bytes a weight for writing and reading where the codes
-// come in at 47 a cycle from HBM, 188 bytes a cycle of the 128 it has.
+// come in at 44 a cycle from HBM, 176 bytes a cycle of the 128 it has.
+//
+// An mma of 128 rows and 16 elements takes 33 cycles with up to 32 tokens, 44 with
+// 64, 72 with 128, 80 with 144 (measured, A in TMEM); to issue one takes some 25,
+// a commit 87, a wait for a barrier that is complete 40 to 60.  So a unit has
+// eight mma: with four, 256 tokens of 64 experts (K = 7168, F = 2048 gated) took
+// 356 us, with eight 226.  There the dequantising warps bound it (instructions: 30
+// weights a cycle and SM), with 8192 rows (K = 2048, F = 7168, 166 us) the mma
+// (127 us) and the tokens' way from L2: three slots of tokens, with two stages
+// of codes more, 185 us; in pairs of blocks that load half the tokens each for
+// both 185 as well, so it is not their bytes.
 #include <cuda_bf16.h>
 
 #include "expert_w4_internal.cuh"
@@ -34,6 +44,9 @@ constexpr int kPartUnits = 512 / kK;  // units of a part of an f32 result's sum
 
 // TMEM holds two accumulators of kTok columns, so that a tile's results leave
 // while the next one is computed, and kSlots slots of 64 columns for weights.
+// kTok = 64 for few tokens, 160 beyond (with 128, experts of a little more have
+// their weights turned into bf16 twice: 8192 rows of 64 experts 199 us against
+// 183; with 192 there is room for three slots of tokens only).
 // For sums in parts the storing warps hold kTok / 2 sums a thread in registers:
 // 896 threads are launched with 72 each, the storing ones take 104 or 120, the
 // dequantising ones keep 64 or 56, the others (with an idle warp, so that they
@@ -46,8 +59,8 @@ struct Shape {
     static constexpr int kSets = kTok == 64 ? 4 : 2, kShare = 4 / kSets;  // sets; fours of warps of one, which share a unit
     static_assert(kSets <= kSlots);
     static constexpr int kHalf = kTok * 128, kRows = 2 * kHalf;  // bytes of half a unit's token rows, of a slot of them
-    static constexpr int kRowSlots = kTok == 192 ? 3 : kTok == 128 ? 4 : 6;
-    static constexpr int kCodeStages = kTok == 64 ? 5 : 3;
+    static constexpr int kRowSlots = kTok == 64 ? 6 : 4;
+    static constexpr int kCodeStages = kTok == 64 ? 5 : kParts ? 3 : 2;
     static constexpr int kThreads = 32 * (kDequantWarps + kStoreWarps + (kParts ? 4 : 3));
     static constexpr int kStoreRegs = kTok == 64 ? 104 : 120, kDequantRegs = kTok == 64 ? 64 : 56;
     static_assert(!kParts || 32 * (kStoreWarps * kStoreRegs + kDequantWarps * kDequantRegs + 4 * 40) <= kThreads * 72);
@@ -320,8 +333,10 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                         q[h] = ld_shared128(codes + ((chunk ^ (row & 7)) << 4));
                         code[h] = ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM);
                     }
-                    __syncwarp();
-                    if (lane == 0) mb_arrive(cempty + 8 * c.slot);  // all of it is in registers
+                    uint32_t loaded = 0;
+#pragma unroll
+                    for (int h = 0; h < kChunks; ++h) loaded ^= q[h].x ^ code[h];
+                    if (lane == reader_lane(loaded)) mb_arrive(cempty + 8 * c.slot);
 #pragma unroll
                     for (int h = 0; h < kChunks; ++h) {
                         const W4Scale s(code[h]);
@@ -502,8 +517,10 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
                                   cudaStream_t stream) {
     if (expert_w4_few(r, K, F, gated))
         return launch_expert_w4_few(r, K, F, gated, group, x, wq, group_scales, row_scales, y, y_f32, stream);
-    const bool parts = K > kWhole || (y_f32 && !gated), small = r.pairs <= 32 * (int64_t)r.E;
-    const int most = small ? 64 : parts ? 128 : 192;
+    // Tiles of 64 tokens up to 48 rows an expert: 32, 48 and 64 rows (64 experts, K = 7168, F = 2048 gated) take 226,
+    // 236 and 338 us with them, 259, 263 and 265 with tiles of 160.
+    const bool parts = K > kWhole || (y_f32 && !gated), small = r.pairs <= 48 * (int64_t)r.E;
+    const int most = small ? 64 : parts ? 128 : 160;
     CUtensorMap map_w;
     TokenMaps map_x;
     if (!encode_w4(&map_w, wq, r.E, K, F, gated, kM)) return cudaErrorInvalidValue;
@@ -520,11 +537,11 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
                  r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift};
     if (gated) {
         if (parts) return small ? launch<64, true, true, false>(map_w, map_x, a, stream) : launch<128, true, true, false>(map_w, map_x, a, stream);
-        return small ? launch<64, true, false, false>(map_w, map_x, a, stream) : launch<192, true, false, false>(map_w, map_x, a, stream);
+        return small ? launch<64, true, false, false>(map_w, map_x, a, stream) : launch<160, true, false, false>(map_w, map_x, a, stream);
     }
     if (y_f32) return small ? launch<64, false, true, true>(map_w, map_x, a, stream) : launch<128, false, true, true>(map_w, map_x, a, stream);
     if (parts) return small ? launch<64, false, true, false>(map_w, map_x, a, stream) : launch<128, false, true, false>(map_w, map_x, a, stream);
-    return small ? launch<64, false, false, false>(map_w, map_x, a, stream) : launch<192, false, false, false>(map_w, map_x, a, stream);
+    return small ? launch<64, false, false, false>(map_w, map_x, a, stream) : launch<160, false, false, false>(map_w, map_x, a, stream);
 }
 
 cudaError_t take_expert_w4_error(int *err) { return take_tc_error(err); }

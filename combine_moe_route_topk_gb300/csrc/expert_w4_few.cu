@@ -6,20 +6,22 @@
 // Codes come to shared memory by TMA, become bf16 in registers (w4_ops.cuh) and
 // are the A fragments of mma.sync as they are: a lane's word of eight
 // consecutive elements serves two products of 16, the order of the reduction
-// being free as long as the tokens' fragments have the same one.  tcgen05 would
-// read them from TMEM, 128 rows by 16 elements at a time, which takes it 64 to 70
-// cycles whatever the number of tokens: 32 weights a cycle where HBM brings 47.
-// mma.sync takes 2 cycles for 16 x 16 weights and eight tokens (measured), 128
-// weights a cycle.  What is left to bound it are integer instructions: 7 for eight
-// weights, of which an SM executes two warps' a cycle, 73 weights.
+// being free as long as the tokens' fragments have the same one.  mma.sync takes
+// 2 cycles of an SM for 16 x 16 weights and eight tokens (measured), 128 weights a
+// cycle where HBM brings 44; what bounds the kernel are instructions: some 320 of
+// a warp for 32 x 128 weights, 112 of them the shifts and logic that take nibbles
+// apart, 38 weights a cycle (32 of 64 experts, 7168 x 4096 each, one token: 110 us,
+// loads alone 82, floor 74).  The tensor core proper would take the same bf16 from
+// TMEM by tiles of 128 rows: more rows at once than a small call has for an SM.
 //
 // A block holds one expert's tokens, at most eight, in shared memory, in the
 // order in which lanes read them, and walks through a run of the matrices'
 // rows, in granules of 32, its share of all there are.  A unit is up to
 // 16 / split granules; the `split` warps of a granule share its reduction by
 // blocks of 128, and their sums are added up in shared memory in the warps'
-// order.  Two more warps load, one of them the groups' scales, whose copies in
-// the same warp as the codes' loads held those up.
+// order.  Two more warps load, one of them the groups' scales: their copies in
+// the same warp as the codes' loads held those up (loads alone 284 us against
+// 187, 32 tokens of 64 experts, 7168 x 4096).
 #include "expert_w4_internal.cuh"
 #include "mem_ops.cuh"
 #include "pdl.cuh"
@@ -280,8 +282,7 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) c[i] = ld_shared128(codes_at[i] + slot * kCodes);
                 const uint32_t sc = ld_shared32(scale_at + slot * kScales);
-                __syncwarp();
-                if (lane == 0) mb_arrive(empty + 8 * slot);  // all of it is in registers
+                if (lane == reader_lane(c[0].x ^ c[1].x ^ c[2].x ^ c[3].x ^ sc)) mb_arrive(empty + 8 * slot);
                 next_slot();
                 const W4Scale s[4] = {W4Scale(sc & 0xff), W4Scale(sc >> 8 & 0xff), W4Scale(sc >> 16 & 0xff), W4Scale(sc >> 24)};
 #pragma unroll
@@ -352,10 +353,21 @@ cudaError_t launch(const CodeMaps &maps, const Args &a, cudaStream_t stream) {
 
 }  // namespace
 
+// Which kernel takes a batch, by what an SM has to do at most: here granules of 32
+// rows by eight tokens, there tiles of 128 rows by 64 tokens in whole rounds.  A
+// tile takes about as long as 4.8 granules (K = 7168, F = 2048 gated, 64 experts,
+// 8 per token: 1, 2, 4, 8 and 32 tokens 37, 64, 105, 154, 221 us here and 41, 70,
+// 101, 158, 206 there, 7, 14, 27, 54, 81 granules against 2, 4, 7, 14, 15 tiles;
+// one matrix of 4096 x 7168 and 1, 8, 16, 32 tokens 13, 17, 21, 31 and 23, 23,
+// 23, 25, 1, 2, 3, 5 granules against one tile; 16 experts of 1024 x 2048, 8
+// tokens 19 and 15, 5 against 1).
 bool expert_w4_few(const ExpertRows &r, int K, int F, int gated) {
-    const int64_t wide = gated ? 2 * (int64_t)F : F;
-    return r.pairs <= 4 * (int64_t)r.E && K <= (1 << 16) && stages_of(r, K, lines_of(r)) >= 2 &&
-           (r.E + r.pairs / kTok) * (wide / kRows + 1) < (1 << 30);  // units are counted in 32 bits
+    const int64_t cols = gated ? kRows / 2 : kRows, granules = (F + cols - 1) / cols, sms = sm_count();
+    const int64_t active = r.pairs < r.E ? r.pairs : r.E;
+    auto token_tiles = [&](int64_t tokens) { return r.pairs < active + r.pairs / tokens ? r.pairs : active + r.pairs / tokens; };
+    const int64_t units = token_tiles(kTok) * granules, tiles = token_tiles(64) * ((granules + 3) / 4);
+    if (sms < 1 || K > (1 << 16) || units >= (1 << 30) || stages_of(r, K, lines_of(r)) < 2) return false;
+    return 5 * ((units + sms - 1) / sms) <= 24 * ((tiles + sms - 1) / sms);
 }
 
 cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, int group, const void *x, const void *wq,

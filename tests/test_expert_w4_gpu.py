@@ -314,3 +314,24 @@ def test_binding_refuses_other_types():
     w.wq = w.wq.to(torch.int64)
     with pytest.raises(ValueError, match="wq must be"):
         call(b, 64, 16, LINEAR, 32, x, w, y)
+
+
+@pytest.mark.parametrize("N,most,E,K,F,group", [(8, 145, 64, 2048, 3584, 32), (1, 40, 32, 4096, 2048, 32), (1, 3, 64, 7168, 1024, 32),
+                                                (1, 8, 24, 4096, 2048, 128)])
+def test_long_runs_of_tiles(N, most, E, K, F, group):
+    """Many tiles in a row for every block, at the pace of a real call: slots of shared memory are filled again as soon as
+    their readers have them in registers, not a moment before."""
+    g = torch.Generator()
+    g.manual_seed(most)
+    counts = [max(1, most - int(torch.randint(0, max(1, most // 4), (1,), generator=g))) for _ in range(E)]
+    b = Batch(N, counts, sum(counts) // N + 200)
+    x, w = b.row_values(K), Weights(b, F, K, group)
+    y = b.out(F, torch.bfloat16)
+    call(b, K, F, LINEAR, group, x, w, y)
+    want, mag = ref.product(b, x, w.w)
+    v = b.valid
+    ref.check(y[v], want[v], (ref.sum_error(K, mag) + F32_HALF * want.abs())[v], BF16_HALF, "y")
+    again = b.out(F, torch.bfloat16)
+    for _ in range(10):
+        call(b, K, F, LINEAR, group, x, w, again)
+        assert torch.equal(again.view(torch.int16), y.view(torch.int16))
