@@ -51,7 +51,7 @@ constexpr int kPartUnits = 512 / kK;  // units of a part of an f32 result's sum
 // 896 threads are launched with 72 each, the storing ones take 104 or 120, the
 // dequantising ones keep 64 or 56, the others (with an idle warp, so that they
 // are four) 40.
-template <int kTok, bool kParts, bool kF32>
+template <int kTok, bool kParts, bool kF32, bool kSplit>
 struct Shape {
     static constexpr int kSlots = (512 - 2 * kTok) / (kK / 2);
     // No more sets than slots: a set that came to a slot's use after the next would take
@@ -60,12 +60,13 @@ struct Shape {
     static_assert(kSets <= kSlots);
     static constexpr int kHalf = kTok * 128, kRows = 2 * kHalf;  // bytes of half a unit's token rows, of a slot of them
     static constexpr int kRowSlots = kTok == 64 ? 6 : 4;
-    static constexpr int kCodeStages = kTok == 64 ? 5 : kParts ? 3 : 2;
+    static constexpr int kCodeStages = kSplit ? (kF32 ? 3 : 4) : kTok == 64 ? 5 : kParts ? 3 : 2;
+    static constexpr int kJoin = kSplit ? 24 << 10 : 0;  // other blocks' sums: 8 / S warps, S - 1 blocks, 4 KB
     static constexpr int kThreads = 32 * (kDequantWarps + kStoreWarps + (kParts ? 4 : 3));
     static constexpr int kStoreRegs = kTok == 64 ? 104 : 120, kDequantRegs = kTok == 64 ? 64 : 56;
     static_assert(!kParts || 32 * (kStoreWarps * kStoreRegs + kDequantWarps * kDequantRegs + 4 * 40) <= kThreads * 72);
     static constexpr int kBuf = kF32 ? 4096 : 2048;  // a storing warp's: 32 tokens' results, to be written as whole sectors
-    static constexpr int kSmem = 1024 + kCodeStages * (kCodes + kScales) + kRowSlots * kRows + kStoreWarps * kBuf;
+    static constexpr int kSmem = 1024 + kCodeStages * (kCodes + kScales) + kRowSlots * kRows + kStoreWarps * kBuf + kJoin;
 };
 
 // Token rows by boxes of 128, 64, 32 and 16 rows of 128 bytes.
@@ -81,6 +82,7 @@ struct Args {
     void *y;
     int64_t cap, most, pairs;
     int E, L, K, F, wide, groups, group_shift;
+    int split;  // blocks that share a tile's reduction
 };
 
 __host__ __device__ constexpr int mma_tokens(int n) { return (n + 15) & ~15; }
@@ -129,23 +131,29 @@ __device__ __forceinline__ void mma_bf16_tmem(uint32_t d, uint32_t a, uint64_t b
         : "memory");
 }
 
-template <int kTok, bool kGated, bool kParts, bool kF32>
-__global__ void __launch_bounds__(Shape<kTok, kParts, kF32>::kThreads, 1)
+// kSplit: a cluster of a.split blocks (two or four) takes a tile, each a part of
+// the reduction.  Block q % S stores the rows of the tile's quarter q, and gets
+// the other blocks' sums of them in its shared memory: 32 rows by 32 tokens
+// of a storing warp at a time, added to its own in the blocks' order.
+template <int kTok, bool kGated, bool kParts, bool kF32, bool kSplit>
+__global__ void __launch_bounds__(Shape<kTok, kParts, kF32, kSplit>::kThreads, 1)
 expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x, const Args a) {
-    using S = Shape<kTok, kParts, kF32>;
+    using S = Shape<kTok, kParts, kF32, kSplit>;
+    static_assert(!kSplit || kTok == 64);  // one piece of 32 tokens a storing warp
     constexpr int kSlots = S::kSlots, kRows = S::kRows, kRowSlots = S::kRowSlots, kCodeStages = S::kCodeStages, kBuf = S::kBuf;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[2 * kCodeStages + 2 * kRowSlots + 2 * kSlots + 5];
+    __shared__ __align__(8) unsigned long long bars[2 * kCodeStages + 2 * kRowSlots + 2 * kSlots + 5 + 2 * kStoreWarps];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t rows_at = smem + kCodeStages * kCodes, scales_at = rows_at + kRowSlots * kRows,
-                   bufs_at = scales_at + kCodeStages * kScales, tables_at = bufs_at + kStoreWarps * kBuf;
+                   bufs_at = scales_at + kCodeStages * kScales, join_at = bufs_at + kStoreWarps * kBuf,
+                   tables_at = join_at + S::kJoin;
     int *tables = reinterpret_cast<int *>(smem_raw + (tables_at - smem_u32(smem_raw)));
     const uint32_t cfull = smem_u32(bars), cempty = cfull + 8 * kCodeStages, xfull = cempty + 8 * kCodeStages,
                    xempty = xfull + 8 * kRowSlots, afull = xempty + 8 * kRowSlots, aempty = afull + 8 * kSlots,
-                   tfull = aempty + 8 * kSlots, tempty = tfull + 16, done = tempty + 16;
+                   tfull = aempty + 8 * kSlots, tempty = tfull + 16, done = tempty + 16, jfull = done + 8, jfree = jfull + 8 * kStoreWarps;
     volatile int *gave_up = &s_gave_up;
     constexpr int kStoreFirst = kDequantWarps, kCodeWarp = kDequantWarps + kStoreWarps, kRowWarp = kCodeWarp + 1,
                   kMmaWarp = kCodeWarp + 2;
@@ -169,24 +177,34 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
             mb_init(tempty + 8 * i, kStoreWarps);
         }
         mb_init(done, 1);
+        for (int i = 0; kSplit && i < kStoreWarps; ++i) {
+            mb_init(jfull + 8 * i, a.split - 1);  // the other blocks' sums are here
+            mb_init(jfree + 8 * i, 1);            // this block's have been read
+        }
         s_gave_up = 0;
         mb_init_fence();
         tma_prefetch_map(&map_w);
         for (int i = map_x.first; i < 4; ++i) tma_prefetch_map(&map_x.m[i]);
     }
+    const int rank = kSplit ? same((int)cluster_rank()) : 0, split = kSplit ? a.split : 1;
     tc_fence_before();
-    __syncthreads();
+    if constexpr (kSplit) cluster_sync();
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)same((int)s_tmem), a_at = tmem + 2 * kTok;
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
     constexpr int kStep = kGated ? kM / 2 : kM;  // result columns of a tile
-    const int m_tiles = (a.F + kStep - 1) / kStep;
+    const int m_tiles = (a.F + kStep - 1) / kStep, tile0 = blockIdx.x / split, tile_step = gridDim.x / split;
     const Groups g = make_groups<0, 0, 1>(
-        tables, a.offsets, a.E, a.L, a.cap, a.most, a.pairs, gridDim.x,
+        tables, a.offsets, a.E, a.L, a.cap, a.most, a.pairs, tile_step,
         [&](int c, int) { return token_tiles<kTok>(c) * m_tiles; }, [](int) { return 0; });  // syncs the block
-    const int tiles = same(g.prefix[a.E]), units = (a.K + kK - 1) / kK;
-    const int part = kParts ? kPartUnits : units;  // units that are summed in TMEM
+    const int tiles = same(g.prefix[a.E]);
+    // this block's units of a tile: whole stages of codes
+    const int all = (a.K + kK - 1) / kK, stages = (all + kUnits - 1) / kUnits;
+    const int first = kSplit ? stages * rank / split * kUnits : 0;
+    const int units = kSplit ? min(all, stages * (rank + 1) / split * kUnits) : all;
+    const int part = kParts ? kPartUnits : units - first;  // units that are summed in TMEM
 
     if constexpr (kParts) {
         if (warp < kDequantWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kDequantRegs));
@@ -198,7 +216,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         int e = 0;
         bool ok = true;
         const int per_stage = 256 >> a.group_shift;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
             const Tile w = get_tile<kTok>(g, a.E, e, t, kStep);
             e = w.e;
             // lanes copy the scales of four matrix rows each
@@ -210,7 +228,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 f += (lane & 2) ? a.F : 0;
             }
             const uint8_t *scales = a.group_scales + (int64_t)w.e * a.groups * a.wide + (inside ? f : 0);
-            for (int u = 0, b = 0; u < units; u += kUnits) {
+            for (int u = first, b = first / kUnits * per_stage; u < units; u += kUnits) {
                 ok = mb_wait_warp(cempty + 8 * r.slot, r.phase ^ 1u, gave_up);
                 if (!ok) break;
                 const uint32_t bar = cfull + 8 * r.slot;
@@ -236,11 +254,11 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         Ring<kRowSlots> r;
         int e = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
             const Tile w = get_tile<kTok>(g, a.E, e, t, kStep);
             e = w.e;
             const int n = mma_tokens(w.n);
-            for (int u = 0; u < units; ++u) {
+            for (int u = first; u < units; ++u) {
                 ok = mb_wait_warp(xempty + 8 * r.slot, r.phase ^ 1u, gave_up);
                 if (!ok) break;
                 if (elect_one()) {
@@ -272,11 +290,11 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         Ring<2> acc;
         int e = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
             const Tile w = get_tile<kTok>(g, a.E, e, t, kStep);
             e = w.e;
             const uint32_t desc = mma_desc(1, false, false, kM, mma_tokens(w.n));
-            for (int u0 = 0; u0 < units && ok; u0 += part) {
+            for (int u0 = first; u0 < units && ok; u0 += part) {
                 const uint32_t d = tmem + acc.slot * kTok;
                 ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
                 for (int u = u0; u < min(u0 + part, units) && ok; ++u) {
@@ -313,8 +331,8 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         Ring<kSlots> r;  // of the next unit
         bool ok = true;
         int turn = 0;    // the set that takes it
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            for (int u0 = 0; u0 < units && ok; u0 += kUnits) {
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
+            for (int u0 = first; u0 < units && ok; u0 += kUnits) {
                 const int n = min(kUnits, units - u0);
                 const int mine = (set - turn) & (kSets - 1);  // this set's unit of the stage, if below n
                 turn = (turn + n) & (kSets - 1);
@@ -426,10 +444,44 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
             }
             __syncwarp();
         };
+        // Joins the blocks' sums of 32 tokens, v(0) to v(31): the owner of the quarter gets them all, the others give
+        // theirs.  A block's sums leave for the owner's memory once what it gave before has been read.
+        const int me = warp - kStoreFirst, owner = quarter % split;
+        uint32_t given = 0;  // parity of the next join
+        auto join = [&](float (&v)[32]) {
+            const uint32_t slot = join_at + (quarter / split * 2 + half) * (split - 1) * 4096 + lane * 16;
+            if (rank != owner) {
+                if (!mb_wait_warp_pair(jfree + 8 * me, given ^ 1u, gave_up, kPolls + all * kStepPolls)) return false;
+                const uint32_t to = at_rank(slot + (rank - (rank > owner)) * 4096, owner);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    st_remote128(to + j * 512, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mb_arrive_remote(at_rank(jfull + 8 * me, owner));
+            } else {
+                if (!mb_wait_warp_pair(jfull + 8 * me, given, gave_up, kPolls + all * kStepPolls)) return false;
+                for (int b = 0; b < split - 1; ++b) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 o = ld_shared128(slot + b * 4096 + j * 512);
+                        v[4 * j] += __uint_as_float(o.x);
+                        v[4 * j + 1] += __uint_as_float(o.y);
+                        v[4 * j + 2] += __uint_as_float(o.z);
+                        v[4 * j + 3] += __uint_as_float(o.w);
+                    }
+                }
+            }
+            given ^= 1u;
+            return true;
+        };
+        auto joined = [&] {  // what the others gave is stored: they may give again
+            if (rank == owner && lane < split && lane != rank) mb_arrive_remote_relaxed(at_rank(jfree + 8 * me, lane));
+        };
         Ring<2> acc;
         int e = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
             const Tile w = get_tile<kTok>(g, a.E, e, t, kStep);
             e = w.e;
             const int f = w.m0 + quarter * (kGated ? 16 : 32) + fl;
@@ -442,7 +494,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 for (int i = 0; i < kTok / 64; ++i)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
-                for (int u0 = 0; u0 < units; u0 += part) {
+                for (int u0 = first; u0 < units; u0 += part) {
                     ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + part * kStepPolls);
                     if (!ok) break;
                     tc_fence_after();
@@ -463,27 +515,53 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < kTok / 64; ++i) {
-                    if (64 * i + 32 * half < w.n) store(w, 64 * i + 32 * half, scale, [&](int j) { return sum[i][j]; });
+                    if (64 * i + 32 * half >= w.n) continue;
+                    if constexpr (kSplit) {
+                        ok = join(sum[i]);
+                        if (!ok || rank != owner) break;
+                    }
+                    store(w, 64 * i + 32 * half, scale, [&](int j) { return sum[i][j]; });
+                    if constexpr (kSplit) joined();
                 }
             } else {  // straight from TMEM
                 ok = mb_wait_warp(tfull + 8 * acc.slot, acc.phase, gave_up, kPolls + units * kStepPolls);
                 if (!ok) break;
                 tc_fence_after();
-                for (int c0 = 0; 32 * half + c0 < w.n; c0 += 64) {
-                    uint32_t v[32];
-                    tmem_load32(src + acc.slot * kTok + c0, v);
-                    store(w, c0 + 32 * half, scale, [&](int j) { return __uint_as_float(v[j]); });
+                if constexpr (kSplit) {
+                    float v[32];
+                    const bool some = 32 * half < w.n;
+                    if (some) tmem_load32(src + acc.slot * kTok, reinterpret_cast<uint32_t *>(v));
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(tempty + 8 * acc.slot);
+                    acc.next();
+                    if (!some) continue;
+                    ok = join(v);
+                    if (!ok) break;
+                    if (rank == owner) {
+                        store(w, 32 * half, scale, [&](int j) { return v[j]; });
+                        joined();
+                    }
+                } else {
+                    for (int c0 = 0; 32 * half + c0 < w.n; c0 += 64) {
+                        uint32_t v[32];
+                        tmem_load32(src + acc.slot * kTok + c0, v);
+                        store(w, c0 + 32 * half, scale, [&](int j) { return __uint_as_float(v[j]); });
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(tempty + 8 * acc.slot);
+                    acc.next();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mb_arrive(tempty + 8 * acc.slot);
-                acc.next();
             }
         }
+        // The owner's last arrival must not come after this block is gone.
+        if (kSplit && ok && rank != owner) mb_wait_warp(jfree + 8 * me, given ^ 1u, gave_up, kPolls + all * kStepPolls);
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if constexpr (kSplit) cluster_sync();  // no block leaves while another may reach it
+    else __syncthreads();
     tc_fence_after();
     if (tid == 0 && s_gave_up) record_timeout();
     if (warp == kMmaWarp) tmem_free(tmem, 512);
@@ -491,17 +569,15 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 
 template <int kTok, bool kGated, bool kParts, bool kF32>
 cudaError_t launch(const CUtensorMap &map_w, const TokenMaps &map_x, const Args &a, cudaStream_t stream) {
-    auto kern = expert_w4_kernel<kTok, kGated, kParts, kF32>;
-    using S = Shape<kTok, kParts, kF32>;
+    auto kern = expert_w4_kernel<kTok, kGated, kParts, kF32, false>;
+    using S = Shape<kTok, kParts, kF32, false>;
     static_assert(S::kSmem + groups_bytes(1024) <= kMostSharedW4);
     static thread_local AttrCache attr;
     cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), S::kSmem + groups_bytes(1024));
     if (e != cudaSuccess) return e;
-    const int sms = sm_count();
-    if (sms < 1) return cudaErrorInvalidDevice;
     cudaLaunchAttribute pdl[1] = {pdl_attribute()};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)sms);
+    cfg.gridDim = dim3((unsigned)sm_count());
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem + groups_bytes(a.E);
     cfg.stream = stream;
@@ -510,16 +586,47 @@ cudaError_t launch(const CUtensorMap &map_w, const TokenMaps &map_x, const Args 
     return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, a);
 }
 
+template <bool kGated, bool kParts, bool kF32>
+cudaError_t launch_split(const CUtensorMap &map_w, const TokenMaps &map_x, const Args &a, cudaStream_t stream) {
+    auto kern = expert_w4_kernel<64, kGated, kParts, kF32, true>;
+    using S = Shape<64, kParts, kF32, true>;
+    static_assert(S::kSmem + groups_bytes(1024) <= kMostSharedW4);
+    static thread_local PairCache caches[2];
+    PairLaunch l(S::kThreads, S::kSmem + groups_bytes(1024), stream, a.split);
+    PairCache &cache = caches[a.split == 4];
+    cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), l.cfg, a.split);
+    if (e != cudaSuccess) return e;
+    l.cfg.gridDim = dim3((unsigned)cache.blocks);
+    l.cfg.dynamicSmemBytes = S::kSmem + groups_bytes(a.E);
+    return cudaLaunchKernelEx(&l.cfg, kern, map_w, map_x, a);
+}
+
+// kTok = 64 (alone or split), or the most that TMEM and the registers hold.
+template <bool kGated, bool kParts, bool kF32>
+cudaError_t launch_any(bool small, const CUtensorMap &map_w, const TokenMaps &map_x, const Args &a, cudaStream_t stream) {
+    if (a.split > 1) return launch_split<kGated, kParts, kF32>(map_w, map_x, a, stream);
+    return small ? launch<64, kGated, kParts, kF32>(map_w, map_x, a, stream)
+                 : launch<kParts ? 128 : 160, kGated, kParts, kF32>(map_w, map_x, a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, int group, const void *x,
                                   const void *wq, const void *group_scales, const float *row_scales, void *y, int y_f32,
                                   cudaStream_t stream) {
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
     if (expert_w4_few(r, K, F, gated))
         return launch_expert_w4_few(r, K, F, gated, group, x, wq, group_scales, row_scales, y, y_f32, stream);
+    const bool parts = K > kWhole || (y_f32 && !gated);
+    // Where all tiles of 64 tokens leave half or more of the SMs idle, two or four blocks share one.
+    const int64_t active = r.pairs < r.E ? r.pairs : r.E, step = gated ? kM / 2 : kM;
+    const int64_t tiles = (r.pairs < active + r.pairs / 64 ? r.pairs : active + r.pairs / 64) * ((F + step - 1) / step);
+    const int stages = (K + kUnits * kK - 1) / (kUnits * kK);
+    const int split = tiles * 4 <= sms && stages >= 4 ? 4 : tiles * 2 <= sms && stages >= 2 ? 2 : 1;
     // Tiles of 64 tokens up to 48 rows an expert: 32, 48 and 64 rows (64 experts, K = 7168, F = 2048 gated) take 226,
     // 236 and 338 us with them, 259, 263 and 265 with tiles of 160.
-    const bool parts = K > kWhole || (y_f32 && !gated), small = r.pairs <= 48 * (int64_t)r.E;
+    const bool small = split > 1 || r.pairs <= 48 * (int64_t)r.E;
     const int most = small ? 64 : parts ? 128 : 160;
     CUtensorMap map_w;
     TokenMaps map_x;
@@ -534,14 +641,10 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
     int shift = 5;
     while ((1 << shift) < group) ++shift;
     const Args a{r.offsets, static_cast<const uint8_t *>(group_scales), row_scales, y, r.cap, r.most, r.pairs,
-                 r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift};
-    if (gated) {
-        if (parts) return small ? launch<64, true, true, false>(map_w, map_x, a, stream) : launch<128, true, true, false>(map_w, map_x, a, stream);
-        return small ? launch<64, true, false, false>(map_w, map_x, a, stream) : launch<160, true, false, false>(map_w, map_x, a, stream);
-    }
-    if (y_f32) return small ? launch<64, false, true, true>(map_w, map_x, a, stream) : launch<128, false, true, true>(map_w, map_x, a, stream);
-    if (parts) return small ? launch<64, false, true, false>(map_w, map_x, a, stream) : launch<128, false, true, false>(map_w, map_x, a, stream);
-    return small ? launch<64, false, false, false>(map_w, map_x, a, stream) : launch<160, false, false, false>(map_w, map_x, a, stream);
+                 r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift, split};
+    if (gated) return parts ? launch_any<true, true, false>(small, map_w, map_x, a, stream) : launch_any<true, false, false>(small, map_w, map_x, a, stream);
+    if (y_f32) return launch_any<false, true, true>(small, map_w, map_x, a, stream);
+    return parts ? launch_any<false, true, false>(small, map_w, map_x, a, stream) : launch_any<false, false, false>(small, map_w, map_x, a, stream);
 }
 
 cudaError_t take_expert_w4_error(int *err) { return take_tc_error(err); }

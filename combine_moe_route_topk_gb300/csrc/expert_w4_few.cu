@@ -35,7 +35,7 @@ constexpr int kWarps = 16, kThreads = 32 * (kWarps + 2);
 constexpr int kTokShift = 3, kTok = 1 << kTokShift;
 constexpr int kRows = 32;        // matrix rows of a granule, which a warp takes: two of mma's 16
 constexpr int kK = 128;          // reduction elements of its step: 16 bytes of codes a lane and row
-constexpr int kPartSteps = 4;    // steps of a part of a sum: 512 elements
+constexpr int kPartSteps = 4;    // steps of a part of an f32 result's sum: 512 elements (bf16 ones: all of a warp's, at most 2^14)
 constexpr int kCodes = kWarps * kRows * kK / 2, kScales = kWarps * kRows * kK / 32;  // bytes of a stage: a step of every warp
 constexpr int kMostStages = 6;
 constexpr int kSums = kRows * kTok;
@@ -298,7 +298,7 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
                         mma_m16n8k16(acc + 4 * m, top[2], low[2], top[3], low[3], b.z, b.w);
                     }
                 }
-                if ((r & (kPartSteps - 1)) == kPartSteps - 1 || r == mine - 1) {
+                if (kF32 && ((r & (kPartSteps - 1)) == kPartSteps - 1 || r == mine - 1)) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) sum[i] += acc[i], acc[i] = 0.f;
                 }
@@ -308,7 +308,7 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
             if (!ok) break;
             float *to = red + buf * (kWarps * (kSumLine + kRows));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) to[warp * kSumLine + i * 32 + lane] = sum[i];
+            for (int i = 0; i < 8; ++i) to[warp * kSumLine + i * 32 + lane] = kF32 ? sum[i] : acc[i];
             to[kWarps * kSumLine + tid] = scale;
             __syncwarp();
             if (lane == 0) mb_arrive(summed);
@@ -366,7 +366,7 @@ bool expert_w4_few(const ExpertRows &r, int K, int F, int gated) {
     const int64_t active = r.pairs < r.E ? r.pairs : r.E;
     auto token_tiles = [&](int64_t tokens) { return r.pairs < active + r.pairs / tokens ? r.pairs : active + r.pairs / tokens; };
     const int64_t units = token_tiles(kTok) * granules, tiles = token_tiles(64) * ((granules + 3) / 4);
-    if (sms < 1 || K > (1 << 16) || units >= (1 << 30) || stages_of(r, K, lines_of(r)) < 2) return false;
+    if (sms < 1 || K > (1 << 15) || units >= (1 << 30) || stages_of(r, K, lines_of(r)) < 2) return false;
     return 5 * ((units + sms - 1) / sms) <= 24 * ((tiles + sms - 1) / sms);
 }
 

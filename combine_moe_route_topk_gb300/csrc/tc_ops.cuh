@@ -323,6 +323,15 @@ __device__ __forceinline__ uint32_t at_leader(uint32_t addr) {  // the same plac
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
     return r;
 }
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {  // in another block's
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_remote128(uint32_t addr, const float4 &v) {  // addr from at_rank
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
 // Arrives at a barrier of the leader (bar from at_leader).  The released form
 // orders the thread's writes before it, for which it waits until its global
 // stores have reached L2: 2000 to 3400 cycles after a tile's results.  What
@@ -601,16 +610,16 @@ struct AttrCache {
     }
 };
 
-// Launch of a persistent kernel in clusters of two blocks.
+// Launch of a persistent kernel in clusters of two blocks (or of another number).
 struct PairLaunch {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
-    PairLaunch(int threads, int smem, cudaStream_t stream) {
+    PairLaunch(int threads, int smem, cudaStream_t stream, int cluster = 2) {
         attr[0] = pdl_attribute();
         attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.x = cluster;
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(2);
+        cfg.gridDim = dim3(cluster);
         cfg.blockDim = dim3(threads);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
@@ -626,14 +635,14 @@ struct PairCache {
     AttrCache attr;
     int dev = -1, blocks = 0;
     unsigned long long ctx = 0;
-    cudaError_t prepare(const void *kernel, const cudaLaunchConfig_t &cfg) {  // cfg with the most shared memory
+    cudaError_t prepare(const void *kernel, const cudaLaunchConfig_t &cfg, int cluster = 2) {  // cfg with the most shared memory
         cudaError_t e = attr.allow_smem(kernel, (int)cfg.dynamicSmemBytes);
         if (e != cudaSuccess || (blocks > 0 && dev == attr.dev && ctx == attr.ctx && ctx != 0)) return e;
         int clusters = 0;
         e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
         if (e != cudaSuccess) return e;
         if (clusters < 1) return cudaErrorLaunchOutOfResources;
-        blocks = 2 * clusters;
+        blocks = cluster * clusters;
         dev = attr.dev;
         ctx = attr.ctx;
         return cudaSuccess;

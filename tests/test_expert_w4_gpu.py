@@ -318,20 +318,49 @@ def test_binding_refuses_other_types():
 
 @pytest.mark.parametrize("N,most,E,K,F,group", [(8, 145, 64, 2048, 3584, 32), (1, 40, 32, 4096, 2048, 32), (1, 3, 64, 7168, 1024, 32),
                                                 (1, 8, 24, 4096, 2048, 128)])
-def test_long_runs_of_tiles(N, most, E, K, F, group):
+@pytest.mark.parametrize("form", ["bf16", "f32", "gated"])
+def test_long_runs_of_tiles(N, most, E, K, F, group, form):
     """Many tiles in a row for every block, at the pace of a real call: slots of shared memory are filled again as soon as
     their readers have them in registers, not a moment before."""
     g = torch.Generator()
     g.manual_seed(most)
     counts = [max(1, most - int(torch.randint(0, max(1, most // 4), (1,), generator=g))) for _ in range(E)]
     b = Batch(N, counts, sum(counts) // N + 200)
-    x, w = b.row_values(K), Weights(b, F, K, group)
-    y = b.out(F, torch.bfloat16)
-    call(b, K, F, LINEAR, group, x, w, y)
+    x, w = b.row_values(K), Weights(b, 2 * F if form == "gated" else F, K, group)
+    t = torch.float32 if form == "f32" else torch.bfloat16
+    act = SWIGLU if form == "gated" else LINEAR
+    y = b.out(F, t)
+    call(b, K, F, act, group, x, w, y, form == "f32")
     want, mag = ref.product(b, x, w.w)
     v = b.valid
-    ref.check(y[v], want[v], (ref.sum_error(K, mag) + F32_HALF * want.abs())[v], BF16_HALF, "y")
-    again = b.out(F, torch.bfloat16)
+    err = (ref.sum_error(K, mag) + F32_HALF * want.abs())[v]
+    if form == "gated":
+        want, err = ref.swiglu(want[v, :F], want[v, F:], err[:, :F], err[:, F:])
+        ref.check(y[v], want, err, BF16_HALF, "y")
+    else:
+        ref.check(y[v], want[v], err, F32_HALF if form == "f32" else BF16_HALF, "y")
+    again = b.out(F, t)
     for _ in range(10):
-        call(b, K, F, LINEAR, group, x, w, again)
-        assert torch.equal(again.view(torch.int16), y.view(torch.int16))
+        call(b, K, F, act, group, x, w, again, form == "f32")
+        assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("T", [33, 64, 65, 128, 200])
+@pytest.mark.parametrize("K,F", [(512, 264), (1056, 512), (7168, 1032), (2304, 4096)])
+@pytest.mark.parametrize("form", ["bf16", "f32", "gated"])
+def test_dense_layer_of_some_tokens(T, K, F, form):
+    """Few tiles: two or four blocks share a reduction and join their sums."""
+    b = Batch(1, [T], T)
+    x, w = b.row_values(K), Weights(b, 2 * F if form == "gated" else F, K, 32)
+    y = b.out(F, torch.float32 if form == "f32" else torch.bfloat16)
+    act = SWIGLU if form == "gated" else LINEAR
+    call(b, K, F, act, 32, x, w, y, form == "f32")
+    want, mag = ref.product(b, x, w.w)
+    err = ref.sum_error(K, mag) + F32_HALF * want.abs()
+    if form == "gated":
+        want, err = ref.swiglu(want[:, :F], want[:, F:], err[:, :F], err[:, F:])
+    ref.check(y, want, err, F32_HALF if form == "f32" else BF16_HALF, "y")
+    again = torch.empty_like(y)
+    for _ in range(5):
+        call(b, K, F, act, 32, x, w, again, form == "f32")
+        assert torch.equal(again, y)
