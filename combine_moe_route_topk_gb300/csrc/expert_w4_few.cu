@@ -353,21 +353,20 @@ cudaError_t launch(const CodeMaps &maps, const Args &a, cudaStream_t stream) {
 
 }  // namespace
 
-// Which kernel takes a batch, by what an SM has to do at most: here granules of 32
-// rows by eight tokens, there tiles of 128 rows by 64 tokens in whole rounds.  A
-// tile takes about as long as 4.8 granules (K = 7168, F = 2048 gated, 64 experts,
-// 8 per token: 1, 2, 4, 8 and 32 tokens 37, 64, 105, 154, 221 us here and 41, 70,
-// 101, 158, 206 there, 7, 14, 27, 54, 81 granules against 2, 4, 7, 14, 15 tiles;
-// one matrix of 4096 x 7168 and 1, 8, 16, 32 tokens 13, 17, 21, 31 and 23, 23,
-// 23, 25, 1, 2, 3, 5 granules against one tile; 16 experts of 1024 x 2048, 8
-// tokens 19 and 15, 5 against 1).
-bool expert_w4_few(const ExpertRows &r, int K, int F, int gated) {
+// Which kernel takes a batch, by what an SM has to do at most: here `share`
+// granules of 32 rows by eight tokens, there `rounds` of tiles of 128 rows by 64
+// tokens, each in `split` blocks.  A tile takes as long as four granules, or more.
+// Here against there, us (granules : tiles / split), K = 7168, F = 2048 gated, 8 of
+// 64 experts a token: 1, 2, 4, 8, 32 tokens 37 : 44 (7 : 2), 64 : 74 (14 : 4),
+// 105 : 101 (27 : 7), 154 : 158 (54 : 14), 222 : 206 (75 : 15); one matrix of 4096
+// x 7168, 1, 8, 16 tokens 15 : 17, 18 : 17, 23 : 17 (1, 1, 2 : 1 / 4); 8 tokens of
+// 16 experts of 1024 x 2048, of 8 of 2048 x 4096 19 : 15, 21 : 19 (4 : 1).
+bool expert_w4_few(const ExpertRows &r, int K, int F, int gated, int64_t rounds, int split) {
     const int64_t cols = gated ? kRows / 2 : kRows, granules = (F + cols - 1) / cols, sms = sm_count();
-    const int64_t active = r.pairs < r.E ? r.pairs : r.E;
-    auto token_tiles = [&](int64_t tokens) { return r.pairs < active + r.pairs / tokens ? r.pairs : active + r.pairs / tokens; };
-    const int64_t units = token_tiles(kTok) * granules, tiles = token_tiles(64) * ((granules + 3) / 4);
-    if (sms < 1 || K > (1 << 15) || units >= (1 << 30) || stages_of(r, K, lines_of(r)) < 2) return false;
-    return 5 * ((units + sms - 1) / sms) <= 24 * ((tiles + sms - 1) / sms);
+    const int64_t active = r.pairs < r.E ? r.pairs : r.E, units = (active + (r.pairs - active) / kTok) * granules;
+    if (K > (1 << 15) || units >= (1 << 30) || stages_of(r, K, lines_of(r)) < 2) return false;
+    const int64_t share = (units + sms - 1) / sms;
+    return share * split < 4 * rounds || (share == 1 && lines_of(r) <= 4);
 }
 
 cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, int group, const void *x, const void *wq,
@@ -378,8 +377,7 @@ cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, i
     // Four warps share a granule, so that a block's units are 128 rows: whole
     // boxes and lines of scales.  More, where a block has less than that to do
     // (one matrix of 4096 x 7168: 15 us with 16 warps a granule, 17 with four).
-    const int64_t active = r.pairs < r.E ? r.pairs : r.E, sms = sm_count();
-    const int64_t share = sms > 0 ? (active * granules + sms - 1) / sms : 1;
+    const int64_t active = r.pairs < r.E ? r.pairs : r.E, sms = sm_count(), share = (active * granules + sms - 1) / sms;
     int split = blocks > 2 ? 2 : 1;  // two at least: a line of shared memory has two blocks
     while (split < 4 && (share << (split + 1)) <= kWarps && (2 << split) <= blocks) ++split;
     CodeMaps maps;

@@ -11,8 +11,9 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
                                   cudaStream_t stream);
 cudaError_t take_expert_w4_error(int *err);
 
-// The form for experts with few rows: whether it takes a batch, and its launch.
-bool expert_w4_few(const ExpertRows &r, int K, int F, int gated);
+// The form for experts with few rows: whether it takes a batch that the other
+// would do in `rounds` of tiles, each in `split` blocks, and its launch.
+bool expert_w4_few(const ExpertRows &r, int K, int F, int gated, int64_t rounds, int split);
 cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, int group, const void *x, const void *wq,
                                  const void *group_scales, const float *row_scales, void *y, int y_f32,
                                  cudaStream_t stream);
