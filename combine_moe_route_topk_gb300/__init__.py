@@ -331,14 +331,18 @@ def dispatch_fused_quant(dims: MoeDims, logits, bias, score_fn, renormalize, x, 
         _stream(stream)))
 
 
-def _expert_call(dims: MoeDims, stream):
-    """(rows of the receive buffers, current device, stream handle) of a call."""
+def _place(stream):
+    """(current device, stream handle) of a call."""
     try:
         dev = _current_device()
-    except RuntimeError:  # no driver: every tensor is refused below
-        return dims.N * buffer_sizes(dims)["cap_rows"], None, None
-    return (dims.N * buffer_sizes(dims)["cap_rows"], dev,
-            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    except RuntimeError:  # no driver: every tensor is refused by _on
+        return None, None
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _expert_call(dims: MoeDims, stream):
+    """(rows of the receive buffers, current device, stream handle) of a call."""
+    return dims.N * buffer_sizes(dims)["cap_rows"], *_place(stream)
 
 
 def _on(dev, t, nbytes: int, name: str, dtype):
@@ -478,7 +482,7 @@ def combine_grad(dims: MoeDims, dout, y, pos, topk_w, dy, dtopk_w, stream=None):
     """Gradient of combine: rows dy[pos] = topk_w * dout and dtopk_w = <dout, y[pos]>."""
     s = buffer_sizes(dims)
     yt = _TORCH_DTYPE[dims.y_dtype]
-    (_, dev, st), f32 = _expert_call(dims, stream), torch.float32
+    (dev, st), f32 = _place(stream), torch.float32
     _check(lib().moe_combine_grad(
         ctypes.byref(dims), _on(dev, dout, s["out_bytes"], "dout", yt), _on(dev, y, s["y_bytes"], "y", yt),
         _on(dev, pos, s["pos_bytes"], "pos", torch.int32), _on(dev, topk_w, s["topk_w_bytes"], "topk_w", f32),
@@ -490,7 +494,7 @@ def dispatch_grad(dims: MoeDims, dpacked, pos, dx, add=None, stream=None):
     None, or dx itself)."""
     s = buffer_sizes(dims)
     xt = _TORCH_DTYPE[dims.x_dtype]
-    _, dev, st = _expert_call(dims, stream)
+    dev, st = _place(stream)
     _check(lib().moe_dispatch_grad(
         ctypes.byref(dims), _on(dev, dpacked, s["packed_x_bytes"], "dpacked", xt),
         _on(dev, pos, s["pos_bytes"], "pos", torch.int32),
@@ -502,7 +506,7 @@ def route_grad(dims: MoeDims, logits, bias, score_fn, renormalize, topk_idx, top
     """Gradient of route_topk's weights: dlogits, and their sum over the tokens as the gradient of
     a bias that is added to the logits."""
     s = buffer_sizes(dims)
-    (_, dev, st), f32 = _expert_call(dims, stream), torch.float32
+    (dev, st), f32 = _place(stream), torch.float32
     _check(lib().moe_route_grad(
         ctypes.byref(dims), _on(dev, logits, s["logits_bytes"], "logits", f32),
         None if bias is None else _on(dev, bias, dims.E * 4, "bias", f32), int(score_fn), int(bool(renormalize)),

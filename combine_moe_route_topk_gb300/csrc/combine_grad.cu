@@ -16,35 +16,44 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
 
-// The token's pairs that have a row, in k order, by the block's first warp:
-// s_p their rows, s_k their places k.  Returns (after a barrier) their number.
+// The threads that share a token: the whole block, or a warp where rows are short.
+template <int kGroup>
+__device__ __forceinline__ void group_sync() {
+    if constexpr (kGroup == 32) __syncwarp();
+    else __syncthreads();
+}
+
+// What a group knows of its token: its pairs that have a row, in k order.
+struct Pairs {
+    int row[32], k[32], n;  // rows, places k, number
+};
+
+// Fills it, by the group's first warp, and syncs the group.
+template <int kGroup>
 __device__ __forceinline__ int gather_pairs(const int32_t *__restrict__ pos, int64_t g, int R, int64_t rows_total,
-                                            int *s_p, int *s_k, int *s_n) {
-    const int tid = threadIdx.x;
-    if (tid < 32) {
-        const int p = tid < R ? __ldg(pos + g * R + tid) : -1;
+                                            Pairs &s) {
+    const int t = threadIdx.x % kGroup;
+    if (t < 32) {
+        const int p = t < R ? __ldg(pos + g * R + t) : -1;
         const bool in = p >= 0 && (int64_t)p < rows_total;
         const unsigned m = __ballot_sync(0xffffffffu, in);
         if (in) {
-            const int j = __popc(m & ((1u << tid) - 1u));
-            s_p[j] = p;
-            s_k[j] = tid;
+            const int j = __popc(m & ((1u << t) - 1u));
+            s.row[j] = p;
+            s.k[j] = t;
         }
-        if (tid == 0) *s_n = __popc(m);
+        if (t == 0) s.n = __popc(m);
     }
-    __syncthreads();
-    return *s_n;
+    group_sync<kGroup>();
+    return s.n;
 }
 
 // ---- combine ----------------------------------------------------------------
 
-// Pairs whose rows a thread loads together.
-constexpr int kPairs = 8;
-// Vectors of a row that go into one f32 sum per thread before the block adds
+// Vectors of a row that go into one f32 sum per thread before the group adds
 // its threads' sums up and the total in 64 bits: 32 vectors a thread.
-constexpr int kChunk = 32 * kThreads;
+constexpr int kRun = 32;
 
 template <int kBf16>
 struct Pair;
@@ -70,23 +79,27 @@ struct Pair<0> {
     }
 };
 
-template <int kBf16>
+// kPairs: pairs whose rows a thread loads together, kU vectors of each: what is
+// under way is kPairs * kU loads a thread whatever R is.
+template <int kBf16, int kGroup, int kPairs, int kU>
 __global__ void __launch_bounds__(kThreads)
 combine_grad_kernel(const uint4 *__restrict__ dout, const uint4 *__restrict__ y, const int32_t *__restrict__ pos,
                     const float *__restrict__ topk_w, int64_t NT, int R, int nvec, int64_t rows_total,
                     uint4 *__restrict__ dy, float *__restrict__ dtopk_w) {
     using VT = Vec<kBf16>;
-    __shared__ int s_p[32], s_k[32], s_n;
-    __shared__ float s_w[32], s_sum[kWarps][kPairs];
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    constexpr int kGroups = kThreads / kGroup, kWarps = kGroup / 32, kChunk = kRun * kGroup;
+    __shared__ Pairs s_pairs[kGroups];
+    __shared__ float s_w[kGroups][32], s_sum[kGroups][kWarps][kPairs];
+    const int which = threadIdx.x / kGroup, t = threadIdx.x % kGroup, warp = t / 32, lane = t % 32;
+    Pairs &s = s_pairs[which];
     grid_dependency_wait();  // every input comes from earlier kernels
     grid_launch_dependents();
-    for (int64_t g = blockIdx.x; g < NT; g += gridDim.x) {
-        if (tid < 32 && tid < R) {
-            s_w[tid] = __ldg(topk_w + g * R + tid);
-            dtopk_w[g * R + tid] = 0.f;  // stays where there is no row
+    for (int64_t g = (int64_t)blockIdx.x * kGroups + which; g < NT; g += (int64_t)gridDim.x * kGroups) {
+        if (t < R) {  // R <= 32
+            s_w[which][t] = __ldg(topk_w + g * R + t);
+            dtopk_w[g * R + t] = 0.f;  // stays where there is no row
         }
-        const int n = gather_pairs(pos, g, R, rows_total, s_p, s_k, &s_n);
+        const int n = gather_pairs<kGroup>(pos, g, R, rows_total, s);
         for (int j0 = 0; j0 < n; j0 += kPairs) {
             double total = 0.0;  // thread j < kPairs: of pair j0 + j
             for (int c1 = 0; c1 < nvec; c1 += kChunk) {
@@ -94,21 +107,31 @@ combine_grad_kernel(const uint4 *__restrict__ dout, const uint4 *__restrict__ y,
 #pragma unroll
                 for (int j = 0; j < kPairs; ++j) acc[j] = 0.f;
                 const int end = min(nvec, c1 + kChunk);
-                for (int c = c1 + tid; c < end; c += kThreads) {
-                    uint4 v[kPairs];
+                for (int c = c1 + t; c < end; c += kGroup * kU) {
+                    uint4 v[kU][kPairs], d[kU];
 #pragma unroll
-                    for (int j = 0; j < kPairs; ++j)
-                        v[j] = j0 + j < n ? ld_stream(y + (int64_t)s_p[j0 + j] * nvec + c) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint4 d = __ldg(dout + g * nvec + c);
+                    for (int u = 0; u < kU; ++u) {
+                        const int cu = c + u * kGroup;
 #pragma unroll
-                    for (int j = 0; j < kPairs; ++j) {
-                        if (j0 + j < n) {
-                            acc[j] = Pair<kBf16>::dot(acc[j], d, v[j]);
-                            float o[VT::kElems];
+                        for (int j = 0; j < kPairs; ++j)
+                            v[u][j] = cu < end && j0 + j < n ? ld_stream(y + (int64_t)s.row[j0 + j] * nvec + cu)
+                                                             : make_uint4(0u, 0u, 0u, 0u);
+                        d[u] = cu < end ? __ldg(dout + g * nvec + cu) : make_uint4(0u, 0u, 0u, 0u);
+                    }
 #pragma unroll
-                            for (int i = 0; i < VT::kElems; ++i) o[i] = 0.f;
-                            VT::fma(o, s_w[s_k[j0 + j]], d);
-                            dy[(int64_t)s_p[j0 + j] * nvec + c] = VT::pack(o);
+                    for (int u = 0; u < kU; ++u) {
+                        const int cu = c + u * kGroup;
+                        if (cu >= end) break;
+#pragma unroll
+                        for (int j = 0; j < kPairs; ++j) {
+                            if (j0 + j < n) {
+                                acc[j] = Pair<kBf16>::dot(acc[j], d[u], v[u][j]);
+                                float o[VT::kElems];
+#pragma unroll
+                                for (int i = 0; i < VT::kElems; ++i) o[i] = 0.f;
+                                VT::fma(o, s_w[which][s.k[j0 + j]], d[u]);
+                                dy[(int64_t)s.row[j0 + j] * nvec + cu] = VT::pack(o);
+                            }
                         }
                     }
                 }
@@ -116,79 +139,79 @@ combine_grad_kernel(const uint4 *__restrict__ dout, const uint4 *__restrict__ y,
                 for (int j = 0; j < kPairs; ++j) {
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-                    if (lane == 0) s_sum[warp][j] = acc[j];
+                    if (lane == 0) s_sum[which][warp][j] = acc[j];
                 }
-                __syncthreads();
-                if (tid < kPairs) {
+                group_sync<kGroup>();
+                if (t < kPairs) {
 #pragma unroll
-                    for (int i = 0; i < kWarps; ++i) total += s_sum[i][tid];
+                    for (int i = 0; i < kWarps; ++i) total += s_sum[which][i][t];
                 }
-                __syncthreads();
+                group_sync<kGroup>();
             }
-            if (tid < kPairs && j0 + tid < n) dtopk_w[g * R + s_k[j0 + tid]] = (float)total;
+            if (t < kPairs && j0 + t < n) dtopk_w[g * R + s.k[j0 + t]] = (float)total;
         }
-        __syncthreads();  // the tables are rewritten for the next token
+        group_sync<kGroup>();  // the tables are rewritten for the next token
     }
 }
 
 // ---- dispatch -----------------------------------------------------------------
 
-constexpr int kU = 2;   // vectors of dx per thread
-constexpr int kKB = 4;  // rows loaded together
+constexpr int kVecs = 2;  // vectors of dx per thread
+constexpr int kLoads = 4;  // rows loaded together
 
-template <int kBf16>
+template <int kBf16, int kGroup>
 __global__ void __launch_bounds__(kThreads, 8)
 dispatch_grad_kernel(const uint4 *__restrict__ dpacked, const int32_t *__restrict__ pos, const uint4 *add, int64_t NT,
                      int R, int nvec, int64_t rows_total, uint4 *dx) {
     using VT = Vec<kBf16>;
-    constexpr int EL = VT::kElems;
-    __shared__ int s_p[32], s_k[32], s_n;
-    const int tid = threadIdx.x;
+    constexpr int EL = VT::kElems, kGroups = kThreads / kGroup;
+    __shared__ Pairs s_pairs[kGroups];
+    const int which = threadIdx.x / kGroup, t = threadIdx.x % kGroup;
+    Pairs &s = s_pairs[which];
     grid_dependency_wait();
     grid_launch_dependents();
-    for (int64_t g = blockIdx.x; g < NT; g += gridDim.x) {
-        const int n = gather_pairs(pos, g, R, rows_total, s_p, s_k, &s_n);
-        for (int c0 = tid; c0 < nvec; c0 += kThreads * kU) {
-            float acc[kU][EL];
+    for (int64_t g = (int64_t)blockIdx.x * kGroups + which; g < NT; g += (int64_t)gridDim.x * kGroups) {
+        const int n = gather_pairs<kGroup>(pos, g, R, rows_total, s);
+        for (int c0 = t; c0 < nvec; c0 += kGroup * kVecs) {
+            float acc[kVecs][EL];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int c = c0 + u * kThreads;
+            for (int u = 0; u < kVecs; ++u) {
+                const int c = c0 + u * kGroup;
 #pragma unroll
                 for (int i = 0; i < EL; ++i) acc[u][i] = 0.f;
                 if (add != nullptr && c < nvec) VT::add(acc[u], add[g * nvec + c]);  // read before dx, where it is the same
             }
-            for (int j0 = 0; j0 < n; j0 += kKB) {
-                uint4 v[kKB][kU];
+            for (int j0 = 0; j0 < n; j0 += kLoads) {
+                uint4 v[kLoads][kVecs];
 #pragma unroll
-                for (int jj = 0; jj < kKB; ++jj)
+                for (int jj = 0; jj < kLoads; ++jj)
 #pragma unroll
-                    for (int u = 0; u < kU; ++u) {
-                        const int c = c0 + u * kThreads;
-                        v[jj][u] = (j0 + jj < n && c < nvec) ? ld_stream(dpacked + (int64_t)s_p[j0 + jj] * nvec + c)
+                    for (int u = 0; u < kVecs; ++u) {
+                        const int c = c0 + u * kGroup;
+                        v[jj][u] = (j0 + jj < n && c < nvec) ? ld_stream(dpacked + (int64_t)s.row[j0 + jj] * nvec + c)
                                                              : make_uint4(0u, 0u, 0u, 0u);
                     }
 #pragma unroll
-                for (int jj = 0; jj < kKB; ++jj)
+                for (int jj = 0; jj < kLoads; ++jj)
 #pragma unroll
-                    for (int u = 0; u < kU; ++u) VT::add(acc[u], v[jj][u]);
+                    for (int u = 0; u < kVecs; ++u) VT::add(acc[u], v[jj][u]);
             }
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int c = c0 + u * kThreads;
+            for (int u = 0; u < kVecs; ++u) {
+                const int c = c0 + u * kGroup;
                 if (c < nvec) dx[g * nvec + c] = VT::pack(acc[u]);
             }
         }
-        __syncthreads();
+        group_sync<kGroup>();
     }
 }
 
-// One block of kThreads per token (the hardware schedules them).
 struct Launch {
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = {};
-    Launch(int64_t NT, cudaStream_t stream) {
+    Launch(int64_t blocks, cudaStream_t stream) {
         attr[0] = pdl_attribute();
-        cfg.gridDim = dim3((unsigned)(NT < 0x7fffffff ? NT : 0x7fffffff));
+        cfg.gridDim = dim3((unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff));
         cfg.blockDim = dim3(kThreads);
         cfg.stream = stream;
         cfg.attrs = attr;
@@ -198,24 +221,39 @@ struct Launch {
 };
 
 int row_vectors(int H, int dtype) { return (int)((int64_t)H * (dtype == MOE_BF16 ? 2 : 4) / 16); }
+// Rows of up to 1 KB are a warp's: a block's threads would not all have a vector.
+bool short_rows(int nvec) { return nvec <= 64; }
+int64_t token_blocks(int64_t NT, int nvec) { return short_rows(nvec) ? (NT + kThreads / 32 - 1) / (kThreads / 32) : NT; }
 
 }  // namespace
 
 cudaError_t launch_combine_grad(const void *dout, const void *y, int y_dtype, const int32_t *pos, const float *topk_w,
                                 int64_t NT, int R, int H, int64_t rows_total, void *dy, float *dtopk_w,
                                 cudaStream_t stream) {
-    Launch l(NT, stream);
-    auto kern = y_dtype == MOE_BF16 ? combine_grad_kernel<1> : combine_grad_kernel<0>;
-    return cudaLaunchKernelEx(&l.cfg, kern, static_cast<const uint4 *>(dout), static_cast<const uint4 *>(y), pos, topk_w,
-                              NT, R, row_vectors(H, y_dtype), rows_total, static_cast<uint4 *>(dy), dtopk_w);
+    const int nvec = row_vectors(H, y_dtype);
+    Launch l(token_blocks(NT, nvec), stream);
+    auto launch = [&](auto kern) {
+        return cudaLaunchKernelEx(&l.cfg, kern, static_cast<const uint4 *>(dout), static_cast<const uint4 *>(y), pos,
+                                  topk_w, NT, R, nvec, rows_total, static_cast<uint4 *>(dy), dtopk_w);
+    };
+    const bool bf16 = y_dtype == MOE_BF16;
+    if (short_rows(nvec))
+        return bf16 ? launch(combine_grad_kernel<1, 32, 4, 1>) : launch(combine_grad_kernel<0, 32, 4, 1>);
+    if (R <= 2) return bf16 ? launch(combine_grad_kernel<1, kThreads, 2, 4>) : launch(combine_grad_kernel<0, kThreads, 2, 4>);
+    if (R <= 4) return bf16 ? launch(combine_grad_kernel<1, kThreads, 4, 2>) : launch(combine_grad_kernel<0, kThreads, 4, 2>);
+    return bf16 ? launch(combine_grad_kernel<1, kThreads, 8, 1>) : launch(combine_grad_kernel<0, kThreads, 8, 1>);
 }
 
 cudaError_t launch_dispatch_grad(const void *dpacked, int x_dtype, const int32_t *pos, const void *add, int64_t NT,
                                  int R, int H, int64_t rows_total, void *dx, cudaStream_t stream) {
-    Launch l(NT, stream);
-    auto kern = x_dtype == MOE_BF16 ? dispatch_grad_kernel<1> : dispatch_grad_kernel<0>;
-    return cudaLaunchKernelEx(&l.cfg, kern, static_cast<const uint4 *>(dpacked), pos, static_cast<const uint4 *>(add), NT,
-                              R, row_vectors(H, x_dtype), rows_total, static_cast<uint4 *>(dx));
+    const int nvec = row_vectors(H, x_dtype);
+    Launch l(token_blocks(NT, nvec), stream);
+    auto launch = [&](auto kern) {
+        return cudaLaunchKernelEx(&l.cfg, kern, static_cast<const uint4 *>(dpacked), pos, static_cast<const uint4 *>(add),
+                                  NT, R, nvec, rows_total, static_cast<uint4 *>(dx));
+    };
+    if (short_rows(nvec)) return x_dtype == MOE_BF16 ? launch(dispatch_grad_kernel<1, 32>) : launch(dispatch_grad_kernel<0, 32>);
+    return x_dtype == MOE_BF16 ? launch(dispatch_grad_kernel<1, kThreads>) : launch(dispatch_grad_kernel<0, kThreads>);
 }
 
 }  // namespace moe
