@@ -592,11 +592,13 @@ cudaError_t launch_split(const CUtensorMap &map_w, const TokenMaps &map_x, const
     using S = Shape<64, kParts, kF32, true>;
     static_assert(S::kSmem + groups_bytes(1024) <= kMostSharedW4);
     static thread_local PairCache caches[2];
-    PairLaunch l(S::kThreads, S::kSmem + groups_bytes(1024), stream, a.split);
+    PairLaunch l(S::kThreads, S::kSmem + groups_bytes(1024), stream);
+    l.attr[1].val.clusterDim.x = a.split;
+    l.cfg.gridDim = dim3(a.split);
     PairCache &cache = caches[a.split == 4];
-    cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), l.cfg, a.split);
+    cudaError_t e = cache.prepare(reinterpret_cast<const void *>(kern), l.cfg);
     if (e != cudaSuccess) return e;
-    l.cfg.gridDim = dim3((unsigned)cache.blocks);
+    l.cfg.gridDim = dim3((unsigned)(cache.blocks / 2 * a.split));  // it counts two blocks a cluster
     l.cfg.dynamicSmemBytes = S::kSmem + groups_bytes(a.E);
     return cudaLaunchKernelEx(&l.cfg, kern, map_w, map_x, a);
 }

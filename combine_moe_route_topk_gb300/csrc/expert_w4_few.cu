@@ -124,7 +124,8 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
         [&](int c, int shift) { return ((c + (1 << shift) - 1) >> shift) * a.granules; }, [](int) { return 0; });
     // A block's granules are a run of all of them: it rarely changes the expert.
     const int total = same(g.prefix[a.E]);
-    const int lo = (int)((int64_t)total * blockIdx.x / gridDim.x), hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+    const int grid = gridDim.x, at = blockIdx.x, each = total / grid, rest = total - each * grid;
+    const int lo = at * each + at * rest / grid, hi = (at + 1) * each + (at + 1) * rest / grid;  // total * at / grid
     if (lo == hi) return;  // the whole block
 
     const int split = 1 << a.split_shift, most = kWarps >> a.split_shift, unit_rows = most * kRows;
@@ -244,14 +245,15 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
                 if (!ok) break;
                 held_i = w.i, held_tt = w.tt;
                 const int chunks = blocks * (kK / 8);
-                for (int tok = 0; tok < w.n; ++tok) {
+                const uint8_t *from = a.x + (int64_t)w.row * a.K * 2;
+                for (int tok = 0; tok < w.n; ++tok, from += (int64_t)a.K * 2) {
                     for (int q = tid; q < chunks; q += 32 * kWarps) {
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (q * 8 < a.K) v = __ldg(reinterpret_cast<const uint4 *>(a.x + ((int64_t)(w.row + tok) * a.K + q * 8) * 2));
                         // lane t reads chunk 4 t + i of a block of 16 in its i-th turn: stored in that order
-                        *reinterpret_cast<uint4 *>(tokens + tok * line + (q >> 4) * 256 + (q & 3) * 64 + (q >> 2 & 3) * 16) = v;
+                        const int to = tok * line + (q >> 4) * 256 + (q & 3) * 64 + (q >> 2 & 3) * 16;
+                        copy_async<16>(smem_u32(tokens) + to, q * 8 < a.K ? from + q * 16 : a.x, q * 8 < a.K ? 16 : 0);
                     }
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mb_arrive(placed);
                 ok = mb_wait_warp(placed, placed_phase, gave_up);

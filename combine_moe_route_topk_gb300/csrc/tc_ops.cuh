@@ -114,13 +114,6 @@ __device__ __forceinline__ bool mb_wait_warp_pair(uint32_t bar, uint32_t parity,
     const bool ok = mb_wait_warp(bar, parity, gave_up, polls);
     return ok && __all_sync(0xffffffffu, mb_try_pair(bar, parity));  // complete: acquires, does not wait
 }
-// Two barriers with one vote where both are complete already.
-__device__ __forceinline__ bool mb_wait_warp2(uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2,
-                                              volatile int *gave_up) {
-    const bool first = mb_try(bar, parity), second = mb_try(bar2, parity2);
-    if (__all_sync(0xffffffffu, first && second)) return true;
-    return mb_wait_warp(bar, parity, gave_up) && mb_wait_warp(bar2, parity2, gave_up);
-}
 __device__ __forceinline__ void mb_drain(uint32_t bar, uint32_t parity) {  // bounded, result not needed
     for (long long i = 0; i < kPolls && !mb_try(bar, parity); ++i) {
     }
@@ -142,16 +135,6 @@ __device__ __forceinline__ uint4 ld_shared128(uint32_t addr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr)
                  : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t ld_shared8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t ld_shared32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
 // Two f32 (bits) rounded to bf16, the first in the low half.
@@ -218,14 +201,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
         "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
         "[%2];" ::"r"(dst),
         "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1, int c2,
-                                            int c3, int c4) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
-        "[%2];" ::"r"(dst),
-        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
         : "memory");
 }
 // Rows of a row-major operand by boxes of 128, 64 and 32 rows of 128 bytes: a
@@ -322,15 +297,6 @@ __device__ __forceinline__ uint32_t at_leader(uint32_t addr) {  // the same plac
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
     return r;
-}
-__device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {  // in another block's
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void st_remote128(uint32_t addr, const float4 &v) {  // addr from at_rank
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
 }
 // Arrives at a barrier of the leader (bar from at_leader).  The released form
 // orders the thread's writes before it, for which it waits until its global
@@ -610,16 +576,16 @@ struct AttrCache {
     }
 };
 
-// Launch of a persistent kernel in clusters of two blocks (or of another number).
+// Launch of a persistent kernel in clusters of two blocks.
 struct PairLaunch {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
-    PairLaunch(int threads, int smem, cudaStream_t stream, int cluster = 2) {
+    PairLaunch(int threads, int smem, cudaStream_t stream) {
         attr[0] = pdl_attribute();
         attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.x = 2;
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(cluster);
+        cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(threads);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
@@ -635,14 +601,14 @@ struct PairCache {
     AttrCache attr;
     int dev = -1, blocks = 0;
     unsigned long long ctx = 0;
-    cudaError_t prepare(const void *kernel, const cudaLaunchConfig_t &cfg, int cluster = 2) {  // cfg with the most shared memory
+    cudaError_t prepare(const void *kernel, const cudaLaunchConfig_t &cfg) {  // cfg with the most shared memory
         cudaError_t e = attr.allow_smem(kernel, (int)cfg.dynamicSmemBytes);
         if (e != cudaSuccess || (blocks > 0 && dev == attr.dev && ctx == attr.ctx && ctx != 0)) return e;
         int clusters = 0;
         e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
         if (e != cudaSuccess) return e;
         if (clusters < 1) return cudaErrorLaunchOutOfResources;
-        blocks = cluster * clusters;
+        blocks = 2 * clusters;
         dev = attr.dev;
         ctx = attr.ctx;
         return cudaSuccess;
@@ -653,21 +619,6 @@ struct PairCache {
 // strides in bytes for dimensions 1.. (false: the driver refused it).
 bool encode_map(CUtensorMap *m, int fp8, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
                 const uint32_t *box);
-
-// The map of matrices of 4-bit codes, boxes of 256 elements (a line of 128 bytes)
-// by `rows` rows; of a gated product's, blocks of 8 gate rows and the up rows of
-// the same 8 features follow one another.
-inline bool encode_w4(CUtensorMap *m, const void *wq, int E, int K, int F, int gated, int rows) {
-    const uint64_t line = (uint64_t)K / 2, f = (uint64_t)F, e = (uint64_t)E;
-    if (gated) {
-        const uint64_t dims[5] = {line, 8, 2, f / 8, e}, strides[4] = {line, line * f, line * 8, line * f * 2};
-        const uint32_t box[5] = {128, 8, 2, (uint32_t)rows / 16, 1};
-        return encode_map(m, 1, 5, wq, dims, strides, box);
-    }
-    const uint64_t dims[3] = {line, f, e}, strides[2] = {line, line * f};
-    const uint32_t box[3] = {128, (uint32_t)rows, 1};
-    return encode_map(m, 1, 3, wq, dims, strides, box);
-}
 
 // The maps of load_rows over rows of `cols` elements (16-bit, or 8-bit: fp8),
 // of which no tile takes more than `most` at once.

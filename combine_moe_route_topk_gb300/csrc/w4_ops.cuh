@@ -13,6 +13,8 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include "tc_ops.cuh"
+
 namespace moe {
 
 // A group's scale, twice, and what takes the codes' offset off.
@@ -63,6 +65,57 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int by
 // Arrives on `bar` (whose count includes it) once this thread's copies so far are done.
 __device__ __forceinline__ void copy_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Two barriers with one vote where both are complete already.
+__device__ __forceinline__ bool mb_wait_warp2(uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2,
+                                              volatile int *gave_up) {
+    const bool first = mb_try(bar, parity), second = mb_try(bar2, parity2);
+    if (__all_sync(0xffffffffu, first && second)) return true;
+    return mb_wait_warp(bar, parity, gave_up) && mb_wait_warp(bar2, parity2, gave_up);
+}
+
+__device__ __forceinline__ uint32_t ld_shared8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {  // the same place in another block of the cluster
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_remote128(uint32_t addr, const float4 &v) {  // addr from at_rank
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
+        "[%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+
+// The map of matrices of 4-bit codes, boxes of 256 elements (a line of 128 bytes)
+// by `rows` rows; of a gated product's, blocks of 8 gate rows and the up rows of
+// the same 8 features follow one another.
+inline bool encode_w4(CUtensorMap *m, const void *wq, int E, int K, int F, int gated, int rows) {
+    const uint64_t line = (uint64_t)K / 2, f = (uint64_t)F, e = (uint64_t)E;
+    if (gated) {
+        const uint64_t dims[5] = {line, 8, 2, f / 8, e}, strides[4] = {line, line * f, line * 8, line * f * 2};
+        const uint32_t box[5] = {128, 8, 2, (uint32_t)rows / 16, 1};
+        return encode_map(m, 1, 5, wq, dims, strides, box);
+    }
+    const uint64_t dims[3] = {line, f, e}, strides[2] = {line, line * f};
+    const uint32_t box[3] = {128, (uint32_t)rows, 1};
+    return encode_map(m, 1, 3, wq, dims, strides, box);
 }
 
 }  // namespace moe
