@@ -734,8 +734,8 @@ int moe_expert_gemm_w4(const MoeDims *dims, int K, int F, int act, int group, co
     if (v.NT == 0) return MOE_OK;
     if (bad_block_pointers(x, wq, y, what, &rc)) return rc;
     if (!group_scales || !row_scales) return set_error(MOE_ERR_INVALID_ARG, "%s: a required pointer is NULL", what);
-    if (!aligned(group_scales, 4) || !aligned(row_scales, 4))
-        return set_error(MOE_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", what);
+    if (!aligned(group_scales, 8) || !aligned(row_scales, 4))  // groups' scales are copied by eight
+        return set_error(MOE_ERR_INVALID_ARG, "%s: group_scales must be 8-byte, row_scales 4-byte aligned", what);
     const int64_t wide = (gated ? 2 : 1) * (int64_t)F;
     const Span out = {y, v.rows_total * F * (!gated && dims->y_dtype == MOE_F32 ? 4 : 2)};
     const Span in[] = {{x, v.rows_total * K * 2},

@@ -33,7 +33,7 @@ extern "C" {
  *   act MOE_EXPERT_SWIGLU: y bf16 [N*cap][F] = silu(g) * u, whatever dims->y_dtype
  * q times its group's scale has at most seven significant bits and is
  * multiplied by x exactly; a row's scale multiplies the f32 sum.  x and wq must
- * be 16-byte aligned, y too, the scales 4-byte.  With N = E = R = 1
+ * be 16-byte aligned, y too, group_scales 8-byte, row_scales 4-byte.  With N = E = R = 1
  * (expert_offsets = {0, T}, cap_rows = T) this is the product of a dense layer,
  * for T = 1 a matrix-vector product. */
 int moe_expert_gemm_w4(const MoeDims *dims, int K, int F, int act, int group, const void *x, const int32_t *wq,

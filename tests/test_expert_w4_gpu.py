@@ -364,3 +364,52 @@ def test_dense_layer_of_some_tokens(T, K, F, form):
     for _ in range(5):
         call(b, K, F, act, 32, x, w, again, form == "f32")
         assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("counts,K,F", [([3, 1], 544, 136), ([40, 70], 544, 136), ([200, 90], 256, 4104)])
+@pytest.mark.parametrize("form", ["bf16", "gated"])
+def test_arrays_at_their_least_alignment(counts, K, F, form):
+    """x, wq and y 16 bytes, group_scales 8 and row_scales 4 past a boundary."""
+    b = Batch(1, counts, 300)
+    x, w = b.row_values(K), Weights(b, 2 * F if form == "gated" else F, K, 32)
+
+    def moved(t, off):
+        buf = torch.empty(t.numel() * t.element_size() + 64, dtype=torch.uint8, device="cuda")
+        view = buf[off:off + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        return view.copy_(t)
+
+    act = SWIGLU if form == "gated" else LINEAR
+    y = b.out(F, torch.bfloat16)
+    call(b, K, F, act, 32, x, w, y)
+    w.wq, w.gs, w.rs = moved(w.wq, 16), moved(w.gs, 8), moved(w.rs, 4)
+    again = moved(b.out(F, torch.bfloat16), 16)
+    call(b, K, F, act, 32, moved(x, 16), w, again)
+    assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("counts", [[3, 1], [40, 70], [200, 900]])
+def test_first_call_of_a_thread_is_captured(counts):
+    """What a call sets up once a thread may be set up during a capture, by a thread that has not used CUDA before."""
+    b = Batch(1, counts, 1200)
+    K, F = 544, 4104
+    x, w = b.row_values(K), Weights(b, F, K, 32)
+    want, y = b.out(F, torch.bfloat16), b.out(F, torch.bfloat16)
+    call(b, K, F, LINEAR, 32, x, w, want)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work():
+        try:
+            with torch.cuda.graph(graph, stream=stream):
+                call(b, K, F, LINEAR, 32, x, w, y)
+        except BaseException as e:  # reported by the test's own thread
+            failed.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    assert not failed, failed
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)

@@ -58,7 +58,7 @@ def test_bad_arguments_are_refused(lib, act):
 def test_missing_misaligned_and_overlapping_arrays_are_refused(lib):
     for i, n in enumerate(NAMES):
         assert _call(lib, **{n: None}) == INVALID, n
-        off = 8 if n in ("x", "wq", "y") else 2
+        off = 8 if n in ("x", "wq", "y") else 4 if n == "group_scales" else 2
         assert _call(lib, **{n: at(i, off)}) == INVALID, n
         assert "aligned" in lib.moe_last_error().decode()
         if n != "y":
@@ -127,3 +127,23 @@ def test_quantised_weights_are_near(group):
     for bad in (w[0, 0], torch.zeros(1, 8, 48)):
         with pytest.raises(ValueError):
             moe.quantize_w4(bad, group)
+
+
+@pytest.mark.parametrize("name", ["expert_w4.cu", "expert_w4_few.cu", "w4_ops.cuh"])
+def test_warps_meet_at_bounded_waits_only(name):
+    """A named barrier of some warps would wait for ever for one that has given up.  Whole blocks and clusters meet
+    before the roles part and after they are all done."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, name)).read())
+    assert not re.search(r"\bbar\.|\bbarrier\.(?!cluster)|__syncthreads_|cooperative_groups", text)
+    assert text.count("__syncthreads()") <= 2
+    for wait in re.findall(r"while \([^\n]*mb_try[^\n]*", text):
+        assert "left > 0" in wait
+
+
+@pytest.mark.parametrize("name", ["expert_w4.cu", "expert_w4_few.cu"])
+def test_slots_are_given_back_by_a_lane_that_depends_on_the_words(name):
+    """An arrival right behind the loads from a slot may pass them: where a warp has read, the arriving lane is chosen by
+    a vote on what it read."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, name)).read())
+    assert len(re.findall(r"if \(lane == reader_lane\([^;]*\)\) mb_arrive\(c?empty", text)) == 1
+    assert len(re.findall(r"mb_arrive\(c?empty", text)) == 2  # the other one is of warps that read nothing
