@@ -5,8 +5,12 @@
 //   dispatch  packed[p] = x[g]:  dx[g] = add[g] + sum_k dpacked[p]
 //
 // Both are streams of whole rows, ordered by token: a token's row of dout is
-// read once for all its pairs, and what is summed (dw, dx) is summed inside
-// one block, in a fixed order.
+// read once for all its pairs (by rows of y it would be read R times, or wait
+// in L2 for a pair that comes much later), and what is summed (dw, dx) is
+// summed inside one block or warp, in a fixed order, without atomics.  HBM
+// bounds them: 65536 pairs of 8192 tokens, rows of 4096 bf16 172 us (1.14 GB,
+// 0.98 of what a copy reaches), dispatch's 65536 rows of 7168 with a first
+// summand 171 us (1.18 GB, 1.01).
 #include "grad_internal.cuh"
 #include "mem_ops.cuh"
 #include "pdl.cuh"
@@ -79,8 +83,11 @@ struct Pair<0> {
     }
 };
 
-// kPairs: pairs whose rows a thread loads together, kU vectors of each: what is
-// under way is kPairs * kU loads a thread whatever R is.
+// kPairs: pairs whose rows a thread loads together, kU vectors of each.  Eight
+// loads a thread are under way: with 8 x 1 for all, 16384 tokens of 1, 2 and
+// 4 rows of 4096 bf16 took 99, 125 and 186 us, with 4 x 2 82, 110 and 180; eight rows
+// 171 and 174.  In warps, 65536 tokens of two rows of 1024: 2 x 2 100, 4 x 1 111, 8 x 1
+// 152; of four 180, 180, 213.
 template <int kBf16, int kGroup, int kPairs, int kU>
 __global__ void __launch_bounds__(kThreads)
 combine_grad_kernel(const uint4 *__restrict__ dout, const uint4 *__restrict__ y, const int32_t *__restrict__ pos,
@@ -221,9 +228,18 @@ struct Launch {
 };
 
 int row_vectors(int H, int dtype) { return (int)((int64_t)H * (dtype == MOE_BF16 ? 2 : 4) / 16); }
-// Rows of up to 1 KB are a warp's: a block's threads would not all have a vector.
-bool short_rows(int nvec) { return nvec <= 64; }
-int64_t token_blocks(int64_t NT, int nvec) { return short_rows(nvec) ? (NT + kThreads / 32 - 1) / (kThreads / 32) : NT; }
+// A token is a warp's where its rows have little together and there are many of them, else a block's.
+// A block costs 3.6 ns a token whatever it reads (positions, rows and sums wait for one
+// another, and an SM has few blocks); a warp reads less at once.  Warps : blocks, us,
+// combine's gradient in bf16, R rows of H: 65536 tokens 2 x 512 61 : 226, 4 x 1024 180 : 252, 2 x 2048 196 :
+// 307, 32768 of 4 x 2048 182 : 186, 16384 of 8 x 2048 182 : 169; 4096 tokens 8 x 512 10 : 15, 8 x 1024 19 : 21;
+// 2048 of them 7.4 : 8.3 and 12 : 11; 1024 6.3 : 4.8 and 10 : 6.5, 2 x 512 3.2 : 3.8; 256 4.2 : 3.8 (8 x 256) and 2.6 :
+// 3.4 (2 x 256).  Dispatch's turns over at the same places (65536 tokens 4 x 1024 98 : 133, 16384 of 8 x 2048 90 : 88).
+bool token_per_warp(int64_t NT, int R, int nvec) {
+    const int64_t vectors = (int64_t)R * nvec;
+    return vectors <= 1024 && vectors * 4 <= NT;
+}
+int64_t token_blocks(int64_t NT, bool warps) { return warps ? (NT + kThreads / 32 - 1) / (kThreads / 32) : NT; }
 
 }  // namespace
 
@@ -231,15 +247,15 @@ cudaError_t launch_combine_grad(const void *dout, const void *y, int y_dtype, co
                                 int64_t NT, int R, int H, int64_t rows_total, void *dy, float *dtopk_w,
                                 cudaStream_t stream) {
     const int nvec = row_vectors(H, y_dtype);
-    Launch l(token_blocks(NT, nvec), stream);
+    const bool warps = token_per_warp(NT, R, nvec);
+    Launch l(token_blocks(NT, warps), stream);
     auto launch = [&](auto kern) {
         return cudaLaunchKernelEx(&l.cfg, kern, static_cast<const uint4 *>(dout), static_cast<const uint4 *>(y), pos,
                                   topk_w, NT, R, nvec, rows_total, static_cast<uint4 *>(dy), dtopk_w);
     };
     const bool bf16 = y_dtype == MOE_BF16;
-    if (short_rows(nvec))
-        return bf16 ? launch(combine_grad_kernel<1, 32, 4, 1>) : launch(combine_grad_kernel<0, 32, 4, 1>);
-    if (R <= 2) return bf16 ? launch(combine_grad_kernel<1, kThreads, 2, 4>) : launch(combine_grad_kernel<0, kThreads, 2, 4>);
+    if (warps && R <= 2) return bf16 ? launch(combine_grad_kernel<1, 32, 2, 2>) : launch(combine_grad_kernel<0, 32, 2, 2>);
+    if (warps) return bf16 ? launch(combine_grad_kernel<1, 32, 4, 1>) : launch(combine_grad_kernel<0, 32, 4, 1>);
     if (R <= 4) return bf16 ? launch(combine_grad_kernel<1, kThreads, 4, 2>) : launch(combine_grad_kernel<0, kThreads, 4, 2>);
     return bf16 ? launch(combine_grad_kernel<1, kThreads, 8, 1>) : launch(combine_grad_kernel<0, kThreads, 8, 1>);
 }
@@ -247,12 +263,13 @@ cudaError_t launch_combine_grad(const void *dout, const void *y, int y_dtype, co
 cudaError_t launch_dispatch_grad(const void *dpacked, int x_dtype, const int32_t *pos, const void *add, int64_t NT,
                                  int R, int H, int64_t rows_total, void *dx, cudaStream_t stream) {
     const int nvec = row_vectors(H, x_dtype);
-    Launch l(token_blocks(NT, nvec), stream);
+    const bool warps = token_per_warp(NT, R, nvec);
+    Launch l(token_blocks(NT, warps), stream);
     auto launch = [&](auto kern) {
         return cudaLaunchKernelEx(&l.cfg, kern, static_cast<const uint4 *>(dpacked), pos, static_cast<const uint4 *>(add),
                                   NT, R, nvec, rows_total, static_cast<uint4 *>(dx));
     };
-    if (short_rows(nvec)) return x_dtype == MOE_BF16 ? launch(dispatch_grad_kernel<1, 32>) : launch(dispatch_grad_kernel<0, 32>);
+    if (warps) return x_dtype == MOE_BF16 ? launch(dispatch_grad_kernel<1, 32>) : launch(dispatch_grad_kernel<0, 32>);
     return x_dtype == MOE_BF16 ? launch(dispatch_grad_kernel<1, kThreads>) : launch(dispatch_grad_kernel<0, kThreads>);
 }
 

@@ -69,6 +69,11 @@ SHAPES = [
     (4, 30, 8, 2, 72, 3, 2.0),
     (1, 64, 4, 1, 7168, 5, 0.0),
     (8, 16, 32, 17, 4104, 100, 1.0),
+    # many tokens of few bytes: a token is a warp's
+    (1, 4099, 7, 2, 1048, 0, 0.0),
+    (2, 1101, 10, 5, 264, 900, 2.0),
+    (1, 703, 40, 32, 40, 0, 0.0),
+    (1, 2050, 3, 1, 2040, 1500, 0.0),
 ]
 
 
