@@ -10,16 +10,15 @@
 // 2 cycles of an SM for 16 x 16 weights and eight tokens (measured), 128 weights a
 // cycle where HBM brings 44; what bounds the kernel are instructions: some 320 of
 // a warp for 32 x 128 weights, 112 of them the shifts and logic that take nibbles
-// apart, 38 weights a cycle (32 of 64 experts, 7168 x 4096 each, one token: 110 us,
-// loads alone 82, floor 74).  The tensor core proper would take the same bf16 from
+// apart, 31 weights a cycle (32 of 64 experts, 7168 x 4096 each, one token: 107 us,
+// loads alone 82, floor 74; two stages of codes are as fast as five).  The tensor core proper would take the same bf16 from
 // TMEM by tiles of 128 rows: more rows at once than a small call has for an SM.
 //
 // A block holds one expert's tokens, at most eight, in shared memory, in the
 // order in which lanes read them, and walks through a run of the matrices'
-// rows, in granules of 32, its share of all there are.  A unit is up to
-// 16 / split granules; the `split` warps of a granule share its reduction by
-// blocks of 128, and their sums are added up in shared memory in the warps'
-// order.  Two more warps load, one of them the groups' scales: their copies in
+// rows, in granules of 32, its share of all there are.  A unit is a few
+// granules; the warps of one share its reduction by blocks of 128, and their
+// sums are added up in shared memory in the warps' order.  Two more warps load, one of them the groups' scales: their copies in
 // the same warp as the codes' loads held those up (loads alone 284 us against
 // 187, 32 tokens of 64 experts, 7168 x 4096).
 #include "expert_w4_internal.cuh"
@@ -50,7 +49,8 @@ struct Args {
     void *y;
     int64_t cap, most, pairs;
     int E, L, K, F, wide, groups, group_shift;
-    int split_shift, granules;  // log2 of the warps that share a granule, granules of a matrix
+    int least_shift, most_shift;  // log2 of the warps that share a granule: its limits
+    int granules;            // of a matrix
     int stages, lines;       // stages of codes, lines of tokens in shared memory
 };
 
@@ -73,17 +73,28 @@ struct CodeMaps {
 struct Unit {
     int i, tt;     // group, token tile
     int m, count;  // first granule in the matrix, granules
+    int shift;     // log2 of the warps that share one of them
     int row, n;    // first token row, tokens
 };
 
+// How many granules of the next `left` a unit takes: as many as least_shift allows,
+// or the power of two below, as long as every warp of a granule has work.  (7
+// granules of 56 blocks of 128: 4, 2 and 1 take a warp 14 + 7 + 4 steps, 4 and 3 would 28.
+// Two tokens of 8 of 64 experts, K = 7168, F = 2048 gated: 60 us, before 64.)
+__device__ __forceinline__ void set_count(Unit &w, int left, int least_shift, int most_shift) {
+    w.count = min(kWarps >> least_shift, left);
+    w.shift = max(least_shift, min(most_shift, 4 - (31 - __clz(w.count))));
+    if (w.count > kWarps >> most_shift) w.count = kWarps >> w.shift;
+}
+
 // The unit at place p of all granules, of which the block's end at hi.
-__device__ __forceinline__ Unit get_unit(const Groups &g, int E, int i, int p, int hi, int most, int granules) {
+__device__ __forceinline__ Unit get_unit(const Groups &g, int i, int p, int hi, const Args &a) {
     Unit r;
-    r.i = same(find_group(g, E, i, p));
+    r.i = same(find_group(g, a.E, i, p));
     const int at = p - same(g.prefix[r.i]), c = same(g.count[r.i]);
-    r.tt = at / granules;
-    r.m = at - r.tt * granules;
-    r.count = min(min(most, granules - r.m), hi - p);
+    r.tt = at / a.granules;
+    r.m = at - r.tt * a.granules;
+    set_count(r, min(a.granules - r.m, hi - p), a.least_shift, a.most_shift);
     r.row = same(g.row[r.i]) + (r.tt << kTokShift);
     r.n = min(kTok, c - (r.tt << kTokShift));
     return r;
@@ -128,15 +139,14 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
     const int lo = at * each + at * rest / grid, hi = (at + 1) * each + (at + 1) * rest / grid;  // total * at / grid
     if (lo == hi) return;  // the whole block
 
-    const int split = 1 << a.split_shift, most = kWarps >> a.split_shift, unit_rows = most * kRows;
     constexpr int kCols = kGated ? kRows / 2 : kRows;  // result columns of a granule
-    const int blocks = (a.K + kK - 1) / kK, rounds = (blocks + split - 1) >> a.split_shift;
+    const int blocks = (a.K + kK - 1) / kK;
     auto advance = [&](Unit &w, int p) {  // to the unit at p, the one behind it
         w.m += w.count;
-        if (w.m == a.granules) w = get_unit(g, a.E, w.i, p, hi, most, a.granules);
-        else w.count = min(min(most, a.granules - w.m), hi - p);
+        if (w.m == a.granules) w = get_unit(g, w.i, p, hi, a);
+        else set_count(w, min(a.granules - w.m, hi - p), a.least_shift, a.most_shift);
     };
-    Unit w = get_unit(g, a.E, 0, lo, hi, most, a.granules);
+    Unit w = get_unit(g, 0, lo, hi, a);
     int slot = 0;
     uint32_t phase = 0;
     auto next_slot = [&] {
@@ -145,11 +155,12 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
 
     if (warp >= kWarps) {  // loads
         const bool scales = warp > kWarps;
-        // A lane copies eight rows' scales of every 32 / (unit_rows / 8)-th group.
-        const int q = lane & (unit_rows / 8 - 1), first = lane / (unit_rows / 8), step = 32 / (unit_rows / 8);
-        const int groups = (split * kK) >> a.group_shift;  // of a stage
         bool ok = true;
         for (int p = lo; p < hi && ok;) {
+            const int split = 1 << w.shift, unit_rows = (kWarps * kRows) >> w.shift, rounds = (blocks + split - 1) >> w.shift;
+            // A lane copies eight rows' scales of every `step`-th group.
+            const int step = split / 2, first = lane >> (6 - w.shift), q = lane & ((64 >> w.shift) - 1);
+            const int groups = (split * kK) >> a.group_shift;  // of a stage
             const int f0 = w.m * kCols, f = kGated ? f0 + (q >> 1) * 8 : f0 + q * 8;
             const uint8_t *from = a.group_scales + (int64_t)w.i * a.groups * a.wide + (int64_t)first * a.wide;
             if (f < a.F) from += f + (kGated && (q & 1) ? a.F : 0);
@@ -191,18 +202,11 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
             while (!mb_try(full + 8 * slot, phase ^ 1u) && left > 0) --left;
         }
     } else {
-        const int part = warp & (split - 1), sub = warp >> a.split_shift;
         const int gr = lane >> 2, t = lane & 3;  // row of a fragment's eight, place in the four lanes of a row
         // A lane's four rows (of two fragments, eight rows apart in each) are four that follow one another in the
         // matrix: their scales are one word, and lanes that read codes at once read different places of the
         // swizzled lines.
         const uint32_t magic = w4_magic(), zeros = smem_u32(behind + kRed) + t * 16, held_at = smem_u32(tokens) + gr * line + t * 16;
-        const int ch = ((part & 1) * 4 + t) ^ ((gr & 1) * 4);  // the lane's chunk of its first row's line
-        uint32_t codes_at[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            codes_at[i] = codes + (part >> 1) * unit_rows * 128 + (sub * kRows + 4 * gr + i) * 128 + ((ch ^ i) << 4);
-        const uint32_t scale_at = scales_at + ((part * kK + t * 32) >> a.group_shift) * unit_rows + sub * kRows + 4 * gr;
         float acc[8], sum[8];
         int held_i = -1, held_tt = -1, buf = 0;
         uint32_t x_at = zeros, x_step = 0, summed_phase = 0, placed_phase = 0;  // the lane's token, from block to block
@@ -212,15 +216,16 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
         // The unit `done`: its warps' sums are added up in their order.  Element j of a warp's 256 lies at (j / 32: fragment register, j % 32: lane).
         auto finish = [&] {
             pending = false;
-            ok = mb_wait_warp(summed, summed_phase, gave_up, kPolls + rounds * kStepPolls);
+            ok = mb_wait_warp(summed, summed_phase, gave_up, kPolls + blocks * kStepPolls);
             summed_phase ^= 1u;
             if (!ok) return;
             const float *from = red + (buf ^ 1) * (kWarps * (kSumLine + kRows)), *scales = from + kWarps * kSumLine;
+            const int split = 1 << done.shift, most = kWarps >> done.shift;
             for (int j = tid; j < most * kSums; j += 32 * kWarps) {
                 int e = j;
                 if constexpr (kGated) e = (e & ~15) + (e & 1) * 8 + (e >> 1 & 7);  // gate and up in neighbouring lanes
                 const int which = e >> 8, i = e >> 5 & 7, l = e & 31;
-                const float *at = from + (which << a.split_shift) * kSumLine + (e & 255);
+                const float *at = from + (which << done.shift) * kSumLine + (e & 255);
                 float v = 0.f;
                 for (int k = 0; k < split; k += 2) v = v + at[k * kSumLine] + at[(k + 1) * kSumLine];
                 // the row of the granule; of a gated one's, 8 are gate rows and the next 8 the same features' up rows
@@ -240,6 +245,8 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
         };
 
         for (int p = lo; p < hi && ok;) {
+            const int split = 1 << w.shift, most = kWarps >> w.shift, unit_rows = most * kRows, rounds = (blocks + split - 1) >> w.shift;
+            const int part = warp & (split - 1), sub = warp >> w.shift;
             if (w.i != held_i || w.tt != held_tt) {  // other tokens
                 if (pending) finish();               // nobody reads the old ones any more
                 if (!ok) break;
@@ -269,9 +276,15 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] = sum[i] = 0.f;
-            const int mine = sub < w.count ? (blocks - part + split - 1) >> a.split_shift : 0;  // blocks of this warp
+            const int mine = sub < w.count ? (blocks - part + split - 1) >> w.shift : 0;  // blocks of this warp
+            const int ch = ((part & 1) * 4 + t) ^ ((gr & 1) * 4);  // the lane's chunk of its first row's line
+            uint32_t codes_at[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                codes_at[i] = codes + (part >> 1) * unit_rows * 128 + (sub * kRows + 4 * gr + i) * 128 + ((ch ^ i) << 4);
+            const uint32_t scale_at = scales_at + ((part * kK + t * 32) >> a.group_shift) * unit_rows + sub * kRows + 4 * gr;
             uint32_t x = x_at + part * x_step;
-            for (int r = 0; r < rounds; ++r, x += x_step << a.split_shift) {
+            for (int r = 0; r < rounds; ++r, x += x_step << w.shift) {
                 ok = mb_wait_warp(full + 8 * slot, phase, gave_up);
                 if (!ok) break;
                 if (r >= mine) {
@@ -359,8 +372,8 @@ cudaError_t launch(const CodeMaps &maps, const Args &a, cudaStream_t stream) {
 // granules of 32 rows by eight tokens, there `rounds` of tiles of 128 rows by 64
 // tokens, each in `split` blocks.  A tile takes as long as four granules, or more.
 // Here against there, us (granules : tiles / split), K = 7168, F = 2048 gated, 8 of
-// 64 experts a token: 1, 2, 4, 8, 32 tokens 37 : 44 (7 : 2), 64 : 74 (14 : 4),
-// 105 : 101 (27 : 7), 154 : 158 (54 : 14), 222 : 206 (75 : 15); one matrix of 4096
+// 64 experts a token: 1, 2, 4, 8, 32 tokens 37 : 44 (7 : 2), 60 : 74 (14 : 4),
+// 101 : 101 (27 : 7), 154 : 158 (54 : 14), 222 : 206 (75 : 15); one matrix of 4096
 // x 7168, 1, 8, 16 tokens 15 : 17, 18 : 17, 23 : 17 (1, 1, 2 : 1 / 4); 8 tokens of
 // 16 experts of 1024 x 2048, of 8 of 2048 x 4096 19 : 15, 21 : 19 (4 : 1).
 bool expert_w4_few(const ExpertRows &r, int K, int F, int gated, int64_t rounds, int split) {
@@ -378,10 +391,11 @@ cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, i
     const int cols = gated ? kRows / 2 : kRows, granules = (F + cols - 1) / cols;
     // Four warps share a granule, so that a block's units are 128 rows: whole
     // boxes and lines of scales.  More, where a block has less than that to do
-    // (one matrix of 4096 x 7168: 15 us with 16 warps a granule, 17 with four).
-    const int64_t active = r.pairs < r.E ? r.pairs : r.E, sms = sm_count(), share = (active * granules + sms - 1) / sms;
-    int split = blocks > 2 ? 2 : 1;  // two at least: a line of shared memory has two blocks
-    while (split < 4 && (share << (split + 1)) <= kWarps && (2 << split) <= blocks) ++split;
+    // (one matrix of 4096 x 7168: 15 us with 16 warps a granule, 17 with four),
+    // as long as each of them has two blocks of 128.
+    const int least = blocks > 2 ? 2 : 1;  // two at least: a line of shared memory has two blocks
+    int most = least;
+    while (most < 4 && (4 << most) <= blocks) ++most;
     CodeMaps maps;
     for (int i = 0; i < 3; ++i)
         if (!encode_w4(&maps.m[i], wq, r.E, K, F, gated, 128 >> i)) return cudaErrorInvalidValue;
@@ -389,8 +403,8 @@ cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, i
     while ((1 << shift) < group) ++shift;
     const int lines = lines_of(r);
     const Args a{r.offsets, static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(group_scales), row_scales, y,
-                 r.cap, r.most, r.pairs, r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift, split,
-                 granules, stages_of(r, K, lines), lines};
+                 r.cap, r.most, r.pairs, r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift, least,
+                 most, granules, stages_of(r, K, lines), lines};
     if (gated) return launch<true, false>(maps, a, stream);
     return y_f32 ? launch<false, true>(maps, a, stream) : launch<false, false>(maps, a, stream);
 }
