@@ -370,18 +370,20 @@ cudaError_t launch(const CodeMaps &maps, const Args &a, cudaStream_t stream) {
 
 // Which kernel takes a batch, by what an SM has to do at most: here `share`
 // granules of 32 rows by eight tokens, there `rounds` of tiles of 128 rows by 64
-// tokens, each in `split` blocks.  A tile takes as long as four granules, or more.
+// tokens, each in `split` blocks.  A tile takes as long as some five granules.
 // Here against there, us (granules : tiles / split), K = 7168, F = 2048 gated, 8 of
-// 64 experts a token: 1, 2, 4, 8, 32 tokens 37 : 44 (7 : 2), 60 : 74 (14 : 4),
-// 101 : 101 (27 : 7), 154 : 158 (54 : 14), 222 : 206 (75 : 15); one matrix of 4096
-// x 7168, 1, 8, 16 tokens 15 : 17, 18 : 17, 23 : 17 (1, 1, 2 : 1 / 4); 8 tokens of
-// 16 experts of 1024 x 2048, of 8 of 2048 x 4096 19 : 15, 21 : 19 (4 : 1).
+// 64 experts a token: 1, 2, 4, 8 tokens 37 : 44 (7 : 2), 60 : 72 (14 : 4), 101 : 105
+// (27 : 7), 148 : 166 (54 : 14), 16, 32, 48 179 : 187 (61 : 14), 212 : 218 (75 : 15), 246 : 232
+// (88 : 15); K = 2048, F = 7168, 8, 24, 48 tokens 87 : 85 (95 : 24), 115 : 113 (118 : 25),
+// 141 : 121 (154 : 26); one matrix of 4096 x 7168, 1, 8, 16, 32 tokens 13 : 17, 15 : 17,
+// 17 : 17, 23 : 17 (1, 1, 2, 4 : 1 / 4); 2 of 8 experts of 2048 x 4096, 8 tokens 17 : 19 (4 : 1),
+// of 4096 x 4096, 32 tokens 35 : 28 (13 : 2).
 bool expert_w4_few(const ExpertRows &r, int K, int F, int gated, int64_t rounds, int split) {
     const int64_t cols = gated ? kRows / 2 : kRows, granules = (F + cols - 1) / cols, sms = sm_count();
     const int64_t active = r.pairs < r.E ? r.pairs : r.E, units = (active + (r.pairs - active) / kTok) * granules;
     if (K > (1 << 15) || units >= (1 << 30) || stages_of(r, K, lines_of(r)) < 2) return false;
     const int64_t share = (units + sms - 1) / sms;
-    return share * split < 4 * rounds || (share == 1 && lines_of(r) <= 4);
+    return share * split <= 5 * rounds;
 }
 
 cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, int group, const void *x, const void *wq,
