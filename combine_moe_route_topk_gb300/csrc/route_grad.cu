@@ -1,5 +1,5 @@
-// Gradient of the router's weights with respect to its logits, one warp per
-// token, and the sum over the tokens that a bias gets.
+// Gradient of the router's weights with respect to its logits, and the sum over
+// the tokens that a bias gets.
 //
 // With h the gradient of the weights w and d = sum_k h_k w_k:
 //   softmax                dz_e = p_e (h_e - d): every logit is read
@@ -75,7 +75,10 @@ __device__ __forceinline__ float sum_same(int e, float v, int lane) {
 
 // Entries at the chosen experts only.  A warp takes 32 / P tokens at once, P the
 // power of two that holds their R experts: its loads are whole lines and it
-// has 32 gathers of logits under way.
+// has 32 gathers of logits under way (65536 tokens, 8 of 256 experts, sigmoid
+// renormalised: 18.7 us; with a token a warp 27.5).  HBM bounds that: the zeros and entries
+// are 67 MB, and a gathered logit costs 64 bytes, 34 MB in all, of which
+// 118 MB a copy would make 17.4 us.
 template <int P, bool kVec4>
 __global__ void __launch_bounds__(kThreads)
 route_grad_chosen_kernel(const float *__restrict__ logits, const float *__restrict__ bias, int64_t NT, int E, int R,
@@ -107,7 +110,9 @@ route_grad_chosen_kernel(const float *__restrict__ logits, const float *__restri
     if (c.e >= 0) dlogits[g * E + c.e] = at;
 }
 
-// Softmax over all experts: lane l holds J of them, four in a row at a time.
+// Softmax over all experts: lane l holds J of them, four in a row at a time.  A
+// token's logits are read once (its chosen ones again, from L1); the row is
+// written as if nothing had been chosen, then the chosen entries.
 template <int J, bool kVec4>
 __global__ void __launch_bounds__(kThreads)
 route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restrict__ bias, int64_t NT, int E, int R,
@@ -176,26 +181,47 @@ route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restr
 // ---- bias ------------------------------------------------------------------
 
 // dbias[e] = sum over the tokens of dlogits[g][e], which the kernel before has
-// just written.  A cluster of kCluster blocks takes `width` columns, at most a
-// 16th of them, so that up to 128 SMs read; a block's threads take one column
-// each of 1024 / width rows at a time.  A thread adds kRunRows values in f32,
-// those sums in 64 bits; the block adds its threads' in a tree and the first
-// block the others' in their order.  (With 32 columns a cluster and 256 threads
-// a block, 25734 tokens of 38 experts took 38.7 us, gradient and sum.)
+// just written.  A cluster of kCluster blocks takes `width` columns, a 32nd of
+// them but whole sectors, so that up to 256 blocks read; a block's threads take
+// one column each of kSumThreads / width rows at a time.  A thread adds kRunRows
+// values in f32 and those sums with what they round off; so does the block its
+// threads' in a tree, and the first block the others' in their order.  No
+// atomics: the same call gives the same bits.  Gradient and sum, us: 4101 tokens of 93
+// experts 7.2 (the gradient alone 3.3), 25734 of 38 16.7 (10.2), 65536 of 256 53 (31), bound by what
+// the threads have under way.  With 1024 threads 8.9, 16.3, 65, 256 7.3, 19.6, 81; in clusters of four
+// 7.7, 20, 85; by a 16th of the columns 7.2, 16.8, 62; 64-bit sums and 1024 threads 11.1, 18.4, 69.
 constexpr int kCluster = 8;
-constexpr int kSumThreads = 1024;
+constexpr int kSumThreads = 512;
 constexpr int kRunRows = 16;
+
+// A sum of f32 numbers and what its roundings took off (Knuth's two-sum): as good
+// as 48 bits, where the GPU has few 64-bit units.
+struct Sum2 {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float v) {
+        const float s = __fadd_rn(hi, v), t = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(v, t)));
+        hi = s;
+    }
+    __device__ __forceinline__ void add(float vhi, float vlo) {
+        add(vhi);
+        lo = __fadd_rn(lo, vlo);
+    }
+    __device__ __forceinline__ float value() const {  // lo is NaN where hi is infinite
+        return isfinite(hi) ? __fadd_rn(hi, lo) : hi;
+    }
+};
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSumThreads)
 column_sum_kernel(const float *__restrict__ d, int64_t NT, int E, int width, float *__restrict__ dbias) {
-    __shared__ double part[kSumThreads];
+    __shared__ float2 part[kSumThreads];
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const int lanes = kSumThreads / width;  // rows at a time
     const int c = threadIdx.x % width, lane = threadIdx.x / width, e = (int)(blockIdx.x / kCluster) * width + c;
     grid_dependency_wait();  // d comes from the kernel before
     grid_launch_dependents();
-    double sum = 0.0;
+    Sum2 sum;
     if (e < E && lane < lanes) {
         const int64_t step = (int64_t)kCluster * lanes;
         for (int64_t g = (int64_t)rank * lanes + lane; g < NT; g += step * kRunRows) {
@@ -207,30 +233,34 @@ column_sum_kernel(const float *__restrict__ d, int64_t NT, int E, int width, flo
             }
 #pragma unroll
             for (int i = 0; i < kRunRows; ++i) run += v[i];
-            sum += run;
+            sum.add(run);
         }
     }
-    part[threadIdx.x] = sum;
+    part[threadIdx.x] = make_float2(sum.hi, sum.lo);
     __syncthreads();
     for (int n = lanes; n > 1;) {
         const int half = (n + 1) / 2;
-        if (lane < n - half) part[threadIdx.x] += part[threadIdx.x + half * width];
+        if (lane < n - half) {
+            const float2 o = part[threadIdx.x + half * width];
+            sum.add(o.x, o.y);
+            part[threadIdx.x] = make_float2(sum.hi, sum.lo);
+        }
         __syncthreads();
         n = half;
     }
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     if (rank == 0 && lane == 0) {
-        double t = 0.0;
+        Sum2 t;
         const uint32_t here = (uint32_t)__cvta_generic_to_shared(&part[c]);
 #pragma unroll
         for (int i = 0; i < kCluster; ++i) {
             uint32_t there;
-            double v;
+            float2 v;
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(i));
-            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(there) : "memory");
-            t += v;
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(there) : "memory");
+            t.add(v.x, v.y);
         }
-        if (e < E) dbias[e] = (float)t;
+        if (e < E) dbias[e] = t.value();
     }
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");  // the sums are read
 }
@@ -280,7 +310,7 @@ cudaError_t launch_route_grad(const float *logits, const float *bias, int64_t NT
 #undef MOE_CASE
     }
     if (e != cudaSuccess || dbias == nullptr) return e;
-    const int width = ((E + 15) / 16 + 7) / 8 * 8;  // whole sectors of a row where E is a multiple of 8
+    const int width = ((E + 31) / 32 + 7) / 8 * 8;  // whole sectors of a row where E is a multiple of 8
     Launch s((E + width - 1) / width * kCluster, stream, kSumThreads);
     return cudaLaunchKernelEx(&s.cfg, column_sum_kernel, static_cast<const float *>(dlogits), NT, E, width, dbias);
 }
