@@ -52,6 +52,8 @@ struct Args {
     int least_shift, most_shift;  // log2 of the warps that share a granule: its limits
     int granules;            // of a matrix
     int stages, lines;       // stages of codes, lines of tokens in shared memory
+    uint32_t grid_inverse;   // 2^32 / blocks, above
+    int first_map;           // of the largest box that a unit can need
 };
 
 // Bytes of a token's line in shared memory: two lines that are read together start 64 bytes apart.
@@ -92,7 +94,7 @@ __device__ __forceinline__ Unit get_unit(const Groups &g, int i, int p, int hi, 
     Unit r;
     r.i = same(find_group(g, a.E, i, p));
     const int at = p - same(g.prefix[r.i]), c = same(g.count[r.i]);
-    r.tt = at / a.granules;
+    r.tt = at < a.granules ? 0 : at / a.granules;
     r.m = at - r.tt * a.granules;
     set_count(r, min(a.granules - r.m, hi - p), a.least_shift, a.most_shift);
     r.row = same(g.row[r.i]) + (r.tt << kTokShift);
@@ -125,7 +127,7 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
         mb_init(placed, kWarps);
         s_gave_up = 0;
         mb_init_fence();
-        for (int i = 0; i < 3; ++i) tma_prefetch_map(&maps.m[i]);
+        for (int i = a.first_map; i < 3; ++i) tma_prefetch_map(&maps.m[i]);
     }
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
@@ -135,8 +137,11 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
         [&](int c, int shift) { return ((c + (1 << shift) - 1) >> shift) * a.granules; }, [](int) { return 0; });
     // A block's granules are a run of all of them: it rarely changes the expert.
     const int total = same(g.prefix[a.E]);
-    const int grid = gridDim.x, at = blockIdx.x, each = total / grid, rest = total - each * grid;
-    const int lo = at * each + at * rest / grid, hi = (at + 1) * each + (at + 1) * rest / grid;  // total * at / grid
+    const int grid = gridDim.x, at = blockIdx.x;
+    int each = (int)__umulhi(total, a.grid_inverse), rest = total - each * grid;
+    if (rest < 0) --each, rest += grid;  // total < 2^30: one too many at most
+    const int lo = at * each + (int)__umulhi(at * rest, a.grid_inverse);  // total * at / grid; products below grid^2 are exact
+    const int hi = (at + 1) * each + (int)__umulhi((at + 1) * rest, a.grid_inverse);
     if (lo == hi) return;  // the whole block
 
     constexpr int kCols = kGated ? kRows / 2 : kRows;  // result columns of a granule
@@ -183,7 +188,7 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
                     for (int b = b0; b < b1; ++b) {
                         const uint32_t dst = codes + slot * kCodes + (b - b0) * unit_rows * 128;
                         for (int q = 0; q < w.count * kRows;) {
-                            const int left = w.count * kRows - q, i = left >= 128 ? 0 : left >= 64 ? 1 : 2;
+                            const int left = w.count * kRows - q, i = max(a.first_map, left >= 128 ? 0 : left >= 64 ? 1 : 2);
                             if constexpr (kGated) tma_load_5d(dst + q * 128, &maps.m[i], bar, b * 128, 0, 0, (f0 + q / 2) / 8, w.i);
                             else tma_load_3d(dst + q * 128, &maps.m[i], bar, b * 128, f0 + q, w.i);
                             q += 128 >> i;
@@ -247,7 +252,8 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
         for (int p = lo; p < hi && ok;) {
             const int split = 1 << w.shift, most = kWarps >> w.shift, unit_rows = most * kRows, rounds = (blocks + split - 1) >> w.shift;
             const int part = warp & (split - 1), sub = warp >> w.shift;
-            if (w.i != held_i || w.tt != held_tt) {  // other tokens
+            const bool fresh = w.i != held_i || w.tt != held_tt;
+            if (fresh) {                             // other tokens
                 if (pending) finish();               // nobody reads the old ones any more
                 if (!ok) break;
                 held_i = w.i, held_tt = w.tt;
@@ -260,12 +266,6 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
                         copy_async<16>(smem_u32(tokens) + to, q * 8 < a.K ? from + q * 16 : a.x, q * 8 < a.K ? 16 : 0);
                     }
                 }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mb_arrive(placed);
-                ok = mb_wait_warp(placed, placed_phase, gave_up);
-                if (!ok) break;
-                placed_phase ^= 1u;
                 x_at = gr < w.n ? held_at : zeros;
                 x_step = gr < w.n ? 2 * kK : 0;
             }
@@ -284,6 +284,14 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
                 codes_at[i] = codes + (part >> 1) * unit_rows * 128 + (sub * kRows + 4 * gr + i) * 128 + ((ch ^ i) << 4);
             const uint32_t scale_at = scales_at + ((part * kK + t * 32) >> a.group_shift) * unit_rows + sub * kRows + 4 * gr;
             uint32_t x = x_at + part * x_step;
+            if (fresh) {  // what a unit needs besides was done while they were on their way
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mb_arrive(placed);
+                ok = mb_wait_warp(placed, placed_phase, gave_up);
+                if (!ok) break;
+                placed_phase ^= 1u;
+            }
             for (int r = 0; r < rounds; ++r, x += x_step << w.shift) {
                 ok = mb_wait_warp(full + 8 * slot, phase, gave_up);
                 if (!ok) break;
@@ -345,6 +353,11 @@ int stages_of(const ExpertRows &r, int K, int lines) {
     const int n = left / (kCodes + kScales);
     return n < kMostStages ? n : kMostStages;
 }
+// Granules of all token tiles, at most.
+int64_t most_units(const ExpertRows &r, int F, int gated) {
+    const int64_t cols = gated ? kRows / 2 : kRows, active = r.pairs < r.E ? r.pairs : r.E;
+    return (active + (r.pairs - active) / kTok) * ((F + cols - 1) / cols);
+}
 int lines_of(const ExpertRows &r) { return r.most < kTok ? (int)r.most : kTok; }
 
 template <bool kGated, bool kF32>
@@ -379,8 +392,7 @@ cudaError_t launch(const CodeMaps &maps, const Args &a, cudaStream_t stream) {
 // 17 : 17, 23 : 17 (1, 1, 2, 4 : 1 / 4); 2 of 8 experts of 2048 x 4096, 8 tokens 17 : 19 (4 : 1),
 // of 4096 x 4096, 32 tokens 35 : 28 (13 : 2).
 bool expert_w4_few(const ExpertRows &r, int K, int F, int gated, int64_t rounds, int split) {
-    const int64_t cols = gated ? kRows / 2 : kRows, granules = (F + cols - 1) / cols, sms = sm_count();
-    const int64_t active = r.pairs < r.E ? r.pairs : r.E, units = (active + (r.pairs - active) / kTok) * granules;
+    const int64_t sms = sm_count(), units = most_units(r, F, gated);
     if (K > (1 << 15) || units >= (1 << 30) || stages_of(r, K, lines_of(r)) < 2) return false;
     const int64_t share = (units + sms - 1) / sms;
     return share * split <= 5 * rounds;
@@ -398,15 +410,19 @@ cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, i
     const int least = blocks > 2 ? 2 : 1;  // two at least: a line of shared memory has two blocks
     int most = least;
     while (most < 4 && (4 << most) <= blocks) ++most;
+    // A block's share bounds its units: of one granule, 32 rows, one map will do.
+    const int64_t sms = sm_count(), share = sms > 0 ? (most_units(r, F, gated) + sms - 1) / sms : 0;
+    if (sms < 2) return cudaErrorInvalidDevice;
+    const int first = share >= 4 ? 0 : share >= 2 ? 1 : 2;
     CodeMaps maps;
     for (int i = 0; i < 3; ++i)
-        if (!encode_w4(&maps.m[i], wq, r.E, K, F, gated, 128 >> i)) return cudaErrorInvalidValue;
+        if (i >= first && !encode_w4(&maps.m[i], wq, r.E, K, F, gated, 128 >> i)) return cudaErrorInvalidValue;
     int shift = 5;
     while ((1 << shift) < group) ++shift;
     const int lines = lines_of(r);
     const Args a{r.offsets, static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(group_scales), row_scales, y,
                  r.cap, r.most, r.pairs, r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift, least,
-                 most, granules, stages_of(r, K, lines), lines};
+                 most, granules, stages_of(r, K, lines), lines, (uint32_t)(0xffffffffu / sms + 1), first};
     if (gated) return launch<true, false>(maps, a, stream);
     return y_f32 ? launch<false, true>(maps, a, stream) : launch<false, false>(maps, a, stream);
 }
