@@ -351,13 +351,16 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                         q[h] = ld_shared128(codes + ((chunk ^ (row & 7)) << 4));
                         code[h] = ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM);
                     }
+                    W4Scales two(0);
+                    static_assert(kChunks % 2 == 0);
                     uint32_t loaded = 0;
 #pragma unroll
                     for (int h = 0; h < kChunks; ++h) loaded ^= q[h].x ^ code[h];
                     if (lane == reader_lane(loaded)) mb_arrive(cempty + 8 * c.slot);
 #pragma unroll
                     for (int h = 0; h < kChunks; ++h) {
-                        const W4Scale s(code[h]);
+                        if (h % 2 == 0) two = W4Scales(code[h] | code[h + 1] << 8);
+                        const W4Scale s = h % 2 == 0 ? two.first : two.second;
                         uint32_t out[16];
                         dequant8(q[h].x, s, magic, out);
                         dequant8(q[h].y, s, magic, out + 4);
@@ -411,9 +414,9 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 // the lanes finishes one
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
-                    const float first = v(j) * scale, second = v(j + 1) * scale;
-                    const float got = __shfl_xor_sync(0xffffffffu, up ? first : second, 8);
-                    const float h = silu_mul(up ? got : first, up ? second : got);
+                    const float one = v(j) * scale, two = v(j + 1) * scale;
+                    const float got = __shfl_xor_sync(0xffffffffu, up ? one : two, 8);
+                    const float h = silu_mul(up ? got : one, up ? two : got);
                     st_shared16(buf + (j + up) * 32 + fl * 2, bf16x2(__float_as_uint(h), 0u));
                 }
                 __syncwarp();

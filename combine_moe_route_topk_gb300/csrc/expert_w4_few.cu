@@ -292,22 +292,17 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
                 if (!ok) break;
                 placed_phase ^= 1u;
             }
-            for (int r = 0; r < rounds; ++r, x += x_step << w.shift) {
+            for (int r = 0; r < mine; ++r, x += x_step << w.shift) {
                 ok = mb_wait_warp(full + 8 * slot, phase, gave_up);
                 if (!ok) break;
-                if (r >= mine) {
-                    __syncwarp();
-                    if (lane == 0) mb_arrive(empty + 8 * slot);
-                    next_slot();
-                    continue;
-                }
                 uint4 c[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) c[i] = ld_shared128(codes_at[i] + slot * kCodes);
                 const uint32_t sc = ld_shared32(scale_at + slot * kScales);
                 if (lane == reader_lane(c[0].x ^ c[1].x ^ c[2].x ^ c[3].x ^ sc)) mb_arrive(empty + 8 * slot);
                 next_slot();
-                const W4Scale s[4] = {W4Scale(sc & 0xff), W4Scale(sc >> 8 & 0xff), W4Scale(sc >> 16 & 0xff), W4Scale(sc >> 24)};
+                const W4Scales s01(sc & 0xffff), s23(sc >> 16);
+                const W4Scale s[4] = {s01.first, s01.second, s23.first, s23.second};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint4 b = ld_shared128(x + j * 64);
@@ -325,6 +320,11 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) sum[i] += acc[i], acc[i] = 0.f;
                 }
+            }
+            for (int r = mine; r < rounds && ok; ++r) {  // of others alone
+                ok = mb_wait_warp(full + 8 * slot, phase, gave_up);
+                if (ok && lane == 0) mb_arrive(empty + 8 * slot);
+                next_slot();
             }
             // The unit before is finished only now: warps that got a block more or less than others need not wait.
             if (ok && pending) finish();

@@ -20,11 +20,21 @@ namespace moe {
 // A group's scale, twice, and what takes the codes' offset off.
 struct W4Scale {
     __nv_bfloat162 s, minus;
-    __device__ __forceinline__ explicit W4Scale(uint32_t code) {  // e4m3; exact in bf16
-        const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
-        const float f = __half2float(__half(h));
+    __device__ __forceinline__ void set(float f) {
         s = __floats2bfloat162_rn(f, f);
         minus = __hmul2(s, __floats2bfloat162_rn(-136.f, -136.f));
+    }
+};
+// Of two e4m3 codes, which are exact in bf16.  (One by one they took seven
+// instructions each, a twelfth of all: 32 of 64 experts, 7168 x 4096 each, one token 103.6 us
+// against 100.7.)
+struct W4Scales {
+    W4Scale first, second;
+    __device__ __forceinline__ explicit W4Scales(uint32_t codes) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        first.set(f.x);
+        second.set(f.y);
     }
 };
 
