@@ -8,11 +8,13 @@
 // consecutive elements serves two products of 16, the order of the reduction
 // being free as long as the tokens' fragments have the same one.  mma.sync takes
 // 2 cycles of an SM for 16 x 16 weights and eight tokens (measured), 128 weights a
-// cycle where HBM brings 44; what bounds the kernel are instructions: some 320 of
+// cycle where HBM brings 44; what bounds the kernel are instructions: some 300 of
 // a warp for 32 x 128 weights, 112 of them the shifts and logic that take nibbles
-// apart, 31 weights a cycle (32 of 64 experts, 7168 x 4096 each, one token: 107 us,
-// loads alone 82, floor 74; two stages of codes are as fast as five).  The tensor core proper would take the same bf16 from
-// TMEM by tiles of 128 rows: more rows at once than a small call has for an SM.
+// apart (each two cycles of its pipe) and 16 mma, 33 weights a cycle (32 of 64
+// experts, 7168 x 4096 each, one token: 100 us, loads alone 82, floor 74; two stages of
+// codes are as fast as five, half the mma 4 us less).  The tensor core proper
+// would take the same bf16 from TMEM by tiles of 128 rows: more rows at once than
+// a small call has for an SM.
 //
 // A block holds one expert's tokens, at most eight, in shared memory, in the
 // order in which lanes read them, and walks through a run of the matrices'
