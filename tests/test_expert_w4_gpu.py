@@ -366,6 +366,27 @@ def test_dense_layer_of_some_tokens(T, K, F, form):
         assert torch.equal(again, y)
 
 
+@pytest.mark.parametrize("share", [1, 2, 3, 5, 6, 7, 11])
+@pytest.mark.parametrize("K,group", [(96, 32), (384, 128), (1056, 32), (2080, 32), (4160, 64)])
+@pytest.mark.parametrize("form", ["bf16", "f32", "gated"])
+def test_blocks_of_any_number_of_granules(share, K, group, form):
+    """Two experts of one and eight rows; `share` granules of 32 matrix rows a block, and an expert's last a part of one."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    b = Batch(1, [1, 8], 12)
+    F = (sms * share // 2 * (16 if form == "gated" else 32)) - 8
+    x, w = b.row_values(K), Weights(b, 2 * F if form == "gated" else F, K, group)
+    y = b.out(F, torch.float32 if form == "f32" else torch.bfloat16)
+    act = SWIGLU if form == "gated" else LINEAR
+    call(b, K, F, act, group, x, w, y, form == "f32")
+    want, mag = ref.product(b, x, w.w)
+    v = b.valid
+    err = ref.sum_error(K, mag) + F32_HALF * want.abs()
+    if form == "gated":
+        want, err = ref.swiglu(want[:, :F], want[:, F:], err[:, :F], err[:, F:])
+    ref.check(y[v], want[v], err[v], F32_HALF if form == "f32" else BF16_HALF, "y")
+    ref.check_untouched(b, y)
+
+
 @pytest.mark.parametrize("counts,K,F", [([3, 1], 544, 136), ([40, 70], 544, 136), ([200, 90], 256, 4104)])
 @pytest.mark.parametrize("form", ["bf16", "gated"])
 def test_arrays_at_their_least_alignment(counts, K, F, form):
