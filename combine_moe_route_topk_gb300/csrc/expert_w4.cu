@@ -102,11 +102,15 @@ __device__ __forceinline__ Tile get_tile(const Groups &g, int E, int e, int t, i
     Tile r;
     r.e = same(find_group(g, E, e, t));
     const int c = same(g.count[r.e]), nt = token_tiles<kTok>(c), at = t - same(g.prefix[r.e]);
-    const int size = mma_tokens(tile_rows(c, nt));
-    const int tt = at % nt;
-    r.m0 = at / nt * m_step;
-    r.row = same(g.row[r.e]) + tt * size;
-    r.n = min(size, c - tt * size);
+    int m = at, first = 0, size = c;
+    if (nt > 1) {  // three divisions, 0.2 us before a block's first load
+        m = at / nt;
+        size = mma_tokens(tile_rows(c, nt));
+        first = (at - m * nt) * size;
+    }
+    r.m0 = m * m_step;
+    r.row = same(g.row[r.e]) + first;
+    r.n = min(size, c - first);
     return r;
 }
 
@@ -178,15 +182,15 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         }
         mb_init(done, 1);
         for (int i = 0; kSplit && i < kStoreWarps; ++i) {
-            mb_init(jfull + 8 * i, a.split - 1);  // the other blocks' sums are here
-            mb_init(jfree + 8 * i, 1);            // this block's have been read
+            mb_init(jfull + 8 * i, 1);  // the other blocks' sums are here: their bytes
+            mb_init(jfree + 8 * i, 1);  // this block's have been read
         }
         s_gave_up = 0;
         mb_init_fence();
         tma_prefetch_map(&map_w);
         for (int i = map_x.first; i < 4; ++i) tma_prefetch_map(&map_x.m[i]);
     }
-    const int rank = kSplit ? same((int)cluster_rank()) : 0, split = kSplit ? a.split : 1;
+    const int rank = kSplit ? same((int)cluster_rank()) : 0, split = kSplit ? a.split : 1, shift = split >> 1;  // its log2
     tc_fence_before();
     if constexpr (kSplit) cluster_sync();
     else __syncthreads();
@@ -195,15 +199,15 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     grid_dependency_wait();  // offsets and rows come from earlier kernels
     grid_launch_dependents();
     constexpr int kStep = kGated ? kM / 2 : kM;  // result columns of a tile
-    const int m_tiles = (a.F + kStep - 1) / kStep, tile0 = blockIdx.x / split, tile_step = gridDim.x / split;
+    const int m_tiles = (a.F + kStep - 1) / kStep, tile0 = blockIdx.x >> shift, tile_step = gridDim.x >> shift;
     const Groups g = make_groups<0, 0, 1>(
         tables, a.offsets, a.E, a.L, a.cap, a.most, a.pairs, tile_step,
         [&](int c, int) { return token_tiles<kTok>(c) * m_tiles; }, [](int) { return 0; });  // syncs the block
     const int tiles = same(g.prefix[a.E]);
     // this block's units of a tile: whole stages of codes
     const int all = (a.K + kK - 1) / kK, stages = (all + kUnits - 1) / kUnits;
-    const int first = kSplit ? stages * rank / split * kUnits : 0;
-    const int units = kSplit ? min(all, stages * (rank + 1) / split * kUnits) : all;
+    const int first = kSplit ? (stages * rank >> shift) * kUnits : 0;
+    const int units = kSplit ? min(all, (stages * (rank + 1) >> shift) * kUnits) : all;
     const int part = kParts ? kPartUnits : units - first;  // units that are summed in TMEM
 
     if constexpr (kParts) {
@@ -449,20 +453,19 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         };
         // Joins the blocks' sums of 32 tokens, v(0) to v(31): the owner of the quarter gets them all, the others give
         // theirs.  A block's sums leave for the owner's memory once what it gave before has been read.
-        const int me = warp - kStoreFirst, owner = quarter % split;
+        const int me = warp - kStoreFirst, owner = quarter & (split - 1);
         uint32_t given = 0;  // parity of the next join
         auto join = [&](float (&v)[32]) {
-            const uint32_t slot = join_at + (quarter / split * 2 + half) * (split - 1) * 4096 + lane * 16;
+            const uint32_t slot = join_at + ((quarter >> shift) * 2 + half) * (split - 1) * 4096 + lane * 16;
             if (rank != owner) {
                 if (!mb_wait_warp_pair(jfree + 8 * me, given ^ 1u, gave_up, kPolls + all * kStepPolls)) return false;
-                const uint32_t to = at_rank(slot + (rank - (rank > owner)) * 4096, owner);
+                const uint32_t to = at_rank(slot + (rank - (rank > owner)) * 4096, owner), bar = at_rank(jfull + 8 * me, owner);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    st_remote128(to + j * 512, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-                asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mb_arrive_remote(at_rank(jfull + 8 * me, owner));
+                    st_async128(to + j * 512, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]), bar);
             } else {
+                if (lane == 0) mb_expect_tx(jfull + 8 * me, (split - 1) * 4096);
+                __syncwarp();
                 if (!mb_wait_warp_pair(jfull + 8 * me, given, gave_up, kPolls + all * kStepPolls)) return false;
                 for (int b = 0; b < split - 1; ++b) {
 #pragma unroll
@@ -558,13 +561,18 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 }
             }
         }
-        // The owner's last arrival must not come after this block is gone.
+        // The owner's last arrival must not come after this block is gone, nor this block's sums after the owner is.
         if (kSplit && ok && rank != owner) mb_wait_warp(jfree + 8 * me, given ^ 1u, gave_up, kPolls + all * kStepPolls);
     }
     __syncwarp();
     tc_fence_before();
-    if constexpr (kSplit) cluster_sync();  // no block leaves while another may reach it
-    else __syncthreads();
+    if constexpr (kSplit) {
+        if (*gave_up) __nanosleep(100000);  // sums that left before it did have landed by then
+        __syncwarp();
+        cluster_sync();  // no block leaves while another may reach it
+    } else {
+        __syncthreads();
+    }
     tc_fence_after();
     if (tid == 0 && s_gave_up) record_timeout();
     if (warp == kMmaWarp) tmem_free(tmem, 512);

@@ -100,8 +100,12 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {  // the s
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_remote128(uint32_t addr, const float4 &v) {  // addr from at_rank
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+// Stores into another block of the cluster (addr and bar from at_rank, of one block) and counts the 16 bytes at `bar`
+// when they are there: nothing to wait for here.  (Plain stores, a fence and an arrival took the one that
+// gives 2000 cycles, the one that gets some 3000 more.)
+__device__ __forceinline__ void st_async128(uint32_t addr, const float4 &v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
                  : "memory");
 }
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1, int c2,
