@@ -192,8 +192,8 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     }
     const int rank = kSplit ? same((int)cluster_rank()) : 0, split = kSplit ? a.split : 1, shift = split >> 1;  // its log2
     tc_fence_before();
-    if constexpr (kSplit) cluster_sync();
-    else __syncthreads();
+    if constexpr (kSplit) cluster_arrive();  // waited for by those who reach the other blocks, and by the others at the end
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)same((int)s_tmem), a_at = tmem + 2 * kTok;
     grid_dependency_wait();  // offsets and rows come from earlier kernels
@@ -395,6 +395,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     } else if (warp < kCodeWarp) {
         // Results: warp w holds matrix rows 32 (w % 4).. of the tile, one per lane, and every other 32 tokens.
         if constexpr (kParts) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kStoreRegs));
+        if constexpr (kSplit) cluster_wait();
         const int quarter = warp & 3, half = (warp - kStoreFirst) >> 2;
         const uint32_t buf = bufs_at + (warp - kStoreFirst) * kBuf;
         const int fl = kGated ? (lane >> 4) * 8 + (lane & 7) : lane, up = (lane >> 3) & 1;
@@ -569,6 +570,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     if constexpr (kSplit) {
         if (*gave_up) __nanosleep(100000);  // sums that left before it did have landed by then
         __syncwarp();
+        if (warp < kStoreFirst || warp >= kCodeWarp) cluster_wait();
         cluster_sync();  // no block leaves while another may reach it
     } else {
         __syncthreads();

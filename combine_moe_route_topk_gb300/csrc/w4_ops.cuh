@@ -100,6 +100,9 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {  // the s
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 // Stores into another block of the cluster (addr and bar from at_rank, of one block) and counts the 16 bytes at `bar`
 // when they are there: nothing to wait for here.  (Plain stores, a fence and an arrival took the one that
 // gives 2000 cycles, the one that gets some 3000 more.)
