@@ -633,16 +633,17 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
     if (sms < 1) return cudaErrorInvalidDevice;
     const bool parts = K > kWhole || (y_f32 && !gated);
     // Where all tiles of 64 tokens leave half or more of the SMs idle, two or four blocks share one (one matrix of
-    // 4096 x 7168, 32 and 64 tokens: 25 and 27 us alone, 21 and 21 in twos, 17 and 19 in fours).
+    // 4096 x 7168, 32, 64 and 128 tokens: 18, 21 and 21 us alone, 13, 15 and 15 in twos, 11, 12 and (not all at once) 16 in fours).
     const int64_t active = r.pairs < r.E ? r.pairs : r.E, step = gated ? kM / 2 : kM;
     const int64_t tiles = (active + (r.pairs - active) / 64) * ((F + step - 1) / step);  // at most
     const int stages = (K + kUnits * kK - 1) / (kUnits * kK);
     const int split = tiles * 4 <= sms && stages >= 4 ? 4 : tiles * 2 <= sms && stages >= 2 ? 2 : 1;
     if (expert_w4_few(r, K, F, gated, (tiles + sms - 1) / sms, split))
         return launch_expert_w4_few(r, K, F, gated, group, x, wq, group_scales, row_scales, y, y_f32, stream);
-    // Tiles of 64 tokens up to 48 rows an expert: 32, 48 and 64 rows (64 experts, K = 7168, F = 2048 gated) take 226,
-    // 236 and 338 us with them, 259, 263 and 265 with tiles of 160.
-    const bool small = split > 1 || r.pairs <= 48 * (int64_t)r.E;
+    // Tiles of 64 tokens up to 48 rows an expert, or where all of them run at once: 48 and 64 rows (64 experts, K = 7168,
+    // F = 2048 gated) take 232 and 330 us with them, 268 and 273 with tiles of 160; one matrix of 4096 x 7168, 160, 256 and
+    // 300 tokens 21, 21 and (160 tiles) 37 against 25, 23 and 25.
+    const bool small = split > 1 || r.pairs <= 48 * (int64_t)r.E || tiles <= sms;
     const int most = small ? 64 : parts ? 128 : 160;
     CUtensorMap map_w;
     TokenMaps map_x;
