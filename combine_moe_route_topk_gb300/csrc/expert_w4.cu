@@ -54,12 +54,15 @@ constexpr int kPartUnits = 512 / kK;  // units of a part of an f32 result's sum
 template <int kTok, bool kParts, bool kF32, bool kSplit>
 struct Shape {
     static constexpr int kSlots = (512 - 2 * kTok) / (kK / 2);
-    // No more sets than slots: a set that came to a slot's use after the next would take
-    // the barrier's phase for the one before.
-    static constexpr int kSets = kTok == 64 ? 4 : 2, kShare = 4 / kSets;  // sets; fours of warps of one, which share a unit
-    static_assert(kSets <= kSlots);
-    static constexpr int kHalf = kTok * 128, kRows = 2 * kHalf;  // bytes of half a unit's token rows, of a slot of them
     static constexpr int kRowSlots = kTok == 64 ? 6 : 4;
+    // Dequantising warps work in sets of four, which take units by turns.  A unit's barriers are those of its slot of
+    // rows; its slot in TMEM is free once the unit kSlots before is done.  Its set waits for that one's barrier: the
+    // barrier's use before is complete then (the set has waited for a unit kSets before that one), and its next use
+    // is this unit or a later one.  Four sets in 8192 rows, call after call: 187 us, two of eight warps 196 (each warp
+    // does what there is besides the codes for half as many of them); two, with barriers for weights and rows apart, 193.
+    static constexpr int kSets = 4;
+    static_assert(kSlots <= kRowSlots && kSets <= kRowSlots && kSets * 4 == kDequantWarps);
+    static constexpr int kHalf = kTok * 128, kRows = 2 * kHalf;  // bytes of half a unit's token rows, of a slot of them
     static constexpr int kCodeStages = kSplit ? (kF32 ? 3 : 4) : kTok == 64 ? 5 : kParts ? 3 : 2;
     static constexpr int kJoin = kSplit ? 24 << 10 : 0;  // other blocks' sums: 8 / S warps, S - 1 blocks, 4 KB
     static constexpr int kThreads = 32 * (kDequantWarps + kStoreWarps + (kParts ? 4 : 3));
@@ -146,7 +149,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     static_assert(!kSplit || kTok == 64);  // one piece of 32 tokens a storing warp
     constexpr int kSlots = S::kSlots, kRows = S::kRows, kRowSlots = S::kRowSlots, kCodeStages = S::kCodeStages, kBuf = S::kBuf;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[2 * kCodeStages + 2 * kRowSlots + 2 * kSlots + 5 + 2 * kStoreWarps];
+    __shared__ __align__(8) unsigned long long bars[2 * kCodeStages + 2 * kRowSlots + 5 + 2 * kStoreWarps];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
@@ -155,9 +158,10 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                    bufs_at = scales_at + kCodeStages * kScales, join_at = bufs_at + kStoreWarps * kBuf,
                    tables_at = join_at + S::kJoin;
     int *tables = reinterpret_cast<int *>(smem_raw + (tables_at - smem_u32(smem_raw)));
-    const uint32_t cfull = smem_u32(bars), cempty = cfull + 8 * kCodeStages, xfull = cempty + 8 * kCodeStages,
-                   xempty = xfull + 8 * kRowSlots, afull = xempty + 8 * kRowSlots, aempty = afull + 8 * kSlots,
-                   tfull = aempty + 8 * kSlots, tempty = tfull + 16, done = tempty + 16, jfull = done + 8, jfree = jfull + 8 * kStoreWarps;
+    // A unit has one pair of barriers, of its rows' slot: `full` counts the rows' bytes and the weights' warps,
+    // `empty` is the mma's one commit for both.
+    const uint32_t cfull = smem_u32(bars), cempty = cfull + 8 * kCodeStages, full = cempty + 8 * kCodeStages,
+                   empty = full + 8 * kRowSlots, tfull = empty + 8 * kRowSlots, tempty = tfull + 16, done = tempty + 16, jfull = done + 8, jfree = jfull + 8 * kStoreWarps;
     volatile int *gave_up = &s_gave_up;
     constexpr int kStoreFirst = kDequantWarps, kCodeWarp = kDequantWarps + kStoreWarps, kRowWarp = kCodeWarp + 1,
                   kMmaWarp = kCodeWarp + 2;
@@ -169,12 +173,8 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
             mb_init(cempty + 8 * i, kDequantWarps);
         }
         for (int i = 0; i < kRowSlots; ++i) {
-            mb_init(xfull + 8 * i, 1);
-            mb_init(xempty + 8 * i, 1);
-        }
-        for (int i = 0; i < kSlots; ++i) {
-            mb_init(afull + 8 * i, 4 * S::kShare);
-            mb_init(aempty + 8 * i, 1);
+            mb_init(full + 8 * i, 1 + 4);
+            mb_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mb_init(tfull + 8 * i, 1);
@@ -263,10 +263,10 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
             e = w.e;
             const int n = mma_tokens(w.n);
             for (int u = first; u < units; ++u) {
-                ok = mb_wait_warp(xempty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                ok = mb_wait_warp(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
                 if (!ok) break;
                 if (elect_one()) {
-                    const uint32_t bar = xfull + 8 * r.slot;
+                    const uint32_t bar = full + 8 * r.slot;
                     mb_expect_tx(bar, 2 * n * 128);
                     uint32_t dst = rows_at + r.slot * kRows;
                     int row = w.row;
@@ -285,11 +285,11 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 r.next();
             }
         }
-        drain_ring(xfull, r);
+        drain_ring(full, r);
     } else if (warp == kMmaWarp) {
         // An mma of few tokens takes 33 cycles, a commit 87 to issue and a wait some 60: what is
         // between the eight mma of a unit is kept short.
-        Ring<kSlots> r;
+        Ring<kSlots> r;  // of weights in TMEM
         Ring<kRowSlots> x;
         Ring<2> acc;
         int e = 0;
@@ -302,7 +302,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 const uint32_t d = tmem + acc.slot * kTok;
                 ok = mb_wait_warp(tempty + 8 * acc.slot, acc.phase ^ 1u, gave_up);
                 for (int u = u0; u < min(u0 + part, units) && ok; ++u) {
-                    ok = mb_wait_warp2(xfull + 8 * x.slot, x.phase, afull + 8 * r.slot, r.phase, gave_up);
+                    ok = mb_wait_warp(full + 8 * x.slot, x.phase, gave_up);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -311,8 +311,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 #pragma unroll
                         for (int i = 0; i < kK / 16; ++i)
                             mma_bf16_tmem(d, da + i * 8, db + (i / 4 * (S::kHalf / 16) + i % 4 * 2), desc, u != u0 || i != 0);
-                        tc_commit(aempty + 8 * r.slot);
-                        tc_commit(xempty + 8 * x.slot);
+                        tc_commit(empty + 8 * x.slot);
                     }
                     __syncwarp();
                     r.next();
@@ -327,14 +326,20 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         __syncwarp();
         mb_drain(done, 0);
     } else if (warp < kDequantWarps) {
-        // A thread has one matrix row and, of a unit, all or a half; the sets take units by turns.
-        constexpr int kSets = S::kSets, kChunks = kK / 32 / S::kShare;
-        const int quarter = warp & 3, set = (warp >> 2) / S::kShare, share = (warp >> 2) % S::kShare, row = quarter * 32 + lane;
+        // A thread has one matrix row; the sets take units by turns.
+        constexpr int kSets = S::kSets, kChunks = kK / 32;
+        const int quarter = warp & 3, set = warp >> 2, row = quarter * 32 + lane;
         const uint32_t magic = w4_magic(), line = smem + row * 128, at = a_at + ((uint32_t)(quarter * 32) << 16);
         Ring<kCodeStages> c;
-        Ring<kSlots> r;  // of the next unit
+        Ring<kSlots> r;     // of the next unit: its slot of TMEM
+        Ring<kRowSlots> x;  // and its barriers, where they are not the same
+        constexpr bool kSame = kSlots == kRowSlots;
+        auto next_unit = [&] {
+            r.next();
+            if constexpr (!kSame) x.next();
+        };
         bool ok = true;
-        int turn = 0;    // the set that takes it
+        int turn = 0;       // the set that takes it
         for (int t = tile0; t < tiles && ok; t += tile_step) {
             for (int u0 = first; u0 < units && ok; u0 += kUnits) {
                 const int n = min(kUnits, units - u0);
@@ -344,14 +349,14 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 ok = mb_wait_warp(cfull + 8 * c.slot, c.phase, gave_up);
                 if (!ok) break;
                 if (mine < n) {
-                    if (mine) r.next();
+                    if (mine) next_unit();
                     const uint32_t codes = line + c.slot * kCodes, scales = scales_at + c.slot * kScales + row;
-                    const uint32_t to = at + r.slot * (kK / 2) + share * (kChunks * 16);
+                    const uint32_t to = at + r.slot * (kK / 2);
                     uint4 q[kChunks];
                     uint32_t code[kChunks];
 #pragma unroll
                     for (int h = 0; h < kChunks; ++h) {  // 32 codes: 16 bytes, of one group
-                        const int chunk = mine * (kK / 32) + share * kChunks + h;
+                        const int chunk = mine * kChunks + h;
                         q[h] = ld_shared128(codes + ((chunk ^ (row & 7)) << 4));
                         code[h] = ld_shared8(scales + (chunk >> (a.group_shift - 5)) * kM);
                     }
@@ -371,7 +376,13 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                         dequant8(q[h].z, s, magic, out + 8);
                         dequant8(q[h].w, s, magic, out + 12);
                         if (h == 0) {
-                            ok = mb_wait_warp(aempty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                            // the unit that had the slot before: kSlots units ago
+                            if constexpr (kSame) {
+                                ok = mb_wait_warp(empty + 8 * r.slot, r.phase ^ 1u, gave_up);
+                            } else {
+                                const int b = x.slot - kSlots;
+                                ok = mb_wait_warp(empty + 8 * (b < 0 ? b + kRowSlots : b), x.phase ^ (b < 0), gave_up);
+                            }
                             if (!ok) break;
                             tc_fence_after();
                         }
@@ -381,13 +392,13 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                     tmem_store_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mb_arrive(afull + 8 * r.slot);
-                    if (mine == 0 && n == 2) r.next();
-                    r.next();
+                    if (lane == 0) mb_arrive(full + 8 * (kSame ? r.slot : x.slot));
+                    if (mine == 0 && n == 2) next_unit();
+                    next_unit();
                 } else {
                     if (lane == 0) mb_arrive(cempty + 8 * c.slot);
-                    if (n == 2) r.next();
-                    r.next();
+                    if (n == 2) next_unit();
+                    next_unit();
                 }
                 c.next();
             }

@@ -77,14 +77,6 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Two barriers with one vote where both are complete already.
-__device__ __forceinline__ bool mb_wait_warp2(uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2,
-                                              volatile int *gave_up) {
-    const bool first = mb_try(bar, parity), second = mb_try(bar2, parity2);
-    if (__all_sync(0xffffffffu, first && second)) return true;
-    return mb_wait_warp(bar, parity, gave_up) && mb_wait_warp(bar2, parity2, gave_up);
-}
-
 __device__ __forceinline__ uint32_t ld_shared8(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
