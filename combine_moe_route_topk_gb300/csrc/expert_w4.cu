@@ -20,10 +20,12 @@
 // a commit 87, a wait for a barrier that is complete 40 to 60.  So a unit has
 // eight mma: with four, 256 tokens of 64 experts (K = 7168, F = 2048 gated) took
 // 356 us, with eight 226.  There the dequantising warps bound it (instructions: 30
-// weights a cycle and SM), with 8192 rows (K = 2048, F = 7168, 166 us) the mma
-// (127 us) and the tokens' way from L2: three slots of tokens, with two stages
-// of codes more, 185 us; in pairs of blocks that load half the tokens each for
-// both 185 as well, so it is not their bytes.
+// weights a cycle and SM), with 8192 rows (K = 2048, F = 7168) the mma, 127 us of
+// 169, and what keeps them waiting: with half the tokens' bytes loaded (for
+// timing alone) it took 6 us less, without the arithmetic on the codes 14, without either 18;
+// call after call the clock comes down and it takes 187.  Three slots of tokens
+// and two stages of codes more: 185 us alone; pairs of blocks that load half the tokens
+// each for both: the same.
 #include <cuda_bf16.h>
 
 #include "expert_w4_internal.cuh"
