@@ -146,6 +146,13 @@ route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restr
         top = fmaxf(top, z[j]);
     }
     top = warp_max(top);
+    bool none = top == -INFINITY;  // nothing to choose from: zeros
+    if (none) {  // uniform; the maximum passes NaN by, whose softmax is NaN
+        bool nan = false;
+#pragma unroll
+        for (int j = 0; j < J; ++j) nan |= isnan(z[j]);
+        none = !__any_sync(kFull, nan);
+    }
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -153,7 +160,6 @@ route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restr
         sum += expert(j) < E ? z[j] : 0.f;
     }
     sum = run_sum<32>(sum);
-    const bool none = top == -INFINITY;  // nothing to choose from: zeros
     const float scale = none ? 0.f : 1.0f / sum, d = none ? 0.f : c.d;
     float *out = dlogits + g * E;
 #pragma unroll

@@ -69,9 +69,10 @@ int moe_dispatch_grad(const MoeDims *dims, const void *dpacked, const int32_t *p
  *   sigmoid                dlogit_e = w_k h_k / (1 + exp(z_e)), else 0
  *   sigmoid, renormalised  dlogit_e = w_k (h_k - d) / (1 + exp(z_e)), else 0
  * Logits of -infinity have weight and gradient 0; softmax over a token's logits
- * that are all -infinity gives zeros.  Weights that are NaN (chosen scores
- * that are all 0, renormalised) give NaN in their token's row.  An expert that a token names twice gets
- * both parts; ids outside [0, E) take no part. */
+ * that are all -infinity gives zeros, over any NaN among them NaN.  Weights
+ * that are NaN (chosen scores that are all 0, renormalised) give NaN in their
+ * token's row.  An expert that a token names twice gets both parts; ids
+ * outside [0, E) take no part. */
 int moe_route_grad(const MoeDims *dims, const float *logits, const float *bias, int score_fn, int renormalize,
                    const int32_t *topk_idx, const float *topk_w, const float *dtopk_w, float *dlogits,
                    float *dbias, void *stream);

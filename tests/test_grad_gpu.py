@@ -252,6 +252,23 @@ def test_route_grad_where_nothing_is_left():
     assert bool((r.dl[1] == 0).all()) and bool(torch.isfinite(r.dl).all()) and bool(torch.isfinite(r.db).all())
 
 
+@pytest.mark.parametrize("E", [3, 36, 93, 1024])
+def test_route_grad_of_logits_that_are_not_numbers(E):
+    """Softmax over a NaN is NaN, whatever the other logits are: also where nothing but NaN and -infinity is left."""
+    r = Router(1, 6, E, 2, "softmax", False, "logit", seed=3)
+    r.logits[1] = float("nan")
+    r.logits[2] = float("-inf")
+    r.logits[2, E - 1] = float("nan")
+    r.logits[3, 0] = float("nan")
+    r.logits[4] = float("-inf")  # nothing left: zeros
+    r.idx.copy_(torch.tensor([[0, E - 1]] * 6, device="cuda"))
+    r.w.fill_(0.25)
+    r.grad()
+    bad = torch.isnan(r.dl)
+    assert bool(bad[1:4].all()) and not bool(bad[[0, 4, 5]].any()) and bool((r.dl[4] == 0).all())
+    assert bool(torch.isnan(r.db).all())
+
+
 @pytest.mark.parametrize("score,renorm,bias", MODES)
 def test_route_grad_of_repeated_and_invalid_ids(score, renorm, bias):
     """An expert that is named twice gets both parts, ids out of range take no part."""
