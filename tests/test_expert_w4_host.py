@@ -147,3 +147,10 @@ def test_slots_are_given_back_by_a_lane_that_depends_on_the_words(name):
     text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, name)).read())
     assert len(re.findall(r"if \(lane == reader_lane\([^;]*\)\) mb_arrive\(c?empty", text)) == 1
     assert len(re.findall(r"mb_arrive\(c?empty", text)) == 2  # the other one is of warps that read nothing
+
+
+def test_a_warps_reads_are_ordered_before_its_one_arrival():
+    """One lane arrives for 32 that have read.  A vote orders no memory, __syncwarp does."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, "w4_ops.cuh")).read())
+    body = re.search(r"int reader_lane\(uint32_t loaded\) \{(.*?)\n\}", text, re.S).group(1)
+    assert "__syncwarp()" in body and "__all_sync" in body
