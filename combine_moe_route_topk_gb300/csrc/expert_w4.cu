@@ -71,6 +71,8 @@ struct Shape {
     static constexpr int kStoreRegs = kTok == 64 ? 104 : 120, kDequantRegs = kTok == 64 ? 64 : 56;
     static_assert(!kParts || 32 * (kStoreWarps * kStoreRegs + kDequantWarps * kDequantRegs + 4 * 40) <= kThreads * 72);
     static constexpr int kBuf = kF32 ? 4096 : 2048;  // a storing warp's: 32 tokens' results, to be written as whole sectors
+    // Barriers: full and empty of the rings, of the two accumulators, the end, and of the storing warps' joins.
+    static constexpr int kBars = 2 * kCodeStages + 2 * kRowSlots + 5 + (kSplit ? 2 * kStoreWarps : 0);
     static constexpr int kSmem = 1024 + kCodeStages * (kCodes + kScales) + kRowSlots * kRows + kStoreWarps * kBuf + kJoin;
 };
 
@@ -151,7 +153,7 @@ expert_w4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     static_assert(!kSplit || kTok == 64);  // one piece of 32 tokens a storing warp
     constexpr int kSlots = S::kSlots, kRows = S::kRows, kRowSlots = S::kRowSlots, kCodeStages = S::kCodeStages, kBuf = S::kBuf;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[2 * kCodeStages + 2 * kRowSlots + 5 + 2 * kStoreWarps];
+    __shared__ __align__(8) unsigned long long bars[S::kBars];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
@@ -597,7 +599,7 @@ template <int kTok, bool kGated, bool kParts, bool kF32>
 cudaError_t launch(const CUtensorMap &map_w, const TokenMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_w4_kernel<kTok, kGated, kParts, kF32, false>;
     using S = Shape<kTok, kParts, kF32, false>;
-    static_assert(S::kSmem + groups_bytes(1024) <= kMostSharedW4);
+    static_assert(S::kSmem + groups_bytes(1024) <= most_shared_w4(S::kBars));
     static thread_local AttrCache attr;
     cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), S::kSmem + groups_bytes(1024));
     if (e != cudaSuccess) return e;
@@ -616,7 +618,7 @@ template <bool kGated, bool kParts, bool kF32>
 cudaError_t launch_split(const CUtensorMap &map_w, const TokenMaps &map_x, const Args &a, cudaStream_t stream) {
     auto kern = expert_w4_kernel<64, kGated, kParts, kF32, true>;
     using S = Shape<64, kParts, kF32, true>;
-    static_assert(S::kSmem + groups_bytes(1024) <= kMostSharedW4);
+    static_assert(S::kSmem + groups_bytes(1024) <= most_shared_w4(S::kBars));
     static thread_local PairCache caches[2];
     PairLaunch l(S::kThreads, S::kSmem + groups_bytes(1024), stream);
     l.attr[1].val.clusterDim.x = a.split;

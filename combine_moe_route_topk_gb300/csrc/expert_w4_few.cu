@@ -38,7 +38,8 @@ constexpr int kRows = 32;        // matrix rows of a granule, which a warp takes
 constexpr int kK = 128;          // reduction elements of its step: 16 bytes of codes a lane and row
 constexpr int kPartSteps = 4;    // steps of a part of an f32 result's sum: 512 elements (bf16 ones: all of a warp's, at most 2^14)
 constexpr int kCodes = kWarps * kRows * kK / 2, kScales = kWarps * kRows * kK / 32;  // bytes of a stage: a step of every warp
-constexpr int kMostStages = 6;
+constexpr int kMostStages = 6, kBars = 2 * kMostStages + 2;
+constexpr int kMostShared = most_shared_w4(kBars);
 constexpr int kSums = kRows * kTok;
 constexpr int kSumLine = kSums;
 constexpr int kRed = 2 * kWarps * (kSumLine + kRows) * 4;  // bytes of the warps' sums and of the rows' scales, twice
@@ -108,7 +109,7 @@ template <bool kGated, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) unsigned long long bars[2 * kMostStages + 2];
+    __shared__ __align__(8) unsigned long long bars[kBars];
     __shared__ int s_gave_up;
     const int tid = threadIdx.x, warp = same(tid / 32), lane = tid % 32;
     const int line = line_bytes(a.K);
@@ -351,7 +352,7 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
 
 // Stages of codes that fit beside the tokens (fewer than two: the kernel does not take the batch).
 int stages_of(const ExpertRows &r, int K, int lines) {
-    const int left = kMostSharedW4 - 1024 - kRed - kZeros - groups_bytes(r.E) - lines * line_bytes(K);
+    const int left = kMostShared - 1024 - kRed - kZeros - groups_bytes(r.E) - lines * line_bytes(K);
     const int n = left / (kCodes + kScales);
     return n < kMostStages ? n : kMostStages;
 }
@@ -366,7 +367,7 @@ template <bool kGated, bool kF32>
 cudaError_t launch(const CodeMaps &maps, const Args &a, cudaStream_t stream) {
     auto kern = expert_w4_few_kernel<kGated, kF32>;
     static thread_local AttrCache attr;
-    cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), kMostSharedW4);
+    cudaError_t e = attr.allow_smem(reinterpret_cast<const void *>(kern), kMostShared);
     if (e != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;

@@ -18,6 +18,8 @@ cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, i
                                  const void *group_scales, const float *row_scales, void *y, int y_f32,
                                  cudaStream_t stream);
 cudaError_t take_expert_w4_few_error(int *err);
-constexpr int kMostSharedW4 = 227 * 1024 - 256;  // dynamic shared memory of a block, beside the few static words
+// Dynamic shared memory that a block may have beside its `bars` barriers and the
+// other static words (two of the kernel's own, two of make_groups).
+constexpr int most_shared_w4(int bars) { return 227 * 1024 - (8 * bars + 64); }
 
 }  // namespace moe

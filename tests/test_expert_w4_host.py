@@ -2,6 +2,7 @@
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -154,3 +155,42 @@ def test_a_warps_reads_are_ordered_before_its_one_arrival():
     text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, "w4_ops.cuh")).read())
     body = re.search(r"int reader_lane\(uint32_t loaded\) \{(.*?)\n\}", text, re.S).group(1)
     assert "__syncwarp()" in body and "__all_sync" in body
+
+
+BOUNDS = """
+#include <stdio.h>
+#include "expert_w4.cu"
+namespace moe {
+template <int kTok, bool kParts, bool kF32, bool kSplit>
+void show() {
+    using S = Shape<kTok, kParts, kF32, kSplit>;
+    printf("%d %d %d %d %d %d\\n", kTok, kParts, kF32, kSplit, S::kSmem + groups_bytes(1024), most_shared_w4(S::kBars));
+}
+void show_all() {
+    show<160, false, false, false>(), show<128, true, false, false>(), show<128, true, true, false>();
+    show<64, false, false, false>(), show<64, true, false, false>(), show<64, true, true, false>();
+    show<64, false, false, true>(), show<64, true, false, true>(), show<64, true, true, true>();
+}
+}
+int main() { moe::show_all(); }
+"""
+
+
+def test_a_blocks_shared_memory_fits_beside_its_static_words(lib, tmp_path):
+    """227 KB hold the largest dynamic part that a kernel asks for and the static words that the compiler finds."""
+    (tmp_path / "bounds.cu").write_text(BOUNDS)
+    r = subprocess.run([_build.nvcc(), *_build.ARCH, *_build.NVCC_FLAGS, "-Xptxas", "-v", "-o", str(tmp_path / "bounds"),
+                        str(tmp_path / "bounds.cu"), _build.LIB, "-Xlinker", "-rpath=" + os.path.dirname(_build.LIB)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    static = {}
+    for kernel, info in re.findall(r"Compiling entry function '(\w*expert_w4_kernel\w*)'.*?Used ([^\n]*)", r.stdout + r.stderr, re.S):
+        tok, _, parts, f32, split = re.search(r"Li(\d+)ELb(\d)ELb(\d)ELb(\d)ELb(\d)E", kernel).groups()
+        key = (tok, parts, f32, split)
+        static[key] = max(static.get(key, 0), int(re.search(r"(\d+) bytes smem", info).group(1)))
+    shown = subprocess.run([str(tmp_path / "bounds")], capture_output=True, text=True, check=True).stdout.splitlines()
+    assert len(shown) == len(static) == 9
+    for line in shown:
+        *key, dynamic, most = line.split()
+        assert int(dynamic) <= int(most), key
+        assert int(most) + static[tuple(key)] <= 227 * 1024, key
