@@ -32,13 +32,12 @@
 #include "pdl.cuh"
 #include "tc_ops.cuh"
 #include "w4_ops.cuh"
+#include "w4_rule.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kM = 128;            // matrix rows of a tile
-constexpr int kK = 128;            // reduction elements of a unit: what one slot of TMEM and one of token rows hold
-constexpr int kUnits = 2;          // units of a stage of codes: 256 codes, one 128-byte line of a row
+using namespace w4_tile;
 constexpr int kCodes = kM * 128, kScales = 8 * kM;  // bytes of a stage
 constexpr int kDequantWarps = 16;  // in sets, which turn units into bf16 by turns
 constexpr int kStoreWarps = 8;
@@ -646,20 +645,11 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
                                   cudaStream_t stream) {
     const int sms = sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
-    const bool parts = K > kWhole || (y_f32 && !gated);
-    // Where all tiles of 64 tokens leave half or more of the SMs idle, two or four blocks share one (one matrix of
-    // 4096 x 7168, 32, 64 and 128 tokens: 18, 21 and 21 us alone, 13, 15 and 15 in twos, 11, 12 and (not all at once) 16 in fours).
-    const int64_t active = r.pairs < r.E ? r.pairs : r.E, step = gated ? kM / 2 : kM;
-    const int64_t tiles = (active + (r.pairs - active) / 64) * ((F + step - 1) / step);  // at most
-    const int stages = (K + kUnits * kK - 1) / (kUnits * kK);
-    const int split = tiles * 4 <= sms && stages >= 4 ? 4 : tiles * 2 <= sms && stages >= 2 ? 2 : 1;
-    if (expert_w4_few(r, K, F, gated, (tiles + sms - 1) / sms, split))
+    const W4Form form = w4_form(r, K, F, gated, y_f32, sms);
+    if (form.tokens == w4_few::kTok)
         return launch_expert_w4_few(r, K, F, gated, group, x, wq, group_scales, row_scales, y, y_f32, stream);
-    // Tiles of 64 tokens up to 48 rows an expert, or where all of them run at once: 48 and 64 rows (64 experts, K = 7168,
-    // F = 2048 gated) take 232 and 330 us with them, 268 and 273 with tiles of 160; one matrix of 4096 x 7168, 160, 256 and
-    // 300 tokens 21, 21 and (160 tiles) 37 against 25, 23 and 25.
-    const bool small = split > 1 || r.pairs <= 48 * (int64_t)r.E || tiles <= sms;
-    const int most = small ? 64 : parts ? 128 : 160;
+    const bool parts = w4_parts(K, gated, y_f32), small = form.tokens == 64;
+    const int most = form.tokens;
     CUtensorMap map_w;
     TokenMaps map_x;
     if (!encode_w4(&map_w, wq, r.E, K, F, gated, kM)) return cudaErrorInvalidValue;
@@ -673,7 +663,7 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
     int shift = 5;
     while ((1 << shift) < group) ++shift;
     const Args a{r.offsets, static_cast<const uint8_t *>(group_scales), row_scales, y, r.cap, r.most, r.pairs,
-                 r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift, split};
+                 r.E, r.L, K, F, gated ? 2 * F : F, K / group, shift, form.split};
     if (gated) return parts ? launch_any<true, true, false>(small, map_w, map_x, a, stream) : launch_any<true, false, false>(small, map_w, map_x, a, stream);
     if (y_f32) return launch_any<false, true, true>(small, map_w, map_x, a, stream);
     return parts ? launch_any<false, true, false>(small, map_w, map_x, a, stream) : launch_any<false, false, false>(small, map_w, map_x, a, stream);

@@ -28,22 +28,14 @@
 #include "pdl.cuh"
 #include "tc_ops.cuh"
 #include "w4_ops.cuh"
+#include "w4_rule.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 16, kThreads = 32 * (kWarps + 2);
-constexpr int kTokShift = 3, kTok = 1 << kTokShift;
-constexpr int kRows = 32;        // matrix rows of a granule, which a warp takes: two of mma's 16
-constexpr int kK = 128;          // reduction elements of its step: 16 bytes of codes a lane and row
+using namespace w4_few;
+constexpr int kThreads = 32 * (kWarps + 2);
 constexpr int kPartSteps = 4;    // steps of a part of an f32 result's sum: 512 elements (bf16 ones: all of a warp's, at most 2^14)
-constexpr int kCodes = kWarps * kRows * kK / 2, kScales = kWarps * kRows * kK / 32;  // bytes of a stage: a step of every warp
-constexpr int kMostStages = 6, kBars = 2 * kMostStages + 2;
-constexpr int kMostShared = most_shared_w4(kBars);
-constexpr int kSums = kRows * kTok;
-constexpr int kSumLine = kSums;
-constexpr int kRed = 2 * kWarps * (kSumLine + kRows) * 4;  // bytes of the warps' sums and of the rows' scales, twice
-constexpr int kZeros = 256;           // bytes that stand for the tokens of a fragment that are not there
 
 struct Args {
     const int32_t *offsets;
@@ -58,9 +50,6 @@ struct Args {
     uint32_t grid_inverse;   // 2^32 / blocks, above
     int first_map;           // of the largest box that a unit can need
 };
-
-// Bytes of a token's line in shared memory: two lines that are read together start 64 bytes apart.
-__host__ __device__ constexpr int line_bytes(int K) { return (K + kK - 1) / kK * (kK * 2) + 64; }
 
 __device__ __forceinline__ void mma_m16n8k16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
@@ -229,7 +218,7 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
             if (!ok) return;
             const float *from = red + (buf ^ 1) * (kWarps * (kSumLine + kRows)), *scales = from + kWarps * kSumLine;
             const int split = 1 << done.shift, most = kWarps >> done.shift;
-            for (int j = tid; j < most * kSums; j += 32 * kWarps) {
+            for (int j = tid; j < most * kSumLine; j += 32 * kWarps) {
                 int e = j;
                 if constexpr (kGated) e = (e & ~15) + (e & 1) * 8 + (e >> 1 & 7);  // gate and up in neighbouring lanes
                 const int which = e >> 8, i = e >> 5 & 7, l = e & 31;
@@ -350,19 +339,6 @@ expert_w4_few_kernel(const __grid_constant__ CodeMaps maps, const Args a) {
     if (tid == 0 && s_gave_up) record_timeout();
 }
 
-// Stages of codes that fit beside the tokens (fewer than two: the kernel does not take the batch).
-int stages_of(const ExpertRows &r, int K, int lines) {
-    const int left = kMostShared - 1024 - kRed - kZeros - groups_bytes(r.E) - lines * line_bytes(K);
-    const int n = left / (kCodes + kScales);
-    return n < kMostStages ? n : kMostStages;
-}
-// Granules of all token tiles, at most.
-int64_t most_units(const ExpertRows &r, int F, int gated) {
-    const int64_t cols = gated ? kRows / 2 : kRows, active = r.pairs < r.E ? r.pairs : r.E;
-    return (active + (r.pairs - active) / kTok) * ((F + cols - 1) / cols);
-}
-int lines_of(const ExpertRows &r) { return r.most < kTok ? (int)r.most : kTok; }
-
 template <bool kGated, bool kF32>
 cudaError_t launch(const CodeMaps &maps, const Args &a, cudaStream_t stream) {
     auto kern = expert_w4_few_kernel<kGated, kF32>;
@@ -384,23 +360,6 @@ cudaError_t launch(const CodeMaps &maps, const Args &a, cudaStream_t stream) {
 
 }  // namespace
 
-// Which kernel takes a batch, by what an SM has to do at most: here `share`
-// granules of 32 rows by eight tokens, there `rounds` of tiles of 128 rows by 64
-// tokens, each in `split` blocks.  A tile takes as long as some five granules.
-// Here against there, us (granules : tiles / split), K = 7168, F = 2048 gated, 8 of
-// 64 experts a token: 1, 2, 4, 8 tokens 37 : 44 (7 : 2), 60 : 72 (14 : 4), 101 : 105
-// (27 : 7), 148 : 166 (54 : 14), 16, 32, 48 179 : 187 (61 : 14), 212 : 218 (75 : 15), 246 : 232
-// (88 : 15); K = 2048, F = 7168, 8, 24, 48 tokens 87 : 85 (95 : 24), 115 : 113 (118 : 25),
-// 141 : 121 (154 : 26); one matrix of 4096 x 7168, 1, 8, 16, 32 tokens 13 : 17, 15 : 17,
-// 17 : 17, 23 : 17 (1, 1, 2, 4 : 1 / 4); 2 of 8 experts of 2048 x 4096, 8 tokens 17 : 19 (4 : 1),
-// of 4096 x 4096, 32 tokens 35 : 28 (13 : 2).
-bool expert_w4_few(const ExpertRows &r, int K, int F, int gated, int64_t rounds, int split) {
-    const int64_t sms = sm_count(), units = most_units(r, F, gated);
-    if (K > (1 << 15) || units >= (1 << 30) || stages_of(r, K, lines_of(r)) < 2) return false;
-    const int64_t share = (units + sms - 1) / sms;
-    return share * split <= 5 * rounds;
-}
-
 cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, int group, const void *x, const void *wq,
                                  const void *group_scales, const float *row_scales, void *y, int y_f32,
                                  cudaStream_t stream) {
@@ -414,7 +373,7 @@ cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, i
     int most = least;
     while (most < 4 && (4 << most) <= blocks) ++most;
     // A block's share bounds its units: of one granule, 32 rows, one map will do.
-    const int64_t sms = sm_count(), share = sms > 0 ? (most_units(r, F, gated) + sms - 1) / sms : 0;
+    const int64_t sms = sm_count(), share = sms > 0 ? (most_granules(r, F, gated) + sms - 1) / sms : 0;
     if (sms < 2) return cudaErrorInvalidDevice;
     const int first = share >= 4 ? 0 : share >= 2 ? 1 : 2;
     CodeMaps maps;

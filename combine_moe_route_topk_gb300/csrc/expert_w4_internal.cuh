@@ -11,15 +11,10 @@ cudaError_t launch_expert_gemm_w4(const ExpertRows &r, int K, int F, int gated, 
                                   cudaStream_t stream);
 cudaError_t take_expert_w4_error(int *err);
 
-// The form for experts with few rows: whether it takes a batch that the other
-// would do in `rounds` of tiles, each in `split` blocks, and its launch.
-bool expert_w4_few(const ExpertRows &r, int K, int F, int gated, int64_t rounds, int split);
+// The form for experts with few rows.
 cudaError_t launch_expert_w4_few(const ExpertRows &r, int K, int F, int gated, int group, const void *x, const void *wq,
                                  const void *group_scales, const float *row_scales, void *y, int y_f32,
                                  cudaStream_t stream);
 cudaError_t take_expert_w4_few_error(int *err);
-// Dynamic shared memory that a block may have beside its `bars` barriers and the
-// other static words (two of the kernel's own, two of make_groups).
-constexpr int most_shared_w4(int bars) { return 227 * 1024 - (8 * bars + 64); }
 
 }  // namespace moe
