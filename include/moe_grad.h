@@ -35,6 +35,8 @@ extern "C" {
  *           rounded once; other rows are left as they were
  *   dtopk_w f32 [N*T][R] (out): sum over h of dout[g][h] y[pos[g][k]][h]
  * Pairs with pos < 0 (or outside [0, N*cap)) have no row and get dtopk_w = 0.
+ * Rows of two pairs, which moe_dispatch_count never gives, end up with one of
+ * their products, not with the sum.
  * dout, y and dy must be 16-byte aligned. */
 int moe_combine_grad(const MoeDims *dims, const void *dout, const void *y, const int32_t *pos,
                      const float *topk_w, void *dy, float *dtopk_w, void *stream);

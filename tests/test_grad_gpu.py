@@ -126,6 +126,66 @@ def test_rows_out_of_range_take_no_part():
     assert bool((dx[0] == 0).all()) and bool((dx[2] == 0).all()) and torch.equal(dx[1], y[0])
 
 
+@pytest.mark.parametrize("kind", TYPES)
+def test_rows_beyond_32_bit_offsets(kind):
+    """The last rows of regions of more than 2^31 elements, for blocks and for warps a token."""
+    for T, R, H in ((4, 2, 4096), (2080, 2, 2056)):
+        cap = (1 << 31) // H + 2 * T * R
+        b = Routed(1, T, 4, R, H, cap, 5, kind=kind)
+        b.pos.copy_(cap - 1 - torch.randperm(T * R, generator=b.g, device="cuda").view(T, R))
+        p = b.pos.long()
+        y = torch.empty(cap, H, dtype=b.t, device="cuda")
+        y[cap - T * R:] = b.randn(T * R, H)
+        dout, w = b.randn(T, H), b.randn(T, R, dtype=torch.float32)
+        dy, dw = torch.full_like(y, SENTINEL), torch.full((T, R), SENTINEL, device="cuda")
+        moe.combine_grad(b.dims, dout, y, b.pos, w, dy, dw)
+        want = w.double().unsqueeze(2) * dout.double().unsqueeze(1)
+        ref.check(dy[p], want, F32_HALF * want.abs(), b.half, "dy")
+        assert all(bool((part == SENTINEL).all()) for part in dy[:cap - T * R].split(1 << 18))
+        yy = y[p].double() * dout.double().unsqueeze(1)
+        ref.check(dw, yy.sum(2), (H + 4) * 2.0 ** -24 * yy.abs().sum(2), F32_HALF, "dtopk_w")
+        del dy
+        dx = torch.full((T, H), SENTINEL, dtype=b.t, device="cuda")
+        moe.dispatch_grad(b.dims, y, b.pos, dx)
+        rows = y[p].double()
+        ref.check(dx, rows.sum(1), (R + 1) * 2.0 ** -24 * rows.abs().sum(1), b.half, "dx")
+
+
+def test_tokens_beyond_32_bit_offsets():
+    """More than 2^31 elements of dout, dx and add; all tokens but the last ones have lost their rows."""
+    H, last = 2056, 300
+    T = (1 << 31) // H + last
+    dims = moe.make_dims(1, T, 2, 1, H, cap_rows=last)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    y, w = torch.randn(last, H, generator=g, device="cuda").to(torch.bfloat16), torch.rand(T, 1, generator=g, device="cuda")
+    pos = torch.full((T, 1), -1, dtype=torch.int32, device="cuda")
+    pos[-last:, 0] = torch.arange(last, dtype=torch.int32, device="cuda").flip(0)
+    dout = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    dout[-last:] = torch.randn(last, H, generator=g, device="cuda").to(torch.bfloat16)
+    dy, dw = torch.full_like(y, SENTINEL), torch.full((T, 1), SENTINEL, device="cuda")
+    moe.combine_grad(dims, dout, y, pos, w, dy, dw)
+    d = dout[-last:].double()
+    ref.check(dy.flip(0), w[-last:].double() * d, F32_HALF * (w[-last:].double() * d).abs(), BF16_HALF, "dy")
+    prod = d * y.flip(0).double()
+    ref.check(dw[-last:, 0], prod.sum(1), (H + 4) * 2.0 ** -24 * prod.abs().sum(1), F32_HALF, "dtopk_w")
+    assert bool((dw[:-last] == 0).all())
+    dx = torch.full_like(dout, SENTINEL)
+    moe.dispatch_grad(dims, y, pos, dx, dout)
+    ref.check(dx[-last:], d + y.flip(0).double(), 2 * 2.0 ** -24 * (d.abs() + y.flip(0).double().abs()), BF16_HALF, "dx")
+    assert all(bool((part == 0).all()) for part in dx[:-last].split(1 << 18))
+
+
+def test_a_row_that_two_pairs_name_is_added_for_both():
+    b = Routed(1, 3, 4, 2, 72, 0, 7)
+    dp = b.randn(b.rows, 72)
+    pos = torch.tensor([[1, 1], [1, 2], [0, -1]], dtype=torch.int32, device="cuda")
+    dx = torch.empty(3, 72, dtype=b.t, device="cuda")
+    moe.dispatch_grad(b.dims, dp, pos, dx)
+    want = torch.stack([2 * dp[1].double(), dp[1].double() + dp[2].double(), dp[0].double()])
+    ref.check(dx, want, 3 * 2.0 ** -24 * want.abs() + 2.0 ** -24 * dp[1:3].double().abs().sum(0), b.half, "dx")
+
+
 def test_long_rows():
     """Rows of 2^20 elements: sums of a thread's vectors are kept short."""
     H = 1 << 20
@@ -315,6 +375,26 @@ def test_route_grad_of_arrays_that_are_not_16_byte_aligned():
         r.logits = torch.cat([torch.zeros(1, device="cuda"), r.logits.flatten()])[1:].view(20, 64)
         r.dl = torch.full((20 * 64 + 3,), SENTINEL, device="cuda")[3:].view(20, 64)
         r.grad().check()
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+def test_logits_beyond_32_bit_offsets(score, renorm):
+    """More than 2^31 logits: the last tokens' gradient is that of a call with them alone."""
+    E, R, last = 1024, 8, 500
+    T = (1 << 31) // E + last
+    few = Router(1, last, E, R, score, renorm, "logit", seed=11).route().grad().check()
+    dims = moe.make_dims(1, T, E, R, 8, cap_rows=8)  # the bound on a region's rows would pass 2^31
+    logits, dl = torch.zeros(T, E, device="cuda"), torch.full((T, E), SENTINEL, device="cuda")
+    idx, w, h = torch.zeros(T, R, dtype=torch.int32, device="cuda"), torch.zeros(T, R, device="cuda"), torch.zeros(T, R, device="cuda")
+    idx[:] = torch.arange(R, device="cuda")
+    logits[-last:], idx[-last:], w[-last:], h[-last:] = few.logits, few.idx, few.w, few.h
+    db = torch.empty(E, device="cuda")
+    moe.route_grad(dims, logits, few.bias, few.fn, renorm, idx, w, h, dl, db)
+    assert torch.equal(dl[-last:], few.dl)
+    assert all(bool((part == 0).all()) for part in dl[:-last].split(1 << 18))
+    # the same numbers in other places of the sum: each of the two within what check allows
+    mag = few.dl.double().abs().sum(0)
+    assert bool(((db.double() - few.db.double()).abs() <= 2 * (16 * 2.0 ** -24 * mag + F32_HALF * (mag + 1e-30))).all())
 
 
 def test_long_sums_over_tokens():
