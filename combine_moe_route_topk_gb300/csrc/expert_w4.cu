@@ -19,11 +19,13 @@
 // 64, 72 with 128, 80 with 144 (measured, A in TMEM); to issue one takes some 25,
 // a commit 87, a wait for a barrier that is complete 40 to 60.  So a unit has
 // eight mma: with four, 256 tokens of 64 experts (K = 7168, F = 2048 gated) took
-// 356 us, with eight 226.  There the dequantising warps bound it (instructions: 30
-// weights a cycle and SM), with 8192 rows (K = 2048, F = 7168) the mma, 127 us of
+// 356 us, with eight 226.  There instructions bound it, 30 weights a cycle and SM: 75 % of
+// the issue slots are in use, by 1650 instructions a unit, 704 of which take codes apart
+// (the others wait, arrive, convert scales, compute addresses and store results); HBM, at
+// 57 %, would bring 44.  With 8192 rows (K = 2048, F = 7168) the mma, 127 us of
 // 169, and what keeps them waiting: with half the tokens' bytes loaded (for
 // timing alone) it took 6 us less, without the arithmetic on the codes 14, without either 18;
-// call after call the clock comes down and it takes 187.  Three slots of tokens
+// call after call the clock comes down and it takes 168 to 198, by the box.  Three slots of tokens
 // and two stages of codes more: 185 us alone; pairs of blocks that load half the tokens
 // each for both: the same.
 #include <cuda_bf16.h>

@@ -8,11 +8,16 @@
 // consecutive elements serves two products of 16, the order of the reduction
 // being free as long as the tokens' fragments have the same one.  mma.sync takes
 // 2 cycles of an SM for 16 x 16 weights and eight tokens (measured), 128 weights a
-// cycle where HBM brings 44; what bounds the kernel are instructions: some 300 of
-// a warp for 32 x 128 weights, 112 of them the shifts and logic that take nibbles
-// apart (each two cycles of its pipe) and 16 mma, 33 weights a cycle (32 of 64
-// experts, 7168 x 4096 each, one token: 100 us, loads alone 82, floor 74; two stages of
-// codes are as fast as five, half the mma 4 us less).  The tensor core proper
+// cycle where HBM brings 44.  The kernel runs at 33 (32 of 64 experts, 7168 x 4096
+// each, one token: 100 us, loads alone 82, floor 74; two stages of codes are as
+// fast as five, half the mma 4 us less) and nothing is used up: a warp takes some 300
+// instructions for 32 x 128 weights, 112 of them the shifts and logic that take nibbles
+// apart (each two cycles of its pipe) and 16 mma, of which the SM could issue
+// 54 weights' worth a cycle.  With 32 tokens of 64 experts (200 to 218 us, floor 148) 60 % of the
+// issue slots are in use, 58 % of the integer and logic pipe, 25 % of the tensor pipe, 63 % of
+// HBM.  What is left are waits: four warps a scheduler, of which 1.5 on average
+// could issue, wait for that pipe, for the results of one another's instructions
+// and for shared memory.  The tensor core proper
 // would take the same bf16 from TMEM by tiles of 128 rows: more rows at once than
 // a small call has for an SM.
 //

@@ -76,9 +76,11 @@ __device__ __forceinline__ float sum_same(int e, float v, int lane) {
 // Entries at the chosen experts only.  A warp takes 32 / P tokens at once, P the
 // power of two that holds their R experts: its loads are whole lines and it
 // has 32 gathers of logits under way (65536 tokens, 8 of 256 experts, sigmoid
-// renormalised: 18.7 us; with a token a warp 27.5).  HBM bounds that: the zeros and entries
-// are 67 MB, and a gathered logit costs 64 bytes, 34 MB in all, of which
-// 118 MB a copy would make 17.4 us.
+// renormalised: 18.7 to 19.4 us; with a token a warp 27.5).  HBM bounds that: call
+// after call (no cache flushed) 67 MB of zeros and entries are written and 51 MB
+// read, 6 of them ids, weights and gradients and 44 the 524288 gathered logits, 85
+// bytes each; a copy of these 118 MB would take 17.4 us.  Without gathers
+// (softmax, renormalised) it writes the same and takes 13 us.
 template <int P, bool kVec4>
 __global__ void __launch_bounds__(kThreads)
 route_grad_chosen_kernel(const float *__restrict__ logits, const float *__restrict__ bias, int64_t NT, int E, int R,
@@ -113,6 +115,11 @@ route_grad_chosen_kernel(const float *__restrict__ logits, const float *__restri
 // Softmax over all experts: lane l holds J of them, four in a row at a time.  A
 // token's logits are read once (its chosen ones again, from L1); the row is
 // written as if nothing had been chosen, then the chosen entries.
+// 65536 tokens of 256 experts 27.7 us, 31 with a bias; a copy of its 140 MB would
+// take 20.7.  Instructions and a warp's one chain bound it: 341 instructions a
+// token fill 76 % of the issue slots, and nothing of the next token is under way
+// while the maximum and the sum go round the warp.  25734 of 38 experts take 11.7
+// from HBM (a copy: 1.3): of a lane's four places there one or two hold a logit.
 template <int J, bool kVec4>
 __global__ void __launch_bounds__(kThreads)
 route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restrict__ bias, int64_t NT, int E, int R,
@@ -193,9 +200,13 @@ route_grad_softmax_kernel(const float *__restrict__ logits, const float *__restr
 // values in f32 and those sums with what they round off; so does the block its
 // threads' in a tree, and the first block the others' in their order.  No
 // atomics: the same call gives the same bits.  Gradient and sum, us: 4101 tokens of 93
-// experts 7.2 (the gradient alone 3.3), 25734 of 38 16.7 (10.2), 65536 of 256 53 (31), bound by what
-// the threads have under way.  With 1024 threads 8.9, 16.3, 65, 256 7.3, 19.6, 81; in clusters of four
-// 7.7, 20, 85; by a 16th of the columns 7.2, 16.8, 62; 64-bit sums and 1024 threads 11.1, 18.4, 69.
+// experts 7.2 (the gradient alone 3.3), 25734 of 38 16.7 (10.2), 65536 of 256 53 (31).  The
+// sum alone then reads 67 MB, half of them still in L2, in 22 us, at half of HBM's rate:
+// a thread's additions of 16 values are one chain, and its next 16 loads are
+// issued behind them, so that little is under way during the additions
+// (loads are half of what the warps wait for).  With 1024 threads 8.9, 16.3, 65, 256 7.3, 19.6,
+// 81; in clusters of four 7.7, 20, 85; by a 16th of the columns 7.2, 16.8, 62; 64-bit sums and
+// 1024 threads 11.1, 18.4, 69.
 constexpr int kCluster = 8;
 constexpr int kSumThreads = 512;
 constexpr int kRunRows = 16;
